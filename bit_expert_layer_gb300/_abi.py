@@ -13,14 +13,17 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_layer.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "moe_layer.h")
-HEADERS = [HEADER, os.path.join(os.path.dirname(_PKG), "include", "gqa_decode.h")]
+HEADERS = [HEADER, os.path.join(os.path.dirname(_PKG), "include", "gqa_decode.h"),
+           os.path.join(os.path.dirname(_PKG), "include", "gqa_kv8.h")]
 
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_ALIGNMENT",
     4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_DEVICE_BOUNDS", 7: "MOE_ERR_WORKSPACE",
+    8: "MOE_ERR_NONFINITE",
 }
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGNMENT = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_BOUNDS, MOE_ERR_WORKSPACE = 4, 5, 6, 7
+MOE_ERR_NONFINITE = 8
 
 
 class MoEError(RuntimeError):
@@ -49,6 +52,25 @@ class MoeWeights(C.Structure):
                 ("sh_gate", MoeQMat), ("sh_up", MoeQMat), ("sh_down", MoeQMat),
                 ("router_w", C.c_void_p), ("router_bias", C.c_void_p), ("shared_gate_w", C.c_void_p),
                 ("norm_w", C.c_void_p)]
+
+
+GQA_KV8_E4M3, GQA_KV8_INT8 = 0, 1
+GQA_ROPE_MAX_PAIRS = 64
+
+
+class GqaKv8Cache(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "error")] + \
+               [(n, C.c_int) for n in ("n_pages", "page_size", "n_kv_heads", "head_size", "format")]
+
+
+class GqaKv8Batch(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("page_table", "lens", "offsets")] + \
+               [(n, C.c_int) for n in ("n_seqs", "max_pages", "n_tokens", "max_new")]
+
+
+class GqaRopePlan(C.Structure):
+    _fields_ = [("turn", C.c_uint64 * GQA_ROPE_MAX_PAIRS), ("axis", C.c_uint8 * GQA_ROPE_MAX_PAIRS),
+                ("head_size", C.c_int), ("rotary", C.c_int), ("n_axes", C.c_int)]
 
 
 _lib = None
@@ -97,6 +119,21 @@ def lib() -> C.CDLL:
         L.gqa_decode_attention.restype = S
         L.gqa_decode_get_error.argtypes = [P]
         L.gqa_decode_get_error.restype = S
+        PC, PB, PR, LL = C.POINTER(GqaKv8Cache), C.POINTER(GqaKv8Batch), C.POINTER(GqaRopePlan), C.c_longlong
+        L.gqa_kv8_append.argtypes = [PC, PB, P, LL, P, LL, P]
+        L.gqa_kv8_append.restype = S
+        L.gqa_kv8_gather.argtypes = [PC, PB, P, P, P]
+        L.gqa_kv8_gather.restype = S
+        L.gqa_kv8_workspace_bytes.argtypes = [PC, I, I]
+        L.gqa_kv8_workspace_bytes.restype = C.c_size_t
+        L.gqa_kv8_attention.argtypes = [PC, PB, P, LL, I, C.c_float, P, P, C.c_size_t, P]
+        L.gqa_kv8_attention.restype = S
+        L.gqa_kv8_get_error.argtypes = [PC]
+        L.gqa_kv8_get_error.restype = S
+        L.gqa_rope_plan_init.argtypes = [PR, I, I, C.c_double, P, P, I, I]
+        L.gqa_rope_plan_init.restype = S
+        L.gqa_rope.argtypes = [PR, P, LL, I, P, LL, I, P, I, P, LL, P, LL, P]
+        L.gqa_rope.restype = S
         L.moe_decode_trace.argtypes = [P, P, C.c_size_t]
         L.moe_decode_trace.restype = S
         L.moe_set_wait_limit_ns.argtypes = [C.c_ulonglong]
@@ -250,6 +287,49 @@ def gqa_decode_attention(q: int, k: int, v: int, lens, B: int, S_max: int, out: 
 
 def gqa_decode_get_error(workspace: int) -> int:
     return int(lib().gqa_decode_get_error(workspace))
+
+
+def gqa_kv8_append(cache: GqaKv8Cache, batch: GqaKv8Batch, k: int, k_stride: int, v: int, v_stride: int,
+                   stream: int = 0) -> None:
+    _check(lib().gqa_kv8_append(cache, batch, k, k_stride, v, v_stride, stream or None), "gqa_kv8_append")
+
+
+def gqa_kv8_gather(cache: GqaKv8Cache, batch: GqaKv8Batch, k_out: int, v_out: int, stream: int = 0) -> None:
+    _check(lib().gqa_kv8_gather(cache, batch, k_out, v_out, stream or None), "gqa_kv8_gather")
+
+
+def gqa_kv8_workspace_bytes(cache: GqaKv8Cache, n_q_heads: int, max_new: int) -> int:
+    return int(lib().gqa_kv8_workspace_bytes(cache, n_q_heads, max_new))
+
+
+def gqa_kv8_attention(cache: GqaKv8Cache, batch: GqaKv8Batch, q: int, q_stride: int, n_q_heads: int, scale: float,
+                      out: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().gqa_kv8_attention(cache, batch, q, q_stride, n_q_heads, scale, out, workspace, workspace_bytes,
+                                   stream or None), "gqa_kv8_attention")
+
+
+def gqa_kv8_get_error(cache: GqaKv8Cache) -> int:
+    return int(lib().gqa_kv8_get_error(cache))
+
+
+def gqa_rope_plan_init(head_size: int, rotary: int, theta: float, inv_freq=None, sections=None,
+                       cyclic: bool = False) -> GqaRopePlan:
+    """inv_freq: rotary / 2 floats or None; sections: the pairs of each axis or None."""
+    plan = GqaRopePlan()
+    f = None if inv_freq is None else (C.c_double * len(inv_freq))(*[float(x) for x in inv_freq])
+    if f is not None and 2 * len(f) != rotary:
+        raise ValueError(f"{len(f)} frequencies given, {rotary // 2} wanted")
+    sec = None if sections is None else (C.c_int * len(sections))(*[int(x) for x in sections])
+    _check(lib().gqa_rope_plan_init(plan, head_size, rotary, theta, None if f is None else C.cast(f, C.c_void_p),
+                                    None if sec is None else C.cast(sec, C.c_void_p),
+                                    1 if sec is None else len(sec), 1 if cyclic else 0), "gqa_rope_plan_init")
+    return plan
+
+
+def gqa_rope(plan: GqaRopePlan, q: int, q_stride: int, n_q_heads: int, k: int, k_stride: int, n_k_heads: int,
+             pos: int, T: int, q_out: int, q_out_stride: int, k_out: int, k_out_stride: int, stream: int = 0) -> None:
+    _check(lib().gqa_rope(plan, q, q_stride, n_q_heads, k or None, k_stride, n_k_heads, pos, T, q_out, q_out_stride,
+                          k_out or None, k_out_stride, stream or None), "gqa_rope")
 
 
 def declared_functions() -> list[str]:

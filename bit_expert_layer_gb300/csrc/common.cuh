@@ -21,7 +21,7 @@ constexpr int GROUP = 64;        // quantisation group along the input dim
 constexpr int SHARED_E = NEXP;   // the shared expert's index in the row tables and token blocks
 
 // ----------------------------------------------------------------- device error word
-enum : uint32_t { ERRBIT_TIMEOUT = 1u, ERRBIT_BOUNDS = 2u };
+enum : uint32_t { ERRBIT_TIMEOUT = 1u, ERRBIT_BOUNDS = 2u, ERRBIT_NONFINITE = 4u };
 // Default time limit of a bounded wait (2 s).  The limit of the waits a launch makes on
 // the work of other threads is a launch parameter (moe_set_wait_limit_ns can shorten it,
 // to exercise the give-up path); the waits of the teardown after a give-up, which let

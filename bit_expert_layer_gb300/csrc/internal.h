@@ -229,6 +229,9 @@ cudaError_t launch_gqa_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v, 
 // A 2-D bf16 tensor map over rows of `cols` elements with a box of 64 x box_rows and the
 // 128-byte swizzle (false, with the failure detail recorded, if encoding fails).
 bool encode_bf16_sw128(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
+// A 2-D byte tensor map over rows of `cols` (64 or 128) bytes with a box of cols x box_rows
+// and the swizzle of the row's width.
+bool encode_u8_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
 cudaError_t set_kernel_attributes();
 // The time limit of the bounded device waits of the next launches (moe_set_wait_limit_ns).
 unsigned long long wait_limit_ns();

@@ -1,0 +1,153 @@
+// kv8_sched.cuh -- how the attention kernels over the 8-bit cache share their work.
+//
+// A tile is TQ consecutive new tokens of one sequence for one key/value head: TQ * G query
+// rows that read the same keys.  Its work is cut into units of U positions, as many as the
+// tile's last token sees.  All tiles' units form one line, ordered by sequence, head and
+// tile, and every CTA takes an equal run of it, so the load is even whatever the lengths
+// are and the lengths can stay on the device.  A CTA's run holds whole tiles and at most
+// one part at either end; the parts of a tile meet through the workspace: each CTA leaves
+// its unnormalised sums in a slot of its own (2 per CTA: a tile that began before the run,
+// a tile that goes on after it), and the last CTA to arrive, by a ticket that belongs to
+// the tile's first CTA, adds them up in the order of the line.  Nothing waits.
+//
+// Nothing is tabulated per tile: a sequence's units up to tile t have a closed form.  With
+// TQ a power of two that divides U, r = U / TQ, `a` the first new token's position and
+// A = (a + U - 1) / TQ, tile i sees a + TQ (i + 1) positions, which is (A + i + 1) / r units
+// (whole divisions; the last tile sees all of the sequence), and the sum of x / r over
+// x = 0 .. X is r q (q - 1) / 2 + q (m + 1) with q = X / r, m = X mod r.
+#pragma once
+
+#include "kv8.cuh"
+
+namespace moe {
+
+constexpr int KV8_MAX_CTAS = 160;
+constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one ticket per CTA
+
+struct Kv8AttnParams {
+  Kv8Cache c;
+  Kv8Batch b;
+  const __nv_bfloat16* q;
+  long long q_stride;
+  __nv_bfloat16* out;
+  int hq, G, tq_shift;
+  float scale_log2;      // score scale * log2(e)
+  unsigned* tickets;     // [KV8_MAX_CTAS], zero between calls
+  float* part;           // [CTA][2][rows][row floats]
+  unsigned long long wait_ns;
+};
+
+// A run of units inside one tile.
+struct Kv8Seg {
+  Kv8Seq s;
+  int b, g, t;           // sequence, key/value head, tile of the sequence
+  int u0, u1, units;     // this run's units, the tile's units
+  int w_first, w_last;   // the CTAs that hold the tile's first and last unit
+};
+
+template <int U>
+__device__ __forceinline__ long long kv8_upto(long long x, int r_shift) {
+  const long long q = x >> r_shift, m = x & ((1ll << r_shift) - 1);
+  return ((q * (q - 1)) << r_shift) / 2 + q * (m + 1);
+}
+
+// Units of tiles 0 .. t - 1 of a sequence (t at most its last tile).
+template <int U>
+__device__ __forceinline__ long long kv8_units_before(const Kv8Seq& s, int tq_shift, int t) {
+  constexpr int US = U == 32 ? 5 : U == 64 ? 6 : U == 128 ? 7 : 8;
+  static_assert((1 << US) == U, "U is 32 to 256");
+  const int rs = US - tq_shift;
+  const long long A = (max(s.first, 0) + U - 1) >> tq_shift;
+  return kv8_upto<U>(A + t, rs) - kv8_upto<U>(A, rs);
+}
+// Units of the last tile: what the sequence's last new token sees, one at least.
+template <int U>
+__device__ __forceinline__ int kv8_units_last(const Kv8Seq& s) {
+  return (max(s.first, 0) + s.n + U - 1) / U;
+}
+template <int U>
+__device__ __forceinline__ long long kv8_units_seq(const Kv8Seq& s, int tq_shift) {
+  if (s.n <= 0) return 0;
+  const int tiles = (s.n + (1 << tq_shift) - 1) >> tq_shift;
+  return kv8_units_before<U>(s, tq_shift, tiles - 1) + kv8_units_last<U>(s);
+}
+
+// The line: prefix[b] = units before sequence b (all heads), in shared memory, filled by
+// the whole CTA (THREADS threads, s_warp: THREADS / 32 words); returns its length.
+template <int U, int THREADS>
+__device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long* prefix, long long* s_warp) {
+  const int tid = threadIdx.x, B = p.b.n_seqs;
+  const int per = (B + THREADS - 1) / THREADS;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
+    if (s.bad && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+    sum += kv8_units_seq<U>(s, p.tq_shift) * p.c.hkv;
+    prefix[b] = sum;                       // inside this thread's run for now
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if ((tid & 31) >= o) incl += v;
+  }
+  if ((tid & 31) == 31) s_warp[tid >> 5] = incl;
+  __syncthreads();
+  long long before = incl - sum, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < (tid >> 5)) before += s_warp[w];
+    total += s_warp[w];
+  }
+  // exclusive: prefix[b] = everything before b
+  long long prev = before;
+  for (int b = b0; b < b1; ++b) {
+    const long long incl_b = before + prefix[b];
+    prefix[b] = prev;
+    prev = incl_b;
+  }
+  if (tid == 0) prefix[B] = total;
+  __syncthreads();
+  return total;
+}
+
+// The segment that starts at unit w of the line and ends with its tile or at w_end.
+template <int U>
+__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w, long long w_end,
+                                          long long share) {
+  Kv8Seg g;
+  int lo = 0, hi = p.b.n_seqs;             // prefix[lo] <= w < prefix[hi]
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (prefix[m] <= w) lo = m; else hi = m;
+  }
+  g.b = lo;
+  g.s = kv8_seq(p.b, p.c.page_shift, lo);
+  const long long per_head = (prefix[lo + 1] - prefix[lo]) / p.c.hkv;
+  const long long x0 = w - prefix[lo];
+  g.g = static_cast<int>(x0 / per_head);
+  const long long x = x0 - g.g * per_head;
+  const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
+  int tl = 0, th = tiles;                  // units before tl <= x < units before th
+  while (th - tl > 1) {
+    const int m = (tl + th) >> 1;
+    if (kv8_units_before<U>(g.s, p.tq_shift, m) <= x) tl = m; else th = m;
+  }
+  g.t = tl;
+  const long long before = kv8_units_before<U>(g.s, p.tq_shift, tl);
+  g.units = tl == tiles - 1 ? kv8_units_last<U>(g.s)
+                            : static_cast<int>(kv8_units_before<U>(g.s, p.tq_shift, tl + 1) - before);
+  g.u0 = static_cast<int>(x - before);
+  const long long left = w_end - w;
+  g.u1 = g.units - g.u0 <= left ? g.units : g.u0 + static_cast<int>(left);
+  g.w_first = static_cast<int>((w - g.u0) / share);
+  g.w_last = static_cast<int>((w - g.u0 + g.units - 1) / share);
+  return g;
+}
+
+// Positions that the tile's last token sees.
+__device__ __forceinline__ int kv8_seg_end(const Kv8Seg& g, int tq_shift) {
+  return max(g.s.first + min((g.t + 1) << tq_shift, g.s.n), 0);
+}
+
+}  // namespace moe

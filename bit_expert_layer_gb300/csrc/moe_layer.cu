@@ -305,6 +305,15 @@ bool moe::encode_bf16_sw128(CUtensorMap* m, const void* base, uint64_t cols, uin
   return encode_bf16_rows(m, base, cols, rows, box_rows);
 }
 
+bool moe::encode_u8_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+  if (!get_encode()) {
+    snprintf(g_detail, sizeof g_detail, "cuTensorMapEncodeTiled entry point unavailable");
+    return false;
+  }
+  return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, cols, rows, cols, static_cast<uint32_t>(cols), box_rows,
+                   cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 namespace {
 
 bool qmat_ok(const moe_qmat_t& q, moe_status_t* st) {
@@ -731,6 +740,7 @@ const char* moe_status_string(moe_status_t s) {
     case MOE_ERR_TIMEOUT: return "device-side wait timed out";
     case MOE_ERR_DEVICE_BOUNDS: return "device-side index out of range";
     case MOE_ERR_WORKSPACE: return "workspace too small";
+    case MOE_ERR_NONFINITE: return "value that is not finite";
   }
   return "unknown status";
 }

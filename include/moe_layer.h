@@ -57,7 +57,8 @@ typedef enum {
     MOE_ERR_CUDA = 4,           /* a CUDA runtime or driver call failed */
     MOE_ERR_TIMEOUT = 5,        /* a device-side bounded wait gave up */
     MOE_ERR_DEVICE_BOUNDS = 6,  /* a device-side index check failed */
-    MOE_ERR_WORKSPACE = 7       /* workspace smaller than moe_workspace_bytes() */
+    MOE_ERR_WORKSPACE = 7,      /* workspace smaller than moe_workspace_bytes() */
+    MOE_ERR_NONFINITE = 8       /* an infinity or a NaN where only finite values can be kept */
 } moe_status_t;
 
 /* The layer's shape.  Only hidden 2048, 256 experts, top-8, intermediate 512, shared
