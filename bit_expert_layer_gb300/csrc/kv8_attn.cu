@@ -1,10 +1,13 @@
 // kv8_attn.cu -- attention over the 8-bit key/value cache: the entry points, and the kernel
 // for few query rows per key/value head (decode, a few drafted tokens).
 //
-// A CTA is 8 warps that share a run of a tile's 32-position pieces, dealt out in turn.  Each
-// warp streams its own pieces (codes of 32 keys and values, TMA boxes with the row's
-// swizzle) through a ring of its own, so that no warp waits for another inside a tile, and
-// computes per piece on mma.sync, R query rows (8 or 16) on the M side:
+// Each of a CTA's 8 warps takes a run of the line of its own (pieces of 32 positions) and
+// works alone: it streams its pieces (codes of 32 keys and values, TMA boxes with the row's
+// swizzle) through a ring of its own, writes out the tiles that lie whole in its run, and
+// leaves the two parts at the run's ends in shared memory for the CTA to join at the end, so
+// the warps meet once per launch.  (A CTA per tile, joined tile by tile, measured 122 us on
+// 64 sequences of 64 to 16384 positions: the short ones cost a barrier round each.)
+// Per piece, on mma.sync, R query rows (8 or 16) on the M side:
 //   S = Q K^T     fp16 with exact operands: codes are exact in fp16, and a query row is
 //                 scaled by a power of two to fit.  The order of the contraction is free, so
 //                 a lane takes 32 consecutive dims of a key, one or two 16-byte loads.
@@ -34,14 +37,25 @@ constexpr int KA_STAGES = 2;                   // pieces in flight per warp
 __host__ __device__ constexpr int ka_half(int D) { return KA_U * D; }       // bytes of a piece's keys (or values)
 __host__ __device__ constexpr int ka_ring(int D) { return KA_WARPS * KA_STAGES * 2 * ka_half(D); }
 __host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, max, sum
-// shared memory: rings (1024-aligned), the warps' partial rows, the line, barriers and words
-__host__ __device__ constexpr int ka_merge(int D, int R) { return KA_WARPS * R * ka_ps(D) * 4; }
+// shared memory: rings (1024-aligned), a part per warp (the tile that began before its run;
+// the tile that goes on after it takes the warp's own ring, which is done by then), the line,
+// what the parts belong to, barriers and words
+__host__ __device__ constexpr int ka_parts(int D, int R) { return KA_WARPS * R * ka_ps(D) * 4; }
+__host__ __device__ constexpr int ka_wsum(int R) { return R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
 __host__ __device__ constexpr int ka_smem(int D, int R, int B) {
-  return 1024 + ka_ring(D) + ka_merge(D, R) + (B + 2) * 8 + KA_WARPS * KA_STAGES * 8 + KA_WARPS * 8 + 64;
+  return 1024 + ka_ring(D) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 + KA_WARPS * (8 + KA_STAGES * 8 + 2 * 32) + 64;
 }
 static_assert(ka_smem(128, 16, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
-static_assert(16 * KV8_MAX_CTAS * 4 <= ka_merge(64, 8) && 16 * KV8_MAX_CTAS * 4 <= ka_merge(64, 16),
-              "the split weights fit the merge scratch");
+static_assert(16 * ka_ps(128) * 4 <= KA_STAGES * 2 * ka_half(128) && 16 * ka_ps(64) * 4 <= KA_STAGES * 2 * ka_half(64),
+              "a warp's part fits its ring");
+
+// What a part belongs to.
+struct __align__(16) KaPart {
+  int b, g, t;           // sequence, key/value head, tile; b < 0: no part
+  int off, n;            // the sequence's first row and new tokens
+  int r_first, r_last;   // the runs of the tile's first and last unit
+  int pad;
+};
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -92,10 +106,12 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   constexpr int PS = ka_ps(D);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* merge = reinterpret_cast<float*>(smem + ka_ring(D));
-  long long* prefix = reinterpret_cast<long long*>(smem + ka_ring(D) + ka_merge(D, R));
-  long long* s_warp = prefix + p.b.n_seqs + 1;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KA_WARPS);
+  float* heads = reinterpret_cast<float*>(smem + ka_ring(D));
+  float* wsum = heads + ka_parts(D, R) / 4;
+  long long* prefix = reinterpret_cast<long long*>(wsum + ka_wsum(R) / 4);
+  long long* s_warp = prefix + p.b.n_seqs + 1 + ((p.b.n_seqs + 1) & 1);      // 16-byte aligned
+  KaPart* meta = reinterpret_cast<KaPart*>(s_warp + KA_WARPS);             // [warp][began before, goes on]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(meta + 2 * KA_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + KA_WARPS * KA_STAGES);
   int* s_last = const_cast<int*>(abort_flag) + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,30 +126,36 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  const long long total = kv8_line<KA_U, KA_THREADS>(p, prefix, s_warp);
-  // a run of at least one piece per warp
-  const long long even = (total + gridDim.x - 1) / gridDim.x;
-  const long long share = even < KA_WARPS ? KA_WARPS : even;
-  const long long w_beg = blockIdx.x * share;
-  const long long w_end = min(total, w_beg + share);
-  if (w_beg >= w_end) return;
+  if (tid < 2 * KA_WARPS) meta[tid].b = -1;
+  Kv8Runs runs;
+  runs.total = kv8_line<KA_U, KA_THREADS>(p, prefix, s_warp);
+  runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x) * KA_WARPS));
+  const int cta = blockIdx.x, run = cta * KA_WARPS + warp;
+  if (cta * KA_WARPS >= runs.n) return;
+  const long long w_beg = run < runs.n ? kv8_run_begin(runs, run) : 0;
+  const long long w_end = run < runs.n ? kv8_run_begin(runs, run + 1) : 0;
 
   // ---- this warp's load cursor: its next piece, and per lane 0..3 the page of one of the
   // piece's blocks (lane & 1: block, lane >> 1: keys or values)
   long long lw = w_beg;
-  Kv8Seg ls = kv8_seg<KA_U>(p, prefix, lw, w_end, share);
-  int lu = ls.u0 + warp, l_end = kv8_seg_end(ls, p.tq_shift);
-  bool more = true;
-  int pid = -1;
-  auto settle = [&] {                 // move on to a segment that has a piece for this warp
-    while (lu >= ls.u1) {
+  Kv8Seg ls;
+  int lu = 0, l_end = 0, pid = -1;
+  bool more = w_beg < w_end;
+  if (more) {
+    ls = kv8_seg<KA_U>(p, prefix, lw, w_end, runs);
+    lu = ls.u0;
+    l_end = kv8_seg_end(ls, p.tq_shift);
+  }
+  auto settle = [&] {                 // the cursor's next piece: its segment and its pages
+    if (!more) return;
+    if (lu >= ls.u1) {
       lw += ls.u1 - ls.u0;
       if (lw >= w_end) {
         more = false;
         return;
       }
-      ls = kv8_seg<KA_U>(p, prefix, lw, w_end, share);
-      lu = ls.u0 + warp;
+      ls = kv8_seg<KA_U>(p, prefix, lw, w_end, runs);
+      lu = ls.u0;
       l_end = kv8_seg_end(ls, p.tq_shift);
     }
     const int pos = lu * KA_U + (lane & 1) * KV8_BLOCK;
@@ -169,7 +191,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
       tma_load_2d_hint(dst, lane >> 1 ? &tm_v : &tm_k, bar, 0, static_cast<int>(row), pol);
     }
     ++issued;
-    lu += KA_WARPS;
+    ++lu;
     settle();
     return sc;
   };
@@ -182,7 +204,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   int taken = 0;
   bool dead = false;      // a wait gave up: nothing more is loaded or computed
   for (long long w = w_beg; w < w_end;) {
-    const Kv8Seg sg = kv8_seg<KA_U>(p, prefix, w, w_end, share);
+    const Kv8Seg sg = kv8_seg<KA_U>(p, prefix, w, w_end, runs);
     const int end = kv8_seg_end(sg, p.tq_shift);
     const int tok0 = sg.t << p.tq_shift;
     const int ntok = min(1 << p.tq_shift, sg.s.n - tok0);
@@ -236,7 +258,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
 #pragma unroll
     for (int i = 0; i < ND; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-    for (int u = sg.u0 + warp; u < sg.u1 && !dead; u += KA_WARPS) {
+    for (int u = sg.u0; u < sg.u1 && !dead; ++u) {
       const int st = taken % KA_STAGES;
       if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, (taken / KA_STAGES) & 1, p.c.err, abort_flag, p.wait_ns))) {
         dead = true;
@@ -359,81 +381,121 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
       sc_next[KA_STAGES - 1] = issue();
     }
 
-    // ---- the warps' rows meet in shared memory: row r of warp w at merge[(w R + r) PS]
+    // ---- the tile's rows: out if the whole tile lies in this run, else a part for the CTA
+    const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
 #pragma unroll
     for (int h = 0; h < R / 8; ++h) {
       float l = l_part[h];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      float* row = merge + (warp * R + g4 + 8 * h) * PS;
-      if (c4 == 0) {
-        row[D] = m_run[h];
-        row[D + 1] = l;
-      }
+      const int r = g4 + 8 * h;
       // block j holds dim (D / 8) n + j of columns n = 2 c4, 2 c4 + 1: this lane's LD dims
-      float* dst = row + LD * c4;
+      if (whole) {
+        if (r < nrows) {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // a row that saw no key: zeros
+          const int tok = r / p.G, hh = r - tok * p.G;
+          __nv_bfloat16* dst =
+              p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + LD * c4;
 #pragma unroll
-      for (int j = 0; j < ND; j += 4) {
-        *reinterpret_cast<float4*>(dst + j) = make_float4(o[j][2 * h], o[j + 1][2 * h], o[j + 2][2 * h], o[j + 3][2 * h]);
-        *reinterpret_cast<float4*>(dst + ND + j) =
-            make_float4(o[j][2 * h + 1], o[j + 1][2 * h + 1], o[j + 2][2 * h + 1], o[j + 3][2 * h + 1]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < ND; j += 8) {
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                x[k] = pack_bf16x2(__float_as_uint(o[j + 2 * k][2 * h + i] * inv),
+                                   __float_as_uint(o[j + 2 * k + 1][2 * h + i] * inv));
+              *reinterpret_cast<uint4*>(dst + ND * i + j) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        }
+      } else {
+        if (sg.u0 == 0) __syncwarp();   // the ring: every lane has read its last piece
+        float* row = (sg.u0 ? heads + warp * R * PS
+                            : reinterpret_cast<float*>(smem + warp * KA_STAGES * 2 * ka_half(D))) + r * PS;
+        if (c4 == 0) {
+          row[D] = m_run[h];
+          row[D + 1] = l;
+        }
+        float* dst = row + LD * c4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < ND; j += 4)
+            *reinterpret_cast<float4*>(dst + ND * i + j) =
+                make_float4(o[j][2 * h + i], o[j + 1][2 * h + i], o[j + 2][2 * h + i], o[j + 3][2 * h + i]);
       }
     }
-    __syncthreads();
-    const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
-    constexpr int TPR = D / 8;                 // threads per row, 8 dims each
-    constexpr int ACT = R * TPR;               // 64 .. 256 threads
-    const int row = tid / TPR, d0 = (tid % TPR) * 8;
+    if (!whole && lane == 0)
+      meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, sg.w_first, sg.w_last, 0};
+    w += sg.u1 - sg.u0;
+  }
+  // a warp that gave up: copies still in flight land before the shared memory goes away
+  for (; taken < issued; ++taken) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar0 + 8 * (taken % KA_STAGES), (taken / KA_STAGES) & 1) &&
+           globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+    }
+  }
+  __syncthreads();
+
+  // ---- the parts meet.  A tile's parts in this CTA are the tail of one warp and the heads
+  // of the warps after it (or heads from warp 0 on, if it began in an earlier CTA).
+  constexpr int TPR = D / 8;                 // threads per row, 8 dims each
+  constexpr int ACT = R * TPR;               // 64 .. 256 threads
+  const int row = tid / TPR, d0 = (tid % TPR) * 8;
+  for (int i0 = -1; i0 < KA_WARPS; ++i0) {
+    const KaPart pt = i0 < 0 ? meta[0] : meta[2 * i0 + 1];
+    if (pt.b < 0) continue;
+    const int last = min(pt.r_last - cta * KA_WARPS, KA_WARPS - 1);   // the tile's last warp here
+    const int c_first = pt.r_first / KA_WARPS, c_last = pt.r_last / KA_WARPS;
+    const auto part = [&](int i) {           // i0: the tail (or nothing, for -1), above: heads
+      return (i == i0 ? reinterpret_cast<const float*>(smem + i * KA_STAGES * 2 * ka_half(D)) : heads + i * R * PS) + row * PS;
+    };
+    const int i1 = max(i0, 0);
     float M = -INFINITY, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (tid < ACT) {
-#pragma unroll
-      for (int i = 0; i < KA_WARPS; ++i) M = fmaxf(M, merge[(i * R + row) * PS + D]);
+      for (int i = i1; i <= last; ++i) M = fmaxf(M, part(i)[D]);
       const float at = M == -INFINITY ? 0.0f : M;
-#pragma unroll
-      for (int i = 0; i < KA_WARPS; ++i) {
-        const float* src = merge + (i * R + row) * PS;
+      for (int i = i1; i <= last; ++i) {
+        const float* src = part(i);
         const float f = exp2f(src[D] - at);
         L = fmaf(f, src[D + 1], L);
 #pragma unroll
         for (int k = 0; k < 8; ++k) O[k] = fmaf(f, src[d0 + k], O[k]);
       }
     }
-    bool write = whole;
-    if (!whole) {
+    bool write = c_first == c_last;
+    if (!write) {
+      const auto slot = [&](int c) { return p.part + ((static_cast<size_t>(c) * 2 + (c == c_first)) * R + row) * PS; };
       if (tid < ACT) {
-        float* dst = p.part + ((static_cast<size_t>(blockIdx.x) * 2 + (sg.u0 == 0)) * R + row) * PS;
+        float* dst = slot(cta);
         *reinterpret_cast<float4*>(dst + d0) = make_float4(O[0], O[1], O[2], O[3]);
         *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(O[4], O[5], O[6], O[7]);
         if (d0 == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, L);
       }
       __threadfence();
       __syncthreads();
+      const int ns = c_last - c_first + 1;
       if (tid == 0) {
-        const unsigned n = static_cast<unsigned>(sg.w_last - sg.w_first + 1);
-        const unsigned k = atomicAdd(p.tickets + sg.w_first, 1u);
-        if (k == n - 1) p.tickets[sg.w_first] = 0u;   // every part has arrived: ready for the next call
-        *s_last = k == n - 1;
+        const bool all = atomicAdd(p.tickets + c_first, 1u) == static_cast<unsigned>(ns) - 1u;
+        if (all) p.tickets[c_first] = 0u;    // every part has arrived: ready for the next call
+        *s_last = all;
       }
       __syncthreads();
       write = *s_last != 0;
       if (write) {
         __threadfence();
-        // slots in the order of the line: the tile's first CTA used its second slot
-        const int ns = sg.w_last - sg.w_first + 1;
-        float* fs = merge;                     // [R][ns] weights of the parts
+        float* fs = wsum;                    // [R][ns] weights of the CTAs' sums, in the order of the line
         L = 0.0f;
-        const auto slot = [&](int i) {
-          return p.part + ((static_cast<size_t>(sg.w_first + i) * 2 + (i == 0)) * R + row) * PS;
-        };
         if (tid < ACT) {
           const int j0 = tid % TPR;
           M = -INFINITY;
-          for (int i = j0; i < ns; i += TPR) M = fmaxf(M, __ldcg(slot(i) + D));
+          for (int i = j0; i < ns; i += TPR) M = fmaxf(M, __ldcg(slot(c_first + i) + D));
 #pragma unroll
           for (int s = TPR / 2; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
           const float at = M == -INFINITY ? 0.0f : M;
           for (int i = j0; i < ns; i += TPR) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(i) + D));
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(c_first + i) + D));
             const float f = exp2f(ml.x - at);
             L = fmaf(f, ml.y, L);
             fs[row * ns + i] = f;
@@ -448,33 +510,24 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
 #pragma unroll 4
           for (int i = 0; i < ns; ++i) {
             const float f = fs[row * ns + i];
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(slot(i) + d0));
-            const float4 b = __ldcg(reinterpret_cast<const float4*>(slot(i) + d0 + 4));
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(slot(c_first + i) + d0));
+            const float4 b = __ldcg(reinterpret_cast<const float4*>(slot(c_first + i) + d0 + 4));
             O[0] = fmaf(f, a.x, O[0]), O[1] = fmaf(f, a.y, O[1]), O[2] = fmaf(f, a.z, O[2]), O[3] = fmaf(f, a.w, O[3]);
             O[4] = fmaf(f, b.x, O[4]), O[5] = fmaf(f, b.y, O[5]), O[6] = fmaf(f, b.z, O[6]), O[7] = fmaf(f, b.w, O[7]);
           }
         }
       }
     }
-    if (write && tid < ACT && row < nrows) {
-      // a row that saw no key has L = 0: zeros
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int tok0 = pt.t << p.tq_shift;
+    if (write && tid < ACT && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
       const int tok = row / p.G, hh = row - tok * p.G;
       uint4 r;
       r.x = pack_bf16x2(__float_as_uint(O[0] * inv), __float_as_uint(O[1] * inv));
       r.y = pack_bf16x2(__float_as_uint(O[2] * inv), __float_as_uint(O[3] * inv));
       r.z = pack_bf16x2(__float_as_uint(O[4] * inv), __float_as_uint(O[5] * inv));
       r.w = pack_bf16x2(__float_as_uint(O[6] * inv), __float_as_uint(O[7] * inv));
-      *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + d0) = r;
-    }
-    __syncthreads();   // the scratch is free for the next segment
-    w += sg.u1 - sg.u0;
-  }
-  // a warp that gave up: copies still in flight land before the shared memory goes away
-  for (; taken < issued; ++taken) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar0 + 8 * (taken % KA_STAGES), (taken / KA_STAGES) & 1) &&
-           globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+      *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(pt.off + tok0 + tok) * p.hq + pt.g * p.G + hh) * D + d0) = r;
     }
   }
 }

@@ -3,12 +3,13 @@
 // A tile is TQ consecutive new tokens of one sequence for one key/value head: TQ * G query
 // rows that read the same keys.  Its work is cut into units of U positions, as many as the
 // tile's last token sees.  All tiles' units form one line, ordered by sequence, head and
-// tile, and every CTA takes an equal run of it, so the load is even whatever the lengths
-// are and the lengths can stay on the device.  A CTA's run holds whole tiles and at most
-// one part at either end; the parts of a tile meet through the workspace: each CTA leaves
-// its unnormalised sums in a slot of its own (2 per CTA: a tile that began before the run,
-// a tile that goes on after it), and the last CTA to arrive, by a ticket that belongs to
-// the tile's first CTA, adds them up in the order of the line.  Nothing waits.
+// tile, and every worker (a CTA, or a warp of it) takes an equal run of the line, so the
+// load is even whatever the lengths are and the lengths can stay on the device.  A run holds
+// whole tiles and at most one part at either end.  The parts of a tile meet first inside
+// the CTA, then through the workspace: each CTA leaves its unnormalised sums in a slot of
+// its own (2 per CTA: a tile that began before the CTA's runs, a tile that goes on after
+// them), and the last CTA to arrive, by a ticket that belongs to the tile's first CTA, adds
+// them up in the order of the line.  Nothing waits.
 //
 // Nothing is tabulated per tile: a sequence's units up to tile t have a closed form.  With
 // TQ a power of two that divides U, r = U / TQ, `a` the first new token's position and
@@ -42,8 +43,23 @@ struct Kv8Seg {
   Kv8Seq s;
   int b, g, t;           // sequence, key/value head, tile of the sequence
   int u0, u1, units;     // this run's units, the tile's units
-  int w_first, w_last;   // the CTAs that hold the tile's first and last unit
+  int w_first, w_last;   // the runs that hold the tile's first and last unit
 };
+
+// The line cut into n runs: run i is units i total / n up to (i + 1) total / n, and unit w
+// belongs to run ((w + 1) n - 1) / total (whole divisions).
+struct Kv8Runs {
+  long long total;
+  int n;
+};
+__device__ __forceinline__ long long kv8_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+__device__ __forceinline__ long long kv8_run_begin(const Kv8Runs& r, int i) { return kv8_div(i * r.total, r.n); }
+__device__ __forceinline__ int kv8_run_of(const Kv8Runs& r, long long w) {
+  return static_cast<int>(kv8_div((w + 1) * r.n - 1, r.total));
+}
 
 template <int U>
 __device__ __forceinline__ long long kv8_upto(long long x, int r_shift) {
@@ -114,7 +130,7 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
 // The segment that starts at unit w of the line and ends with its tile or at w_end.
 template <int U>
 __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w, long long w_end,
-                                          long long share) {
+                                          const Kv8Runs& runs) {
   Kv8Seg g;
   int lo = 0, hi = p.b.n_seqs;             // prefix[lo] <= w < prefix[hi]
   while (hi - lo > 1) {
@@ -123,9 +139,9 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
   }
   g.b = lo;
   g.s = kv8_seq(p.b, p.c.page_shift, lo);
-  const long long per_head = (prefix[lo + 1] - prefix[lo]) / p.c.hkv;
+  const long long per_head = kv8_div(prefix[lo + 1] - prefix[lo], p.c.hkv);
   const long long x0 = w - prefix[lo];
-  g.g = static_cast<int>(x0 / per_head);
+  g.g = static_cast<int>(kv8_div(x0, per_head));
   const long long x = x0 - g.g * per_head;
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
   int tl = 0, th = tiles;                  // units before tl <= x < units before th
@@ -140,8 +156,8 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
   g.u0 = static_cast<int>(x - before);
   const long long left = w_end - w;
   g.u1 = g.units - g.u0 <= left ? g.units : g.u0 + static_cast<int>(left);
-  g.w_first = static_cast<int>((w - g.u0) / share);
-  g.w_last = static_cast<int>((w - g.u0 + g.units - 1) / share);
+  g.w_first = kv8_run_of(runs, w - g.u0);
+  g.w_last = kv8_run_of(runs, w - g.u0 + g.units - 1);
   return g;
 }
 
