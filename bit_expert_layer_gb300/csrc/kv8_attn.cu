@@ -542,19 +542,22 @@ int floor_log2(int n) {
   return s;
 }
 
-// Query rows of a tile: 8 when the group's rows of all new tokens fit.
-int ka_rows(int G, int max_new) { return static_cast<long long>(G) * max_new <= 8 ? 8 : 16; }
-
-size_t kv8_ws_bytes(int D, int rows) {
-  return KV8_TICKET_BYTES + static_cast<size_t>(KV8_MAX_CTAS) * 2 * rows * ka_ps(D) * sizeof(float);
+// Query rows of a tile: 8 or 16 when the group's rows of all new tokens fit, else 0 (the
+// prompt kernel).
+int ka_rows(int G, int max_new) {
+  const long long n = static_cast<long long>(G) * max_new;
+  return n <= 8 ? 8 : n <= 16 ? 16 : 0;
 }
 
-constexpr int MAX_DEVICES = 64;
+size_t kv8_ws_bytes(int D, int rows) {
+  if (!rows) return kv8_prompt_ws_bytes(D);
+  return KV8_TICKET_BYTES + static_cast<size_t>(KV8_MAX_CTAS) * 2 * rows * ka_ps(D) * sizeof(float);
+}
 
 template <int D, int R, int FMT>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8AttnParams& p, int box, int grid, int dev,
                           cudaStream_t s) {
-  static bool set[MAX_DEVICES] = {};
+  static bool set[KV8_MAX_DEVICES] = {};
   auto* k = kv8_decode_kernel<D, R, FMT>;
   if (!set[dev]) {
     const cudaError_t e =
@@ -598,8 +601,8 @@ extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gq
 
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev < 0 || dev >= MAX_DEVICES)) e = cudaErrorInvalidDevice;
-  static int sm_count[MAX_DEVICES] = {};
+  if (e == cudaSuccess && (dev < 0 || dev >= KV8_MAX_DEVICES)) e = cudaErrorInvalidDevice;
+  static int sm_count[KV8_MAX_DEVICES] = {};
   if (e == cudaSuccess && !sm_count[dev]) {
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) sm_count[dev] = sms;
@@ -619,18 +622,26 @@ extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gq
   p.out = static_cast<__nv_bfloat16*>(out);
   p.hq = n_q_heads;
   p.G = G;
-  p.tq_shift = floor_log2(R / G);
+  p.tq_shift = R ? floor_log2(R / G) : 0;
   p.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(D))) * 1.4426950408889634f;
   p.tickets = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KV8_TICKET_BYTES);
   p.wait_ns = wait_limit_ns();
 
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!R) {
+    e = launch_kv8_prompt(p, D, cache->format, grid, dev, s);
+    if (e != cudaSuccess) {
+      set_error_detail("gqa_kv8_attention: launch", e);
+      return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+  }
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(cache->n_pages) * cache->n_kv_heads * cache->page_size;
   const int box = cache->page_size >= KA_U ? KA_U : KV8_BLOCK;
   if (!encode_u8_rows(&tk, cache->k_codes, D, rows, box) || !encode_u8_rows(&tv, cache->v_codes, D, rows, box))
     return MOE_ERR_CUDA;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool e4 = cache->format == GQA_KV8_E4M3;
   if (D == 128 && R == 8)
     e = e4 ? launch_decode<128, 8, GQA_KV8_E4M3>(tk, tv, p, box, grid, dev, s)

@@ -3,7 +3,7 @@
 #pragma once
 
 #include "gqa_kv8.h"
-#include "kv8.cuh"
+#include "kv8_sched.cuh"
 
 namespace moe {
 
@@ -15,5 +15,10 @@ bool kv8_rows_ok(const void* p, long long stride, long long width, moe_status_t*
 
 Kv8Cache kv8_cache(const gqa_kv8_cache_t* c);
 Kv8Batch kv8_batch(const gqa_kv8_batch_t* b);
+
+// Attention with many query rows per key/value head (kv8_prompt.cu): its workspace, and its
+// launch on `grid` CTAs of device `dev` (sets p.tq_shift itself).
+size_t kv8_prompt_ws_bytes(int D);
+cudaError_t launch_kv8_prompt(Kv8AttnParams p, int D, int format, int grid, int dev, cudaStream_t s);
 
 }  // namespace moe

@@ -15,7 +15,8 @@
 // TQ a power of two that divides U, r = U / TQ, `a` the first new token's position and
 // A = (a + U - 1) / TQ, tile i sees a + TQ (i + 1) positions, which is (A + i + 1) / r units
 // (whole divisions; the last tile sees all of the sequence), and the sum of x / r over
-// x = 0 .. X is r q (q - 1) / 2 + q (m + 1) with q = X / r, m = X mod r.
+// x = 0 .. X is r q (q - 1) / 2 + q (m + 1) with q = X / r, m = X mod r.  With TQ = c U it is
+// (a + U - 1) / U + c (i + 1) units.
 #pragma once
 
 #include "kv8.cuh"
@@ -23,6 +24,7 @@
 namespace moe {
 
 constexpr int KV8_MAX_CTAS = 160;
+constexpr int KV8_MAX_DEVICES = 64;
 constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one ticket per CTA
 
 struct Kv8AttnParams {
@@ -72,6 +74,10 @@ template <int U>
 __device__ __forceinline__ long long kv8_units_before(const Kv8Seq& s, int tq_shift, int t) {
   constexpr int US = U == 32 ? 5 : U == 64 ? 6 : U == 128 ? 7 : 8;
   static_assert((1 << US) == U, "U is 32 to 256");
+  if (tq_shift > US) {
+    const long long n = t;
+    return n * ((max(s.first, 0) + U - 1) / U) + ((n * (n + 1) / 2) << (tq_shift - US));
+  }
   const int rs = US - tq_shift;
   const long long A = (max(s.first, 0) + U - 1) >> tq_shift;
   return kv8_upto<U>(A + t, rs) - kv8_upto<U>(A, rs);

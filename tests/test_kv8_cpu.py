@@ -204,6 +204,8 @@ def test_block_units_do_not_meet():
 
 def _before(first, U, tq, t):
     """Units of a sequence's tiles 0 .. t - 1, in closed form."""
+    if tq > U:
+        return t * -(-max(first, 0) // U) + tq // U * t * (t + 1) // 2
     r = U // tq
     F = lambda X: r * (X // r) * (X // r - 1) // 2 + (X // r) * (X % r + 1)  # noqa: E731
     A = (max(first, 0) + U - 1) // tq
@@ -217,7 +219,7 @@ def test_line_of_units(U):
     either end of a run, so that two slots and one ticket per CTA suffice."""
     rng = random.Random(2)
     for _ in range(1500):
-        tq = rng.choice([1, 2, 4, 8, 16, 32])
+        tq = rng.choice([1, 2, 4, 8, 16, 32] + ([64, 128, 256] if U == 128 else []))
         hkv = rng.randint(1, 3)
         seqs = [(rng.choice([0, rng.randint(0, 700)]), rng.choice([1, 1, rng.randint(1, 90)]))
                 for _ in range(rng.randint(1, 6))]
