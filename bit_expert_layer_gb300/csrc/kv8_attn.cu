@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   // ---- this warp's load cursor: its next piece, and per lane 0..3 the page of one of the
   // piece's blocks (lane & 1: block, lane >> 1: keys or values)
   long long lw = w_beg;
-  Kv8Seg ls;
+  Kv8Seg ls = {};
   int lu = 0, l_end = 0, pid = -1;
   bool more = w_beg < w_end;
   if (more) {
@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     lu = ls.u0;
     l_end = kv8_seg_end(ls, p.tq_shift);
   }
+  const Kv8Seg first_seg = ls;
   auto settle = [&] {                 // the cursor's next piece: its segment and its pages
     if (!more) return;
     if (lu >= ls.u1) {
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
         more = false;
         return;
       }
-      ls = kv8_seg<KA_U>(p, prefix, lw, w_end, runs);
+      kv8_next<KA_U>(ls, p, prefix, lw, w_end, runs);
       lu = ls.u0;
       l_end = kv8_seg_end(ls, p.tq_shift);
     }
@@ -203,8 +204,9 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
 
   int taken = 0;
   bool dead = false;      // a wait gave up: nothing more is loaded or computed
+  Kv8Seg sg = first_seg;
   for (long long w = w_beg; w < w_end;) {
-    const Kv8Seg sg = kv8_seg<KA_U>(p, prefix, w, w_end, runs);
+    if (w > w_beg) kv8_next<KA_U>(sg, p, prefix, w, w_end, runs);
     const int end = kv8_seg_end(sg, p.tq_shift);
     const int tok0 = sg.t << p.tq_shift;
     const int ntok = min(1 << p.tq_shift, sg.s.n - tok0);

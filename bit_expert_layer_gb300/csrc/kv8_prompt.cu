@@ -22,6 +22,7 @@
 // Bound: per tile and two row blocks 16.8 MFLOP of MMA (2048 cycles at the nominal rate), and
 // 32768 exponentials.
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv8_host.h"
@@ -40,7 +41,7 @@ constexpr float KP_GROW = 8.0f;                   // the maximum may outgrow the
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 2 * KP_NB * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 16 * 8 + 64;
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 3 * KP_NB * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 16 * 8 + 64;
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
 
@@ -97,12 +98,53 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void bar_softmax(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+// Two fp32 fused multiply-adds / additions in one instruction.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_get(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A tile whose parts lie in several CTAs, left by its first CTA for the kernel that joins them.
+struct __align__(16) KpTile {
+  int ns;                // CTAs (0: no such tile)
+  int t, g, off, n;      // tile, key/value head, the sequence's first row and new tokens
+  int pad[3];
+};
+
+// Workspace of a part: floats of a row (O, reference, normaliser), the rows of CTA c's part of
+// a tile that began in CTA c_first, and the tiles to join, one entry per CTA.
+__host__ __device__ constexpr int kp_ps(int D) { return D + 4; }
+constexpr size_t KP_TILES_BYTES = KV8_MAX_CTAS * sizeof(KpTile);
+__device__ __forceinline__ KpTile* kp_tiles(float* part) { return reinterpret_cast<KpTile*>(part); }
+template <int D>
+__device__ __forceinline__ float* kp_slot(float* part, int c, int c_first, int row) {
+  return part + KP_TILES_BYTES / 4 + ((static_cast<size_t>(c) * 2 + (c == c_first)) * (2 * KP_ROWS) + row) * kp_ps(D);
+}
 
 }  // namespace
 
@@ -111,20 +153,20 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_constant__ Kv8AttnParams p, int nblk) {
   constexpr int TILE = kp_tile(D);
   constexpr int BOX = KP_U * 128;               // bytes of 64 dims of a tile
-  constexpr int PS = D + 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_q = smem;
   uint8_t* s_k = smem + 2 * TILE;
   uint8_t* s_v = smem + 4 * TILE;
-  float* s_ks = reinterpret_cast<float*>(smem + 6 * TILE);    // [slot][8]: K scale, negative: no such block
-  float* s_ve = s_ks + KP_SLOTS * KP_NB;                      // [slot][8]: exponent of the V scale
-  long long* prefix = reinterpret_cast<long long*>(s_ve + KP_SLOTS * KP_NB);
+  // [slot][8] each: K scale, exponent e of the V scale (-inf: no such block), 2^-e
+  float* s_ks = reinterpret_cast<float*>(smem + 6 * TILE);
+  float* s_ve = s_ks + KP_SLOTS * KP_NB;
+  float* s_vi = s_ve + KP_SLOTS * KP_NB;
+  long long* prefix = reinterpret_cast<long long*>(s_vi + KP_SLOTS * KP_NB);
   long long* s_warp = prefix + p.b.n_seqs + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
-  int* s_last = const_cast<int*>(abort_flag) + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_last + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(abort_flag) + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * i; };
@@ -148,7 +190,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   runs.total = kv8_line<KP_U, KP_THREADS>(p, prefix, s_warp);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x)));
   const int cta = blockIdx.x;
-  if (cta >= runs.n) return;                    // the whole CTA, before any TMEM is held
+  if (cta >= runs.n) {                          // the whole CTA, before any TMEM is held
+    if (tid == 0) kp_tiles(p.part)[cta].ns = 0;
+    return;
+  }
   const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
   if (warp == 12) {
     tmem_alloc(smem_u32(s_tmem), 512);
@@ -171,8 +216,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns))) dead = true;
       };
       int it = 0;
+      KpTile tile = {0, 0, 0, 0, 0, {0, 0, 0}};
+      Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w_beg, w_end, runs);
       for (long long w = w_beg; w < w_end;) {
-        const Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w, w_end, runs);
+        if (w > w_beg) kv8_next<KP_U>(sg, p, prefix, w, w_end, runs);
         const int tok = (sg.t << p.tq_shift) + blk * blk_tokens + r / p.G, hh = r % p.G;
         const bool live = r / p.G < blk_tokens && tok < sg.s.n;
         // positions that the row sees; a row without a token (zeros) needs no mask
@@ -217,28 +264,47 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           tc_fence_after();
           const float* ks = s_ks + (it & (KP_SLOTS - 1)) * KP_NB;
           const float* ve = s_ve + (it & (KP_SLOTS - 1)) * KP_NB;
+          const float* vi = s_vi + (it & (KP_SLOTS - 1)) * KP_NB;
           const int left = see - u * KP_U;                       // positions of the tile that the row sees
           const bool edge = __any_sync(0xffffffffu, left < KP_U);
-          // ---- pass 1: the tile's maximum of s_i + e_i
+          // A tile at the causal edge takes a path of its own (EDGE), so that the others carry
+          // no mask: 2 of 5 instructions per score, measured.  The scores are read twice, 32
+          // columns at a time, the next ones while these are worked on: 128 of them in
+          // registers do not fit beside the rest.
+          uint32_t sc[2][32];
+          // ---- pass 1: the maximum of s_i + e_i
           float mx = -INFINITY;
+          const auto largest = [&](auto edge_c) {
+            constexpr bool EDGE = decltype(edge_c)::value;
+            tmem_ld32(t_s, sc[0]);
+#pragma unroll 1
+            for (int c2 = 0; c2 < KP_U / 64; ++c2)
 #pragma unroll
-          for (int c = 0; c < KP_U / 32; ++c) {
-            uint32_t s[32];
-            tmem_ld32(t_s + 32 * c, s);
-            tmem_ld_wait();
-            if (edge)
+              for (int k = 0; k < 2; ++k) {
+                const int c = 2 * c2 + k;
+                tmem_ld_wait();
+                tmem_ld32(t_s + 32 * ((c + 1) & (KP_U / 32 - 1)), sc[k ^ 1]);   // last: pass 2's first
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (32 * c + j >= left) s[j] = 0xFF800000u;
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t* x = sc[k] + 16 * h;
+                  const float f = fminf(rs * ks[2 * c + h], 1e37f), e = ve[2 * c + h];
+                  if (EDGE) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float m = -INFINITY;
+                    for (int j = 0; j < 16; ++j)
+                      if (32 * c + 16 * h + j < left) mx = fmaxf(mx, fmaf(__uint_as_float(x[j]), f, e));
+                  } else {
+                    float m[5];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) m = fmaxf(m, __uint_as_float(s[16 * h + j]));
-              const float k = ks[2 * c + h];
-              if (k >= 0.0f) mx = fmaxf(mx, fmaf(m, fminf(rs * k, 1e38f), ve[2 * c + h]));
-            }
-          }
+                    for (int j = 0; j < 5; ++j)
+                      m[j] = max3(__uint_as_float(x[3 * j]), __uint_as_float(x[3 * j + 1]), __uint_as_float(x[3 * j + 2]));
+                    m[0] = max3(m[0], m[1], __uint_as_float(x[15]));
+                    m[2] = max3(m[2], m[3], m[4]);
+                    mx = fmaxf(mx, fmaf(fmaxf(m[0], m[2]), f, e));
+                  }
+                }
+              }
+          };
+          if (edge) largest(std::true_type{}); else largest(std::false_type{});
           // ---- the reference moves: O and the normaliser follow
           const bool grow = mx > m_ref + KP_GROW;                // also the first finite maximum
           if (__any_sync(0xffffffffu, grow)) {
@@ -263,33 +329,41 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           }
           const float m_at = m_ref == -INFINITY ? 0.0f : m_ref;
           // ---- pass 2: weights, over the scores that were read
+          const auto weights = [&](auto edge_c) {
+            constexpr bool EDGE = decltype(edge_c)::value;
+#pragma unroll 1
+            for (int c2 = 0; c2 < KP_U / 64; ++c2)
 #pragma unroll
-          for (int c = 0; c < KP_U / 32; ++c) {
-            uint32_t s[32];
-            tmem_ld32(t_s + 32 * c, s);
-            tmem_ld_wait();
-            uint32_t w16[16];
+              for (int k = 0; k < 2; ++k) {
+                const int c = 2 * c2 + k;
+                tmem_ld_wait();
+                tmem_ld32(t_s + 32 * ((c + 1) & (KP_U / 32 - 1)), sc[k ^ 1]);   // last: not used
+                uint32_t w16[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float k = ks[2 * c + h], v = ve[2 * c + h];
-              const float f = k >= 0.0f ? fminf(rs * k, 1e38f) : 0.0f;
-              const float add = k >= 0.0f ? v - m_at : -INFINITY;
-              float sum = 0.0f;
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t* x = sc[k] + 16 * h;
+                  const float f = fminf(rs * ks[2 * c + h], 1e37f), add = ve[2 * c + h] - m_at;
+                  const uint64_t f2 = f32x2(f, f), a2 = f32x2(add, add);
+                  uint64_t sum[2] = {0, 0};
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float w0 = ex2(fmaf(__uint_as_float(s[16 * h + j]), f, add));
-                float w1 = ex2(fmaf(__uint_as_float(s[16 * h + j + 1]), f, add));
-                if (edge) {
-                  if (32 * c + 16 * h + j >= left) w0 = 0.0f;
-                  if (32 * c + 16 * h + j + 1 >= left) w1 = 0.0f;
+                  for (int j = 0; j < 8; ++j) {
+                    const float2 y = f32x2_get(fma2(f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2, a2));
+                    float w0 = ex2(y.x), w1 = ex2(y.y);
+                    if (EDGE) {
+                      if (32 * c + 16 * h + 2 * j >= left) w0 = 0.0f;
+                      if (32 * c + 16 * h + 2 * j + 1 >= left) w1 = 0.0f;
+                    }
+                    sum[j & 1] = add2(sum[j & 1], f32x2(w0, w1));
+                    w16[8 * h + j] = pack2h(w0, w1);
+                  }
+                  const float2 t = f32x2_get(add2(sum[0], sum[1]));
+                  l = fmaf(t.x + t.y, vi[2 * c + h], l);
                 }
-                sum += w0 + w1;
-                w16[8 * h + j / 2] = pack2h(w0, w1);
+                tmem_st16(t_s + 16 * c, w16);
               }
-              l = fmaf(sum, pow2i(-static_cast<int>(v)), l);
-            }
-            tmem_st16(t_s + 16 * c, w16);
-          }
+            tmem_ld_wait();
+          };
+          if (edge) weights(std::true_type{}); else weights(std::false_type{});
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -299,20 +373,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         wait(BAR_PV + blk, it - 1);
         tc_fence_after();
         const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
-        const auto out_row = [&](int rr) {
-          const int b2 = rr >> 7, r2 = rr & 127;
-          const int t2 = (sg.t << p.tq_shift) + b2 * blk_tokens + r2 / p.G;
-          __nv_bfloat16* q = nullptr;
-          if (r2 / p.G < blk_tokens && t2 < sg.s.n)
-            q = p.out + (static_cast<size_t>(sg.s.off + t2) * p.hq + sg.g * p.G + r2 % p.G) * D;
-          return q;
-        };
-        const auto slot = [&](int c, int rr) {
-          return p.part + ((static_cast<size_t>(c) * 2 + (c == sg.w_first)) * (2 * KP_ROWS) + rr) * PS;
-        };
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // a row that saw no key: zeros
-        __nv_bfloat16* dst = out_row(blk * KP_ROWS + r);
-        float* part = slot(cta, blk * KP_ROWS + r);
+        __nv_bfloat16* dst =
+            live ? p.out + (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh) * D : nullptr;
+        float* part = kp_slot<D>(p.part, cta, sg.w_first, blk * KP_ROWS + r);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -339,55 +403,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         tc_fence_before();
         if (!whole) {
           *reinterpret_cast<float2*>(part + D) = make_float2(m_ref, l);
-          // ---- the tile's parts meet: the last CTA adds them up, a warp per row
-          __threadfence();
-          bar_softmax(nblk * 128);
-          const int ns = sg.w_last - sg.w_first + 1;
-          if (tid == 0) {
-            const bool all = atomicAdd(p.tickets + sg.w_first, 1u) == static_cast<unsigned>(ns) - 1u;
-            if (all) p.tickets[sg.w_first] = 0u;
-            *s_last = all;
-          }
-          bar_softmax(nblk * 128);
-          if (*s_last) {
-            __threadfence();
-            for (int rr = warp; rr < nblk * KP_ROWS; rr += 4 * nblk) {
-              __nv_bfloat16* q = out_row(rr);
-              if (!q) continue;
-              float M = -INFINITY, L = 0.0f;
-              for (int i = lane; i < ns; i += 32) M = fmaxf(M, __ldcg(slot(sg.w_first + i, rr) + D));
-#pragma unroll
-              for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-              const float at = M == -INFINITY ? 0.0f : M;
-              constexpr int PL = D / 32;                         // dims per lane
-              float O[PL];
-#pragma unroll
-              for (int k = 0; k < PL; ++k) O[k] = 0.0f;
-#pragma unroll 4
-              for (int i = 0; i < ns; ++i) {
-                const float* src = slot(sg.w_first + i, rr);
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + D));
-                const float f = exp2f(ml.x - at);
-                L = fmaf(f, ml.y, L);
-                if (f != 0.0f) {
-#pragma unroll
-                  for (int k = 0; k < PL; k += 2) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src + PL * lane + k));
-                    O[k] = fmaf(f, v.x, O[k]);
-                    O[k + 1] = fmaf(f, v.y, O[k + 1]);
-                  }
-                }
-              }
-              const float li = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-              for (int k = 0; k < PL; k += 2)
-                *reinterpret_cast<uint32_t*>(q + PL * lane + k) =
-                    pack_bf16x2(__float_as_uint(O[k] * li), __float_as_uint(O[k + 1] * li));
-            }
-          }
+          if (tid == 0 && sg.w_first == cta) tile = KpTile{sg.w_last - sg.w_first + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
         w += sg.u1 - sg.u0;
       }
+      if (tid == 0) kp_tiles(p.part)[cta] = tile;
     }
   } else if (warp < 12) {
     // ================================================ dequantise
@@ -413,7 +433,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         w += sg.u1 - sg.u0;
         more = w < w_end;
         if (more) {
-          sg = kv8_seg<KP_U>(p, prefix, w, w_end, runs);
+          kv8_next<KP_U>(sg, p, prefix, w, w_end, runs);
           u = sg.u0;
           end = kv8_seg_end(sg, p.tq_shift);
         }
@@ -421,20 +441,20 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       look();
     };
     uint4 kreg[NI], vreg[NI];
-    long long rows = -1;                        // lane b: first code row of block b (negative: none)
+    int rows = -1;                              // lane b: first code row of block b (negative: none)
     int valid = 0;                              // positions of the tile before the sequence's end
-    float ksc = -1.0f, vex = 0.0f;
+    float ksc = 0.0f, vex = -INFINITY;
     auto resolve = [&] {                        // the looked-up tile's rows and scales
       const int pos = u * KP_U + (lane & 7) * KV8_BLOCK;
       rows = -1;
       valid = end - u * KP_U;
-      ksc = -1.0f;
-      vex = 0.0f;
+      ksc = 0.0f;
+      vex = -INFINITY;
       if (more && pos < end) {
         if (pid < 0 || pid >= p.c.n_pages) {
           if (lane < 8) atomicOr(p.c.err, ERRBIT_BOUNDS);
         } else {
-          rows = ((static_cast<long long>(pid) * p.c.hkv + sg.g) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));
+          rows = ((pid * p.c.hkv + sg.g) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));   // below 2^31
           ksc = fmaxf(__ldg(p.c.scales[0] + rows / KV8_BLOCK), 0.0f);
           vex = static_cast<float>(max(scale_exp(fmaxf(__ldg(p.c.scales[1] + rows / KV8_BLOCK), 0.0f)), KV8_MIN_EXP));
         }
@@ -444,9 +464,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
-        const long long at = __shfl_sync(0xffffffffu, rows, row / KV8_BLOCK);
+        const int at = __shfl_sync(0xffffffffu, rows, row / KV8_BLOCK);
         reg[i] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && row < valid) reg[i] = ldg_nc_v4(codes + (at + row % KV8_BLOCK) * D + 16 * cc);
+        if (at >= 0 && row < valid) reg[i] = ldg_nc_v4(codes + static_cast<size_t>(at + row % KV8_BLOCK) * D + 16 * cc);
       }
     };
     auto store = [&](const uint4 (&reg)[NI], uint8_t* tile) {
@@ -471,15 +491,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     resolve();
     load(kreg, p.c.codes[0]);
     load(vreg, p.c.codes[1]);
-    const long long tiles = w_end - w_beg;
+    const int tiles = static_cast<int>(w_end - w_beg);
     float ksc_now = ksc, vex_now = vex;
     step();
-    for (long long it = 0; it < tiles; ++it) {
+    for (int it = 0; it < tiles; ++it) {
       const int s = it & 1, ph = (it >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(BAR_KE + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
       if (warp == 8 && lane < KP_NB) {
         s_ks[(it & (KP_SLOTS - 1)) * KP_NB + lane] = ksc_now;
         s_ve[(it & (KP_SLOTS - 1)) * KP_NB + lane] = vex_now;
+        s_vi[(it & (KP_SLOTS - 1)) * KP_NB + lane] = vex_now == -INFINITY ? 0.0f : pow2i(-static_cast<int>(vex_now));
       }
       store(kreg, s_k + s * TILE);
       if (lane == 0) mbar_arrive(bar(BAR_KF + s));
@@ -520,8 +541,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     };
     int it = 0, seg = 0;
     bool ok = true;
+    Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w_beg, w_end, runs);
     for (long long w = w_beg; ok && w < w_end; ++seg) {
-      const Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w, w_end, runs);
+      if (w > w_beg) kv8_next<KP_U>(sg, p, prefix, w, w_end, runs);
       const int n = sg.u1 - sg.u0;
       ok = wait(BAR_Q, seg) && wait(BAR_KF + (it & 1), it >> 1);
       if (!ok) break;
@@ -560,9 +582,53 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   }
 }
 
+// Joins the parts of the tiles that lie in several CTAs: a block per tile (by its first CTA)
+// and 8 rows, a warp per row, the parts in the order of the line.  (The last CTA of a tile
+// joining them itself took over 60 us of a 150 us prompt: 256 rows by one CTA's 8 warps.)
+template <int D>
+__global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk) {
+  grid_dep_wait();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const KpTile tl = kp_tiles(p.part)[c0];
+  if (tl.ns == 0) return;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int blk_tokens = (1 << p.tq_shift) / nblk, r = row & (KP_ROWS - 1), tb = r / p.G;
+  const int tok = (tl.t << p.tq_shift) + row / KP_ROWS * blk_tokens + tb;
+  if (tb >= blk_tokens || tok >= tl.n) return;
+  constexpr int PL = D / 32;                    // dims per lane
+  const auto slot = [&](int i) { return kp_slot<D>(p.part, c0 + i, c0, row); };
+  float M = -INFINITY;
+  for (int i = lane; i < tl.ns; i += 32) M = fmaxf(M, slot(i)[D]);
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+  const float at = M == -INFINITY ? 0.0f : M;
+  float O[PL], L = 0.0f;
+#pragma unroll
+  for (int k = 0; k < PL; ++k) O[k] = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < tl.ns; ++i) {
+    const float* src = slot(i);
+    const float2 ml = *reinterpret_cast<const float2*>(src + D);
+    const float f = exp2f(ml.x - at);
+    L = fmaf(f, ml.y, L);
+#pragma unroll
+    for (int k = 0; k < PL; k += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + PL * lane + k);
+      O[k] = fmaf(f, v.x, O[k]);
+      O[k + 1] = fmaf(f, v.y, O[k + 1]);
+    }
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
+  __nv_bfloat16* dst = p.out + (static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G) * D + PL * lane;
+#pragma unroll
+  for (int k = 0; k < PL; k += 2)
+    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2(__float_as_uint(O[k] * inv), __float_as_uint(O[k + 1] * inv));
+}
+
 // ---------------------------------------------------------------- host side
 size_t kv8_prompt_ws_bytes(int D) {
-  return KV8_TICKET_BYTES + static_cast<size_t>(KV8_MAX_CTAS) * 2 * (2 * KP_ROWS) * (D + 4) * sizeof(float);
+  return KV8_TICKET_BYTES + KP_TILES_BYTES +
+         static_cast<size_t>(KV8_MAX_CTAS) * 2 * (2 * KP_ROWS) * kp_ps(D) * sizeof(float);
 }
 
 namespace {
@@ -576,7 +642,9 @@ cudaError_t launch_prompt(const Kv8AttnParams& p, int nblk, int grid, int dev, c
     set[dev] = true;
   }
   k<<<grid, KP_THREADS, kp_smem(D, p.b.n_seqs), s>>>(p, nblk);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_prompt_join_kernel<D>, dim3(grid, nblk * KP_ROWS / 8), dim3(256), 0, s, p, nblk);
 }
 }  // namespace
 

@@ -45,7 +45,7 @@ struct Kv8Seg {
   Kv8Seq s;
   int b, g, t;           // sequence, key/value head, tile of the sequence
   int u0, u1, units;     // this run's units, the tile's units
-  int w_first, w_last;   // the runs that hold the tile's first and last unit
+  int w_first, w_last;   // the runs that hold the tile's first and last unit (where they differ)
 };
 
 // The line cut into n runs: run i is units i total / n up to (i + 1) total / n, and unit w
@@ -133,7 +133,23 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   return total;
 }
 
-// The segment that starts at unit w of the line and ends with its tile or at w_end.
+// Units of one tile.
+template <int U>
+__device__ __forceinline__ int kv8_units_tile(const Kv8Seq& s, int tq_shift, int t) {
+  return (max(s.first, 0) + min((t + 1) << tq_shift, s.n) + U - 1) / U;
+}
+
+// Ends the segment that starts at unit w with its tile or at w_end.
+__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, long long w, long long w_end, const Kv8Runs& runs) {
+  const long long left = w_end - w;
+  g.u1 = g.units - g.u0 <= left ? g.units : g.u0 + static_cast<int>(left);
+  if (g.u0 > 0 || g.u1 < g.units) {
+    g.w_first = kv8_run_of(runs, w - g.u0);
+    g.w_last = kv8_run_of(runs, w - g.u0 + g.units - 1);
+  }
+}
+
+// The segment that starts at unit w of the line.
 template <int U>
 __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w, long long w_end,
                                           const Kv8Runs& runs) {
@@ -157,14 +173,29 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
   }
   g.t = tl;
   const long long before = kv8_units_before<U>(g.s, p.tq_shift, tl);
-  g.units = tl == tiles - 1 ? kv8_units_last<U>(g.s)
-                            : static_cast<int>(kv8_units_before<U>(g.s, p.tq_shift, tl + 1) - before);
+  g.units = kv8_units_tile<U>(g.s, p.tq_shift, tl);
   g.u0 = static_cast<int>(x - before);
-  const long long left = w_end - w;
-  g.u1 = g.units - g.u0 <= left ? g.units : g.u0 + static_cast<int>(left);
-  g.w_first = kv8_run_of(runs, w - g.u0);
-  g.w_last = kv8_run_of(runs, w - g.u0 + g.units - 1);
+  kv8_seg_close(g, w, w_end, runs);
   return g;
+}
+
+// The segment after `g`, at unit w of the line (g was not the run's last): it begins a tile,
+// the sequence's next one, or the first of the next head or sequence.
+template <int U>
+__device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const long long* prefix, long long w,
+                                         long long w_end, const Kv8Runs& runs) {
+  const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
+  if (++g.t >= tiles) {
+    g.t = 0;
+    if (++g.g >= p.c.hkv) {
+      g.g = 0;
+      do ++g.b; while (prefix[g.b + 1] <= w);      // sequences without new tokens have no units
+      g.s = kv8_seq(p.b, p.c.page_shift, g.b);
+    }
+  }
+  g.units = kv8_units_tile<U>(g.s, p.tq_shift, g.t);
+  g.u0 = 0;
+  kv8_seg_close(g, w, w_end, runs);
 }
 
 // Positions that the tile's last token sees.
