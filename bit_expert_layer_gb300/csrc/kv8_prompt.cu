@@ -3,11 +3,12 @@
 // rows hold), on tcgen05.
 //
 // A CTA works on one or two blocks of 128 query rows (TQ tokens x G heads each) that share
-// their keys, in tiles of 128 positions; its 16 warps have roles:
+// their keys, in tiles of 128 positions; its 20 warps have roles:
 //   warps 0-7    softmax, one query row per thread, four warps per row block
-//   warps 8-11   dequantise: codes from global memory into fp16 tiles in shared memory,
-//                128-byte rows with the 128-byte swizzle, two buffers each for K and V
-//   warp 12      issues the MMAs
+//   warps 8-11   dequantise K: codes from global memory into fp16 tiles in shared memory,
+//                128-byte rows with the 128-byte swizzle, two buffers
+//   warps 12-15  the same for V (K and V by the same four warps took 6000 cycles a tile)
+//   warp 16      issues the MMAs
 // Per tile and row block, TMEM lane = query row:
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
@@ -32,20 +33,26 @@ namespace moe {
 
 namespace {
 
-constexpr int KP_THREADS = 512;
+constexpr int KP_THREADS = 640;
 constexpr int KP_U = 128;                         // positions per tile
 constexpr int KP_ROWS = 128;                      // query rows per block
 constexpr int KP_NB = KP_U / KV8_BLOCK;           // scales per tile
 constexpr int KP_SLOTS = 4;                       // tiles whose scales are kept
 constexpr float KP_GROW = 8.0f;                   // the maximum may outgrow the reference by 2^8
+// Blocks of a tile are brought to the tile's largest scale in fp16, 2^head on top of it: the
+// largest code (448; for int8 the offset 1152 of its conversion) lands just under fp16's
+// largest number, and a block whose scale is down to 2^-21 of the tile's largest keeps every
+// bit of its codes.
+__host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 ? 6 : 5; }
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 3 * KP_NB * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 16 * 8 + 64;
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 18 * 8 + 64;
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
 
-enum { BAR_KF = 0, BAR_KE = 2, BAR_VF = 4, BAR_VE = 6, BAR_Q = 8, BAR_S = 9, BAR_P = 11, BAR_PV = 13, BAR_END = 15, BAR_N = 16 };
+// barriers: two each of the K and V buffers (full, empty) and of the row blocks, and the end
+enum { BAR_KF = 0, BAR_KE = 2, BAR_VF = 4, BAR_VE = 6, BAR_Q = 8, BAR_S = 10, BAR_P = 12, BAR_PV = 14, BAR_END = 16, BAR_N = 17 };
 
 // kind::f16 with fp16 A and B, fp32 D; A K-major, B K-major or (b_mn) N-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -108,6 +115,16 @@ __device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 // Two fp32 fused multiply-adds / additions in one instruction.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;
@@ -129,6 +146,40 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Registers per thread of a warpgroup: the kernel starts with 96, and the shares stay within
+// its 640 * 96.
+constexpr int KP_REG_SOFTMAX = 144, KP_REG_DEQUANT = 72, KP_REG_MMA = 48;
+static_assert(2 * 128 * KP_REG_SOFTMAX + 2 * 128 * KP_REG_DEQUANT + 128 * KP_REG_MMA <= KP_THREADS * 96,
+              "register shares within the launch's total");
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two codes to fp16 times a power of two, one rounding (for int8 the offset 1152 goes with
+// the multiplication: (1152 + code) f - 1152 f).
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_scaled_offset(uint32_t f2) {
+  uint32_t r = 0;
+  if constexpr (FMT == GQA_KV8_INT8) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f2), "r"(0xE480E480u));
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t kv8_half2_scaled(uint32_t w, int hi, uint32_t f2, uint32_t off) {
+  uint32_t d;
+  if constexpr (FMT == GQA_KV8_E4M3) {
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(kv8_half2<FMT>(w, hi)), "r"(f2));
+  } else {
+    const uint32_t x = __byte_perm(w, 0x64646464u, hi ? 0x4342 : 0x4140);
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(f2), "r"(off));
+  }
+  return d;
+}
+
 // A tile whose parts lie in several CTAs, left by its first CTA for the kernel that joins them.
 struct __align__(16) KpTile {
   int ns;                // CTAs (0: no such tile)
@@ -158,15 +209,15 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   uint8_t* s_q = smem;
   uint8_t* s_k = smem + 2 * TILE;
   uint8_t* s_v = smem + 4 * TILE;
-  // [slot][8] each: K scale, exponent e of the V scale (-inf: no such block), 2^-e
-  float* s_ks = reinterpret_cast<float*>(smem + 6 * TILE);
-  float* s_ve = s_ks + KP_SLOTS * KP_NB;
-  float* s_vi = s_ve + KP_SLOTS * KP_NB;
-  long long* prefix = reinterpret_cast<long long*>(s_vi + KP_SLOTS * KP_NB);
+  // per tile {K scale, e, 2^-e of its V scale 2^e, blocks without a page (bits)}
+  float4* s_scale = reinterpret_cast<float4*>(smem + 6 * TILE);
+  float* s_rs = reinterpret_cast<float*>(s_scale + KP_SLOTS);      // [256] factor of a query row's scores
+  long long* prefix = reinterpret_cast<long long*>(s_rs + 2 * KP_ROWS);
   long long* s_warp = prefix + p.b.n_seqs + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(abort_flag) + 1);
+  volatile int* s_n = reinterpret_cast<volatile int*>(s_tmem + 1);    // [2]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * i; };
@@ -180,8 +231,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       mbar_init(bar(BAR_S + i), 1);
       mbar_init(bar(BAR_P + i), 4);
       mbar_init(bar(BAR_PV + i), 1);
+      mbar_init(bar(BAR_Q + i), 4);
     }
-    mbar_init(bar(BAR_Q), 4 * nblk);
     mbar_init(bar(BAR_END), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -195,7 +246,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     return;
   }
   const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
@@ -206,6 +257,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   const int blk_tokens = (1 << p.tq_shift) / nblk;
 
   if (warp < 8) {
+    reg_inc<KP_REG_SOFTMAX>();
     // ================================================ softmax: row `r` of block `blk`
     const int blk = warp >> 2, r = tid & 127;
     if (blk < nblk) {
@@ -215,7 +267,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       auto wait = [&](int b, int phase) {
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns))) dead = true;
       };
-      int it = 0;
+      int it = 0, seg = 0;
       KpTile tile = {0, 0, 0, 0, 0, {0, 0, 0}};
       Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w_beg, w_end, runs);
       for (long long w = w_beg; w < w_end;) {
@@ -224,87 +276,93 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         const bool live = r / p.G < blk_tokens && tok < sg.s.n;
         // positions that the row sees; a row without a token (zeros) needs no mask
         const int see = live ? sg.s.first + tok + 1 : 1 << 30;
-        // ---- the query row, scaled into fp16, into the swizzled tile
-        float rs;
+        // ---- the warp's 32 query rows, scaled into fp16, into the swizzled tile: a row per
+        // D / 8 lanes, so that loads and stores are whole lines
         {
-          const __nv_bfloat16* src = p.q + static_cast<size_t>(sg.s.off + tok) * p.q_stride + (sg.g * p.G + hh) * D;
-          uint32_t big = 0;
-          if (live)
+          constexpr int LPR = D / 8, RPS = 32 / LPR;             // lanes per row, rows per step
+          const int qc = lane % LPR;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32; i0 += 8 * RPS) {
+            uint4 v[8];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 v = ldg_nc_v4(src + 8 * c);
-              const uint32_t* x = &v.x;
+            for (int i = 0; i < 8; ++i) {
+              const int r2 = 32 * (warp & 3) + i0 + i * RPS + lane / LPR, tb = r2 / p.G;
+              const int t2 = (sg.t << p.tq_shift) + blk * blk_tokens + tb;
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (tb < blk_tokens && t2 < sg.s.n)
+                v[i] = ldg_nc_v4(p.q + static_cast<size_t>(sg.s.off + t2) * p.q_stride +
+                                 (sg.g * p.G + r2 - tb * p.G) * D + 8 * qc);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r2 = 32 * (warp & 3) + i0 + i * RPS + lane / LPR;
+              uint32_t* x = &v[i].x;
+              uint32_t big = 0;
 #pragma unroll
               for (int j = 0; j < 4; ++j) big = max(big, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
-            }
-          const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, -100), 100);
-          const float f = pow2i(-e);
-          rs = pow2i(e) * p.scale_log2;
-          uint8_t* dst = s_q + blk * TILE + r * 128;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (live) v = ldg_nc_v4(src + 8 * c);
-            uint4 o;
-            o.x = pack2h(bf16lo(v.x) * f, bf16hi(v.x) * f);
-            o.y = pack2h(bf16lo(v.y) * f, bf16hi(v.y) * f);
-            o.z = pack2h(bf16lo(v.z) * f, bf16hi(v.z) * f);
-            o.w = pack2h(bf16lo(v.w) * f, bf16hi(v.w) * f);
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * BOX + (((c & 7) ^ (r & 7)) << 4)) = o;
+              for (int m = LPR / 2; m >= 1; m >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, m));
+              const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, -100), 100);
+              const float f = pow2i(-e);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = pack2h(bf16lo(x[j]) * f, bf16hi(x[j]) * f);
+              *reinterpret_cast<uint4*>(s_q + blk * TILE + (qc >> 3) * BOX + r2 * 128 + (((qc & 7) ^ (r2 & 7)) << 4)) = v[i];
+              // the factor stays below 2^62, so that its product with a K scale is finite
+              if (qc == 0) s_rs[blk * KP_ROWS + r2] = fminf(pow2i(e) * p.scale_log2, 0x1p62f);
+            }
           }
         }
+        if (tid == 0) s_n[seg & 1] = sg.u1 - sg.u0;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_Q));
+        if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
+        const float rs = s_rs[blk * KP_ROWS + r];
 
         float m_ref = -INFINITY, l = 0.0f;
         for (int u = sg.u0; u < sg.u1; ++u, ++it) {
           wait(BAR_S + blk, it);
           if (dead) continue;
           tc_fence_after();
-          const float* ks = s_ks + (it & (KP_SLOTS - 1)) * KP_NB;
-          const float* ve = s_ve + (it & (KP_SLOTS - 1)) * KP_NB;
-          const float* vi = s_vi + (it & (KP_SLOTS - 1)) * KP_NB;
+          const float4 sc4 = s_scale[it & (KP_SLOTS - 1)];
+          const float f = rs * sc4.x, e = sc4.y;
+          const uint32_t bad = __float_as_uint(sc4.w);
           const int left = see - u * KP_U;                       // positions of the tile that the row sees
-          const bool edge = __any_sync(0xffffffffu, left < KP_U);
-          // A tile at the causal edge takes a path of its own (EDGE), so that the others carry
-          // no mask: 2 of 5 instructions per score, measured.  The scores are read twice, 32
-          // columns at a time, the next ones while these are worked on: 128 of them in
-          // registers do not fit beside the rest.
+          // A tile at the causal edge (or with a page missing) takes a path of its own, so that
+          // the others carry no mask: 2 of 5 instructions per score, measured.
+          const bool edge = __any_sync(0xffffffffu, left < KP_U) || bad;
+          const auto hidden = [&](int j) { return j >= left || ((bad >> (j / KV8_BLOCK)) & 1); };
+          // The scores are read twice, 32 columns at a time, the next ones while these are worked
+          // on: 128 of them in registers do not fit beside the rest.
           uint32_t sc[2][32];
-          // ---- pass 1: the maximum of s_i + e_i
+          // ---- pass 1: the maximum of s_i + e
           float mx = -INFINITY;
-          const auto largest = [&](auto edge_c) {
-            constexpr bool EDGE = decltype(edge_c)::value;
-            tmem_ld32(t_s, sc[0]);
+          if (edge) {
 #pragma unroll 1
-            for (int c2 = 0; c2 < KP_U / 64; ++c2)
+            for (int c = 0; c < KP_U / 32; ++c) {
+              tmem_ld32(t_s + 32 * c, sc[0]);
+              tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int c = 2 * c2 + k;
-                tmem_ld_wait();
-                tmem_ld32(t_s + 32 * ((c + 1) & (KP_U / 32 - 1)), sc[k ^ 1]);   // last: pass 2's first
+              for (int j = 0; j < 32; ++j)
+                if (!hidden(32 * c + j)) mx = fmaxf(mx, __uint_as_float(sc[0][j]));
+            }
+          } else {
+            tmem_ld32(t_s, sc[0]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t* x = sc[k] + 16 * h;
-                  const float f = fminf(rs * ks[2 * c + h], 1e37f), e = ve[2 * c + h];
-                  if (EDGE) {
+            for (int c = 0; c < KP_U / 32; ++c) {
+              tmem_ld_wait();
+              tmem_ld32(t_s + 32 * ((c + 1) % (KP_U / 32)), sc[(c + 1) & 1]);   // last: pass 2's first
+              const uint32_t* x = sc[c & 1];
+              float m[10];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                      if (32 * c + 16 * h + j < left) mx = fmaxf(mx, fmaf(__uint_as_float(x[j]), f, e));
-                  } else {
-                    float m[5];
+              for (int j = 0; j < 10; ++j)
+                m[j] = max3(__uint_as_float(x[3 * j]), __uint_as_float(x[3 * j + 1]), __uint_as_float(x[3 * j + 2]));
+              m[0] = max3(m[0], __uint_as_float(x[30]), __uint_as_float(x[31]));
 #pragma unroll
-                    for (int j = 0; j < 5; ++j)
-                      m[j] = max3(__uint_as_float(x[3 * j]), __uint_as_float(x[3 * j + 1]), __uint_as_float(x[3 * j + 2]));
-                    m[0] = max3(m[0], m[1], __uint_as_float(x[15]));
-                    m[2] = max3(m[2], m[3], m[4]);
-                    mx = fmaxf(mx, fmaf(fmaxf(m[0], m[2]), f, e));
-                  }
-                }
-              }
-          };
-          if (edge) largest(std::true_type{}); else largest(std::false_type{});
+              for (int j = 0; j < 3; ++j) m[j] = max3(m[j], m[3 + j], m[6 + j]);
+              mx = max3(mx, max3(m[0], m[1], m[2]), m[9]);
+            }
+          }
+          mx = mx == -INFINITY ? mx : fmaf(mx, f, e);
           // ---- the reference moves: O and the normaliser follow
           const bool grow = mx > m_ref + KP_GROW;                // also the first finite maximum
           if (__any_sync(0xffffffffu, grow)) {
@@ -316,7 +374,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
               wait(BAR_PV + blk, it - 1);
               if (dead) continue;
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(t_o + 32 * c, o);
@@ -329,41 +387,46 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           }
           const float m_at = m_ref == -INFINITY ? 0.0f : m_ref;
           // ---- pass 2: weights, over the scores that were read
-          const auto weights = [&](auto edge_c) {
-            constexpr bool EDGE = decltype(edge_c)::value;
+          {
+            const float add = e - m_at;
+            const uint64_t f2 = f32x2(f, f), a2 = f32x2(add, add);
+            uint64_t sum[2] = {0, 0};
+            if (edge) {
 #pragma unroll 1
-            for (int c2 = 0; c2 < KP_U / 64; ++c2)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int c = 2 * c2 + k;
+              for (int c = 0; c < KP_U / 32; ++c) {
+                tmem_ld32(t_s + 32 * c, sc[0]);
                 tmem_ld_wait();
-                tmem_ld32(t_s + 32 * ((c + 1) & (KP_U / 32 - 1)), sc[k ^ 1]);   // last: not used
                 uint32_t w16[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t* x = sc[k] + 16 * h;
-                  const float f = fminf(rs * ks[2 * c + h], 1e37f), add = ve[2 * c + h] - m_at;
-                  const uint64_t f2 = f32x2(f, f), a2 = f32x2(add, add);
-                  uint64_t sum[2] = {0, 0};
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    const float2 y = f32x2_get(fma2(f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2, a2));
-                    float w0 = ex2(y.x), w1 = ex2(y.y);
-                    if (EDGE) {
-                      if (32 * c + 16 * h + 2 * j >= left) w0 = 0.0f;
-                      if (32 * c + 16 * h + 2 * j + 1 >= left) w1 = 0.0f;
-                    }
-                    sum[j & 1] = add2(sum[j & 1], f32x2(w0, w1));
-                    w16[8 * h + j] = pack2h(w0, w1);
-                  }
-                  const float2 t = f32x2_get(add2(sum[0], sum[1]));
-                  l = fmaf(t.x + t.y, vi[2 * c + h], l);
+                for (int j = 0; j < 32; j += 2) {
+                  float w0 = ex2(fmaf(__uint_as_float(sc[0][j]), f, add)), w1 = ex2(fmaf(__uint_as_float(sc[0][j + 1]), f, add));
+                  if (hidden(32 * c + j)) w0 = 0.0f;
+                  if (hidden(32 * c + j + 1)) w1 = 0.0f;
+                  sum[0] = add2(sum[0], f32x2(w0, w1));
+                  w16[j / 2] = pack2h(w0, w1);
                 }
                 tmem_st16(t_s + 16 * c, w16);
               }
-            tmem_ld_wait();
-          };
-          if (edge) weights(std::true_type{}); else weights(std::false_type{});
+            } else {
+#pragma unroll
+              for (int c = 0; c < KP_U / 32; ++c) {
+                tmem_ld_wait();
+                if (c + 1 < KP_U / 32) tmem_ld32(t_s + 32 * (c + 1), sc[(c + 1) & 1]);
+                const uint32_t* x = sc[c & 1];
+                uint32_t w16[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float2 y = f32x2_get(fma2(f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2, a2));
+                  const float w0 = ex2(y.x), w1 = ex2(y.y);
+                  sum[j & 1] = add2(sum[j & 1], f32x2(w0, w1));
+                  w16[j] = pack2h(w0, w1);
+                }
+                tmem_st16(t_s + 16 * c, w16);
+              }
+            }
+            const float2 t = f32x2_get(add2(sum[0], sum[1]));
+            l = fmaf(t.x + t.y, sc4.z, l);
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -377,7 +440,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         __nv_bfloat16* dst =
             live ? p.out + (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh) * D : nullptr;
         float* part = kp_slot<D>(p.part, cta, sg.w_first, blk * KP_ROWS + r);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(t_o + 32 * c, o);
@@ -406,30 +469,40 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           if (tid == 0 && sg.w_first == cta) tile = KpTile{sg.w_last - sg.w_first + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
         w += sg.u1 - sg.u0;
+        ++seg;
       }
       if (tid == 0) kp_tiles(p.part)[cta] = tile;
     }
-  } else if (warp < 12) {
-    // ================================================ dequantise
+  } else if (warp < 16) {
+    reg_dec<KP_REG_DEQUANT>();
+    // ================================================ dequantise K (warps 8-11) or V (12-15)
     constexpr int CPR = D / 16;                 // 16-byte chunks of codes per row
     constexpr int RPI = 128 / CPR;              // rows per step of the 128 threads
     constexpr int NI = KP_U / RPI;              // steps per tile
-    const int dt = tid - 256, cc = dt % CPR, r0 = dt / CPR;
+    const int is_v = warp >= 12;
+    const int dt = tid & 127, cc = dt % CPR, r0 = dt / CPR;
+    const uint8_t* codes = p.c.codes[is_v];
+    uint8_t* tiles = is_v ? s_v : s_k;
+    const int b_full = is_v ? BAR_VF : BAR_KF, b_empty = is_v ? BAR_VE : BAR_KE;
+    // Every tile passes through four stages, one per iteration, so that no load is waited for:
+    // page lookup, scales, codes, conversion.  Lanes 0-7 hold the tile's 8 K blocks, lanes
+    // 8-15 its V blocks.
+    const int lb = lane & 7;
     long long w = w_beg;
     Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w, w_end, runs);
     int u = sg.u0, end = kv8_seg_end(sg, p.tq_shift);
     bool more = true;
-    // lane b < 8 of every warp: the page of the cursor's tile's block b, then its code row
-    int pid = -1;
-    auto look = [&] {
-      const int pos = u * KP_U + (lane & 7) * KV8_BLOCK;
-      pid = -1;
-      if (more && pos < end) {
-        pid = __ldg(p.b.page_table + static_cast<size_t>(sg.b) * p.b.max_pages + (pos >> p.c.page_shift));
-      }
-    };
-    auto step = [&] {                           // the cursor's next tile
-      if (++u >= sg.u1) {
+    int pid = -1, pid_at = 0, pid_valid = 0;    // looked up: page; offset in the page; positions before the end
+    bool pid_live = false;
+    int pid_g = 0;
+    auto look = [&] {                           // stage 1 of the cursor's tile, then on to the next one
+      const int pos = u * KP_U + lb * KV8_BLOCK;
+      pid_live = more && pos < end;
+      pid_valid = more ? end - u * KP_U : 0;
+      pid_at = pos & ((1 << p.c.page_shift) - 1);
+      pid_g = sg.g;
+      if (pid_live) pid = __ldg(p.b.page_table + static_cast<size_t>(sg.b) * p.b.max_pages + (pos >> p.c.page_shift));
+      if (more && ++u >= sg.u1) {
         w += sg.u1 - sg.u0;
         more = w < w_end;
         if (more) {
@@ -438,29 +511,24 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           end = kv8_seg_end(sg, p.tq_shift);
         }
       }
-      look();
     };
-    uint4 kreg[NI], vreg[NI];
-    int rows = -1;                              // lane b: first code row of block b (negative: none)
-    int valid = 0;                              // positions of the tile before the sequence's end
-    float ksc = 0.0f, vex = -INFINITY;
-    auto resolve = [&] {                        // the looked-up tile's rows and scales
-      const int pos = u * KP_U + (lane & 7) * KV8_BLOCK;
+    int rows = -1, valid = 0;                   // stage 2: first code row of the lane's block (negative: none)
+    float scale = 0.0f;
+    bool bad = false;
+    auto locate = [&] {
+      bad = pid_live && (pid < 0 || pid >= p.c.n_pages);
       rows = -1;
-      valid = end - u * KP_U;
-      ksc = 0.0f;
-      vex = -INFINITY;
-      if (more && pos < end) {
-        if (pid < 0 || pid >= p.c.n_pages) {
-          if (lane < 8) atomicOr(p.c.err, ERRBIT_BOUNDS);
-        } else {
-          rows = ((pid * p.c.hkv + sg.g) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));   // below 2^31
-          ksc = fmaxf(__ldg(p.c.scales[0] + rows / KV8_BLOCK), 0.0f);
-          vex = static_cast<float>(max(scale_exp(fmaxf(__ldg(p.c.scales[1] + rows / KV8_BLOCK), 0.0f)), KV8_MIN_EXP));
-        }
+      scale = 0.0f;
+      valid = pid_valid;
+      if (pid_live && !bad) {
+        rows = ((pid * p.c.hkv + pid_g) << p.c.page_shift) + pid_at;   // below 2^31
+        scale = __ldg(p.c.scales[(lane >> 3) & 1] + rows / KV8_BLOCK);
       }
     };
-    auto load = [&](uint4 (&reg)[NI], const uint8_t* codes) {
+    uint4 reg[NI];
+    uint32_t fac = 0;                           // of the tile in reg: the lane's block's factor to the tile's scale
+    float4 now = make_float4(0, 0, 0, 0);       // of the tile in reg: what the softmax needs
+    auto load = [&] {                           // stage 3
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
@@ -468,15 +536,28 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         reg[i] = make_uint4(0, 0, 0, 0);
         if (at >= 0 && row < valid) reg[i] = ldg_nc_v4(codes + static_cast<size_t>(at + row % KV8_BLOCK) * D + 16 * cc);
       }
+      const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xFFu;
+      if (bads && lane == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+      constexpr int HEAD = kp_head(FMT);
+      const int e = rows >= 0 ? max(scale_exp(fmaxf(scale, 0.0f)), KV8_MIN_EXP) : KV8_MIN_EXP;
+      int t = e;                                // the largest of the 8 blocks
+#pragma unroll
+      for (int m = 4; m >= 1; m >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, m));
+      const float f = pow2i(max(e - t + HEAD, -126));
+      fac = pack2h(f, f);
+      const int kt = __shfl_sync(0xffffffffu, t, 0), vt = __shfl_sync(0xffffffffu, t, 8);
+      now = make_float4(pow2i(min(kt - HEAD, 62)), static_cast<float>(vt - HEAD), pow2i(HEAD - vt), __uint_as_float(bads));
     };
-    auto store = [&](const uint4 (&reg)[NI], uint8_t* tile) {
+    auto store = [&](uint8_t* tile) {           // stage 4
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
+        const uint32_t fc = __shfl_sync(0xffffffffu, fac, row / KV8_BLOCK + 8 * is_v), fo = kv8_scaled_offset<FMT>(fc);
+        const auto h2 = [&](uint32_t x, int hi) { return kv8_half2_scaled<FMT>(x, hi, fc, fo); };
         const uint32_t w0 = kv8_flip<FMT>(reg[i].x), w1 = kv8_flip<FMT>(reg[i].y);
         const uint32_t w2 = kv8_flip<FMT>(reg[i].z), w3 = kv8_flip<FMT>(reg[i].w);
-        const uint4 a = make_uint4(kv8_half2<FMT>(w0, 0), kv8_half2<FMT>(w0, 1), kv8_half2<FMT>(w1, 0), kv8_half2<FMT>(w1, 1));
-        const uint4 b = make_uint4(kv8_half2<FMT>(w2, 0), kv8_half2<FMT>(w2, 1), kv8_half2<FMT>(w3, 0), kv8_half2<FMT>(w3, 1));
+        const uint4 a = make_uint4(h2(w0, 0), h2(w0, 1), h2(w1, 0), h2(w1, 1));
+        const uint4 b = make_uint4(h2(w2, 0), h2(w2, 1), h2(w3, 0), h2(w3, 1));
         // 8 lanes write one row: the upper box's lanes take their odd chunk first, so that the
         // 8 chunks of a store lie in 8 different bank groups
         uint8_t* dst = tile + (cc >> 2) * BOX + row * 128;
@@ -488,95 +569,100 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       __syncwarp();
     };
     look();
-    resolve();
-    load(kreg, p.c.codes[0]);
-    load(vreg, p.c.codes[1]);
-    const int tiles = static_cast<int>(w_end - w_beg);
-    float ksc_now = ksc, vex_now = vex;
-    step();
-    for (int it = 0; it < tiles; ++it) {
+    locate();
+    look();
+    load();
+    locate();
+    look();
+    const int n_tiles = static_cast<int>(w_end - w_beg);
+    for (int it = 0; it < n_tiles; ++it) {
       const int s = it & 1, ph = (it >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(BAR_KE + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
-      if (warp == 8 && lane < KP_NB) {
-        s_ks[(it & (KP_SLOTS - 1)) * KP_NB + lane] = ksc_now;
-        s_ve[(it & (KP_SLOTS - 1)) * KP_NB + lane] = vex_now;
-        s_vi[(it & (KP_SLOTS - 1)) * KP_NB + lane] = vex_now == -INFINITY ? 0.0f : pow2i(-static_cast<int>(vex_now));
-      }
-      store(kreg, s_k + s * TILE);
-      if (lane == 0) mbar_arrive(bar(BAR_KF + s));
-      resolve();
-      load(kreg, p.c.codes[0]);
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(BAR_VE + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
-      store(vreg, s_v + s * TILE);
-      if (lane == 0) mbar_arrive(bar(BAR_VF + s));
-      load(vreg, p.c.codes[1]);
-      ksc_now = ksc;
-      vex_now = vex;
-      step();
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
+      if (tid == 256) s_scale[it & (KP_SLOTS - 1)] = now;
+      store(tiles + s * TILE);
+      if (lane == 0) mbar_arrive(bar(b_full + s));
+      load();
+      locate();
+      look();
     }
-  } else if (warp == 12 && lane == 0) {
-    // ================================================ MMA issue
-    constexpr uint32_t ID_S = idesc_f16(KP_ROWS, KP_U, 0), ID_O = idesc_f16(KP_ROWS, D, 1);
-    auto qk = [&](int i, int s) {
+  } else {
+    reg_dec<KP_REG_MMA>();
+    if (warp == 16) {
+      // ================================================ MMA issue
+      // The whole warp follows the loop and one elected lane issues: with the control flow
+      // uniform, descriptors stay in uniform registers.  (A loop of one lane's own took about
+      // 120 cycles per MMA.  A warp per row block let the blocks fall into step, both in their
+      // softmax and then both on the tensor cores: 560 us where this order takes 470.)
+      constexpr uint32_t ID_S = idesc_f16(KP_ROWS, KP_U, 0), ID_O = idesc_f16(KP_ROWS, D, 1);
+      const bool leader = elect_one();
+      const uint64_t d_q = sdesc_sw128(smem_u32(s_q)), d_k = sdesc_sw128(smem_u32(s_k));
+      const uint64_t d_v = sdesc_sw128_mn(smem_u32(s_v), BOX);
+      auto qk = [&](int i, int s, bool last) {    // descriptors advance in units of 16 bytes
+        if (leader) {
+          const uint64_t a = d_q + i * (TILE >> 4), b = d_k + s * (TILE >> 4);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t a = sdesc_sw128(smem_u32(s_q + i * TILE) + (k >> 2) * BOX) + 2 * (k & 3);
-        const uint64_t b = sdesc_sw128(smem_u32(s_k + s * TILE) + (k >> 2) * BOX) + 2 * (k & 3);
-        umma_bf16(tmem + 128 * i, a, b, ID_S, k > 0);
-      }
-      umma_commit(bar(BAR_S + i));
-    };
-    auto pv = [&](int i, int s, bool acc) {
+          for (int k = 0; k < D / 16; ++k) {
+            const int at = (k >> 2) * (BOX >> 4) + 2 * (k & 3);
+            umma_bf16(tmem + 128 * i, a + at, b + at, ID_S, k > 0);
+          }
+          umma_commit(bar(BAR_S + i));
+          if (last) umma_commit(bar(BAR_KE + s));
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int i, int s, bool acc, bool last) {
+        if (leader) {
+          const uint64_t b = d_v + s * (TILE >> 4);
 #pragma unroll
-      for (int k = 0; k < KP_U / 16; ++k) {
-        const uint64_t b = sdesc_sw128_mn(smem_u32(s_v + s * TILE) + k * 2048, BOX);
-        umma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, b, ID_O, acc || k > 0);
-      }
-      umma_commit(bar(BAR_PV + i));
-    };
-    auto wait = [&](int b, int phase) {
-      const bool ok = mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns);
-      tc_fence_after();
-      return ok;
-    };
-    int it = 0, seg = 0;
-    bool ok = true;
-    Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w_beg, w_end, runs);
-    for (long long w = w_beg; ok && w < w_end; ++seg) {
-      if (w > w_beg) kv8_next<KP_U>(sg, p, prefix, w, w_end, runs);
-      const int n = sg.u1 - sg.u0;
-      ok = wait(BAR_Q, seg) && wait(BAR_KF + (it & 1), it >> 1);
-      if (!ok) break;
-      for (int i = 0; i < nblk; ++i) qk(i, it & 1);
-      umma_commit(bar(BAR_KE + (it & 1)));
-      for (int j = 0; ok && j < n; ++j, ++it) {
-        const int s = it & 1;
-        ok = wait(BAR_VF + s, it >> 1);
+          for (int k = 0; k < KP_U / 16; ++k)
+            umma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, b + k * (2048 >> 4), ID_O, acc || k > 0);
+          umma_commit(bar(BAR_PV + i));
+          if (last) umma_commit(bar(BAR_VE + s));
+        }
+        __syncwarp();
+      };
+      auto wait = [&](int b, int phase) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns));
+        tc_fence_after();
+        return ok;
+      };
+      const int n_tiles = static_cast<int>(w_end - w_beg);
+      int it = 0;
+      bool ok = true;
+      for (int seg = 0; ok && it < n_tiles; ++seg) {
+        ok = wait(BAR_KF + (it & 1), it >> 1);
         for (int i = 0; ok && i < nblk; ++i) {
-          ok = wait(BAR_P + i, it);
-          if (!ok) break;
-          pv(i, s, j > 0);
-          if (i == nblk - 1) umma_commit(bar(BAR_VE + s));
-          if (j + 1 < n) {
-            if (i == 0) ok = wait(BAR_KF + (s ^ 1), (it + 1) >> 1);
+          ok = wait(BAR_Q + i, seg);
+          if (ok) qk(i, it & 1, i == nblk - 1);
+        }
+        const int n = s_n[seg & 1];               // the segment's tiles, told by the softmax
+        for (int j = 0; ok && j < n; ++j, ++it) {
+          const int s = it & 1;
+          ok = wait(BAR_VF + s, it >> 1);
+          for (int i = 0; ok && i < nblk; ++i) {
+            ok = wait(BAR_P + i, it);
             if (!ok) break;
-            qk(i, s ^ 1);
-            if (i == nblk - 1) umma_commit(bar(BAR_KE + (s ^ 1)));
+            pv(i, s, j > 0, i == nblk - 1);
+            if (j + 1 < n) {
+              if (i == 0) ok = wait(BAR_KF + (s ^ 1), (it + 1) >> 1);
+              if (!ok) break;
+              qk(i, s ^ 1, i == nblk - 1);
+            }
           }
         }
       }
-      w += n;
-    }
-    // every MMA issued has to land before the memory goes away
-    umma_commit(bar(BAR_END));
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar(BAR_END), 0) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+      // every MMA issued has to land before the memory goes away
+      if (leader) umma_commit(bar(BAR_END));
+      __syncwarp();
+      const unsigned long long t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar(BAR_END), 0) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
