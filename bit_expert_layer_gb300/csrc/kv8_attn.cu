@@ -34,6 +34,7 @@ constexpr int KA_WARPS = 8;
 constexpr int KA_THREADS = KA_WARPS * 32;
 constexpr int KA_U = 32;                       // positions per piece
 constexpr int KA_STAGES = 2;                   // pieces in flight per warp
+constexpr int KA_COST = 2;                     // a tile's start, in pieces
 __host__ __device__ constexpr int ka_half(int D) { return KA_U * D; }       // bytes of a piece's keys (or values)
 __host__ __device__ constexpr int ka_ring(int D) { return KA_WARPS * KA_STAGES * 2 * ka_half(D); }
 __host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, max, sum
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   }
   if (tid < 2 * KA_WARPS) meta[tid].b = -1;
   Kv8Runs runs;
-  runs.total = kv8_line<KA_U, KA_THREADS>(p, prefix, s_warp);
+  runs.total = kv8_line<KA_U, KA_COST, KA_THREADS>(p, prefix, s_warp);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x) * KA_WARPS));
   const int cta = blockIdx.x, run = cta * KA_WARPS + warp;
   if (cta * KA_WARPS >= runs.n) return;
@@ -142,20 +143,20 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   int lu = 0, l_end = 0, pid = -1;
   bool more = w_beg < w_end;
   if (more) {
-    ls = kv8_seg<KA_U>(p, prefix, lw, w_end, runs);
+    ls = kv8_seg<KA_U, KA_COST>(p, prefix, lw, w_end, runs);
     lu = ls.u0;
     l_end = kv8_seg_end(ls, p.tq_shift);
   }
   const Kv8Seg first_seg = ls;
   auto settle = [&] {                 // the cursor's next piece: its segment and its pages
     if (!more) return;
-    if (lu >= ls.u1) {
-      lw += ls.u1 - ls.u0;
+    while (lu >= ls.u1) {
+      lw += ls.len;
       if (lw >= w_end) {
         more = false;
         return;
       }
-      kv8_next<KA_U>(ls, p, prefix, lw, w_end, runs);
+      kv8_next<KA_U, KA_COST>(ls, p, prefix, lw, w_end, runs);
       lu = ls.u0;
       l_end = kv8_seg_end(ls, p.tq_shift);
     }
@@ -206,7 +207,9 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   bool dead = false;      // a wait gave up: nothing more is loaded or computed
   Kv8Seg sg = first_seg;
   for (long long w = w_beg; w < w_end;) {
-    if (w > w_beg) kv8_next<KA_U>(sg, p, prefix, w, w_end, runs);
+    if (w > w_beg) kv8_next<KA_U, KA_COST>(sg, p, prefix, w, w_end, runs);
+    w += sg.len;
+    if (sg.u1 <= sg.u0) continue;     // the run ends before the tile's first piece
     const int end = kv8_seg_end(sg, p.tq_shift);
     const int tok0 = sg.t << p.tq_shift;
     const int ntok = min(1 << p.tq_shift, sg.s.n - tok0);
@@ -429,7 +432,6 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     }
     if (!whole && lane == 0)
       meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, sg.w_first, sg.w_last, 0};
-    w += sg.u1 - sg.u0;
   }
   // a warp that gave up: copies still in flight land before the shared memory goes away
   for (; taken < issued; ++taken) {
@@ -622,6 +624,7 @@ extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gq
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.out = static_cast<__nv_bfloat16*>(out);
+  p.out_wide = (o0 & 31u) == 0;
   p.hq = n_q_heads;
   p.G = G;
   p.tq_shift = R ? floor_log2(R / G) : 0;

@@ -35,6 +35,7 @@ namespace {
 
 constexpr int KP_THREADS = 640;
 constexpr int KP_U = 128;                         // positions per tile
+constexpr int KP_COST = 2;                        // a tile's start, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
 constexpr int KP_NB = KP_U / KV8_BLOCK;           // scales per tile
 constexpr int KP_SLOTS = 4;                       // tiles whose scales are kept
@@ -98,6 +99,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// 32 bytes, a whole sector, from one thread (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
@@ -189,11 +196,12 @@ struct __align__(16) KpTile {
 
 // Workspace of a part: floats of a row (O, reference, normaliser), the rows of CTA c's part of
 // a tile that began in CTA c_first, and the tiles to join, one entry per CTA.
-__host__ __device__ constexpr int kp_ps(int D) { return D + 4; }
+__host__ __device__ constexpr int kp_ps(int D) { return D + 8; }      // 32-byte rows
 constexpr size_t KP_TILES_BYTES = KV8_MAX_CTAS * sizeof(KpTile);
 __device__ __forceinline__ KpTile* kp_tiles(float* part) { return reinterpret_cast<KpTile*>(part); }
 template <int D>
 __device__ __forceinline__ float* kp_slot(float* part, int c, int c_first, int row) {
+  static_assert(KP_TILES_BYTES % 32 == 0 && KV8_TICKET_BYTES % 32 == 0, "rows 32-byte aligned");
   return part + KP_TILES_BYTES / 4 + ((static_cast<size_t>(c) * 2 + (c == c_first)) * (2 * KP_ROWS) + row) * kp_ps(D);
 }
 
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     fence_mbar_init();
   }
   Kv8Runs runs;
-  runs.total = kv8_line<KP_U, KP_THREADS>(p, prefix, s_warp);
+  runs.total = kv8_line<KP_U, KP_COST, KP_THREADS>(p, prefix, s_warp);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x)));
   const int cta = blockIdx.x;
   if (cta >= runs.n) {                          // the whole CTA, before any TMEM is held
@@ -267,13 +275,17 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       auto wait = [&](int b, int phase) {
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns))) dead = true;
       };
+      const uint32_t inv_g = (65535u + p.G) / p.G;       // r / G = r inv_g >> 16 for r < 128, G <= 16
       int it = 0, seg = 0;
       KpTile tile = {0, 0, 0, 0, 0, {0, 0, 0}};
-      Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w_beg, w_end, runs);
+      Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end, runs);
       for (long long w = w_beg; w < w_end;) {
-        if (w > w_beg) kv8_next<KP_U>(sg, p, prefix, w, w_end, runs);
-        const int tok = (sg.t << p.tq_shift) + blk * blk_tokens + r / p.G, hh = r % p.G;
-        const bool live = r / p.G < blk_tokens && tok < sg.s.n;
+        if (w > w_beg) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end, runs);
+        w += sg.len;
+        if (sg.u1 <= sg.u0) continue;      // the run ends before the tile's first positions
+        const int tok0 = (sg.t << p.tq_shift) + blk * blk_tokens;
+        const int tr = (r * inv_g) >> 16, tok = tok0 + tr, hh = r - tr * p.G;
+        const bool live = tr < blk_tokens && tok < sg.s.n;
         // positions that the row sees; a row without a token (zeros) needs no mask
         const int see = live ? sg.s.first + tok + 1 : 1 << 30;
         // ---- the warp's 32 query rows, scaled into fp16, into the swizzled tile: a row per
@@ -286,8 +298,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             uint4 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int r2 = 32 * (warp & 3) + i0 + i * RPS + lane / LPR, tb = r2 / p.G;
-              const int t2 = (sg.t << p.tq_shift) + blk * blk_tokens + tb;
+              const int r2 = 32 * (warp & 3) + i0 + i * RPS + lane / LPR, tb = (r2 * inv_g) >> 16;
+              const int t2 = tok0 + tb;
               v[i] = make_uint4(0, 0, 0, 0);
               if (tb < blk_tokens && t2 < sg.s.n)
                 v[i] = ldg_nc_v4(p.q + static_cast<size_t>(sg.s.off + t2) * p.q_stride +
@@ -297,11 +309,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             for (int i = 0; i < 8; ++i) {
               const int r2 = 32 * (warp & 3) + i0 + i * RPS + lane / LPR;
               uint32_t* x = &v[i].x;
-              uint32_t big = 0;
+              uint32_t big2 = 0;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) big = max(big, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+              for (int j = 0; j < 4; ++j) big2 = __vmaxu2(big2, x[j] & 0x7FFF7FFFu);
 #pragma unroll
-              for (int m = LPR / 2; m >= 1; m >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, m));
+              for (int m = LPR / 2; m >= 1; m >>= 1) big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, m));
+              const uint32_t big = max(big2 >> 16, big2 & 0xFFFFu);
               const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, -100), 100);
               const float f = pow2i(-e);
 #pragma unroll
@@ -324,45 +337,49 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           if (dead) continue;
           tc_fence_after();
           const float4 sc4 = s_scale[it & (KP_SLOTS - 1)];
-          const float f = rs * sc4.x, e = sc4.y;
+          const float f = fmaxf(rs * sc4.x, 1e-37f), e = sc4.y;  // positive, so that -inf stays -inf
           const uint32_t bad = __float_as_uint(sc4.w);
           const int left = see - u * KP_U;                       // positions of the tile that the row sees
-          // A tile at the causal edge (or with a page missing) takes a path of its own, so that
-          // the others carry no mask: 2 of 5 instructions per score, measured.
-          const bool edge = __any_sync(0xffffffffu, left < KP_U) || bad;
-          const auto hidden = [&](int j) { return j >= left || ((bad >> (j / KV8_BLOCK)) & 1); };
-          // The scores are read twice, 32 columns at a time, the next ones while these are worked
-          // on: 128 of them in registers do not fit beside the rest.
           uint32_t sc[2][32];
-          // ---- pass 1: the maximum of s_i + e
-          float mx = -INFINITY;
-          if (edge) {
+          // A tile at the causal edge, or with a page missing: what the row does not see becomes
+          // -inf in TMEM first, so that the passes below carry no mask (2 of 5 instructions per
+          // score, measured).
+          if (__any_sync(0xffffffffu, left < KP_U) || bad) {
 #pragma unroll 1
             for (int c = 0; c < KP_U / 32; ++c) {
               tmem_ld32(t_s + 32 * c, sc[0]);
+              const int n = left - 32 * c;
+              uint32_t seen = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+              if ((bad >> (2 * c)) & 1) seen &= 0xFFFF0000u;
+              if ((bad >> (2 * c + 1)) & 1) seen &= 0x0000FFFFu;
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (!hidden(32 * c + j)) mx = fmaxf(mx, __uint_as_float(sc[0][j]));
+                if (!(seen & (1u << j))) sc[0][j] = 0xFF800000u;
+              tmem_st32(t_s + 32 * c, sc[0]);
             }
-          } else {
-            tmem_ld32(t_s, sc[0]);
-#pragma unroll
-            for (int c = 0; c < KP_U / 32; ++c) {
-              tmem_ld_wait();
-              tmem_ld32(t_s + 32 * ((c + 1) % (KP_U / 32)), sc[(c + 1) & 1]);   // last: pass 2's first
-              const uint32_t* x = sc[c & 1];
-              float m[10];
-#pragma unroll
-              for (int j = 0; j < 10; ++j)
-                m[j] = max3(__uint_as_float(x[3 * j]), __uint_as_float(x[3 * j + 1]), __uint_as_float(x[3 * j + 2]));
-              m[0] = max3(m[0], __uint_as_float(x[30]), __uint_as_float(x[31]));
-#pragma unroll
-              for (int j = 0; j < 3; ++j) m[j] = max3(m[j], m[3 + j], m[6 + j]);
-              mx = max3(mx, max3(m[0], m[1], m[2]), m[9]);
-            }
+            tmem_st_wait();
           }
-          mx = mx == -INFINITY ? mx : fmaf(mx, f, e);
+          // The scores are read twice, 32 columns at a time, the next ones while these are worked
+          // on: 128 of them in registers do not fit beside the rest.
+          // ---- pass 1: the maximum of s_i + e
+          float mx = -INFINITY;
+          tmem_ld32(t_s, sc[0]);
+#pragma unroll
+          for (int c = 0; c < KP_U / 32; ++c) {
+            tmem_ld_wait();
+            tmem_ld32(t_s + 32 * ((c + 1) % (KP_U / 32)), sc[(c + 1) & 1]);   // last: pass 2's first
+            const uint32_t* x = sc[c & 1];
+            float m[10];
+#pragma unroll
+            for (int j = 0; j < 10; ++j)
+              m[j] = max3(__uint_as_float(x[3 * j]), __uint_as_float(x[3 * j + 1]), __uint_as_float(x[3 * j + 2]));
+            m[0] = max3(m[0], __uint_as_float(x[30]), __uint_as_float(x[31]));
+#pragma unroll
+            for (int j = 0; j < 3; ++j) m[j] = max3(m[j], m[3 + j], m[6 + j]);
+            mx = max3(mx, max3(m[0], m[1], m[2]), m[9]);
+          }
+          mx = fmaf(mx, f, e);
           // ---- the reference moves: O and the normaliser follow
           const bool grow = mx > m_ref + KP_GROW;                // also the first finite maximum
           if (__any_sync(0xffffffffu, grow)) {
@@ -391,38 +408,20 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             const float add = e - m_at;
             const uint64_t f2 = f32x2(f, f), a2 = f32x2(add, add);
             uint64_t sum[2] = {0, 0};
-            if (edge) {
-#pragma unroll 1
-              for (int c = 0; c < KP_U / 32; ++c) {
-                tmem_ld32(t_s + 32 * c, sc[0]);
-                tmem_ld_wait();
-                uint32_t w16[16];
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                  float w0 = ex2(fmaf(__uint_as_float(sc[0][j]), f, add)), w1 = ex2(fmaf(__uint_as_float(sc[0][j + 1]), f, add));
-                  if (hidden(32 * c + j)) w0 = 0.0f;
-                  if (hidden(32 * c + j + 1)) w1 = 0.0f;
-                  sum[0] = add2(sum[0], f32x2(w0, w1));
-                  w16[j / 2] = pack2h(w0, w1);
-                }
-                tmem_st16(t_s + 16 * c, w16);
+            for (int c = 0; c < KP_U / 32; ++c) {
+              tmem_ld_wait();
+              if (c + 1 < KP_U / 32) tmem_ld32(t_s + 32 * (c + 1), sc[(c + 1) & 1]);
+              const uint32_t* x = sc[c & 1];
+              uint32_t w16[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 y = f32x2_get(fma2(f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2, a2));
+                const float w0 = ex2(y.x), w1 = ex2(y.y);
+                sum[j & 1] = add2(sum[j & 1], f32x2(w0, w1));
+                w16[j] = pack2h(w0, w1);
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < KP_U / 32; ++c) {
-                tmem_ld_wait();
-                if (c + 1 < KP_U / 32) tmem_ld32(t_s + 32 * (c + 1), sc[(c + 1) & 1]);
-                const uint32_t* x = sc[c & 1];
-                uint32_t w16[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float2 y = f32x2_get(fma2(f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2, a2));
-                  const float w0 = ex2(y.x), w1 = ex2(y.y);
-                  sum[j & 1] = add2(sum[j & 1], f32x2(w0, w1));
-                  w16[j] = pack2h(w0, w1);
-                }
-                tmem_st16(t_s + 16 * c, w16);
-              }
+              tmem_st16(t_s + 16 * c, w16);
             }
             const float2 t = f32x2_get(add2(sum[0], sum[1]));
             l = fmaf(t.x + t.y, sc4.z, l);
@@ -448,19 +447,23 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           if (whole) {
             if (dst && !dead)
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                uint32_t x[4];
+              for (int j = 0; j < 32; j += 16) {
+                uint32_t x[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 8; ++k)
                   x[k] = l == 0.0f ? 0u
                                    : pack_bf16x2(__float_as_uint(__uint_as_float(o[j + 2 * k]) * inv),
                                                  __float_as_uint(__uint_as_float(o[j + 2 * k + 1]) * inv));
-                *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(x[0], x[1], x[2], x[3]);
+                if (p.out_wide) {
+                  st_global_v8(dst + 32 * c + j, x);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + 32 * c + j) = make_uint4(x[0], x[1], x[2], x[3]);
+                  *reinterpret_cast<uint4*>(dst + 32 * c + j + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                }
               }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(part + 32 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            for (int j = 0; j < 32; j += 8) st_global_v8(part + 32 * c + j, o + j);
           }
         }
         tc_fence_before();
@@ -468,10 +471,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           *reinterpret_cast<float2*>(part + D) = make_float2(m_ref, l);
           if (tid == 0 && sg.w_first == cta) tile = KpTile{sg.w_last - sg.w_first + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
-        w += sg.u1 - sg.u0;
         ++seg;
       }
-      if (tid == 0) kp_tiles(p.part)[cta] = tile;
+      if (tid == 0) {
+        kp_tiles(p.part)[cta] = tile;
+        s_n[seg & 1] = 0;                  // no more segments
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
     }
   } else if (warp < 16) {
     reg_dec<KP_REG_DEQUANT>();
@@ -489,33 +496,38 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     // 8-15 its V blocks.
     const int lb = lane & 7;
     long long w = w_beg;
-    Kv8Seg sg = kv8_seg<KP_U>(p, prefix, w, w_end, runs);
+    Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w, w_end, runs);
     int u = sg.u0, end = kv8_seg_end(sg, p.tq_shift);
     bool more = true;
     int pid = -1, pid_at = 0, pid_valid = 0;    // looked up: page; offset in the page; positions before the end
-    bool pid_live = false;
     int pid_g = 0;
+    bool pid_live = false, looked = false;      // the lane's block exists; the tile exists
+    const auto advance = [&] {                  // to the next segment with positions
+      while (u >= sg.u1) {
+        w += sg.len;
+        more = w < w_end;
+        if (!more) break;
+        kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end, runs);
+        u = sg.u0;
+        end = kv8_seg_end(sg, p.tq_shift);
+      }
+    };
     auto look = [&] {                           // stage 1 of the cursor's tile, then on to the next one
       const int pos = u * KP_U + lb * KV8_BLOCK;
+      looked = more;
       pid_live = more && pos < end;
       pid_valid = more ? end - u * KP_U : 0;
       pid_at = pos & ((1 << p.c.page_shift) - 1);
       pid_g = sg.g;
       if (pid_live) pid = __ldg(p.b.page_table + static_cast<size_t>(sg.b) * p.b.max_pages + (pos >> p.c.page_shift));
-      if (more && ++u >= sg.u1) {
-        w += sg.u1 - sg.u0;
-        more = w < w_end;
-        if (more) {
-          kv8_next<KP_U>(sg, p, prefix, w, w_end, runs);
-          u = sg.u0;
-          end = kv8_seg_end(sg, p.tq_shift);
-        }
-      }
+      ++u;
+      if (more) advance();
     };
     int rows = -1, valid = 0;                   // stage 2: first code row of the lane's block (negative: none)
     float scale = 0.0f;
-    bool bad = false;
+    bool bad = false, located = false;
     auto locate = [&] {
+      located = looked;
       bad = pid_live && (pid < 0 || pid >= p.c.n_pages);
       rows = -1;
       scale = 0.0f;
@@ -528,7 +540,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     uint4 reg[NI];
     uint32_t fac = 0;                           // of the tile in reg: the lane's block's factor to the tile's scale
     float4 now = make_float4(0, 0, 0, 0);       // of the tile in reg: what the softmax needs
+    bool loaded = false;
     auto load = [&] {                           // stage 3
+      loaded = located;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
@@ -568,14 +582,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       fence_proxy_async_smem();
       __syncwarp();
     };
+    advance();
     look();
     locate();
     look();
     load();
     locate();
     look();
-    const int n_tiles = static_cast<int>(w_end - w_beg);
-    for (int it = 0; it < n_tiles; ++it) {
+    for (int it = 0; loaded; ++it) {
       const int s = it & 1, ph = (it >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
       if (tid == 256) s_scale[it & (KP_SLOTS - 1)] = now;
@@ -626,16 +640,18 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         tc_fence_after();
         return ok;
       };
-      const int n_tiles = static_cast<int>(w_end - w_beg);
       int it = 0;
       bool ok = true;
-      for (int seg = 0; ok && it < n_tiles; ++seg) {
+      for (int seg = 0; ok; ++seg) {
+        ok = wait(BAR_Q, seg);
+        if (!ok) break;
+        const int n = s_n[seg & 1];               // the segment's tiles, told by the softmax (0: no more)
+        if (n == 0) break;
         ok = wait(BAR_KF + (it & 1), it >> 1);
         for (int i = 0; ok && i < nblk; ++i) {
-          ok = wait(BAR_Q + i, seg);
+          if (i) ok = wait(BAR_Q + i, seg);
           if (ok) qk(i, it & 1, i == nblk - 1);
         }
-        const int n = s_n[seg & 1];               // the segment's tiles, told by the softmax
         for (int j = 0; ok && j < n; ++j, ++it) {
           const int s = it & 1;
           ok = wait(BAR_VF + s, it >> 1);

@@ -17,6 +17,9 @@
 // (whole divisions; the last tile sees all of the sequence), and the sum of x / r over
 // x = 0 .. X is r q (q - 1) / 2 + q (m + 1) with q = X / r, m = X mod r.  With TQ = c U it is
 // (a + U - 1) / U + c (i + 1) units.
+// Starting a tile costs as much as some units (its queries are fetched, its result written),
+// so each has C more units in the line than positions to see; they come first, and a run
+// that ends inside them leaves the tile to the next.
 #pragma once
 
 #include "kv8.cuh"
@@ -35,6 +38,7 @@ struct Kv8AttnParams {
   __nv_bfloat16* out;
   int hq, G, tq_shift;
   float scale_log2;      // score scale * log2(e)
+  int out_wide;          // out is 32-byte aligned
   unsigned* tickets;     // [KV8_MAX_CTAS], zero between calls
   float* part;           // [CTA][2][rows][row floats]
   unsigned long long wait_ns;
@@ -44,8 +48,9 @@ struct Kv8AttnParams {
 struct Kv8Seg {
   Kv8Seq s;
   int b, g, t;           // sequence, key/value head, tile of the sequence
-  int u0, u1, units;     // this run's units, the tile's units
-  int w_first, w_last;   // the runs that hold the tile's first and last unit (where they differ)
+  int u0, u1, units;     // this run's units of positions (none: u1 <= u0), the tile's
+  int len;               // units of the line that the segment takes
+  int w_first, w_last;   // the runs that hold the tile's first and last units of positions (where they differ)
 };
 
 // The line cut into n runs: run i is units i total / n up to (i + 1) total / n, and unit w
@@ -63,40 +68,37 @@ __device__ __forceinline__ int kv8_run_of(const Kv8Runs& r, long long w) {
   return static_cast<int>(kv8_div((w + 1) * r.n - 1, r.total));
 }
 
-template <int U>
 __device__ __forceinline__ long long kv8_upto(long long x, int r_shift) {
   const long long q = x >> r_shift, m = x & ((1ll << r_shift) - 1);
   return ((q * (q - 1)) << r_shift) / 2 + q * (m + 1);
 }
 
 // Units of tiles 0 .. t - 1 of a sequence (t at most its last tile).
-template <int U>
+template <int U, int C>
 __device__ __forceinline__ long long kv8_units_before(const Kv8Seq& s, int tq_shift, int t) {
   constexpr int US = U == 32 ? 5 : U == 64 ? 6 : U == 128 ? 7 : 8;
   static_assert((1 << US) == U, "U is 32 to 256");
-  if (tq_shift > US) {
-    const long long n = t;
-    return n * ((max(s.first, 0) + U - 1) / U) + ((n * (n + 1) / 2) << (tq_shift - US));
-  }
+  const long long n = t;
+  if (tq_shift > US) return n * ((max(s.first, 0) + U - 1) / U + C) + ((n * (n + 1) / 2) << (tq_shift - US));
   const int rs = US - tq_shift;
   const long long A = (max(s.first, 0) + U - 1) >> tq_shift;
-  return kv8_upto<U>(A + t, rs) - kv8_upto<U>(A, rs);
+  return kv8_upto(A + t, rs) - kv8_upto(A, rs) + C * n;
 }
-// Units of the last tile: what the sequence's last new token sees, one at least.
-template <int U>
-__device__ __forceinline__ int kv8_units_last(const Kv8Seq& s) {
-  return (max(s.first, 0) + s.n + U - 1) / U;
+// Units of one tile: what its last token sees, one at least, and C.
+template <int U, int C>
+__device__ __forceinline__ int kv8_units_tile(const Kv8Seq& s, int tq_shift, int t) {
+  return (max(s.first, 0) + min((t + 1) << tq_shift, s.n) + U - 1) / U + C;
 }
-template <int U>
+template <int U, int C>
 __device__ __forceinline__ long long kv8_units_seq(const Kv8Seq& s, int tq_shift) {
   if (s.n <= 0) return 0;
   const int tiles = (s.n + (1 << tq_shift) - 1) >> tq_shift;
-  return kv8_units_before<U>(s, tq_shift, tiles - 1) + kv8_units_last<U>(s);
+  return kv8_units_before<U, C>(s, tq_shift, tiles - 1) + kv8_units_tile<U, C>(s, tq_shift, tiles - 1);
 }
 
 // The line: prefix[b] = units before sequence b (all heads), in shared memory, filled by
 // the whole CTA (THREADS threads, s_warp: THREADS / 32 words); returns its length.
-template <int U, int THREADS>
+template <int U, int C, int THREADS>
 __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long* prefix, long long* s_warp) {
   const int tid = threadIdx.x, B = p.b.n_seqs;
   const int per = (B + THREADS - 1) / THREADS;
@@ -105,7 +107,7 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   for (int b = b0; b < b1; ++b) {
     const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
     if (s.bad && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
-    sum += kv8_units_seq<U>(s, p.tq_shift) * p.c.hkv;
+    sum += kv8_units_seq<U, C>(s, p.tq_shift) * p.c.hkv;
     prefix[b] = sum;                       // inside this thread's run for now
   }
   long long incl = sum;
@@ -133,24 +135,24 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   return total;
 }
 
-// Units of one tile.
-template <int U>
-__device__ __forceinline__ int kv8_units_tile(const Kv8Seq& s, int tq_shift, int t) {
-  return (max(s.first, 0) + min((t + 1) << tq_shift, s.n) + U - 1) / U;
-}
-
-// Ends the segment that starts at unit w with its tile or at w_end.
-__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, long long w, long long w_end, const Kv8Runs& runs) {
+// Ends the segment that starts at unit w, x units into its tile of `all` units, with the tile or
+// at w_end.
+template <int C>
+__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, int x, int all, long long w, long long w_end, const Kv8Runs& runs) {
   const long long left = w_end - w;
-  g.u1 = g.units - g.u0 <= left ? g.units : g.u0 + static_cast<int>(left);
+  const int end = all - x <= left ? all : x + static_cast<int>(left);
+  g.len = end - x;
+  g.units = all - C;
+  g.u0 = max(x - C, 0);
+  g.u1 = end - C;
   if (g.u0 > 0 || g.u1 < g.units) {
-    g.w_first = kv8_run_of(runs, w - g.u0);
-    g.w_last = kv8_run_of(runs, w - g.u0 + g.units - 1);
+    g.w_first = kv8_run_of(runs, w - x + C);
+    g.w_last = kv8_run_of(runs, w - x + all - 1);
   }
 }
 
 // The segment that starts at unit w of the line.
-template <int U>
+template <int U, int C>
 __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w, long long w_end,
                                           const Kv8Runs& runs) {
   Kv8Seg g;
@@ -169,19 +171,17 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
   int tl = 0, th = tiles;                  // units before tl <= x < units before th
   while (th - tl > 1) {
     const int m = (tl + th) >> 1;
-    if (kv8_units_before<U>(g.s, p.tq_shift, m) <= x) tl = m; else th = m;
+    if (kv8_units_before<U, C>(g.s, p.tq_shift, m) <= x) tl = m; else th = m;
   }
   g.t = tl;
-  const long long before = kv8_units_before<U>(g.s, p.tq_shift, tl);
-  g.units = kv8_units_tile<U>(g.s, p.tq_shift, tl);
-  g.u0 = static_cast<int>(x - before);
-  kv8_seg_close(g, w, w_end, runs);
+  const int in_tile = static_cast<int>(x - kv8_units_before<U, C>(g.s, p.tq_shift, tl));
+  kv8_seg_close<C>(g, in_tile, kv8_units_tile<U, C>(g.s, p.tq_shift, tl), w, w_end, runs);
   return g;
 }
 
 // The segment after `g`, at unit w of the line (g was not the run's last): it begins a tile,
 // the sequence's next one, or the first of the next head or sequence.
-template <int U>
+template <int U, int C>
 __device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const long long* prefix, long long w,
                                          long long w_end, const Kv8Runs& runs) {
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
@@ -193,9 +193,7 @@ __device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, cons
       g.s = kv8_seq(p.b, p.c.page_shift, g.b);
     }
   }
-  g.units = kv8_units_tile<U>(g.s, p.tq_shift, g.t);
-  g.u0 = 0;
-  kv8_seg_close(g, w, w_end, runs);
+  kv8_seg_close<C>(g, 0, kv8_units_tile<U, C>(g.s, p.tq_shift, g.t), w, w_end, runs);
 }
 
 // Positions that the tile's last token sees.

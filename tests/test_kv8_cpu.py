@@ -202,47 +202,61 @@ def test_block_units_do_not_meet():
                 assert max(s for s in range(B) if off[s] // 16 + 2 * s <= u) == b
 
 
-def _before(first, U, tq, t):
+def _before(first, U, C, tq, t):
     """Units of a sequence's tiles 0 .. t - 1, in closed form."""
     if tq > U:
-        return t * -(-max(first, 0) // U) + tq // U * t * (t + 1) // 2
+        return t * (-(-max(first, 0) // U) + C) + tq // U * t * (t + 1) // 2
     r = U // tq
     F = lambda X: r * (X // r) * (X // r - 1) // 2 + (X // r) * (X % r + 1)  # noqa: E731
     A = (max(first, 0) + U - 1) // tq
-    return F(A + t) - F(A)
+    return F(A + t) - F(A) + C * t
 
 
-@pytest.mark.parametrize("U", [32, 128])
-def test_line_of_units(U):
-    """The closed form of a sequence's units against a sum over its tiles; and a line cut
-    into equal runs covers every tile's units once, with at most one part of a tile at
-    either end of a run, so that two slots and one ticket per CTA suffice."""
+@pytest.mark.parametrize("U,C,per_cta", [(32, 2, 8), (128, 2, 1), (32, 0, 8)])
+def test_line_of_units(U, C, per_cta):
+    """The closed form of a sequence's units against a sum over its tiles.  And a line cut into
+    runs: every run's segments cover each tile's units of positions once, in order; a run
+    holds at most one tile that began before it and one that goes on after it; a CTA's runs
+    share a ticket and two workspace slots with other CTAs without conflict."""
     rng = random.Random(2)
     for _ in range(1500):
         tq = rng.choice([1, 2, 4, 8, 16, 32] + ([64, 128, 256] if U == 128 else []))
         hkv = rng.randint(1, 3)
-        seqs = [(rng.choice([0, rng.randint(0, 700)]), rng.choice([1, 1, rng.randint(1, 90)]))
+        seqs = [(rng.choice([0, rng.randint(0, 700)]), rng.choice([1, 1, rng.randint(1, 90), rng.randint(200, 900)]))
                 for _ in range(rng.randint(1, 6))]
-        tiles = []
+        tiles = []                                   # (name, units of positions)
         for b, (first, n) in enumerate(seqs):
             nt = -(-n // tq)
             per = [-(-(first + min((t + 1) * tq, n)) // U) for t in range(nt)]
             for t in range(nt):
-                assert _before(first, U, tq, t) == sum(per[:t])
+                assert _before(first, U, C, tq, t) == sum(per[:t]) + C * t
             for g in range(hkv):
-                tiles += [(b, g, t, per[t]) for t in range(nt)]
-        total = sum(x[3] for x in tiles)
-        grid = rng.choice([1, 3, 16, 152])
-        share = max(rng.choice([1, 8]), -(-total // grid))
-        assert -(-total // share) <= grid
-        start, slots, tickets = 0, set(), {}
-        for tile in tiles:
-            end = start + tile[3]
-            c0, c1 = start // share, (end - 1) // share
+                tiles += [((b, g, t), per[t]) for t in range(nt)]
+        total = sum(n + C for _, n in tiles)
+        ctas = rng.choice([1, 3, 16, 152])
+        runs = min(total, ctas * per_cta)
+        run_of = lambda w: ((w + 1) * runs - 1) // total  # noqa: E731
+        begin = [i * total // runs for i in range(runs + 1)]
+        assert all(run_of(w) == i for i in range(runs) for w in (begin[i], begin[i + 1] - 1))
+        start, seen, slots, tickets = 0, {}, set(), {}
+        for name, n in tiles:
+            first, last = run_of(start + C), run_of(start + C + n - 1)
+            done = 0
+            for i in range(first, last + 1):
+                u0 = max(begin[i] - start - C, 0)
+                u1 = min(begin[i + 1] - start - C, n)
+                assert u0 == done and u1 > u0            # a run between holds some of the tile
+                done = u1
+                if u0 > 0:
+                    assert seen.setdefault((i, "began before"), name) == name
+                elif u1 < n:
+                    assert seen.setdefault((i, "goes on"), name) == name
+            assert done == n
+            c0, c1 = first // per_cta, last // per_cta
             if c0 != c1:
-                assert tickets.setdefault(c0, tile) == tile       # a ticket serves one tile
+                assert tickets.setdefault(c0, name) == name       # a ticket serves one tile
                 for c in range(c0, c1 + 1):
                     slot = (c, 1 if c == c0 else 0)
                     assert slot not in slots
                     slots.add(slot)
-            start = end
+            start += n + C
