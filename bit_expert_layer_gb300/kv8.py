@@ -18,7 +18,7 @@ only the device can see is collected in the cache's error word (``get_error``).
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
 
 import torch
 
@@ -27,30 +27,33 @@ from ._abi import GqaKv8Batch, GqaKv8Cache
 
 BLOCK = 16                                   # positions that share a scale
 FORMATS = {"e4m3": _abi.GQA_KV8_E4M3, "int8": _abi.GQA_KV8_INT8}
-_HERE = contextlib.nullcontext()
+_BF16 = torch.bfloat16
+_empty, _current_device = torch.empty, torch.cuda.current_device
 
 
-def _on(device: torch.device, stream=None):
-    """Makes `device` and `stream` the current ones for a call, so that what the call
-    allocates belongs to the stream that uses it (nothing to do where they already are)."""
+def _elsewhere(device: torch.device, stream):
+    """None where `device` and the stream to use are the current ones; else what makes them so
+    for a call, so that what the call allocates belongs to the stream that uses it."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return None if device.index == _current_device() else torch.cuda.device(device)
 
 
-def _handle(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _handle(index: int) -> int:
+    """The current stream's handle (torch.cuda.current_stream takes 2 us to wrap it)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _rows(x: torch.Tensor, name: str, heads: int, head_size: int, device) -> int:
     """The row stride of a [T, heads, head_size] tensor whose rows are contiguous."""
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.device != device:
+    shape = x.shape
+    if x.dtype is not _BF16 or len(shape) != 3 or x.device != device:
         raise ValueError(f"{name}: a 3-dimensional bfloat16 tensor on {device} is wanted")
-    t, h, d = x.shape
+    t, h, d = shape
     if h != heads or d != head_size:
-        raise ValueError(f"{name}: shape [T, {heads}, {head_size}] is wanted, got {list(x.shape)}")
+        raise ValueError(f"{name}: shape [T, {heads}, {head_size}] is wanted, got {list(shape)}")
     st, sh, sd = x.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: the heads of a row have to be contiguous")
@@ -83,13 +86,15 @@ class KV8Batch:
         self.max_new = int(max_new)
         self._c = {}
 
-    def c(self, n_tokens: int) -> GqaKv8Batch:
-        c = self._c.get(n_tokens)
-        if c is None:
+    def c(self, n_tokens: int):
+        """The C description (by reference) for token tensors of n_tokens rows."""
+        ref = self._c.get(n_tokens)
+        if ref is None:
             c = GqaKv8Batch(self.page_table.data_ptr(), self.lens.data_ptr(), self.offsets.data_ptr(),
                             self.page_table.shape[0], self.page_table.shape[1], n_tokens, self.max_new)
-            self._c = {n_tokens: c}
-        return c
+            ref = ctypes.byref(c)
+            self._c = {n_tokens: ref}
+        return ref
 
 
 class KV8Cache:
@@ -115,9 +120,9 @@ class KV8Cache:
         self.device = k.device
         self.n_pages, self.n_kv_heads, self.page_size, self.head_size = k.shape
         self.error = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._c = GqaKv8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                              self.error.data_ptr(), self.n_pages, self.page_size, self.n_kv_heads, self.head_size,
-                              FORMATS[fmt])
+        self._c = ctypes.byref(GqaKv8Cache(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.error.data_ptr(), self.n_pages,
+            self.page_size, self.n_kv_heads, self.head_size, FORMATS[fmt]))
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int = 2, page_size: int = 64, head_size: int = 128, fmt: str = "e4m3",
@@ -127,7 +132,7 @@ class KV8Cache:
         ks, vs = (torch.ones(shape[:2] + (page_size // BLOCK,), dtype=torch.float32, device=device) for _ in range(2))
         return cls(k, v, ks, vs, fmt)
 
-    def _batch(self, batch: KV8Batch, n_tokens: int) -> GqaKv8Batch:
+    def _batch(self, batch: KV8Batch, n_tokens: int):
         if batch.device != self.device:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
         return batch.c(n_tokens)
@@ -135,28 +140,36 @@ class KV8Cache:
     def append(self, batch: KV8Batch, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
         """Quantise the new tokens' keys and values (bf16 [T, n_kv_heads, head_size], rows may
         be slices of a wider tensor) and write them into the cache."""
-        ks = _rows(k, "k", self.n_kv_heads, self.head_size, self.device)
-        vs = _rows(v, "v", self.n_kv_heads, self.head_size, self.device)
-        if k.shape[0] != v.shape[0]:
-            raise ValueError(f"k has {k.shape[0]} rows and v {v.shape[0]}")
-        with _on(self.device, stream):
-            _abi.gqa_kv8_append(self._c, self._batch(batch, k.shape[0]), k.data_ptr(), ks, v.data_ptr(), vs,
-                                _handle(self.device))
+        dev = self.device
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return self.append(batch, k, v)
+        ks = _rows(k, "k", self.n_kv_heads, self.head_size, dev)
+        vs = _rows(v, "v", self.n_kv_heads, self.head_size, dev)
+        t = k.shape[0]
+        if v.shape[0] != t:
+            raise ValueError(f"k has {t} rows and v {v.shape[0]}")
+        _abi.gqa_kv8_append(self._c, self._batch(batch, t), k.data_ptr(), ks, v.data_ptr(), vs, _handle(dev.index))
 
     def gather(self, batch: KV8Batch, n_tokens: int, out=None, stream=None):
         """The batch's rows read back: (k, v), bf16 [n_tokens, n_kv_heads, head_size].  Rows at
         or past offsets[n_seqs] stay as they are."""
-        with _on(self.device, stream):
-            if out is None:
-                shape = (n_tokens, self.n_kv_heads, self.head_size)
-                out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
-            else:
-                for name, x in zip(("k_out", "v_out"), out):
-                    _rows(x, name, self.n_kv_heads, self.head_size, self.device)
-                    if x.shape[0] != n_tokens or not x.is_contiguous():
-                        raise ValueError(f"{name}: a contiguous tensor of {n_tokens} rows is wanted")
-            _abi.gqa_kv8_gather(self._c, self._batch(batch, n_tokens), out[0].data_ptr(), out[1].data_ptr(),
-                                _handle(self.device))
+        dev = self.device
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return self.gather(batch, n_tokens, out)
+        if out is None:
+            shape = (n_tokens, self.n_kv_heads, self.head_size)
+            out = (_empty(shape, dtype=_BF16, device=dev), _empty(shape, dtype=_BF16, device=dev))
+        else:
+            for name, x in zip(("k_out", "v_out"), out):
+                _rows(x, name, self.n_kv_heads, self.head_size, dev)
+                if x.shape[0] != n_tokens or not x.is_contiguous():
+                    raise ValueError(f"{name}: a contiguous tensor of {n_tokens} rows is wanted")
+        _abi.gqa_kv8_gather(self._c, self._batch(batch, n_tokens), out[0].data_ptr(), out[1].data_ptr(),
+                            _handle(dev.index))
         return out
 
     def new_workspace(self, n_q_heads: int, max_new: int) -> torch.Tensor:
@@ -171,28 +184,29 @@ class KV8Cache:
         """Causal attention of the new tokens' queries (bf16 [T, n_q_heads, head_size]) over
         the cache, their own positions among it; scale 0 means 1 / sqrt(head_size).  The
         workspace is allocated for the call if none is given."""
-        if q.dim() != 3:
-            raise ValueError("q: a 3-dimensional bfloat16 tensor is wanted")
-        heads = q.shape[1]
-        qs = _rows(q, "q", heads, self.head_size, self.device)
-        if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != self.device or
-                                not out.is_contiguous()):
+        dev = self.device
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return self.attention(batch, q, scale, out, workspace)
+        shape = q.shape
+        heads = shape[1] if len(shape) == 3 else 0
+        qs = _rows(q, "q", heads, self.head_size, dev)
+        if out is None:
+            out = _empty(shape, dtype=_BF16, device=dev)
+        elif out.shape != shape or out.dtype is not _BF16 or out.device != dev or not out.is_contiguous():
             raise ValueError("out: a contiguous bfloat16 tensor of q's shape is wanted")
-        with _on(self.device, stream):
-            if out is None:
-                out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
-            if workspace is None:
-                workspace = self.new_workspace(heads, batch.max_new)
-            elif workspace.device != self.device or not workspace.is_contiguous():
-                raise ValueError(f"workspace: a contiguous tensor on {self.device} is wanted")
-            _abi.gqa_kv8_attention(self._c, self._batch(batch, q.shape[0]), q.data_ptr(), qs, heads, scale,
-                                   out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   _handle(self.device))
+        if workspace is None:
+            workspace = self.new_workspace(heads, batch.max_new)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: a contiguous tensor on {dev} is wanted")
+        _abi.gqa_kv8_attention(self._c, self._batch(batch, shape[0]), q.data_ptr(), qs, heads, scale, out.data_ptr(),
+                               workspace.data_ptr(), workspace.nbytes, _handle(dev.index))
         return out
 
     def get_error(self) -> int:
         """Synchronises, then reads and clears the error word (a status of ``_abi.STATUS``)."""
-        with _on(self.device):
+        with torch.cuda.device(self.device):
             return _abi.gqa_kv8_get_error(self._c)
 
 
@@ -206,32 +220,41 @@ class Rope:
         self.plan = _abi.gqa_rope_plan_init(head_size, head_size if rotary is None else rotary, theta, inv_freq,
                                             sections, cyclic)
         self.head_size, self.n_axes = self.plan.head_size, self.plan.n_axes
+        self._plan = ctypes.byref(self.plan)
 
     def __call__(self, q: torch.Tensor, k: torch.Tensor | None, pos: torch.Tensor, out=None, stream=None):
         """q, k: bf16 [T, heads, head_size] (rows may be slices of a wider tensor; k may be
         None); pos: int32 [n_axes, T], or [T] with one axis; out: (q_out, k_out), which may
         be q and k themselves.  Returns (q_out, k_out)."""
+        dev, d = q.device, self.head_size
         if not q.is_cuda or q.dim() != 3:
             raise ValueError("q: a 3-dimensional bfloat16 CUDA tensor is wanted")
-        dev, d = q.device, self.head_size
-        t, hq = q.shape[0], q.shape[1]
-        if k is not None and (k.dim() != 3 or k.shape[0] != t):
-            raise ValueError(f"k: [{t}, heads, {d}] is wanted")
-        hk = 0 if k is None else k.shape[1]
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return self(q, k, pos, out)
+        t, hq = q.shape[:2]
+        hk = 0
+        qs, ks, kp = _rows(q, "q", hq, d, dev), 0, 0
+        if k is not None:
+            if k.dim() != 3 or k.shape[0] != t:
+                raise ValueError(f"k: [{t}, heads, {d}] is wanted")
+            hk, kp = k.shape[1], k.data_ptr()
+            ks = _rows(k, "k", hk, d, dev)
         _ints(pos, "pos", pos.dim(), dev)
         if tuple(pos.shape) != (self.n_axes, t) and not (self.n_axes == 1 and tuple(pos.shape) == (t,)):
             raise ValueError(f"pos: shape [{self.n_axes}, {t}] is wanted, got {list(pos.shape)}")
-        qs, ks = _rows(q, "q", hq, d, dev), 0 if k is None else _rows(k, "k", hk, d, dev)
-        with _on(dev, stream):
-            if out is None:
-                out = (torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev),
-                       None if k is None else torch.empty((t, hk, d), dtype=torch.bfloat16, device=dev))
+        qos, kos = hq * d, hk * d
+        if out is None:
+            qo = _empty((t, hq, d), dtype=_BF16, device=dev)
+            ko = None if k is None else _empty((t, hk, d), dtype=_BF16, device=dev)
+        else:
             qo, ko = out
-            if (k is None) != (ko is None):
-                raise ValueError("out: as many tensors as there are inputs are wanted")
-            if qo.shape != q.shape or (k is not None and ko.shape != k.shape):
+            if (k is None) != (ko is None) or qo.shape != q.shape or (k is not None and ko.shape != k.shape):
                 raise ValueError("out: tensors of q's and k's shapes are wanted")
-            qos, kos = _rows(qo, "q_out", hq, d, dev), 0 if k is None else _rows(ko, "k_out", hk, d, dev)
-            _abi.gqa_rope(self.plan, q.data_ptr(), qs, hq, 0 if k is None else k.data_ptr(), ks, hk, pos.data_ptr(),
-                          t, qo.data_ptr(), qos, 0 if k is None else ko.data_ptr(), kos, _handle(dev))
+            qos = _rows(qo, "q_out", hq, d, dev)
+            if ko is not None:
+                kos = _rows(ko, "k_out", hk, d, dev)
+        _abi.gqa_rope(self._plan, q.data_ptr(), qs, hq, kp, ks, hk, pos.data_ptr(), t, qo.data_ptr(), qos,
+                      0 if ko is None else ko.data_ptr(), kos, _handle(dev.index))
         return qo, ko
