@@ -123,6 +123,11 @@ __device__ __forceinline__ uint32_t kv8_encode4(float a, float b, float c, float
   }
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 // The exponent of a power-of-two scale.

@@ -7,19 +7,22 @@
 // leaves the two parts at the run's ends in shared memory for the CTA to join at the end, so
 // the warps meet once per launch.  (A CTA per tile, joined tile by tile, measured 122 us on
 // 64 sequences of 64 to 16384 positions: the short ones cost a barrier round each.)
-// Per piece, on mma.sync, R query rows (8 or 16) on the M side:
-//   S = Q K^T     fp16 with exact operands: codes are exact in fp16, and a query row is
-//                 scaled by a power of two to fit.  The order of the contraction is free, so
-//                 a lane takes 32 consecutive dims of a key, one or two 16-byte loads.
+// Per piece, on mma.sync (m16n8k16, fp16 in, fp32 out), with the R query rows (8 or 16) on the
+// N side, so that a full tile of 16 keys or 16 dims meets them:
+//   S^T = K Q^T   exact operands: codes are exact in fp16, and a query row is scaled by a power
+//                 of two to fit.  The order of the contraction is free, so a lane takes 32
+//                 consecutive dims of a key, two 16-byte loads.
 //   weights       in base 2, with the value block's scale folded in: w_i = 2^(s_i + e_i - m)
-//                 for values of scale 2^e_i, m the running maximum of s_i + e_i.  The value
-//                 product takes fp16(w_i) and the bare codes, the normaliser sums
-//                 w_i 2^-e_i in fp32; so the scales cost one fused multiply-add per score.
-//   O += w V      a lane takes 16 consecutive dims of 4 keys and interleaves their bytes, so
-//                 that a pair of codes of one dim becomes an fp16 pair; column n of the
-//                 MMA's j-th block is dim 16 n + j.
-// Bound: the cache's bytes.  Per 32 positions and SM (8 KB, about 350 cycles at the measured
-// copy rate) a warp issues about 350 instructions, spread over 4 schedulers.
+//                 for values of scale 2^e_i.  The value product takes fp16(w_i) and the bare
+//                 codes, the normaliser sums w_i 2^-e_i in fp32; so the scales cost nothing
+//                 per score.  The reference m moves only when some s_i + e_i outgrows it by
+//                 more than 8: fp16 holds weights up to 2^8 as exactly as smaller ones, and a
+//                 piece that does not move it needs no exchange between lanes.
+//   O^T += V^T w  a lane takes 16 consecutive dims of 4 keys and interleaves their bytes, so
+//                 that a pair of codes of one dim becomes an fp16 pair; the weights change
+//                 from S's layout to B's by a transposing move.
+// Bound: the cache's bytes.  With the rows on the M side (half of each MMA and of O's registers
+// empty at 8 rows) a piece took 750 instructions and 8 x 32768 positions 36.7 us.
 #include <cstring>
 
 #include "internal.h"
@@ -93,6 +96,15 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 
 // One 16-position block of a piece: bad or past the tile's end when scale < 0.
 constexpr float KA_NO_BLOCK = -1.0f;
+constexpr float KA_NO_REF = -1e30f;
+constexpr float KA_GROW = 8.0f;
+
+// An 8x8 fp16 matrix held as rows lane / 4, columns 2 (lane % 4) and + 1, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
 }  // namespace
 
@@ -101,9 +113,12 @@ template <int D, int R, int FMT>
 __global__ void __launch_bounds__(KA_THREADS, 1)
     kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Kv8AttnParams p, int box) {
-  constexpr int NJ = D / 16;          // MMAs of a score block's contraction
-  constexpr int ND = D / 8;           // 8-column blocks of O
-  constexpr int LD = D / 4;           // dims of a row that a lane's quad member holds
+  constexpr int NJ = D / 16;          // MMAs of a score tile's contraction
+  constexpr int NM = D / 16;          // 16-dim tiles of O^T
+  constexpr int NB = R / 8;           // 8-row blocks of queries
+  constexpr int NK = KA_U / 16;       // 16-key tiles of a piece
+  constexpr int LD = D / 4;           // dims of a key that a lane's quad member holds
+  constexpr int VD = D / 8;           // dims of O and V that a lane holds
   constexpr int PS = ka_ps(D);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -214,54 +229,65 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     const int tok0 = sg.t << p.tq_shift;
     const int ntok = min(1 << p.tq_shift, sg.s.n - tok0);
     const int nrows = ntok * p.G;
-    // ---- query fragments: rows g4 and g4 + 8, dims LD c4 ..
-    uint32_t qa[2][NJ][2];            // [row half][MMA][register]
-    float rs[2];
-    int see[2];                       // positions that the row's token sees
+    // ---- query fragments (B: row g4 of each block, dims LD c4 ..), then what this lane needs of
+    // the rows whose scores it gets, 8 b + 2 c4 + i
+    uint32_t qb[NB][NJ][2];
+    float rs[NB][2];                  // factor of the row's scores
+    int see[NB][2];                   // positions that the row's token sees
 #pragma unroll
-    for (int h = 0; h < R / 8; ++h) {
-      const int r = g4 + 8 * h;
+    for (int b = 0; b < NB; ++b) {
+      const int r = g4 + 8 * b;
       const int tok = r / p.G, hh = r - tok * p.G;
       uint4 v[LD / 8];
 #pragma unroll
       for (int i = 0; i < LD / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
-      see[h] = 0;
+      int sees = 0;
       if (r < nrows) {
         const __nv_bfloat16* src =
             p.q + static_cast<size_t>(sg.s.off + tok0 + tok) * p.q_stride + (sg.g * p.G + hh) * D + LD * c4;
 #pragma unroll
         for (int i = 0; i < LD / 8; ++i) v[i] = ldg_nc_v4(src + 8 * i);
-        see[h] = sg.s.first + tok0 + tok + 1;
+        sees = sg.s.first + tok0 + tok + 1;
       }
-      uint32_t big = 0;
+      uint32_t big2 = 0;
 #pragma unroll
       for (int i = 0; i < LD / 8; ++i) {
         const uint32_t* x = &v[i].x;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) big = max(big, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+        for (int j = 0; j < 4; ++j) big2 = __vmaxu2(big2, x[j] & 0x7FFF7FFFu);
       }
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 1));
+      big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 2));
+      const uint32_t big = max(big2 >> 16, big2 & 0xFFFFu);
       // the row's largest magnitude lands in [2^13, 2^14): bf16's 8 bits stay exact in fp16
       // down to 2^-28 of it
       const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, -100), 100);
       const float f = pow2i(-e);
-      rs[h] = pow2i(e) * p.scale_log2;
+      // the factor stays below 2^62, so that its product with a K scale is finite
+      const float rf = fminf(pow2i(e) * p.scale_log2, 0x1p62f);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint32_t* x = &v[j >> 1].x + (j & 1) * 2;
-        qa[h][j][0] = pack2_f16(bf16lo(x[0]) * f, bf16hi(x[0]) * f);
-        qa[h][j][1] = pack2_f16(bf16lo(x[1]) * f, bf16hi(x[1]) * f);
+        qb[b][j][0] = pack2_f16(bf16lo(x[0]) * f, bf16hi(x[0]) * f);
+        qb[b][j][1] = pack2_f16(bf16lo(x[1]) * f, bf16hi(x[1]) * f);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rs[b][i] = __shfl_sync(0xffffffffu, rf, 4 * (2 * c4 + i));
+        see[b][i] = __shfl_sync(0xffffffffu, sees, 4 * (2 * c4 + i));
       }
     }
-    if (R == 8) {
-      rs[1] = 0.0f;
-      see[1] = 0;
-    }
-    float m_run[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.0f, 0.0f};
-    float o[ND][4];
+    const int least = sg.s.first + tok0 + 1;       // positions that every row sees
+    // m: reference of a row's weights (-1e30: none yet); l: this lane's share of the normaliser
+    float m[NB][2], l[NB][2];
+    float o[NB][NM][4];
 #pragma unroll
-    for (int i = 0; i < ND; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    for (int b = 0; b < NB; ++b) {
+      m[b][0] = m[b][1] = KA_NO_REF;
+      l[b][0] = l[b][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
+    }
 
     for (int u = sg.u0; u < sg.u1 && !dead; ++u) {
       const int st = taken % KA_STAGES;
@@ -272,78 +298,113 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
       ++taken;
       const uint32_t kb = ring + st * 2 * ka_half(D), vb = kb + ka_half(D);
       const float sc = sc_next[0];
-      float ksc[2], vsc[2];
+      // ---- scores of the piece's 16-key tiles: x[.][k][2 h + i]: key 16 k + 8 h + g4, row 2 c4 + i
+      float x[NB][NK][4], ksc[NK], ve[NK];
+      bool live[NK];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ksc[i] = __shfl_sync(0xffffffffu, sc, i);
-        vsc[i] = __shfl_sync(0xffffffffu, sc, 2 + i);
-      }
-      // ---- scores of the piece's 4 blocks of 8 keys
-      float x[4][4];
+      for (int k = 0; k < NK; ++k) {
+        ksc[k] = __shfl_sync(0xffffffffu, sc, k);
+        const float vs = __shfl_sync(0xffffffffu, sc, 2 + k);
+        live[k] = ksc[k] >= 0.0f;
+        ksc[k] = fminf(fmaxf(ksc[k], 0.0f), 0x1p62f);
+        ve[k] = static_cast<float>(max(scale_exp(vs), KV8_MIN_EXP));
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        x[nb][0] = x[nb][1] = x[nb][2] = x[nb][3] = 0.0f;
-        if (ksc[nb >> 1] < 0.0f || vsc[nb >> 1] < 0.0f) continue;
-        const int r = 8 * nb + g4;
+        for (int b = 0; b < NB; ++b) x[b][k][0] = x[b][k][1] = x[b][k][2] = x[b][k][3] = 0.0f;
+        if (!live[k]) continue;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          const uint4 kv = lds128(kb + code_off<D>(r, (D / 64) * c4 + i));
-          const uint32_t* kw = &kv.x;
+          const uint4 k0 = lds128(kb + code_off<D>(16 * k + g4, (D / 64) * c4 + i));
+          const uint4 k1 = lds128(kb + code_off<D>(16 * k + 8 + g4, (D / 64) * c4 + i));
+          const uint32_t *w0 = &k0.x, *w1 = &k1.x;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t wd = kv8_flip<FMT>(kw[j]);
-            const int jj = 4 * i + j;
-            mma_f16_16816(x[nb], qa[0][jj][0], R == 16 ? qa[1][jj][0] : 0u, qa[0][jj][1], R == 16 ? qa[1][jj][1] : 0u,
-                          kv8_half2<FMT>(wd, 0), kv8_half2<FMT>(wd, 1));
+            const uint32_t d0 = kv8_flip<FMT>(w0[j]), d1 = kv8_flip<FMT>(w1[j]);
+            const uint32_t a0 = kv8_half2<FMT>(d0, 0), a1 = kv8_half2<FMT>(d1, 0);
+            const uint32_t a2 = kv8_half2<FMT>(d0, 1), a3 = kv8_half2<FMT>(d1, 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma_f16_16816(x[b][k], a0, a1, a2, a3, qb[b][4 * i + j][0], qb[b][4 * i + j][1]);
           }
         }
       }
-      // ---- s_i + e_i in base 2, masked; running maximum
-      int ve[2];
+      // ---- s + e - m, masked where a row may not see the whole piece
+      const bool masked = u * KA_U + KA_U > least || !live[0] || !live[NK - 1];
+      bool grow = false;
+      float y[NB][NK][4];
+      const auto hidden = [&](int b, int k, int h, int i) {
+        return !live[k] || u * KA_U + 16 * k + 8 * h + g4 >= see[b][i];
+      };
 #pragma unroll
-      for (int i = 0; i < 2; ++i) ve[i] = max(scale_exp(vsc[i]), KV8_MIN_EXP);
-      float mx[2] = {-INFINITY, -INFINITY};
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const bool live = !(ksc[nb >> 1] < 0.0f || vsc[nb >> 1] < 0.0f);
-        const int pos = u * KA_U + 8 * nb + 2 * c4;
-        const float add = static_cast<float>(ve[nb >> 1]);
+        for (int k = 0; k < NK; ++k)
 #pragma unroll
-        for (int i = 0; i < (R == 16 ? 4 : 2); ++i) {
-          const int h = i >> 1;
-          const bool ok = live && pos + (i & 1) < see[h];
-          x[nb][i] = ok ? fmaf(x[nb][i] * rs[h], ksc[nb >> 1], add) : -INFINITY;
-          mx[h] = fmaxf(mx[h], x[nb][i]);
-        }
+          for (int i = 0; i < 2; ++i) {
+            const float f = rs[b][i] * ksc[k], add = ve[k] - m[b][i];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y[b][k][2 * h + i] = fmaf(x[b][k][2 * h + i], f, add);
+          }
+      if (masked) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (hidden(b, k, j >> 1, j & 1)) y[b][k][j] = -INFINITY;
       }
-      uint32_t pa[4][2];              // weights of key pairs: [8-key block][row half]
 #pragma unroll
-      for (int h = 0; h < R / 8; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        const float m_new = fmaxf(m_run[h], mx[h]);
-        const float m_at = m_new == -INFINITY ? 0.0f : m_new;   // no key so far: every weight is 0
-        const float corr = exp2f(m_run[h] - m_at);
-        m_run[h] = m_new;
-        float l = l_part[h] * corr;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-          const float w0 = exp2f(x[nb][2 * h] - m_at), w1 = exp2f(x[nb][2 * h + 1] - m_at);
-          l = fmaf(w0 + w1, pow2i(-ve[nb >> 1]), l);
-          pa[nb][h] = pack2_f16(w0, w1);
-        }
-        l_part[h] = l;
+        for (int k = 0; k < NK; ++k)
+          grow |= fmaxf(fmaxf(y[b][k][0], y[b][k][1]), fmaxf(y[b][k][2], y[b][k][3])) > KA_GROW;
+      if (__any_sync(0xffffffffu, grow)) {
+        // the references move to the rows' maxima; what was summed so far follows
 #pragma unroll
-        for (int i = 0; i < ND; ++i) {
-          o[i][2 * h] *= corr;
-          o[i][2 * h + 1] *= corr;
-        }
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = m[b][i];
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!hidden(b, k, h, i)) mx = fmaxf(mx, fmaf(x[b][k][2 * h + i], rs[b][i] * ksc[k], ve[k]));
+#pragma unroll
+            for (int s = 4; s <= 16; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            const float corr = ex2(m[b][i] - mx);    // from no reference: 0
+            m[b][i] = mx;
+            l[b][i] *= corr;
+#pragma unroll
+            for (int t = 0; t < NM; ++t) {
+              o[b][t][i] *= corr;
+              o[b][t][2 + i] *= corr;
+            }
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                y[b][k][2 * h + i] = hidden(b, k, h, i) ? -INFINITY : fmaf(x[b][k][2 * h + i], rs[b][i] * ksc[k], ve[k] - mx);
+          }
       }
-      // ---- O += w V, 16 keys a step; rows past the tile's end are not looked at
+      uint32_t pb[NB][NK][2];         // weights as B: keys 16 k + 8 h + 2 c4 and + 1 of row g4
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (ksc[ks] < 0.0f || vsc[ks] < 0.0f) continue;
-        const int r = 16 * ks + 2 * c4;
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          float w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = ex2(y[b][k][j]);
+          const float inv = pow2i(-static_cast<int>(ve[k]));
+          l[b][0] = fmaf(w[0] + w[2], inv, l[b][0]);
+          l[b][1] = fmaf(w[1] + w[3], inv, l[b][1]);
+          pb[b][k][0] = transpose8x8(pack2_f16(w[0], w[1]));
+          pb[b][k][1] = transpose8x8(pack2_f16(w[2], w[3]));
+        }
+      // ---- O^T += V^T w, 16 keys a step; rows past the tile's end are not looked at
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        if (!live[k]) continue;
+        const int r = 16 * k + 2 * c4;
         constexpr int W = D / 32;     // words of a row per lane
         uint32_t rw[4][W];
 #pragma unroll
@@ -357,7 +418,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
             rw[i][0] = v.x, rw[i][1] = v.y;
           }
         }
-        const int base = u * KA_U + 16 * ks;
+        const int base = u * KA_U + 16 * k;
         if (base + 16 > end) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -365,18 +426,21 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
 #pragma unroll
               for (int j = 0; j < W; ++j) rw[i][j] = 0;
         }
-        const uint32_t a0 = pa[2 * ks][0], a2 = pa[2 * ks + 1][0];
-        const uint32_t a1 = R == 16 ? pa[2 * ks][1] : 0u, a3 = R == 16 ? pa[2 * ks + 1][1] : 0u;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           const uint32_t lo01 = kv8_flip<FMT>(__byte_perm(rw[0][j], rw[1][j], 0x5140));
           const uint32_t hi01 = kv8_flip<FMT>(__byte_perm(rw[0][j], rw[1][j], 0x7362));
           const uint32_t lo23 = kv8_flip<FMT>(__byte_perm(rw[2][j], rw[3][j], 0x5140));
           const uint32_t hi23 = kv8_flip<FMT>(__byte_perm(rw[2][j], rw[3][j], 0x7362));
-          mma_f16_16816(o[4 * j + 0], a0, a1, a2, a3, kv8_half2<FMT>(lo01, 0), kv8_half2<FMT>(lo23, 0));
-          mma_f16_16816(o[4 * j + 1], a0, a1, a2, a3, kv8_half2<FMT>(lo01, 1), kv8_half2<FMT>(lo23, 1));
-          mma_f16_16816(o[4 * j + 2], a0, a1, a2, a3, kv8_half2<FMT>(hi01, 0), kv8_half2<FMT>(hi23, 0));
-          mma_f16_16816(o[4 * j + 3], a0, a1, a2, a3, kv8_half2<FMT>(hi01, 1), kv8_half2<FMT>(hi23, 1));
+          // tile 2 j + t: dims VD g4 + 4 j + 2 t (rows g4) and + 1 (rows g4 + 8)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t w01 = t ? hi01 : lo01, w23 = t ? hi23 : lo23;
+            const uint32_t a0 = kv8_half2<FMT>(w01, 0), a1 = kv8_half2<FMT>(w01, 1);
+            const uint32_t a2 = kv8_half2<FMT>(w23, 0), a3 = kv8_half2<FMT>(w23, 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma_f16_16816(o[b][2 * j + t], a0, a1, a2, a3, pb[b][k][0], pb[b][k][1]);
+          }
         }
       }
       // the stage is free once every lane has read it
@@ -386,50 +450,46 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
       sc_next[KA_STAGES - 1] = issue();
     }
 
-    // ---- the tile's rows: out if the whole tile lies in this run, else a part for the CTA
+    // ---- the tile's rows: out if the whole tile lies in this run, else a part for the CTA.
+    // This lane has dims VD g4 .. of rows 8 b + 2 c4 + i, two per 16-dim tile.
     const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
+    if (!whole && sg.u0 == 0) __syncwarp();   // the part goes into the ring: every lane has read its last piece
 #pragma unroll
-    for (int h = 0; h < R / 8; ++h) {
-      float l = l_part[h];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const int r = g4 + 8 * h;
-      // block j holds dim (D / 8) n + j of columns n = 2 c4, 2 c4 + 1: this lane's LD dims
-      if (whole) {
-        if (r < nrows) {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // a row that saw no key: zeros
-          const int tok = r / p.G, hh = r - tok * p.G;
-          __nv_bfloat16* dst =
-              p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + LD * c4;
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        float sum = l[b][i];
 #pragma unroll
-            for (int j = 0; j < ND; j += 8) {
-              uint32_t x[4];
+        for (int s = 4; s <= 16; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        const int r = 8 * b + 2 * c4 + i;
+        if (whole) {
+          if (r < nrows) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw no key: zeros
+            const int tok = r / p.G, hh = r - tok * p.G;
+            __nv_bfloat16* dst =
+                p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + VD * g4;
+#pragma unroll
+            for (int t = 0; t < NM; t += 4) {
+              uint32_t v[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                x[k] = pack_bf16x2(__float_as_uint(o[j + 2 * k][2 * h + i] * inv),
-                                   __float_as_uint(o[j + 2 * k + 1][2 * h + i] * inv));
-              *reinterpret_cast<uint4*>(dst + ND * i + j) = make_uint4(x[0], x[1], x[2], x[3]);
+                v[k] = pack_bf16x2(__float_as_uint(o[b][t + k][i] * inv), __float_as_uint(o[b][t + k][2 + i] * inv));
+              *reinterpret_cast<uint4*>(dst + 2 * t) = make_uint4(v[0], v[1], v[2], v[3]);
             }
-        }
-      } else {
-        if (sg.u0 == 0) __syncwarp();   // the ring: every lane has read its last piece
-        float* row = (sg.u0 ? heads + warp * R * PS
-                            : reinterpret_cast<float*>(smem + warp * KA_STAGES * 2 * ka_half(D))) + r * PS;
-        if (c4 == 0) {
-          row[D] = m_run[h];
-          row[D + 1] = l;
-        }
-        float* dst = row + LD * c4;
+          }
+        } else {
+          float* row = (sg.u0 ? heads + warp * R * PS
+                              : reinterpret_cast<float*>(smem + warp * KA_STAGES * 2 * ka_half(D))) + r * PS;
+          if (g4 == 0) {
+            row[D] = m[b][i] == KA_NO_REF ? -INFINITY : m[b][i];
+            row[D + 1] = sum;
+          }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < ND; j += 4)
-            *reinterpret_cast<float4*>(dst + ND * i + j) =
-                make_float4(o[j][2 * h + i], o[j + 1][2 * h + i], o[j + 2][2 * h + i], o[j + 3][2 * h + i]);
+          for (int t = 0; t < NM; t += 2)
+            *reinterpret_cast<float4*>(row + VD * g4 + 2 * t) =
+                make_float4(o[b][t][i], o[b][t][2 + i], o[b][t + 1][i], o[b][t + 1][2 + i]);
+        }
       }
-    }
     if (!whole && lane == 0)
       meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, sg.w_first, sg.w_last, 0};
   }
