@@ -33,24 +33,31 @@ namespace moe {
 
 namespace {
 
-constexpr int KA_WARPS = 8;
-constexpr int KA_THREADS = KA_WARPS * 32;
-constexpr int KA_U = 32;                       // positions per piece
-constexpr int KA_STAGES = 2;                   // pieces in flight per warp
+// Warps per CTA and positions per piece: (8 rows, 16 rows).
+constexpr int KA_W8 = 8, KA_W16 = 8;
+constexpr int KA_U8 = 32, KA_U16 = 32;
+constexpr int KA_ST8 = 2, KA_ST16 = 2;         // pieces in flight per warp
+__host__ __device__ constexpr int ka_warps(int R) { return R == 8 ? KA_W8 : KA_W16; }
+__host__ __device__ constexpr int ka_u(int R) { return R == 8 ? KA_U8 : KA_U16; }
+__host__ __device__ constexpr int ka_stages(int R) { return R == 8 ? KA_ST8 : KA_ST16; }
 constexpr int KA_COST = 2;                     // a tile's start, in pieces
-__host__ __device__ constexpr int ka_half(int D) { return KA_U * D; }       // bytes of a piece's keys (or values)
-__host__ __device__ constexpr int ka_ring(int D) { return KA_WARPS * KA_STAGES * 2 * ka_half(D); }
+__host__ __device__ constexpr int ka_half(int D, int R) { return ka_u(R) * D; }       // bytes of a piece's keys (or values)
+__host__ __device__ constexpr int ka_own(int D, int R) { return ka_stages(R) * 2 * ka_half(D, R); }   // a warp's ring
 __host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, max, sum
 // shared memory: rings (1024-aligned), a part per warp (the tile that began before its run;
 // the tile that goes on after it takes the warp's own ring, which is done by then), the line,
 // what the parts belong to, barriers and words
-__host__ __device__ constexpr int ka_parts(int D, int R) { return KA_WARPS * R * ka_ps(D) * 4; }
+__host__ __device__ constexpr int ka_parts(int D, int R) { return ka_warps(R) * R * ka_ps(D) * 4; }
 __host__ __device__ constexpr int ka_wsum(int R) { return R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
 __host__ __device__ constexpr int ka_smem(int D, int R, int B) {
-  return 1024 + ka_ring(D) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 + KA_WARPS * (8 + KA_STAGES * 8 + 2 * 32) + 64;
+  return 1024 + ka_warps(R) * ka_own(D, R) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 +
+         ka_warps(R) * (8 + ka_stages(R) * 8 + 2 * 32) + 64;
 }
-static_assert(ka_smem(128, 16, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
-static_assert(16 * ka_ps(128) * 4 <= KA_STAGES * 2 * ka_half(128) && 16 * ka_ps(64) * 4 <= KA_STAGES * 2 * ka_half(64),
+static_assert(ka_smem(128, 16, KV8_MAX_SEQS) <= 232448 && ka_smem(128, 8, KV8_MAX_SEQS) <= 232448,
+              "shared memory per CTA exceeds 227 KB");
+static_assert(ka_warps(8) * ka_stages(8) <= 32 && ka_warps(16) * ka_stages(16) <= 32, "one lane per barrier");
+static_assert(16 * ka_ps(128) * 4 <= ka_own(128, 16) && 16 * ka_ps(64) * 4 <= ka_own(64, 16) &&
+                  8 * ka_ps(128) * 4 <= ka_own(128, 8) && 8 * ka_ps(64) * 4 <= ka_own(64, 8),
               "a warp's part fits its ring");
 
 // What a part belongs to.
@@ -110,9 +117,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // box: rows of the tensor maps' box, 16 (pages of 16 positions) or 32.
 template <int D, int R, int FMT>
-__global__ void __launch_bounds__(KA_THREADS, 1)
+__global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Kv8AttnParams p, int box) {
+  constexpr int KA_WARPS = ka_warps(R), KA_THREADS = KA_WARPS * 32, KA_U = ka_u(R), KA_STAGES = ka_stages(R);
+  constexpr int HALF = ka_half(D, R), OWN = ka_own(D, R);
   constexpr int NJ = D / 16;          // MMAs of a score tile's contraction
   constexpr int NM = D / 16;          // 16-dim tiles of O^T
   constexpr int NB = R / 8;           // 8-row blocks of queries
@@ -122,7 +131,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   constexpr int PS = ka_ps(D);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* heads = reinterpret_cast<float*>(smem + ka_ring(D));
+  float* heads = reinterpret_cast<float*>(smem + KA_WARPS * OWN);
   float* wsum = heads + ka_parts(D, R) / 4;
   long long* prefix = reinterpret_cast<long long*>(wsum + ka_wsum(R) / 4);
   long long* s_warp = prefix + p.b.n_seqs + 1 + ((p.b.n_seqs + 1) & 1);      // 16-byte aligned
@@ -132,15 +141,14 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   int* s_last = const_cast<int*>(abort_flag) + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, c4 = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * KA_STAGES * 2 * ka_half(D);
+  const uint32_t ring = smem_u32(smem) + warp * OWN;
   const uint32_t bar0 = smem_u32(bars) + warp * KA_STAGES * 8;
 
-  if (tid == 0) {
-    for (int i = 0; i < KA_WARPS * KA_STAGES; ++i) mbar_init(smem_u32(bars) + 8 * i, 1);
-    *abort_flag = 0;
+  if (warp == KA_WARPS - 1) {
+    if (lane < KA_WARPS * KA_STAGES) mbar_init(smem_u32(bars) + 8 * lane, 1);
+    if (lane == 0) *abort_flag = 0;
+    if (lane < 2) tma_prefetch_desc(lane ? &tm_v : &tm_k);
     fence_mbar_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
   }
   if (tid < 2 * KA_WARPS) meta[tid].b = -1;
   Kv8Runs runs;
@@ -151,14 +159,16 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   const long long w_beg = run < runs.n ? kv8_run_begin(runs, run) : 0;
   const long long w_end = run < runs.n ? kv8_run_begin(runs, run + 1) : 0;
 
-  // ---- this warp's load cursor: its next piece, and per lane 0..3 the page of one of the
-  // piece's blocks (lane & 1: block, lane >> 1: keys or values)
+  // ---- this warp's load cursor: its next piece, and in the first lanes the page of one of the
+  // piece's blocks each (first those of the keys, then those of the values)
+  const int block = lane % NK, which = lane / NK;
+  const bool loader = lane < 2 * NK;
   long long lw = w_beg;
   Kv8Seg ls = {};
   int lu = 0, l_end = 0, pid = -1;
   bool more = w_beg < w_end;
   if (more) {
-    ls = kv8_seg<KA_U, KA_COST>(p, prefix, lw, w_end, runs);
+    ls = kv8_seg<KA_U, KA_COST>(p, prefix, lw, w_end);
     lu = ls.u0;
     l_end = kv8_seg_end(ls, p.tq_shift);
   }
@@ -171,24 +181,25 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
         more = false;
         return;
       }
-      kv8_next<KA_U, KA_COST>(ls, p, prefix, lw, w_end, runs);
+      kv8_next<KA_U, KA_COST>(ls, p, prefix, lw, w_end);
       lu = ls.u0;
       l_end = kv8_seg_end(ls, p.tq_shift);
     }
-    const int pos = lu * KA_U + (lane & 1) * KV8_BLOCK;
+    const int pos = lu * KA_U + block * KV8_BLOCK;
     pid = -1;
-    if (lane < 4 && pos < l_end)
+    if (loader && pos < l_end)
       pid = __ldg(p.b.page_table + static_cast<size_t>(ls.b) * p.b.max_pages + (pos >> p.c.page_shift));
   };
-  const uint64_t pol = l2_policy_evict_first();
+  // codes that one tile alone reads need no place in L2
+  const uint64_t pol = p.b.max_new <= (1 << p.tq_shift) ? l2_policy_evict_first() : l2_policy_evict_last();
   int issued = 0;
-  // Issue the cursor's piece into its stage; returns this lane's block scale (lanes 0..3).
+  // Issue the cursor's piece into its stage; returns this lane's block scale (the loaders).
   auto issue = [&]() -> float {
     float sc = KA_NO_BLOCK;
     if (!more) return sc;
     const int st = issued % KA_STAGES;
-    const int pos = lu * KA_U + (lane & 1) * KV8_BLOCK;
-    bool live = lane < 4 && pos < l_end;
+    const int pos = lu * KA_U + block * KV8_BLOCK;
+    bool live = loader && pos < l_end;
     if (live && (pid < 0 || pid >= p.c.n_pages)) {
       atomicOr(p.c.err, ERRBIT_BOUNDS);
       live = false;
@@ -196,16 +207,16 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     size_t row = 0;
     if (live) {
       row = ((static_cast<size_t>(pid) * p.c.hkv + ls.g) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));
-      sc = fmaxf(__ldg(p.c.scales[lane >> 1] + row / KV8_BLOCK), 0.0f);
+      sc = __ldg(p.c.scales[which] + row / KV8_BLOCK);     // not looked at before the piece is
     }
-    const bool copies = live && (box == KV8_BLOCK || (lane & 1) == 0);   // a box of 32 rows brings both blocks
+    const bool copies = live && (box == KV8_BLOCK || block == 0);   // a box of 32 rows brings both blocks
     const unsigned n = __popc(__ballot_sync(0xffffffffu, copies));
     const uint32_t bar = bar0 + 8 * st;
     if (lane == 0) mbar_arrive_expect_tx(bar, n * box * D);
     __syncwarp();
     if (copies) {
-      const uint32_t dst = ring + st * 2 * ka_half(D) + (lane >> 1) * ka_half(D) + (lane & 1) * KV8_BLOCK * D;
-      tma_load_2d_hint(dst, lane >> 1 ? &tm_v : &tm_k, bar, 0, static_cast<int>(row), pol);
+      const uint32_t dst = ring + st * 2 * HALF + which * HALF + block * KV8_BLOCK * D;
+      tma_load_2d_hint(dst, which ? &tm_v : &tm_k, bar, 0, static_cast<int>(row), pol);
     }
     ++issued;
     ++lu;
@@ -213,6 +224,24 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     return sc;
   };
 
+  // The query rows of the first segment are on their way before the first codes are.
+  uint4 qv[NB][LD / 8];
+  const auto fetch_q = [&](const Kv8Seg& g) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int r = g4 + 8 * b, tok = r / p.G, t0 = g.t << p.tq_shift;
+#pragma unroll
+      for (int i = 0; i < LD / 8; ++i) qv[b][i] = make_uint4(0, 0, 0, 0);
+      if (tok < min(1 << p.tq_shift, g.s.n - t0)) {
+        const __nv_bfloat16* src =
+            p.q + static_cast<size_t>(g.s.off + t0 + tok) * p.q_stride + (g.g * p.G + r - tok * p.G) * D + LD * c4;
+#pragma unroll
+        for (int i = 0; i < LD / 8; ++i) qv[b][i] = ldg_nc_v4(src + 8 * i);
+      }
+    }
+  };
+  if (more) fetch_q(ls);
+  bool fetched = more;
   settle();
   float sc_next[KA_STAGES];
 #pragma unroll
@@ -222,7 +251,10 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
   bool dead = false;      // a wait gave up: nothing more is loaded or computed
   Kv8Seg sg = first_seg;
   for (long long w = w_beg; w < w_end;) {
-    if (w > w_beg) kv8_next<KA_U, KA_COST>(sg, p, prefix, w, w_end, runs);
+    if (w > w_beg) {
+      kv8_next<KA_U, KA_COST>(sg, p, prefix, w, w_end);
+      fetched = false;
+    }
     w += sg.len;
     if (sg.u1 <= sg.u0) continue;     // the run ends before the tile's first piece
     const int end = kv8_seg_end(sg, p.tq_shift);
@@ -232,23 +264,14 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     // ---- query fragments (B: row g4 of each block, dims LD c4 ..), then what this lane needs of
     // the rows whose scores it gets, 8 b + 2 c4 + i
     uint32_t qb[NB][NJ][2];
+    if (!fetched) fetch_q(sg);
     float rs[NB][2];                  // factor of the row's scores
     int see[NB][2];                   // positions that the row's token sees
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int r = g4 + 8 * b;
-      const int tok = r / p.G, hh = r - tok * p.G;
-      uint4 v[LD / 8];
-#pragma unroll
-      for (int i = 0; i < LD / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
-      int sees = 0;
-      if (r < nrows) {
-        const __nv_bfloat16* src =
-            p.q + static_cast<size_t>(sg.s.off + tok0 + tok) * p.q_stride + (sg.g * p.G + hh) * D + LD * c4;
-#pragma unroll
-        for (int i = 0; i < LD / 8; ++i) v[i] = ldg_nc_v4(src + 8 * i);
-        sees = sg.s.first + tok0 + tok + 1;
-      }
+      const uint4* v = qv[b];
+      const int sees = r < nrows ? sg.s.first + tok0 + r / p.G + 1 : 0;
       uint32_t big2 = 0;
 #pragma unroll
       for (int i = 0; i < LD / 8; ++i) {
@@ -296,7 +319,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
         break;
       }
       ++taken;
-      const uint32_t kb = ring + st * 2 * ka_half(D), vb = kb + ka_half(D);
+      const uint32_t kb = ring + st * 2 * HALF, vb = kb + HALF;
       const float sc = sc_next[0];
       // ---- scores of the piece's 16-key tiles: x[.][k][2 h + i]: key 16 k + 8 h + g4, row 2 c4 + i
       float x[NB][NK][4], ksc[NK], ve[NK];
@@ -304,7 +327,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
         ksc[k] = __shfl_sync(0xffffffffu, sc, k);
-        const float vs = __shfl_sync(0xffffffffu, sc, 2 + k);
+        const float vs = __shfl_sync(0xffffffffu, sc, NK + k);
         live[k] = ksc[k] >= 0.0f;
         ksc[k] = fminf(fmaxf(ksc[k], 0.0f), 0x1p62f);
         ve[k] = static_cast<float>(max(scale_exp(vs), KV8_MIN_EXP));
@@ -479,7 +502,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
           }
         } else {
           float* row = (sg.u0 ? heads + warp * R * PS
-                              : reinterpret_cast<float*>(smem + warp * KA_STAGES * 2 * ka_half(D))) + r * PS;
+                              : reinterpret_cast<float*>(smem + warp * OWN)) + r * PS;
           if (g4 == 0) {
             row[D] = m[b][i] == KA_NO_REF ? -INFINITY : m[b][i];
             row[D + 1] = sum;
@@ -490,8 +513,10 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
                 make_float4(o[b][t][i], o[b][t][2 + i], o[b][t + 1][i], o[b][t + 1][2 + i]);
         }
       }
-    if (!whole && lane == 0)
-      meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, sg.w_first, sg.w_last, 0};
+    if (!whole) {
+      const int2 own = kv8_owners<KA_COST>(sg, w - sg.len, runs);
+      if (lane == 0) meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, own.x, own.y, 0};
+    }
   }
   // a warp that gave up: copies still in flight land before the shared memory goes away
   for (; taken < issued; ++taken) {
@@ -513,7 +538,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
     const int last = min(pt.r_last - cta * KA_WARPS, KA_WARPS - 1);   // the tile's last warp here
     const int c_first = pt.r_first / KA_WARPS, c_last = pt.r_last / KA_WARPS;
     const auto part = [&](int i) {           // i0: the tail (or nothing, for -1), above: heads
-      return (i == i0 ? reinterpret_cast<const float*>(smem + i * KA_STAGES * 2 * ka_half(D)) : heads + i * R * PS) + row * PS;
+      return (i == i0 ? reinterpret_cast<const float*>(smem + i * OWN) : heads + i * R * PS) + row * PS;
     };
     const int i1 = max(i0, 0);
     float M = -INFINITY, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -537,18 +562,18 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
         *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(O[4], O[5], O[6], O[7]);
         if (d0 == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, L);
       }
-      __threadfence();
       __syncthreads();
       const int ns = c_last - c_first + 1;
       if (tid == 0) {
+        __threadfence();                     // after the barrier: the whole CTA's sums come before the ticket
         const bool all = atomicAdd(p.tickets + c_first, 1u) == static_cast<unsigned>(ns) - 1u;
+        __threadfence();
         if (all) p.tickets[c_first] = 0u;    // every part has arrived: ready for the next call
         *s_last = all;
       }
       __syncthreads();
       write = *s_last != 0;
       if (write) {
-        __threadfence();
         float* fs = wsum;                    // [R][ns] weights of the CTAs' sums, in the order of the line
         L = 0.0f;
         if (tid < ACT) {
@@ -571,7 +596,7 @@ __global__ void __launch_bounds__(KA_THREADS, 1)
         if (tid < ACT) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) O[k] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
           for (int i = 0; i < ns; ++i) {
             const float f = fs[row * ns + i];
             const float4 a = __ldcg(reinterpret_cast<const float4*>(slot(c_first + i) + d0));
@@ -606,11 +631,13 @@ int floor_log2(int n) {
   return s;
 }
 
-// Query rows of a tile: 8 or 16 when the group's rows of all new tokens fit, else 0 (the
-// prompt kernel).
+// Query rows of a tile, or 0 for the prompt kernel.  Up to 32 rows go through the decode
+// kernel in tiles of 16, which read the codes twice, the second time mostly from L2: 16
+// sequences of 4 new tokens and 8 rows each over 8 thousand positions took 29 us that way and
+// 41 us in one block of 128 rows, three quarters empty.
 int ka_rows(int G, int max_new) {
   const long long n = static_cast<long long>(G) * max_new;
-  return n <= 8 ? 8 : n <= 16 ? 16 : 0;
+  return n <= 8 ? 8 : n <= 32 ? 16 : 0;
 }
 
 size_t kv8_ws_bytes(int D, int rows) {
@@ -629,7 +656,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const Kv
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  k<<<grid, KA_THREADS, ka_smem(D, R, p.b.n_seqs), s>>>(tk, tv, p, box);
+  k<<<grid, ka_warps(R) * 32, ka_smem(D, R, p.b.n_seqs), s>>>(tk, tv, p, box);
   return cudaGetLastError();
 }
 
@@ -704,7 +731,7 @@ extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gq
   }
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(cache->n_pages) * cache->n_kv_heads * cache->page_size;
-  const int box = cache->page_size >= KA_U ? KA_U : KV8_BLOCK;
+  const int box = cache->page_size >= ka_u(R) ? ka_u(R) : KV8_BLOCK;
   if (!encode_u8_rows(&tk, cache->k_codes, D, rows, box) || !encode_u8_rows(&tv, cache->v_codes, D, rows, box))
     return MOE_ERR_CUDA;
   const bool e4 = cache->format == GQA_KV8_E4M3;

@@ -273,9 +273,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       const uint32_t inv_g = (65535u + p.G) / p.G;       // r / G = r inv_g >> 16 for r < 128, G <= 16
       int it = 0, seg = 0;
       KpTile tile = {0, 0, 0, 0, 0, {0, 0, 0}};
-      Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end, runs);
+      Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end);
       for (long long w = w_beg; w < w_end;) {
-        if (w > w_beg) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end, runs);
+        if (w > w_beg) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
         w += sg.len;
         if (sg.u1 <= sg.u0) continue;      // the run ends before the tile's first positions
         const int tok0 = (sg.t << p.tq_shift) + blk * blk_tokens;
@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // a row that saw no key: zeros
         __nv_bfloat16* dst =
             live ? p.out + (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh) * D : nullptr;
-        float* part = kp_slot<D>(p.part, cta, sg.w_first, blk * KP_ROWS + r);
+        const int2 own = whole ? make_int2(cta, cta) : kv8_owners<KP_COST>(sg, w - sg.len, runs);
+        float* part = kp_slot<D>(p.part, cta, own.x, blk * KP_ROWS + r);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         tc_fence_before();
         if (!whole) {
           *reinterpret_cast<float2*>(part + D) = make_float2(m_ref, l);
-          if (tid == 0 && sg.w_first == cta) tile = KpTile{sg.w_last - sg.w_first + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
+          if (tid == 0 && own.x == cta) tile = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
         ++seg;
       }
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     // 8-15 its V blocks.
     const int lb = lane & 7;
     long long w = w_beg;
-    Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w, w_end, runs);
+    Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w, w_end);
     int u = sg.u0, end = kv8_seg_end(sg, p.tq_shift);
     bool more = true;
     int pid = -1, pid_at = 0, pid_valid = 0;    // looked up: page; offset in the page; positions before the end
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         w += sg.len;
         more = w < w_end;
         if (!more) break;
-        kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end, runs);
+        kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
         u = sg.u0;
         end = kv8_seg_end(sg, p.tq_shift);
       }

@@ -50,7 +50,7 @@ struct Kv8Seg {
   int b, g, t;           // sequence, key/value head, tile of the sequence
   int u0, u1, units;     // this run's units of positions (none: u1 <= u0), the tile's
   int len;               // units of the line that the segment takes
-  int w_first, w_last;   // the runs that hold the tile's first and last units of positions (where they differ)
+  int x;                 // units of the line before it in its tile
 };
 
 // The line cut into n runs: run i is units i total / n up to (i + 1) total / n, and unit w
@@ -76,8 +76,8 @@ __device__ __forceinline__ long long kv8_upto(long long x, int r_shift) {
 // Units of tiles 0 .. t - 1 of a sequence (t at most its last tile).
 template <int U, int C>
 __device__ __forceinline__ long long kv8_units_before(const Kv8Seq& s, int tq_shift, int t) {
-  constexpr int US = U == 32 ? 5 : U == 64 ? 6 : U == 128 ? 7 : 8;
-  static_assert((1 << US) == U, "U is 32 to 256");
+  constexpr int US = U == 16 ? 4 : U == 32 ? 5 : U == 64 ? 6 : 7;
+  static_assert((1 << US) == U, "U is 16 to 128");
   const long long n = t;
   if (tq_shift > US) return n * ((max(s.first, 0) + U - 1) / U + C) + ((n * (n + 1) / 2) << (tq_shift - US));
   const int rs = US - tq_shift;
@@ -92,6 +92,7 @@ __device__ __forceinline__ int kv8_units_tile(const Kv8Seq& s, int tq_shift, int
 template <int U, int C>
 __device__ __forceinline__ long long kv8_units_seq(const Kv8Seq& s, int tq_shift) {
   if (s.n <= 0) return 0;
+  if (s.n <= (1 << tq_shift)) return kv8_units_tile<U, C>(s, tq_shift, 0);
   const int tiles = (s.n + (1 << tq_shift) - 1) >> tq_shift;
   return kv8_units_before<U, C>(s, tq_shift, tiles - 1) + kv8_units_tile<U, C>(s, tq_shift, tiles - 1);
 }
@@ -138,23 +139,27 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
 // Ends the segment that starts at unit w, x units into its tile of `all` units, with the tile or
 // at w_end.
 template <int C>
-__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, int x, int all, long long w, long long w_end, const Kv8Runs& runs) {
+__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, int x, int all, long long w, long long w_end) {
   const long long left = w_end - w;
   const int end = all - x <= left ? all : x + static_cast<int>(left);
+  g.x = x;
   g.len = end - x;
   g.units = all - C;
   g.u0 = max(x - C, 0);
   g.u1 = end - C;
-  if (g.u0 > 0 || g.u1 < g.units) {
-    g.w_first = kv8_run_of(runs, w - x + C);
-    g.w_last = kv8_run_of(runs, w - x + all - 1);
-  }
+}
+// The runs that hold the first and the last unit of positions of the segment's tile (the
+// segment starts at unit w).
+template <int C>
+__device__ __forceinline__ int2 kv8_owners(const Kv8Seg& g, long long w, const Kv8Runs& runs) {
+  const long long start = w - g.x;
+  return make_int2(kv8_run_of(runs, start + C), kv8_run_of(runs, start + C + g.units - 1));
 }
 
 // The segment that starts at unit w of the line.
 template <int U, int C>
-__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w, long long w_end,
-                                          const Kv8Runs& runs) {
+__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w,
+                                          long long w_end) {
   Kv8Seg g;
   int lo = 0, hi = p.b.n_seqs;             // prefix[lo] <= w < prefix[hi]
   while (hi - lo > 1) {
@@ -163,10 +168,15 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
   }
   g.b = lo;
   g.s = kv8_seq(p.b, p.c.page_shift, lo);
-  const long long per_head = kv8_div(prefix[lo + 1] - prefix[lo], p.c.hkv);
-  const long long x0 = w - prefix[lo];
-  g.g = static_cast<int>(kv8_div(x0, per_head));
-  const long long x = x0 - g.g * per_head;
+  long long x = w - prefix[lo];
+  const long long per_head = kv8_units_seq<U, C>(g.s, p.tq_shift);
+  g.g = 0;
+  if (p.c.hkv > 4) {
+    g.g = static_cast<int>(kv8_div(x, per_head));
+    x -= g.g * per_head;
+  } else {
+    for (; x >= per_head; x -= per_head) ++g.g;
+  }
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
   int tl = 0, th = tiles;                  // units before tl <= x < units before th
   while (th - tl > 1) {
@@ -174,8 +184,8 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
     if (kv8_units_before<U, C>(g.s, p.tq_shift, m) <= x) tl = m; else th = m;
   }
   g.t = tl;
-  const int in_tile = static_cast<int>(x - kv8_units_before<U, C>(g.s, p.tq_shift, tl));
-  kv8_seg_close<C>(g, in_tile, kv8_units_tile<U, C>(g.s, p.tq_shift, tl), w, w_end, runs);
+  const int in_tile = static_cast<int>(tl ? x - kv8_units_before<U, C>(g.s, p.tq_shift, tl) : x);
+  kv8_seg_close<C>(g, in_tile, kv8_units_tile<U, C>(g.s, p.tq_shift, tl), w, w_end);
   return g;
 }
 
@@ -183,7 +193,7 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
 // the sequence's next one, or the first of the next head or sequence.
 template <int U, int C>
 __device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const long long* prefix, long long w,
-                                         long long w_end, const Kv8Runs& runs) {
+                                         long long w_end) {
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
   if (++g.t >= tiles) {
     g.t = 0;
@@ -193,7 +203,7 @@ __device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, cons
       g.s = kv8_seq(p.b, p.c.page_shift, g.b);
     }
   }
-  kv8_seg_close<C>(g, 0, kv8_units_tile<U, C>(g.s, p.tq_shift, g.t), w, w_end, runs);
+  kv8_seg_close<C>(g, 0, kv8_units_tile<U, C>(g.s, p.tq_shift, g.t), w, w_end);
 }
 
 // Positions that the tile's last token sees.
