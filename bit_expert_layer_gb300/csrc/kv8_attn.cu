@@ -106,6 +106,12 @@ constexpr float KA_NO_BLOCK = -1.0f;
 constexpr float KA_NO_REF = -1e30f;
 constexpr float KA_GROW = 8.0f;
 
+// One more part of a tile: the parts that came before.
+__device__ __forceinline__ unsigned ticket_add(unsigned* p) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
 // An 8x8 fp16 matrix held as rows lane / 4, columns 2 (lane % 4) and + 1, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -543,14 +549,28 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     const int i1 = max(i0, 0);
     float M = -INFINITY, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (tid < ACT) {
-      for (int i = i1; i <= last; ++i) M = fmaxf(M, part(i)[D]);
-      const float at = M == -INFINITY ? 0.0f : M;
-      for (int i = i1; i <= last; ++i) {
-        const float* src = part(i);
-        const float f = exp2f(src[D] - at);
-        L = fmaf(f, src[D + 1], L);
+      // unrolled over all warps, so that the loads do not wait for one another
+      float mw[KA_WARPS], lw2[KA_WARPS];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) O[k] = fmaf(f, src[d0 + k], O[k]);
+      for (int i = 0; i < KA_WARPS; ++i) {
+        mw[i] = -INFINITY;
+        lw2[i] = 0.0f;
+        if (i >= i1 && i <= last) {
+          const float2 v = *reinterpret_cast<const float2*>(part(i) + D);
+          mw[i] = v.x;
+          lw2[i] = v.y;
+        }
+        M = fmaxf(M, mw[i]);
+      }
+      const float at = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+      for (int i = 0; i < KA_WARPS; ++i) {
+        if (i < i1 || i > last) continue;
+        const float4 v0 = *reinterpret_cast<const float4*>(part(i) + d0), v1 = *reinterpret_cast<const float4*>(part(i) + d0 + 4);
+        const float f = ex2(mw[i] - at);
+        L = fmaf(f, lw2[i], L);
+        O[0] = fmaf(f, v0.x, O[0]), O[1] = fmaf(f, v0.y, O[1]), O[2] = fmaf(f, v0.z, O[2]), O[3] = fmaf(f, v0.w, O[3]);
+        O[4] = fmaf(f, v1.x, O[4]), O[5] = fmaf(f, v1.y, O[5]), O[6] = fmaf(f, v1.z, O[6]), O[7] = fmaf(f, v1.w, O[7]);
       }
     }
     bool write = c_first == c_last;
@@ -565,9 +585,9 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       __syncthreads();
       const int ns = c_last - c_first + 1;
       if (tid == 0) {
-        __threadfence();                     // after the barrier: the whole CTA's sums come before the ticket
-        const bool all = atomicAdd(p.tickets + c_first, 1u) == static_cast<unsigned>(ns) - 1u;
-        __threadfence();
+        // release after the barrier, so the whole CTA's sums come before the ticket; acquire for
+        // the CTA that adds them up
+        const bool all = ticket_add(p.tickets + c_first) == static_cast<unsigned>(ns) - 1u;
         if (all) p.tickets[c_first] = 0u;    // every part has arrived: ready for the next call
         *s_last = all;
       }
@@ -578,16 +598,25 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         L = 0.0f;
         if (tid < ACT) {
           const int j0 = tid % TPR;
+          constexpr int PER = (KV8_MAX_CTAS + TPR - 1) / TPR;
+          float2 ml[PER];
           M = -INFINITY;
-          for (int i = j0; i < ns; i += TPR) M = fmaxf(M, __ldcg(slot(c_first + i) + D));
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int i = j0 + k * TPR;
+            ml[k] = i < ns ? __ldcg(reinterpret_cast<const float2*>(slot(c_first + i) + D)) : make_float2(-INFINITY, 0.0f);
+          }
+#pragma unroll
+          for (int k = 0; k < PER; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
           for (int s = TPR / 2; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
           const float at = M == -INFINITY ? 0.0f : M;
-          for (int i = j0; i < ns; i += TPR) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(c_first + i) + D));
-            const float f = exp2f(ml.x - at);
-            L = fmaf(f, ml.y, L);
-            fs[row * ns + i] = f;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int i = j0 + k * TPR;
+            const float f = ex2(ml[k].x - at);
+            L = fmaf(f, ml[k].y, L);
+            if (i < ns) fs[row * ns + i] = f;
           }
 #pragma unroll
           for (int s = TPR / 2; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);

@@ -120,9 +120,11 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   if ((tid & 31) == 31) s_warp[tid >> 5] = incl;
   __syncthreads();
   long long before = incl - sum, total = 0;
+#pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < (tid >> 5)) before += s_warp[w];
-    total += s_warp[w];
+    const long long v = s_warp[w];
+    if (w < (tid >> 5)) before += v;
+    total += v;
   }
   // exclusive: prefix[b] = everything before b
   long long prev = before;
