@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   const Kv8Seg first_seg = ls;
   auto settle = [&] {                 // the cursor's next piece: its segment and its pages
     if (!more) return;
+#pragma unroll 1
     while (lu >= ls.u1) {
       lw += ls.len;
       if (lw >= w_end) {
@@ -256,6 +257,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   int taken = 0;
   bool dead = false;      // a wait gave up: nothing more is loaded or computed
   Kv8Seg sg = first_seg;
+#pragma unroll 1
   for (long long w = w_beg; w < w_end;) {
     if (w > w_beg) {
       kv8_next<KA_U, KA_COST>(sg, p, prefix, w, w_end);
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       for (int i = 0; i < NM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
     }
 
+#pragma unroll 1
     for (int u = sg.u0; u < sg.u1 && !dead; ++u) {
       const int st = taken % KA_STAGES;
       if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, (taken / KA_STAGES) & 1, p.c.err, abort_flag, p.wait_ns))) {
@@ -538,6 +541,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   constexpr int TPR = D / 8;                 // threads per row, 8 dims each
   constexpr int ACT = R * TPR;               // 64 .. 256 threads
   const int row = tid / TPR, d0 = (tid % TPR) * 8;
+#pragma unroll 1
   for (int i0 = -1; i0 < KA_WARPS; ++i0) {
     const KaPart pt = i0 < 0 ? meta[0] : meta[2 * i0 + 1];
     if (pt.b < 0) continue;

@@ -92,45 +92,48 @@ __global__ void __launch_bounds__(KC_WARPS * 32) kv8_append_kernel(const __grid_
   }
   float s_old = 0.0f;
   if (held) s_old = *scale;
-  uint32_t amax = 0, odd = 0;
+  uint32_t big2 = 0;                     // largest magnitudes, as pairs of bf16 bits
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    uint32_t* w = &x[i].x;
+  for (int i = 0; i < NI; ++i)
+    big2 = __vmaxu2(__vmaxu2(big2, __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu)),
+                    __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+  uint32_t amax = __reduce_max_sync(0xffffffffu, max(big2 & 0xFFFFu, big2 >> 16));
+  if (amax >= 0x7F80u) {
+    // something is not finite: it does not count, and a NaN becomes zero
+    if (lane == 0) atomicOr(p.c.err, ERRBIT_NONFINITE);
+    amax = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < NI; ++i) {
+      uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t bits = (w[j] >> (16 * h)) & 0x7FFFu;
-        if (bits < 0x7F80u) {
-          amax = max(amax, bits);
-        } else {
-          odd = 1;
-          if (bits > 0x7F80u) w[j] &= h ? 0x0000FFFFu : 0xFFFF0000u;   // NaN: zero
-        }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+        if (lo < 0x7F80u) amax = max(amax, lo);
+        if (hi < 0x7F80u) amax = max(amax, hi);
+        if (lo > 0x7F80u) w[j] &= 0xFFFF0000u;
+        if (hi > 0x7F80u) w[j] &= 0x0000FFFFu;
       }
+      x[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    amax = __reduce_max_sync(0xffffffffu, amax);
   }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if (odd) atomicOr(p.c.err, ERRBIT_NONFINITE);
   int e = kv8_exp_of<FMT>(amax);
   if (held) {
     const int e_old = max(scale_exp(s_old), KV8_MIN_EXP);
     if (e > e_old) {
       // the earlier rows' codes, rounded again to the larger scale
       const float f = pow2i(max(e_old - e, -126));
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = r0 + i * RPI;
-        if (r >= lo) continue;
-        uint2 c = *reinterpret_cast<const uint2*>(codes + r * D);
-        uint32_t* w = &c.x;
+#pragma unroll 1
+      for (int r = r0; r < lo; r += RPI) {
+        const uint2 c = *reinterpret_cast<const uint2*>(codes + r * D);
+        uint32_t w[2] = {c.x, c.y};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t v = kv8_flip<FMT>(w[j]);
           const float2 a = half2_floats(kv8_half2<FMT>(v, 0)), b = half2_floats(kv8_half2<FMT>(v, 1));
           w[j] = kv8_encode4<FMT>(a.x * f, a.y * f, b.x * f, b.y * f);
         }
-        *reinterpret_cast<uint2*>(codes + r * D) = c;
+        *reinterpret_cast<uint2*>(codes + r * D) = make_uint2(w[0], w[1]);
       }
     } else {
       e = e_old;
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(KC_WARPS * 32) kv8_append_kernel(const __grid_
   for (int i = 0; i < NI; ++i) {
     const int r = r0 + i * RPI;
     if (r < lo || r >= hi) continue;
-    const uint32_t* w = &x[i].x;
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint2 c;
     c.x = kv8_encode4<FMT>(bf16lo(w[0]) * inv, bf16hi(w[0]) * inv, bf16lo(w[1]) * inv, bf16hi(w[1]) * inv);
     c.y = kv8_encode4<FMT>(bf16lo(w[2]) * inv, bf16hi(w[2]) * inv, bf16lo(w[3]) * inv, bf16hi(w[3]) * inv);
@@ -200,7 +203,8 @@ struct RopeParams {
   long long in_stride[2], out_stride[2];
   int heads[2];
   const int* pos;
-  int T, n_axes, half, tokens;   // tokens per CTA
+  int T, n_axes, half, tokens;   // tokens per CTA, at most 4
+  uint32_t inv_heads;            // th / heads = th inv_heads >> 21 for th < 4 heads, heads <= 512
   uint64_t turn[GQA_ROPE_MAX_PAIRS];
   uint8_t axis[GQA_ROPE_MAX_PAIRS];
 };
@@ -218,6 +222,41 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
   float* s_cos = s_cs;
   float* s_sin = s_cs + p.tokens * p.half;
+  constexpr int IPH = D / 16;            // items per head
+  constexpr int NB = 3;                  // items of a thread in flight: 4 tokens of 18 heads of 128
+  const int rot_items = p.half / 8, nh = p.heads[0] + p.heads[1], n = nt * nh * IPH;
+  struct Item {
+    const __nv_bfloat16* src;
+    __nv_bfloat16* dst;
+    int ca, cb, at;                      // its chunks' first elements; of its sines, or -1
+  };
+  const auto item = [&](int i) {
+    Item r;
+    const int part = i % IPH, th = i / IPH;
+    const int t = static_cast<int>((static_cast<uint32_t>(th) * p.inv_heads) >> 21), hh = th - t * nh;
+    const int which = hh >= p.heads[0];
+    const int h = which ? hh - p.heads[0] : hh;
+    r.src = p.in[which] + static_cast<size_t>(t0 + t) * p.in_stride[which] + h * D;
+    r.dst = p.out[which] + static_cast<size_t>(t0 + t) * p.out_stride[which] + h * D;
+    const bool rot = part < rot_items;
+    r.ca = rot ? part * 8 : 2 * p.half + (part - rot_items) * 16;
+    r.cb = rot ? r.ca + p.half : r.ca + 8;
+    r.at = rot ? t * p.half + part * 8 : -1;
+    return r;
+  };
+  uint4 a[NB], b[NB];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = i0 + k * RP_THREADS;
+      if (i < n) {
+        const Item r = item(i);
+        a[k] = *reinterpret_cast<const uint4*>(r.src + r.ca);
+        b[k] = *reinterpret_cast<const uint4*>(r.src + r.cb);
+      }
+    }
+  };
+  load(threadIdx.x);                     // on their way while the sines are computed
   for (int i = threadIdx.x; i < nt * p.half; i += RP_THREADS) {
     const int t = i / p.half, j = i - t * p.half;
     const long long pos = __ldg(p.pos + static_cast<size_t>(p.axis[j]) * p.T + t0 + t);
@@ -228,33 +267,27 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     s_sin[i] = s;
   }
   __syncthreads();
-  constexpr int IPH = D / 16;            // items per head
-  const int rot_items = p.half / 8, nh = p.heads[0] + p.heads[1];
-  for (int i = threadIdx.x; i < nt * nh * IPH; i += RP_THREADS) {
-    const int item = i % IPH, th = i / IPH;
-    const int t = th / nh, hh = th - t * nh;
-    const int which = hh >= p.heads[0];
-    const int h = which ? hh - p.heads[0] : hh;
-    const __nv_bfloat16* src = p.in[which] + static_cast<size_t>(t0 + t) * p.in_stride[which] + h * D;
-    __nv_bfloat16* dst = p.out[which] + static_cast<size_t>(t0 + t) * p.out_stride[which] + h * D;
-    const bool rot = item < rot_items;
-    const int ca = rot ? item * 8 : 2 * p.half + (item - rot_items) * 16;
-    const int cb = rot ? ca + p.half : ca + 8;
-    uint4 a = *reinterpret_cast<const uint4*>(src + ca), b = *reinterpret_cast<const uint4*>(src + cb);
-    if (rot) {
-      const float* c = s_cos + t * p.half + item * 8;
-      const float* s = s_sin + t * p.half + item * 8;
-      uint32_t *wa = &a.x, *wb = &b.x;
+  for (int i0 = threadIdx.x; i0 < n; i0 += NB * RP_THREADS) {
+    if (i0 != threadIdx.x) load(i0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a0 = bf16lo(wa[j]), a1 = bf16hi(wa[j]), b0 = bf16lo(wb[j]), b1 = bf16hi(wb[j]);
-        const float c0 = c[2 * j], c1 = c[2 * j + 1], s0 = s[2 * j], s1 = s[2 * j + 1];
-        wa[j] = pack_bf16x2(__float_as_uint(a0 * c0 - b0 * s0), __float_as_uint(a1 * c1 - b1 * s1));
-        wb[j] = pack_bf16x2(__float_as_uint(b0 * c0 + a0 * s0), __float_as_uint(b1 * c1 + a1 * s1));
+    for (int k = 0; k < NB; ++k) {
+      const int i = i0 + k * RP_THREADS;
+      if (i >= n) break;
+      const Item r = item(i);
+      if (r.at >= 0) {
+        uint32_t *wa = &a[k].x, *wb = &b[k].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 c = *reinterpret_cast<const float2*>(s_cos + r.at + 2 * j);
+          const float2 s = *reinterpret_cast<const float2*>(s_sin + r.at + 2 * j);
+          const float a0 = bf16lo(wa[j]), a1 = bf16hi(wa[j]), b0 = bf16lo(wb[j]), b1 = bf16hi(wb[j]);
+          wa[j] = pack_bf16x2(__float_as_uint(a0 * c.x - b0 * s.x), __float_as_uint(a1 * c.y - b1 * s.y));
+          wb[j] = pack_bf16x2(__float_as_uint(b0 * c.x + a0 * s.x), __float_as_uint(b1 * c.y + a1 * s.y));
+        }
       }
+      *reinterpret_cast<uint4*>(r.dst + r.ca) = a[k];
+      *reinterpret_cast<uint4*>(r.dst + r.cb) = b[k];
     }
-    *reinterpret_cast<uint4*>(dst + ca) = a;
-    *reinterpret_cast<uint4*>(dst + cb) = b;
   }
 }
 
@@ -483,6 +516,7 @@ extern "C" moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, lon
   p.T = T;
   p.n_axes = plan->n_axes;
   p.tokens = T >= 2048 ? 4 : 1;
+  p.inv_heads = ((1u << 21) + n_q_heads + n_k_heads - 1) / (n_q_heads + n_k_heads);
   const dim3 grid((T + p.tokens - 1) / p.tokens);
   const size_t smem = 2ull * p.tokens * p.half * sizeof(float);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -37,7 +37,6 @@ constexpr int KP_THREADS = 640;
 constexpr int KP_U = 128;                         // positions per tile
 constexpr int KP_COST = 2;                        // a tile's start, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
-constexpr int KP_NB = KP_U / KV8_BLOCK;           // scales per tile
 constexpr int KP_SLOTS = 4;                       // tiles whose scales are kept
 constexpr float KP_GROW = 8.0f;                   // the maximum may outgrow the reference by 2^8
 // Blocks of a tile are brought to the tile's largest scale in fp16, 2^head on top of it: the
@@ -249,6 +248,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     return;
   }
   const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
+  const Kv8Seg first = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end);   // where every role begins
   if (warp == 16) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       const uint32_t inv_g = (65535u + p.G) / p.G;       // r / G = r inv_g >> 16 for r < 128, G <= 16
       int it = 0, seg = 0;
       KpTile tile = {0, 0, 0, 0, 0, {0, 0, 0}};
-      Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end);
+      Kv8Seg sg = first;
+#pragma unroll 1
       for (long long w = w_beg; w < w_end;) {
         if (w > w_beg) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
         w += sg.len;
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         const float rs = s_rs[blk * KP_ROWS + r];
 
         float m_ref = -INFINITY, l = 0.0f;
+#pragma unroll 1
         for (int u = sg.u0; u < sg.u1; ++u, ++it) {
           wait(BAR_S + blk, it);
           if (dead) continue;
@@ -492,13 +494,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     // 8-15 its V blocks.
     const int lb = lane & 7;
     long long w = w_beg;
-    Kv8Seg sg = kv8_seg<KP_U, KP_COST>(p, prefix, w, w_end);
+    Kv8Seg sg = first;
     int u = sg.u0, end = kv8_seg_end(sg, p.tq_shift);
     bool more = true;
     int pid = -1, pid_at = 0, pid_valid = 0;    // looked up: page; offset in the page; positions before the end
     int pid_g = 0;
     bool pid_live = false, looked = false;      // the lane's block exists; the tile exists
     const auto advance = [&] {                  // to the next segment with positions
+#pragma unroll 1
       while (u >= sg.u1) {
         w += sg.len;
         more = w < w_end;
@@ -585,6 +588,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     load();
     locate();
     look();
+#pragma unroll 1
     for (int it = 0; loaded; ++it) {
       const int s = it & 1, ph = (it >> 1) & 1;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
@@ -638,19 +642,23 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       };
       int it = 0;
       bool ok = true;
+#pragma unroll 1
       for (int seg = 0; ok; ++seg) {
         ok = wait(BAR_Q, seg);
         if (!ok) break;
         const int n = s_n[seg & 1];               // the segment's tiles, told by the softmax (0: no more)
         if (n == 0) break;
         ok = wait(BAR_KF + (it & 1), it >> 1);
+#pragma unroll 1
         for (int i = 0; ok && i < nblk; ++i) {
           if (i) ok = wait(BAR_Q + i, seg);
           if (ok) qk(i, it & 1, i == nblk - 1);
         }
+#pragma unroll 1
         for (int j = 0; ok && j < n; ++j, ++it) {
           const int s = it & 1;
           ok = wait(BAR_VF + s, it >> 1);
+#pragma unroll 1
           for (int i = 0; ok && i < nblk; ++i) {
             ok = wait(BAR_P + i, it);
             if (!ok) break;

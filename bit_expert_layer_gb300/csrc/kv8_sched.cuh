@@ -59,9 +59,12 @@ struct Kv8Runs {
   long long total;
   int n;
 };
+// Code that is fetched once per launch costs more than its arithmetic (some 250 cycles per 8
+// instructions that come from L2), so the rare long division is a function of its own.
+static __device__ __noinline__ long long kv8_div_long(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long kv8_div(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
+  return kv8_div_long(a, b);
 }
 __device__ __forceinline__ long long kv8_run_begin(const Kv8Runs& r, int i) { return kv8_div(i * r.total, r.n); }
 __device__ __forceinline__ int kv8_run_of(const Kv8Runs& r, long long w) {
@@ -105,6 +108,7 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long sum = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
     if (s.bad && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
@@ -128,6 +132,7 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   }
   // exclusive: prefix[b] = everything before b
   long long prev = before;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const long long incl_b = before + prefix[b];
     prefix[b] = prev;
@@ -164,6 +169,7 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
                                           long long w_end) {
   Kv8Seg g;
   int lo = 0, hi = p.b.n_seqs;             // prefix[lo] <= w < prefix[hi]
+#pragma unroll 1
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
     if (prefix[m] <= w) lo = m; else hi = m;
@@ -177,10 +183,12 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
     g.g = static_cast<int>(kv8_div(x, per_head));
     x -= g.g * per_head;
   } else {
+#pragma unroll 1
     for (; x >= per_head; x -= per_head) ++g.g;
   }
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
   int tl = 0, th = tiles;                  // units before tl <= x < units before th
+#pragma unroll 1
   while (th - tl > 1) {
     const int m = (tl + th) >> 1;
     if (kv8_units_before<U, C>(g.s, p.tq_shift, m) <= x) tl = m; else th = m;
