@@ -9,6 +9,7 @@
 //                128-byte rows with the 128-byte swizzle, two buffers
 //   warps 12-15  the same for V (K and V by the same four warps took 6000 cycles a tile)
 //   warp 16      issues the MMAs
+//   warp 17      plans: looks up the tiles' pages and scales ahead of the dequantising warps
 // Per tile and row block, TMEM lane = query row:
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
@@ -37,7 +38,8 @@ constexpr int KP_THREADS = 640;
 constexpr int KP_U = 128;                         // positions per tile
 constexpr int KP_COST = 2;                        // a tile's start, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
-constexpr int KP_SLOTS = 4;                       // tiles whose scales are kept
+constexpr int KP_SLOTS = 8;                       // tiles whose scales the softmax can ask for
+constexpr int KP_PLANS = 4;                       // tiles planned ahead
 constexpr float KP_GROW = 8.0f;                   // the maximum may outgrow the reference by 2^8
 // Blocks of a tile are brought to the tile's largest scale in fp16, 2^head on top of it: the
 // largest code (448; for int8 the offset 1152 of its conversion) lands just under fp16's
@@ -47,12 +49,13 @@ __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 18 * 8 + 64;
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128;
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
 
-// barriers: two each of the K and V buffers (full, empty) and of the row blocks, and the end
-enum { BAR_KF = 0, BAR_KE = 2, BAR_VF = 4, BAR_VE = 6, BAR_Q = 8, BAR_S = 10, BAR_P = 12, BAR_PV = 14, BAR_END = 16, BAR_N = 17 };
+// barriers: two each of the K and V buffers (full, empty) and of the row blocks, the end, and one
+// per plan slot (full, empty)
+enum { BAR_KF = 0, BAR_KE = 2, BAR_VF = 4, BAR_VE = 6, BAR_Q = 8, BAR_S = 10, BAR_P = 12, BAR_PV = 14, BAR_END = 16, BAR_LF = 17, BAR_LE = 21, BAR_N = 25 };
 
 // kind::f16 with fp16 A and B, fp32 D; A K-major, B K-major or (b_mn) N-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -147,9 +150,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// A tile's codes, as the dequantising warps need to know them.
+struct __align__(16) KpPlan {
+  int rows[8];           // first code row of each 16-position block (negative: none)
+  uint32_t kfac[8];      // factor of each block to the tile's scale, an fp16 pair
+  uint32_t vfac[8];
+  int valid;             // positions before the tile's last token's; negative: no more tiles
+  int pad[7];
+};
+static_assert(sizeof(KpPlan) == 128, "one line of shared memory");
+
 // Registers per thread of a warpgroup: the kernel starts with 96, and the shares stay within
 // its 640 * 96.
-constexpr int KP_REG_SOFTMAX = 144, KP_REG_DEQUANT = 72, KP_REG_MMA = 48;
+constexpr int KP_REG_SOFTMAX = 136, KP_REG_DEQUANT = 72, KP_REG_MMA = 64;
 static_assert(2 * 128 * KP_REG_SOFTMAX + 2 * 128 * KP_REG_DEQUANT + 128 * KP_REG_MMA <= KP_THREADS * 96,
               "register shares within the launch's total");
 template <int N>
@@ -213,7 +226,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   uint8_t* s_v = smem + 4 * TILE;
   // per tile {K scale, e, 2^-e of its V scale 2^e, blocks without a page (bits)}
   float4* s_scale = reinterpret_cast<float4*>(smem + 6 * TILE);
-  float* s_rs = reinterpret_cast<float*>(s_scale + KP_SLOTS);      // [256] factor of a query row's scores
+  KpPlan* s_plan = reinterpret_cast<KpPlan*>(s_scale + KP_SLOTS);
+  float* s_rs = reinterpret_cast<float*>(s_plan + KP_PLANS);       // [256] factor of a query row's scores
   long long* prefix = reinterpret_cast<long long*>(s_rs + 2 * KP_ROWS);
   long long* s_warp = prefix + p.b.n_seqs + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
@@ -236,6 +250,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       mbar_init(bar(BAR_Q + i), 4);
     }
     mbar_init(bar(BAR_END), 1);
+    for (int i = 0; i < KP_PLANS; ++i) {
+      mbar_init(bar(BAR_LF + i), 1);
+      mbar_init(bar(BAR_LE + i), 8);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -489,83 +507,28 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     const uint8_t* codes = p.c.codes[is_v];
     uint8_t* tiles = is_v ? s_v : s_k;
     const int b_full = is_v ? BAR_VF : BAR_KF, b_empty = is_v ? BAR_VE : BAR_KE;
-    // Every tile passes through four stages, one per iteration, so that no load is waited for:
-    // page lookup, scales, codes, conversion.  Lanes 0-7 hold the tile's 8 K blocks, lanes
-    // 8-15 its V blocks.
-    const int lb = lane & 7;
-    long long w = w_beg;
-    Kv8Seg sg = first;
-    int u = sg.u0, end = kv8_seg_end(sg, p.tq_shift);
-    bool more = true;
-    int pid = -1, pid_at = 0, pid_valid = 0;    // looked up: page; offset in the page; positions before the end
-    int pid_g = 0;
-    bool pid_live = false, looked = false;      // the lane's block exists; the tile exists
-    const auto advance = [&] {                  // to the next segment with positions
-#pragma unroll 1
-      while (u >= sg.u1) {
-        w += sg.len;
-        more = w < w_end;
-        if (!more) break;
-        kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
-        u = sg.u0;
-        end = kv8_seg_end(sg, p.tq_shift);
-      }
-    };
-    auto look = [&] {                           // stage 1 of the cursor's tile, then on to the next one
-      const int pos = u * KP_U + lb * KV8_BLOCK;
-      looked = more;
-      pid_live = more && pos < end;
-      pid_valid = more ? end - u * KP_U : 0;
-      pid_at = pos & ((1 << p.c.page_shift) - 1);
-      pid_g = sg.g;
-      if (pid_live) pid = __ldg(p.b.page_table + static_cast<size_t>(sg.b) * p.b.max_pages + (pos >> p.c.page_shift));
-      ++u;
-      if (more) advance();
-    };
-    int rows = -1, valid = 0;                   // stage 2: first code row of the lane's block (negative: none)
-    float scale = 0.0f;
-    bool bad = false, located = false;
-    auto locate = [&] {
-      located = looked;
-      bad = pid_live && (pid < 0 || pid >= p.c.n_pages);
-      rows = -1;
-      scale = 0.0f;
-      valid = pid_valid;
-      if (pid_live && !bad) {
-        rows = ((pid * p.c.hkv + pid_g) << p.c.page_shift) + pid_at;   // below 2^31
-        scale = __ldg(p.c.scales[(lane >> 3) & 1] + rows / KV8_BLOCK);
-      }
-    };
     uint4 reg[NI];
-    uint32_t fac = 0;                           // of the tile in reg: the lane's block's factor to the tile's scale
-    float4 now = make_float4(0, 0, 0, 0);       // of the tile in reg: what the softmax needs
-    bool loaded = false;
-    auto load = [&] {                           // stage 3
-      loaded = located;
+    // The codes of the tile planned in slot `it`, if there is one.
+    auto load = [&](int it) {
+      const int s = it & (KP_PLANS - 1);
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(bar(BAR_LF + s), (it / KP_PLANS) & 1, p.c.err, abort_flag, p.wait_ns)))
+        return false;
+      const int valid = s_plan[s].valid;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
-        const int at = __shfl_sync(0xffffffffu, rows, row / KV8_BLOCK);
+        const int at = s_plan[s].rows[row / KV8_BLOCK];
         reg[i] = make_uint4(0, 0, 0, 0);
         if (at >= 0 && row < valid) reg[i] = ldg_nc_v4(codes + static_cast<size_t>(at + row % KV8_BLOCK) * D + 16 * cc);
       }
-      const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xFFu;
-      if (bads && lane == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
-      constexpr int HEAD = kp_head(FMT);
-      const int e = rows >= 0 ? max(scale_exp(fmaxf(scale, 0.0f)), KV8_MIN_EXP) : KV8_MIN_EXP;
-      int t = e;                                // the largest of the 8 blocks
-#pragma unroll
-      for (int m = 4; m >= 1; m >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, m));
-      const float f = pow2i(max(e - t + HEAD, -126));
-      fac = pack2h(f, f);
-      const int kt = __shfl_sync(0xffffffffu, t, 0), vt = __shfl_sync(0xffffffffu, t, 8);
-      now = make_float4(pow2i(min(kt - HEAD, 62)), static_cast<float>(vt - HEAD), pow2i(HEAD - vt), __uint_as_float(bads));
+      return valid >= 0;
     };
-    auto store = [&](uint8_t* tile) {           // stage 4
+    auto store = [&](uint8_t* tile, const uint32_t* fac) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
-        const uint32_t fc = __shfl_sync(0xffffffffu, fac, row / KV8_BLOCK + 8 * is_v), fo = kv8_scaled_offset<FMT>(fc);
+        const uint32_t fc = fac[row / KV8_BLOCK], fo = kv8_scaled_offset<FMT>(fc);
         const auto h2 = [&](uint32_t x, int hi) { return kv8_half2_scaled<FMT>(x, hi, fc, fo); };
         const uint32_t w0 = kv8_flip<FMT>(reg[i].x), w1 = kv8_flip<FMT>(reg[i].y);
         const uint32_t w2 = kv8_flip<FMT>(reg[i].z), w3 = kv8_flip<FMT>(reg[i].w);
@@ -581,57 +544,121 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       fence_proxy_async_smem();
       __syncwarp();
     };
-    advance();
-    look();
-    locate();
-    look();
-    load();
-    locate();
-    look();
+    bool have = load(0);
 #pragma unroll 1
-    for (int it = 0; loaded; ++it) {
-      const int s = it & 1, ph = (it >> 1) & 1;
+    for (int it = 0; have; ++it) {
+      const int s = it & 1, ph = (it >> 1) & 1, slot = it & (KP_PLANS - 1);
       if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
-      if (tid == 256) s_scale[it & (KP_SLOTS - 1)] = now;
-      store(tiles + s * TILE);
-      if (lane == 0) mbar_arrive(bar(b_full + s));
-      load();
-      locate();
-      look();
+      store(tiles + s * TILE, is_v ? s_plan[slot].vfac : s_plan[slot].kfac);
+      if (lane == 0) {
+        mbar_arrive(bar(b_full + s));
+        mbar_arrive(bar(BAR_LE + slot));
+      }
+      have = load(it + 1);
     }
   } else {
     reg_dec<KP_REG_MMA>();
-    if (warp == 16) {
+    if (warp == 17) {
+      // ================================================ plan: the tiles' pages and scales
+      // Lanes 0-7 look after the tile's 8 K blocks, lanes 8-15 after its V blocks.  (With the
+      // dequantising warps doing this themselves, their loads went through spilled registers,
+      // which waited for the data: 4400 cycles a tile.)
+      const int lb = lane & 7;
+      Kv8Seg sg = first;
+      bool ok = true;
+      int it = 0;
+#pragma unroll 1
+      for (long long w = w_beg; ok; w += sg.len) {
+        if (w > w_beg && w < w_end) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
+        const bool more = w < w_end;
+        const int end = kv8_seg_end(sg, p.tq_shift);
+        const int* table = p.b.page_table + static_cast<size_t>(sg.b) * p.b.max_pages;
+        int u = more ? sg.u0 : 0;
+        const int u1 = more ? sg.u1 : 1;               // at the end one more plan: no more tiles
+        int pid = -1;
+        const auto look = [&] {
+          const int pos = u * KP_U + lb * KV8_BLOCK;
+          pid = more && u < u1 && pos < end ? __ldg(table + (pos >> p.c.page_shift)) : -1;
+        };
+        look();
+#pragma unroll 1
+        while (u < u1) {
+          const int pos = u * KP_U + lb * KV8_BLOCK;
+          const bool exists = more && pos < end, bad = exists && (pid < 0 || pid >= p.c.n_pages);
+          int row = -1;
+          float scale = 0.0f;
+          if (exists && !bad) {
+            row = ((pid * p.c.hkv + sg.g) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));   // below 2^31
+            scale = __ldg(p.c.scales[(lane >> 3) & 1] + row / KV8_BLOCK);
+          }
+          const int valid = more ? end - u * KP_U : -1;
+          ++u;
+          look();                                      // the next tile's pages meanwhile
+          const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xFFu;
+          if (bads && lane == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+          constexpr int HEAD = kp_head(FMT);
+          const int e = row >= 0 ? max(scale_exp(fmaxf(scale, 0.0f)), KV8_MIN_EXP) : KV8_MIN_EXP;
+          int t = e;                                   // the largest of the 8 blocks
+#pragma unroll
+          for (int m = 4; m >= 1; m >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, m));
+          const float f = pow2i(max(e - t + HEAD, -126));
+          const int kt = __shfl_sync(0xffffffffu, t, 0), vt = __shfl_sync(0xffffffffu, t, 8);
+          const int slot = it & (KP_PLANS - 1);
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_LE + slot), ((it / KP_PLANS) & 1) ^ 1, p.c.err, abort_flag, p.wait_ns));
+          if (!ok) break;
+          KpPlan* plan = s_plan + slot;
+          if (lane < 8) {
+            plan->rows[lane] = row;
+            plan->kfac[lane] = pack2h(f, f);
+          } else if (lane < 16) {
+            plan->vfac[lane - 8] = pack2h(f, f);
+          } else if (lane == 16) {
+            plan->valid = valid;
+            s_scale[it & (KP_SLOTS - 1)] =
+                make_float4(pow2i(min(kt - HEAD, 62)), static_cast<float>(vt - HEAD), pow2i(HEAD - vt), __uint_as_float(bads));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BAR_LF + slot));
+          ++it;
+        }
+        if (!more) break;
+      }
+    } else if (warp == 16) {
       // ================================================ MMA issue
-      // The whole warp follows the loop and one elected lane issues: with the control flow
-      // uniform, descriptors stay in uniform registers.  (A loop of one lane's own took about
-      // 120 cycles per MMA.  A warp per row block let the blocks fall into step, both in their
-      // softmax and then both on the tensor cores: 560 us where this order takes 470.)
+      // The whole warp follows the loop and one elected lane issues, with the row block and the
+      // buffer known at compile time, so that every descriptor is a uniform base plus a constant.
+      // (With either in a variable, an MMA took 125 cycles to issue; by itself it takes 64.  A
+      // warp per row block let the blocks fall into step, both in their softmax and then both on
+      // the tensor cores: 560 us where this order took 470.)
       constexpr uint32_t ID_S = idesc_f16(KP_ROWS, KP_U, 0), ID_O = idesc_f16(KP_ROWS, D, 1);
       const bool leader = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t d_q = sdesc_sw128(smem_u32(s_q)), d_k = sdesc_sw128(smem_u32(s_k));
       const uint64_t d_v = sdesc_sw128_mn(smem_u32(s_v), BOX);
-      auto qk = [&](int i, int s, bool last) {    // descriptors advance in units of 16 bytes
+      using Zero = std::integral_constant<int, 0>;
+      using One = std::integral_constant<int, 1>;
+      auto qk = [&](auto block, auto buffer) {    // descriptors advance in units of 16 bytes
+        constexpr int i = decltype(block)::value, s = decltype(buffer)::value;
         if (leader) {
-          const uint64_t a = d_q + i * (TILE >> 4), b = d_k + s * (TILE >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const int at = (k >> 2) * (BOX >> 4) + 2 * (k & 3);
-            umma_bf16(tmem + 128 * i, a + at, b + at, ID_S, k > 0);
+            umma_bf16(tm + 128 * i, d_q + (i * (TILE >> 4) + at), d_k + (s * (TILE >> 4) + at), ID_S, k > 0);
           }
           umma_commit(bar(BAR_S + i));
-          if (last) umma_commit(bar(BAR_KE + s));
+          if (i == nblk - 1) umma_commit(bar(BAR_KE + s));
         }
         __syncwarp();
       };
-      auto pv = [&](int i, int s, bool acc, bool last) {
+      auto pv = [&](auto block, auto buffer, uint32_t acc) {
+        constexpr int i = decltype(block)::value, s = decltype(buffer)::value;
         if (leader) {
-          const uint64_t b = d_v + s * (TILE >> 4);
 #pragma unroll
           for (int k = 0; k < KP_U / 16; ++k)
-            umma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, b + k * (2048 >> 4), ID_O, acc || k > 0);
+            umma_f16_ts(tm + 256 + 128 * i, tm + 128 * i + 8 * k, d_v + (s * (TILE >> 4) + k * (2048 >> 4)), ID_O,
+                        k > 0 ? 1u : acc);
           umma_commit(bar(BAR_PV + i));
-          if (last) umma_commit(bar(BAR_VE + s));
+          if (i == nblk - 1) umma_commit(bar(BAR_VE + s));
         }
         __syncwarp();
       };
@@ -641,6 +668,23 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         return ok;
       };
       int it = 0;
+      // tile `it`, in buffer S: PV of each block, then QK of its next tile
+      auto step = [&](auto buffer, bool begun, bool next) {
+        constexpr int s = decltype(buffer)::value;
+        using Other = std::integral_constant<int, 1 - s>;
+        if (!wait(BAR_VF + s, it >> 1) || !wait(BAR_P, it)) return false;
+        pv(Zero{}, buffer, begun);
+        if (next) {
+          if (!wait(BAR_KF + 1 - s, (it + 1) >> 1)) return false;
+          qk(Zero{}, Other{});
+        }
+        if (nblk == 2) {
+          if (!wait(BAR_P + 1, it)) return false;
+          pv(One{}, buffer, begun);
+          if (next) qk(One{}, Other{});
+        }
+        return true;
+      };
       bool ok = true;
 #pragma unroll 1
       for (int seg = 0; ok; ++seg) {
@@ -648,28 +692,17 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!ok) break;
         const int n = s_n[seg & 1];               // the segment's tiles, told by the softmax (0: no more)
         if (n == 0) break;
-        ok = wait(BAR_KF + (it & 1), it >> 1);
-#pragma unroll 1
-        for (int i = 0; ok && i < nblk; ++i) {
-          if (i) ok = wait(BAR_Q + i, seg);
-          if (ok) qk(i, it & 1, i == nblk - 1);
+        ok = wait(BAR_KF + (it & 1), it >> 1) && (nblk == 1 || wait(BAR_Q + 1, seg));
+        if (!ok) break;
+        if (it & 1) {
+          qk(Zero{}, One{});
+          if (nblk == 2) qk(One{}, One{});
+        } else {
+          qk(Zero{}, Zero{});
+          if (nblk == 2) qk(One{}, Zero{});
         }
 #pragma unroll 1
-        for (int j = 0; ok && j < n; ++j, ++it) {
-          const int s = it & 1;
-          ok = wait(BAR_VF + s, it >> 1);
-#pragma unroll 1
-          for (int i = 0; ok && i < nblk; ++i) {
-            ok = wait(BAR_P + i, it);
-            if (!ok) break;
-            pv(i, s, j > 0, i == nblk - 1);
-            if (j + 1 < n) {
-              if (i == 0) ok = wait(BAR_KF + (s ^ 1), (it + 1) >> 1);
-              if (!ok) break;
-              qk(i, s ^ 1, i == nblk - 1);
-            }
-          }
-        }
+        for (int j = 0; ok && j < n; ++j, ++it) ok = it & 1 ? step(One{}, j > 0, j + 1 < n) : step(Zero{}, j > 0, j + 1 < n);
       }
       // every MMA issued has to land before the memory goes away
       if (leader) umma_commit(bar(BAR_END));
