@@ -3,13 +3,14 @@
 // rows hold), on tcgen05.
 //
 // A CTA works on one or two blocks of 128 query rows (TQ tokens x G heads each) that share
-// their keys, in tiles of 128 positions; its 20 warps have roles:
+// their keys, in tiles of 128 positions; its 16 warps (128 registers each; with 20 there are
+// 96, and the scores spill) have roles:
 //   warps 0-7    softmax, one query row per thread, four warps per row block
-//   warps 8-11   dequantise K: codes from global memory into fp16 tiles in shared memory,
+//   warps 8-10   dequantise K: codes from global memory into fp16 tiles in shared memory,
 //                128-byte rows with the 128-byte swizzle, two buffers
-//   warps 12-15  the same for V (K and V by the same four warps took 6000 cycles a tile)
-//   warp 16      issues the MMAs
-//   warp 17      plans: looks up the tiles' pages and scales ahead of the dequantising warps
+//   warps 11-13  the same for V
+//   warp 14      issues the MMAs
+//   warp 15      plans: looks up the tiles' pages and scales ahead of the dequantising warps
 // Per tile and row block, TMEM lane = query row:
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
@@ -34,7 +35,8 @@ namespace moe {
 
 namespace {
 
-constexpr int KP_THREADS = 640;
+constexpr int KP_THREADS = 512;
+constexpr int KP_DEQ = 3;                         // dequantising warps for K, and as many for V
 constexpr int KP_U = 128;                         // positions per tile
 constexpr int KP_COST = 2;                        // a tile's start, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
@@ -160,20 +162,6 @@ struct __align__(16) KpPlan {
 };
 static_assert(sizeof(KpPlan) == 128, "one line of shared memory");
 
-// Registers per thread of a warpgroup: the kernel starts with 96, and the shares stay within
-// its 640 * 96.
-constexpr int KP_REG_SOFTMAX = 136, KP_REG_DEQUANT = 72, KP_REG_MMA = 64;
-static_assert(2 * 128 * KP_REG_SOFTMAX + 2 * 128 * KP_REG_DEQUANT + 128 * KP_REG_MMA <= KP_THREADS * 96,
-              "register shares within the launch's total");
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Two codes to fp16 times a power of two, one rounding (for int8 the offset 1152 goes with
 // the multiplication: (1152 + code) f - 1152 f).
 template <int FMT>
@@ -240,9 +228,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(BAR_KF + i), 4);
+      mbar_init(bar(BAR_KF + i), KP_DEQ);
       mbar_init(bar(BAR_KE + i), 1);
-      mbar_init(bar(BAR_VF + i), 4);
+      mbar_init(bar(BAR_VF + i), KP_DEQ);
       mbar_init(bar(BAR_VE + i), 1);
       mbar_init(bar(BAR_S + i), 1);
       mbar_init(bar(BAR_P + i), 4);
@@ -252,7 +240,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     mbar_init(bar(BAR_END), 1);
     for (int i = 0; i < KP_PLANS; ++i) {
       mbar_init(bar(BAR_LF + i), 1);
-      mbar_init(bar(BAR_LE + i), 8);
+      mbar_init(bar(BAR_LE + i), 2 * KP_DEQ);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -267,7 +255,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   }
   const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
   const Kv8Seg first = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end);   // where every role begins
-  if (warp == 16) {
+  if (warp == 8 + 2 * KP_DEQ) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
@@ -278,7 +266,6 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   const int blk_tokens = (1 << p.tq_shift) / nblk;
 
   if (warp < 8) {
-    reg_inc<KP_REG_SOFTMAX>();
     // ================================================ softmax: row `r` of block `blk`
     const int blk = warp >> 2, r = tid & 127;
     if (blk < nblk) {
@@ -496,14 +483,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
     }
-  } else if (warp < 16) {
-    reg_dec<KP_REG_DEQUANT>();
-    // ================================================ dequantise K (warps 8-11) or V (12-15)
+  } else if (warp < 8 + 2 * KP_DEQ) {
+    // ================================================ dequantise K or V
     constexpr int CPR = D / 16;                 // 16-byte chunks of codes per row
-    constexpr int RPI = 128 / CPR;              // rows per step of the 128 threads
-    constexpr int NI = KP_U / RPI;              // steps per tile
-    const int is_v = warp >= 12;
-    const int dt = tid & 127, cc = dt % CPR, r0 = dt / CPR;
+    constexpr int RPI = KP_DEQ * 32 / CPR;      // rows per step of the threads
+    constexpr int NI = (KP_U + RPI - 1) / RPI;  // steps per tile
+    const int is_v = warp >= 8 + KP_DEQ;
+    const int dt = tid - (is_v ? 8 + KP_DEQ : 8) * 32, cc = dt % CPR, r0 = dt / CPR;
     const uint8_t* codes = p.c.codes[is_v];
     uint8_t* tiles = is_v ? s_v : s_k;
     const int b_full = is_v ? BAR_VF : BAR_KF, b_empty = is_v ? BAR_VE : BAR_KE;
@@ -518,7 +504,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
-        const int at = s_plan[s].rows[row / KV8_BLOCK];
+        const int at = row < KP_U ? s_plan[s].rows[row / KV8_BLOCK] : -1;
         reg[i] = make_uint4(0, 0, 0, 0);
         if (at >= 0 && row < valid) reg[i] = ldg_nc_v4(codes + static_cast<size_t>(at + row % KV8_BLOCK) * D + 16 * cc);
       }
@@ -528,6 +514,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
+        if (row >= KP_U) break;
         const uint32_t fc = fac[row / KV8_BLOCK], fo = kv8_scaled_offset<FMT>(fc);
         const auto h2 = [&](uint32_t x, int hi) { return kv8_half2_scaled<FMT>(x, hi, fc, fo); };
         const uint32_t w0 = kv8_flip<FMT>(reg[i].x), w1 = kv8_flip<FMT>(reg[i].y);
@@ -557,8 +544,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       have = load(it + 1);
     }
   } else {
-    reg_dec<KP_REG_MMA>();
-    if (warp == 17) {
+    if (warp == 9 + 2 * KP_DEQ) {
       // ================================================ plan: the tiles' pages and scales
       // Lanes 0-7 look after the tile's 8 K blocks, lanes 8-15 after its V blocks.  (With the
       // dequantising warps doing this themselves, their loads went through spilled registers,
@@ -623,7 +609,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         }
         if (!more) break;
       }
-    } else if (warp == 16) {
+    } else if (warp == 8 + 2 * KP_DEQ) {
       // ================================================ MMA issue
       // The whole warp follows the loop and one elected lane issues, with the row block and the
       // buffer known at compile time, so that every descriptor is a uniform base plus a constant.
@@ -672,12 +658,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       auto step = [&](auto buffer, bool begun, bool next) {
         constexpr int s = decltype(buffer)::value;
         using Other = std::integral_constant<int, 1 - s>;
-        if (!wait(BAR_VF + s, it >> 1) || !wait(BAR_P, it)) return false;
+        // a poll takes 300 cycles even when nothing is left to wait for: the buffers' come first
+        if (!wait(BAR_VF + s, it >> 1) || (next && !wait(BAR_KF + 1 - s, (it + 1) >> 1)) || !wait(BAR_P, it)) return false;
         pv(Zero{}, buffer, begun);
-        if (next) {
-          if (!wait(BAR_KF + 1 - s, (it + 1) >> 1)) return false;
-          qk(Zero{}, Other{});
-        }
+        if (next) qk(Zero{}, Other{});
         if (nblk == 2) {
           if (!wait(BAR_P + 1, it)) return false;
           pv(One{}, buffer, begun);
@@ -715,7 +699,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 8 + 2 * KP_DEQ) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
