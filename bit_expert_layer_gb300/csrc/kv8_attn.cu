@@ -106,6 +106,11 @@ constexpr float KA_NO_BLOCK = -1.0f;
 constexpr float KA_NO_REF = -1e30f;
 constexpr float KA_GROW = 8.0f;
 
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // One more part of a tile: the parts that came before.
 __device__ __forceinline__ unsigned ticket_add(unsigned* p) {
   unsigned old;
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       pid = __ldg(p.b.page_table + static_cast<size_t>(ls.b) * p.b.max_pages + (pos >> p.c.page_shift));
   };
   // codes that one tile alone reads need no place in L2
-  const uint64_t pol = p.b.max_new <= (1 << p.tq_shift) ? l2_policy_evict_first() : l2_policy_evict_last();
+  const uint64_t pol = p.b.max_new <= (1 << p.tq_shift) ? l2_policy_evict_first() : l2_policy_evict_normal();
   int issued = 0;
   // Issue the cursor's piece into its stage; returns this lane's block scale (the loaders).
   auto issue = [&]() -> float {

@@ -226,24 +226,25 @@ class Rope:
         """q, k: bf16 [T, heads, head_size] (rows may be slices of a wider tensor; k may be
         None); pos: int32 [n_axes, T], or [T] with one axis; out: (q_out, k_out), which may
         be q and k themselves.  Returns (q_out, k_out)."""
-        dev, d = q.device, self.head_size
-        if not q.is_cuda or q.dim() != 3:
+        dev, d, shape, at = q.device, self.head_size, q.shape, pos.shape
+        if not q.is_cuda or len(shape) != 3:
             raise ValueError("q: a 3-dimensional bfloat16 CUDA tensor is wanted")
         there = _elsewhere(dev, stream)
         if there is not None:
             with there:
                 return self(q, k, pos, out)
-        t, hq = q.shape[:2]
-        hk = 0
-        qs, ks, kp = _rows(q, "q", hq, d, dev), 0, 0
+        t, hq, _ = shape
+        hk = ks = kp = 0
+        qs = _rows(q, "q", hq, d, dev)
         if k is not None:
             if k.dim() != 3 or k.shape[0] != t:
                 raise ValueError(f"k: [{t}, heads, {d}] is wanted")
             hk, kp = k.shape[1], k.data_ptr()
             ks = _rows(k, "k", hk, d, dev)
-        _ints(pos, "pos", pos.dim(), dev)
-        if tuple(pos.shape) != (self.n_axes, t) and not (self.n_axes == 1 and tuple(pos.shape) == (t,)):
-            raise ValueError(f"pos: shape [{self.n_axes}, {t}] is wanted, got {list(pos.shape)}")
+        if at != (self.n_axes, t) and (self.n_axes != 1 or at != (t,)):
+            raise ValueError(f"pos: shape [{self.n_axes}, {t}] is wanted, got {list(at)}")
+        if pos.dtype is not torch.int32 or pos.device != dev or not pos.is_contiguous():
+            raise ValueError(f"pos: a contiguous int32 tensor on {dev} is wanted")
         qos, kos = hq * d, hk * d
         if out is None:
             qo = _empty((t, hq, d), dtype=_BF16, device=dev)

@@ -74,6 +74,8 @@ class Setup:
 
     def check_attention(self, out, ref=None, scale=None):
         n = int(self.offsets[-1])
+        if n == 0:
+            return
         want, bound = (ref or self.ref()).attention(self.table, self.lens, self.offsets, self.q[:n].double(), scale)
         err = (out[:n].double() - want).abs()
         assert torch.isfinite(out[:n]).all()
@@ -425,6 +427,94 @@ def test_other_stream_and_short_wait_limit(kv8):
     assert big.cache.get_error() == _abi.MOE_ERR_TIMEOUT
     assert torch.equal(big.cache.attention(big.batch, big.q, workspace=ws), b)
     assert big.cache.get_error() == 0
+
+
+def test_prompt_with_a_short_wait_limit(kv8):
+    """The prompt kernel's waits give up, too: recorded, and the next call is whole again."""
+    from bit_expert_layer_gb300 import _abi
+    s = Setup(kv8, [3000, 700], [600, 700], seed=23)
+    a = s.cache.attention(s.batch, s.q)
+    ws = s.cache.new_workspace(16, 700)
+    _abi.moe_set_wait_limit_ns(1)
+    try:
+        s.cache.attention(s.batch, s.q, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        _abi.moe_set_wait_limit_ns(0)
+    assert s.cache.get_error() == _abi.MOE_ERR_TIMEOUT
+    assert torch.equal(s.cache.attention(s.batch, s.q, workspace=ws), a)
+    assert s.cache.get_error() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_two_calls_at_once(kv8, new):
+    """Two streams, one cache, a workspace each."""
+    s = Setup(kv8, [4000, 900, 60], [new] * 3, seed=24)
+    a = s.cache.attention(s.batch, s.q)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [s.cache.new_workspace(16, new) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [s.cache.attention(s.batch, s.q, workspace=spaces[i % 2], stream=streams[i % 2]) for i in range(12)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for o in outs) and s.cache.get_error() == 0
+
+
+@pytest.mark.parametrize("lens,new,bound", [([700, 33], [1, 1], 300), ([300, 40], [5, 2], 64), ([90, 64], [0, 0], 9)])
+def test_a_loose_bound_on_the_new_tokens(kv8, lens, new, bound):
+    s = Setup(kv8, lens, new, seed=25, pad=1)
+    b = kv8.KV8Batch(s.batch.page_table, s.batch.lens, s.batch.offsets, bound)
+    out = torch.full(s.q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    s.cache.attention(b, s.q, out=out)
+    s.check_attention(out)
+    assert (out[int(s.offsets[-1]):] == 5).all() and s.cache.get_error() == 0
+
+
+def test_prompts_of_the_largest_batch(kv8):
+    rng = np.random.RandomState(5)
+    new = [int(x) for x in rng.choice([0, 1, 17, 40], 1024)]
+    s = Setup(kv8, [n + int(rng.choice([0, 3, 150])) for n in new], new, (4, 2, 64), 16, seed=26)
+    s.check_attention(s.cache.attention(s.batch, s.q))
+    assert s.cache.get_error() == 0
+
+
+@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_three_million_positions(kv8, fmt, new):
+    """A sequence that reads the same four pages 750 times over: what all its tokens see is, but
+    for the last few positions, what one round of the pages gives (each weight 1 / 750).  Of
+    sum_i p_i |v_i|: 2^-11 for the weights, (n / 128 + 64) 2^-23 < 2^-8.4 for the fp32 sums over
+    n positions, 2^-8 for the last rounding; together under 2^-7."""
+    s = Setup(kv8, [4096], [new], (8, 1, 64), 1024, fmt, seed=27)
+    rounds = 750
+    b = kv8.KV8Batch(ints(np.tile(s.table, (1, rounds))), ints([4096 * rounds]), s.batch.offsets, new)
+    out = s.cache.attention(b, s.q).double()
+    k, v, _ = s.ref().values(s.table[0], 4096)
+    for i in range(new):
+        n = torch.full((4096,), float(rounds), device="cuda", dtype=torch.float64)
+        n[4096 - new + i + 1:] -= 1
+        for h in range(8):
+            p = torch.softmax(k[:, 0] @ s.q[i, h].double() / 8 + n.log(), 0)
+            assert ((out[i, h] - p @ v[:, 0]).abs() <= 2.0 ** -7 * (p @ v[:, 0].abs())).all()
+    assert s.cache.get_error() == 0
+
+
+def test_captured_prompt(kv8):
+    s = Setup(kv8, [300, 77], [120, 33], seed=28)
+    ws = s.cache.new_workspace(16, 120)
+    want = s.cache.attention(s.batch, s.q, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = s.cache.attention(s.batch, s.q, workspace=ws)
+    for lens in ([300, 77], [411, 200], [120, 33]):
+        s.lens = [min(a, 5 * 64 if i == 0 else 2 * 64) for i, a in enumerate(lens)]
+        s.batch.lens.copy_(ints(s.lens))
+        out.zero_()
+        graph.replay()
+        s.check_attention(out)
+    s.batch.lens.copy_(ints([300, 77]))
+    graph.replay()
+    assert torch.equal(out, want) and s.cache.get_error() == 0
 
 
 def test_refusals(kv8):
