@@ -3,14 +3,13 @@
 // rows hold), on tcgen05.
 //
 // A CTA works on one or two blocks of 128 query rows (TQ tokens x G heads each) that share
-// their keys, in tiles of 128 positions; its 16 warps (128 registers each; with 20 there are
-// 96, and the scores spill) have roles:
+// their keys, in tiles of 128 positions; its 14 warps (128 registers each; with more than 16
+// there are 96, and the scores spill) have roles:
 //   warps 0-7    softmax, one query row per thread, four warps per row block
-//   warps 8-10   dequantise K: codes from global memory into fp16 tiles in shared memory,
-//                128-byte rows with the 128-byte swizzle, two buffers
-//   warps 11-13  the same for V
-//   warp 14      issues the MMAs
-//   warp 15      plans: looks up the tiles' pages and scales ahead of the dequantising warps
+//   warps 8-11   dequantise: codes from global memory into fp16 tiles in shared memory,
+//                128-byte rows with the 128-byte swizzle, two buffers each for K and V
+//   warp 12      issues the MMAs
+//   warp 13      plans: looks up the tiles' pages and scales ahead of the dequantising warps
 // Per tile and row block, TMEM lane = query row:
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
@@ -35,8 +34,8 @@ namespace moe {
 
 namespace {
 
-constexpr int KP_THREADS = 512;
-constexpr int KP_DEQ = 3;                         // dequantising warps for K, and as many for V
+constexpr int KP_DEQ = 4;                         // dequantising warps
+constexpr int KP_THREADS = (8 + KP_DEQ + 2) * 32;
 constexpr int KP_U = 128;                         // positions per tile
 constexpr int KP_COST = 2;                        // a tile's start, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     mbar_init(bar(BAR_END), 1);
     for (int i = 0; i < KP_PLANS; ++i) {
       mbar_init(bar(BAR_LF + i), 1);
-      mbar_init(bar(BAR_LE + i), 2 * KP_DEQ);
+      mbar_init(bar(BAR_LE + i), KP_DEQ);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   }
   const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
   const Kv8Seg first = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end);   // where every role begins
-  if (warp == 8 + 2 * KP_DEQ) {
+  if (warp == 8 + KP_DEQ) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
@@ -483,68 +482,70 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
     }
-  } else if (warp < 8 + 2 * KP_DEQ) {
-    // ================================================ dequantise K or V
+  } else if (warp < 8 + KP_DEQ) {
+    // ================================================ dequantise
     constexpr int CPR = D / 16;                 // 16-byte chunks of codes per row
     constexpr int RPI = KP_DEQ * 32 / CPR;      // rows per step of the threads
-    constexpr int NI = (KP_U + RPI - 1) / RPI;  // steps per tile
-    const int is_v = warp >= 8 + KP_DEQ;
-    const int dt = tid - (is_v ? 8 + KP_DEQ : 8) * 32, cc = dt % CPR, r0 = dt / CPR;
-    const uint8_t* codes = p.c.codes[is_v];
-    uint8_t* tiles = is_v ? s_v : s_k;
-    const int b_full = is_v ? BAR_VF : BAR_KF, b_empty = is_v ? BAR_VE : BAR_KE;
-    uint4 reg[NI];
-    // The codes of the tile planned in slot `it`, if there is one.
-    auto load = [&](int it) {
-      const int s = it & (KP_PLANS - 1);
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(bar(BAR_LF + s), (it / KP_PLANS) & 1, p.c.err, abort_flag, p.wait_ns)))
-        return false;
+    constexpr int NI = KP_U / RPI;              // steps per tile
+    static_assert(RPI % KV8_BLOCK == 0, "a step's rows are whole blocks, and share their place in the swizzle");
+    // 8 lanes take 4 chunks of 2 rows: what they store then lies in 8 different bank groups
+    const int dt = tid - 256;
+    const int cc = D == 128 ? (dt & 3) | ((dt >> 1) & 4) : dt & 3;
+    const int r0 = D == 128 ? ((dt >> 2) & 1) | ((dt >> 4) << 1) : dt >> 2;
+    uint8_t* const to = s_k + (cc >> 2) * BOX + r0 * 128;         // V's tiles lie 2 TILE on
+    const int at0 = ((2 * (cc & 3)) ^ (r0 & 7)) << 4, at1 = ((2 * (cc & 3) + 1) ^ (r0 & 7)) << 4;
+    uint4 kreg[NI], vreg[NI];
+    // The codes of the tile planned in slot s.
+    auto load = [&](uint4 (&reg)[NI], const uint8_t* codes, int s) {
       const int valid = s_plan[s].valid;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int row = r0 + i * RPI;
-        const int at = row < KP_U ? s_plan[s].rows[row / KV8_BLOCK] : -1;
+        const int at = s_plan[s].rows[row / KV8_BLOCK];
         reg[i] = make_uint4(0, 0, 0, 0);
         if (at >= 0 && row < valid) reg[i] = ldg_nc_v4(codes + static_cast<size_t>(at + row % KV8_BLOCK) * D + 16 * cc);
       }
-      return valid >= 0;
     };
-    auto store = [&](uint8_t* tile, const uint32_t* fac) {
+    auto store = [&](const uint4 (&reg)[NI], uint8_t* tile, const uint32_t* fac) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int row = r0 + i * RPI;
-        if (row >= KP_U) break;
-        const uint32_t fc = fac[row / KV8_BLOCK], fo = kv8_scaled_offset<FMT>(fc);
+        const uint32_t fc = fac[(r0 + i * RPI) / KV8_BLOCK], fo = kv8_scaled_offset<FMT>(fc);
         const auto h2 = [&](uint32_t x, int hi) { return kv8_half2_scaled<FMT>(x, hi, fc, fo); };
         const uint32_t w0 = kv8_flip<FMT>(reg[i].x), w1 = kv8_flip<FMT>(reg[i].y);
         const uint32_t w2 = kv8_flip<FMT>(reg[i].z), w3 = kv8_flip<FMT>(reg[i].w);
-        const uint4 a = make_uint4(h2(w0, 0), h2(w0, 1), h2(w1, 0), h2(w1, 1));
-        const uint4 b = make_uint4(h2(w2, 0), h2(w2, 1), h2(w3, 0), h2(w3, 1));
-        // 8 lanes write one row: the upper box's lanes take their odd chunk first, so that the
-        // 8 chunks of a store lie in 8 different bank groups
-        uint8_t* dst = tile + (cc >> 2) * BOX + row * 128;
-        const int c0 = 2 * (cc & 3), odd = cc >> 2;
-        *reinterpret_cast<uint4*>(dst + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? b : a;
-        *reinterpret_cast<uint4*>(dst + (((c0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? a : b;
+        *reinterpret_cast<uint4*>(tile + i * RPI * 128 + at0) = make_uint4(h2(w0, 0), h2(w0, 1), h2(w1, 0), h2(w1, 1));
+        *reinterpret_cast<uint4*>(tile + i * RPI * 128 + at1) = make_uint4(h2(w2, 0), h2(w2, 1), h2(w3, 0), h2(w3, 1));
       }
       fence_proxy_async_smem();
       __syncwarp();
     };
-    bool have = load(0);
+    const auto wait = [&](int b, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns)) != 0;
+    };
+    bool ok = wait(BAR_LF, 0) && s_plan[0].valid >= 0;
+    if (ok) {
+      load(kreg, p.c.codes[0], 0);
+      load(vreg, p.c.codes[1], 0);
+    }
 #pragma unroll 1
-    for (int it = 0; have; ++it) {
-      const int s = it & 1, ph = (it >> 1) & 1, slot = it & (KP_PLANS - 1);
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + s), ph ^ 1, p.c.err, abort_flag, p.wait_ns))) break;
-      store(tiles + s * TILE, is_v ? s_plan[slot].vfac : s_plan[slot].kfac);
+    for (int it = 0; ok; ++it) {
+      const int s = it & 1, ph = (it >> 1) & 1, slot = it & (KP_PLANS - 1), next = (it + 1) & (KP_PLANS - 1);
+      if (!wait(BAR_KE + s, ph ^ 1)) break;
+      store(kreg, to + s * TILE, s_plan[slot].kfac);
+      if (lane == 0) mbar_arrive(bar(BAR_KF + s));
+      if (!wait(BAR_LF + next, (it + 1) / KP_PLANS)) break;
+      ok = s_plan[next].valid >= 0;
+      if (ok) load(kreg, p.c.codes[0], next);
+      if (!wait(BAR_VE + s, ph ^ 1)) break;
+      store(vreg, to + (2 + s) * TILE, s_plan[slot].vfac);
       if (lane == 0) {
-        mbar_arrive(bar(b_full + s));
+        mbar_arrive(bar(BAR_VF + s));
         mbar_arrive(bar(BAR_LE + slot));
       }
-      have = load(it + 1);
+      if (ok) load(vreg, p.c.codes[1], next);
     }
   } else {
-    if (warp == 9 + 2 * KP_DEQ) {
+    if (warp == 9 + KP_DEQ) {
       // ================================================ plan: the tiles' pages and scales
       // Lanes 0-7 look after the tile's 8 K blocks, lanes 8-15 after its V blocks.  (With the
       // dequantising warps doing this themselves, their loads went through spilled registers,
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         }
         if (!more) break;
       }
-    } else if (warp == 8 + 2 * KP_DEQ) {
+    } else if (warp == 8 + KP_DEQ) {
       // ================================================ MMA issue
       // The whole warp follows the loop and one elected lane issues, with the row block and the
       // buffer known at compile time, so that every descriptor is a uniform base plus a constant.
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 + 2 * KP_DEQ) {
+  if (warp == 8 + KP_DEQ) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
