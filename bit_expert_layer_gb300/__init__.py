@@ -3,7 +3,8 @@ MLX affine 4-bit (group-64) expert weights.
 
 The compute lives in ``libmoe_layer.so`` (hand-written CUDA, C ABI in
 ``include/moe_layer.h``); this package is a ctypes binding (``_abi``, same names as
-the C entry points) plus torch-facing wrappers (``layer``).  Build with
+the C entry points) plus torch-facing wrappers: ``layer`` (the MoE layer and stacks)
+and ``kv8`` (the 8-bit key/value cache, its attention and rotary positions).  Build with
 ``bit_expert_layer_gb300.build.build()``.
 """
 from . import _abi

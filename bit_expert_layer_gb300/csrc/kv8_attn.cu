@@ -21,8 +21,13 @@
 //   O^T += V^T w  a lane takes 16 consecutive dims of 4 keys and interleaves their bytes, so
 //                 that a pair of codes of one dim becomes an fp16 pair; the weights change
 //                 from S's layout to B's by a transposing move.
-// Bound: the cache's bytes.  With the rows on the M side (half of each MMA and of O's registers
-// empty at 8 rows) a piece took 750 instructions and 8 x 32768 positions 36.7 us.
+// Bound: the cache's bytes.  8 x 32768 positions of e4m3 (2 heads of 128, 134 MB) take 30 us; a
+// plain copy's rate would take 20.  Between its first piece and its last a CTA runs at the
+// memory's rate (8 KB per warp and 2400 cycles); 7000 cycles before it (the line, the first
+// segment, the first page, the first codes) and 8000 after it (the CTA's join, the ticket, the
+// tile's join) are what is left.  With the query rows on the M side (half of each MMA and of O's
+// registers empty at 8 rows) a piece took 750 instructions and the same case 36.7 us; 16 warps of
+// 16-key pieces took 33.5 us, 12 of three stages 31.8, where 8 warps of 32 keys took 31.6.
 #include <cstring>
 
 #include "internal.h"

@@ -21,8 +21,14 @@
 //   O += w V     w from TMEM, V from shared memory, its rows as they are (N-major operand)
 // The two row blocks alternate: while one is in its softmax the tensor cores work for the
 // other (order of issue: PV of block 0, next QK of block 0, PV of block 1, next QK of block 1).
-// Bound: per tile and two row blocks 16.8 MFLOP of MMA (2048 cycles at the nominal rate), and
-// 32768 exponentials.
+// Bound: the tensor cores' 16.8 MFLOP per tile and two row blocks, 2048 cycles at the nominal
+// rate (2400 at the 75 cycles that an M128 N128 K16 instruction takes in a chain), 32768
+// exponentials (1024 cycles) beside them.  Measured: 2048 tokens over 31000 positions of int8,
+// 16 query and 2 key/value heads of 128, in 390 us, 1.29 PFLOP/s, 0.65 of the measured bf16 rate;
+// the tensor pipe is active 56 % of the time, and what is left is a block's chain from scores
+// through weights to the next scores, which the other block's covers only in part.  A prompt of
+// 2048 tokens from the start takes 43 us: 128 tiles of 1 to 16 units each, where a tile's start
+// and end (queries in, result out, some 10 thousand cycles) weigh as much as its units.
 #include <cstring>
 #include <type_traits>
 
@@ -343,8 +349,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           const int left = see - u * KP_U;                       // positions of the tile that the row sees
           uint32_t sc[2][32];
           // A tile at the causal edge, or with a page missing: what the row does not see becomes
-          // -inf in TMEM first, so that the passes below carry no mask (2 of 5 instructions per
-          // score, measured).
+          // -inf in TMEM first, so that the passes below carry no mask (with it in them, the
+          // compiler masked every tile: 767 us against 557).
           if (__any_sync(0xffffffffu, left < KP_U) || bad) {
 #pragma unroll 1
             for (int c = 0; c < KP_U / 32; ++c) {
@@ -362,7 +368,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             tmem_st_wait();
           }
           // The scores are read twice, 32 columns at a time, the next ones while these are worked
-          // on: 128 of them in registers do not fit beside the rest.
+          // on: 128 of them in registers do not fit beside the rest.  (One pass against the
+          // reference of the tiles before, the weights waiting in registers until all scores are
+          // seen: 518 us where two passes took 499.)
           // ---- pass 1: the maximum of s_i + e
           float mx = -INFINITY;
           tmem_ld32(t_s, sc[0]);
@@ -547,9 +555,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   } else {
     if (warp == 9 + KP_DEQ) {
       // ================================================ plan: the tiles' pages and scales
-      // Lanes 0-7 look after the tile's 8 K blocks, lanes 8-15 after its V blocks.  (With the
-      // dequantising warps doing this themselves, their loads went through spilled registers,
-      // which waited for the data: 4400 cycles a tile.)
+      // Lanes 0-7 look after the tile's 8 K blocks, lanes 8-15 after its V blocks.  The
+      // dequantising warps are left with loads, conversions and stores, whose instructions are
+      // what the softmax competes with (8900 warp instructions a tile in all: 499 us; 7150: 390).
       const int lb = lane & 7;
       Kv8Seg sg = first;
       bool ok = true;
@@ -614,9 +622,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       // ================================================ MMA issue
       // The whole warp follows the loop and one elected lane issues, with the row block and the
       // buffer known at compile time, so that every descriptor is a uniform base plus a constant.
-      // (With either in a variable, an MMA took 125 cycles to issue; by itself it takes 64.  A
-      // warp per row block let the blocks fall into step, both in their softmax and then both on
-      // the tensor cores: 560 us where this order took 470.)
+      // (A lane with a loop of its own issued an MMA every 120 cycles: 570 us where this took
+      // 470.  A warp per row block let the blocks fall into step, both in their softmax and then
+      // both on the tensor cores: 560 us.)
       constexpr uint32_t ID_S = idesc_f16(KP_ROWS, KP_U, 0), ID_O = idesc_f16(KP_ROWS, D, 1);
       const bool leader = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
