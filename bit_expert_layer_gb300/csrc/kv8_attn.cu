@@ -675,9 +675,10 @@ int floor_log2(int n) {
 }
 
 // Query rows of a tile, or 0 for the prompt kernel.  Up to 32 rows go through the decode
-// kernel in tiles of 16, which read the codes twice, the second time mostly from L2: 16
-// sequences of 4 new tokens and 8 rows each over 8 thousand positions took 29 us that way and
-// 41 us in one block of 128 rows, three quarters empty.
+// kernel in tiles of 16, which read the codes twice, the second time mostly from L2: 4 new
+// tokens of 8 query heads each took 28 us that way over 16 sequences of 8 thousand positions and
+// 18 over one, and 36 and 25 in one block of 128 rows, three quarters empty.  With 64 rows it was
+// 53 and 17 against 36 and 25.
 int ka_rows(int G, int max_new) {
   const long long n = static_cast<long long>(G) * max_new;
   return n <= 8 ? 8 : n <= 32 ? 16 : 0;

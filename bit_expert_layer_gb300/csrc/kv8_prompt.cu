@@ -47,6 +47,7 @@ constexpr int KP_COST = 2;                        // a tile's start, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
 constexpr int KP_SLOTS = 8;                       // tiles whose scales the softmax can ask for
 constexpr int KP_PLANS = 4;                       // tiles planned ahead
+constexpr int KP_FEW = 4;                         // parts of a tile that a join loads at once
 constexpr float KP_GROW = 8.0f;                   // the maximum may outgrow the reference by 2^8
 // Blocks of a tile are brought to the tile's largest scale in fp16, 2^head on top of it: the
 // largest code (448; for int8 the offset 1152 of its conversion) lands just under fp16's
@@ -729,25 +730,70 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
   if (tb >= blk_tokens || tok >= tl.n) return;
   constexpr int PL = D / 32;                    // dims per lane
   const auto slot = [&](int i) { return kp_slot<D>(p.part, c0 + i, c0, row); };
-  float M = -INFINITY;
-  for (int i = lane; i < tl.ns; i += 32) M = fmaxf(M, slot(i)[D]);
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-  const float at = M == -INFINITY ? 0.0f : M;
-  float O[PL], L = 0.0f;
+  float M = -INFINITY, L = 0.0f, O[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) O[k] = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < tl.ns; ++i) {
-    const float* src = slot(i);
-    const float2 ml = *reinterpret_cast<const float2*>(src + D);
-    const float f = exp2f(ml.x - at);
-    L = fmaf(f, ml.y, L);
+  const auto fetch = [&](int i, float (&v)[PL]) {
+    const float* src = slot(i) + PL * lane;
+    if constexpr (PL == 4)
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+    else
+      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+  };
+  if (tl.ns <= KP_FEW) {
+    // few parts (tiles of a long prompt): all loads at once
+    float2 ml[KP_FEW];
+    float v[KP_FEW][PL];
 #pragma unroll
-    for (int k = 0; k < PL; k += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(src + PL * lane + k);
-      O[k] = fmaf(f, v.x, O[k]);
-      O[k + 1] = fmaf(f, v.y, O[k + 1]);
+    for (int i = 0; i < KP_FEW; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.0f);
+      if (i < tl.ns) {
+        ml[i] = *reinterpret_cast<const float2*>(slot(i) + D);
+        fetch(i, v[i]);
+      }
+      M = fmaxf(M, ml[i].x);
+    }
+    const float at = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+    for (int i = 0; i < KP_FEW; ++i) {
+      if (i >= tl.ns) break;
+      const float f = ex2(ml[i].x - at);
+      L = fmaf(f, ml[i].y, L);
+#pragma unroll
+      for (int k = 0; k < PL; ++k) O[k] = fmaf(f, v[i][k], O[k]);
+    }
+  } else {
+    // many (few query rows over a long cache): lane i keeps the weights of parts i, i + 32, ...
+    constexpr int PER = (KV8_MAX_CTAS + 31) / 32;
+    float2 ml[PER];
+    float wt[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = lane + 32 * k;
+      ml[k] = i < tl.ns ? *reinterpret_cast<const float2*>(slot(i) + D) : make_float2(-INFINITY, 0.0f);
+      M = fmaxf(M, ml[k].x);
+    }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    const float at = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      wt[k] = ex2(ml[k].x - at);
+      L = fmaf(wt[k], ml[k].y, L);
+    }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int n = min(tl.ns - 32 * k, 32);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float f = __shfl_sync(0xffffffffu, wt[k], i);
+        float v[PL];
+        fetch(32 * k + i, v);
+#pragma unroll
+        for (int j = 0; j < PL; ++j) O[j] = fmaf(f, v[j], O[j]);
+      }
     }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros

@@ -163,17 +163,29 @@ __device__ __forceinline__ int2 kv8_owners(const Kv8Seg& g, long long w, const K
   return make_int2(kv8_run_of(runs, start + C), kv8_run_of(runs, start + C + g.units - 1));
 }
 
-// The segment that starts at unit w of the line.
+// The last of 0 .. n - 1 that satisfies `ok`, which holds up to some point and not after it, and
+// for 0: a search by the whole (converged) warp, 32 ways a step.
+template <typename F>
+__device__ __forceinline__ int kv8_last_of(int n, F ok) {
+  const int lane = lane_id();
+  int lo = 0;
+#pragma unroll 1
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const bool in = i < n && (lane == 0 || ok(lo + i));
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, in));
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+// The segment that starts at unit w of the line (asked for by whole warps).
 template <int U, int C>
 __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w,
                                           long long w_end) {
   Kv8Seg g;
-  int lo = 0, hi = p.b.n_seqs;             // prefix[lo] <= w < prefix[hi]
-#pragma unroll 1
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (prefix[m] <= w) lo = m; else hi = m;
-  }
+  const int lo = kv8_last_of(p.b.n_seqs, [&](int i) { return prefix[i] <= w; });
   g.b = lo;
   g.s = kv8_seq(p.b, p.c.page_shift, lo);
   long long x = w - prefix[lo];
@@ -187,12 +199,7 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
     for (; x >= per_head; x -= per_head) ++g.g;
   }
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
-  int tl = 0, th = tiles;                  // units before tl <= x < units before th
-#pragma unroll 1
-  while (th - tl > 1) {
-    const int m = (tl + th) >> 1;
-    if (kv8_units_before<U, C>(g.s, p.tq_shift, m) <= x) tl = m; else th = m;
-  }
+  const int tl = kv8_last_of(tiles, [&](int t) { return kv8_units_before<U, C>(g.s, p.tq_shift, t) <= x; });
   g.t = tl;
   const int in_tile = static_cast<int>(tl ? x - kv8_units_before<U, C>(g.s, p.tq_shift, tl) : x);
   kv8_seg_close<C>(g, in_tile, kv8_units_tile<U, C>(g.s, p.tq_shift, tl), w, w_end);
