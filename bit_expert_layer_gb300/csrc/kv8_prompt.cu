@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       };
       const uint32_t inv_g = (65535u + p.G) / p.G;       // r / G = r inv_g >> 16 for r < 128, G <= 16
       int it = 0, seg = 0;
-      KpTile tile = {0, 0, 0, 0, 0, {0, 0, 0}};
+      if (tid == 0) kp_tiles(p.part)[cta].ns = 0;        // unless a tile that begins here goes on
       Kv8Seg sg = first;
 #pragma unroll 1
       for (long long w = w_beg; w < w_end;) {
@@ -480,14 +480,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         tc_fence_before();
         if (!whole) {
           *reinterpret_cast<float2*>(part + D) = make_float2(m_ref, l);
-          if (tid == 0 && own.x == cta) tile = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
+          if (tid == 0 && own.x == cta)
+            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
         ++seg;
       }
-      if (tid == 0) {
-        kp_tiles(p.part)[cta] = tile;
-        s_n[seg & 1] = 0;                  // no more segments
-      }
+      if (tid == 0) s_n[seg & 1] = 0;      // no more segments
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
     }
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     constexpr int CPR = D / 16;                 // 16-byte chunks of codes per row
     constexpr int RPI = KP_DEQ * 32 / CPR;      // rows per step of the threads
     constexpr int NI = KP_U / RPI;              // steps per tile
-    static_assert(RPI % KV8_BLOCK == 0, "a step's rows are whole blocks, and share their place in the swizzle");
+    static_assert(RPI % 8 == 0 && KP_U % RPI == 0, "a thread's rows share their place in the swizzle");
     // 8 lanes take 4 chunks of 2 rows: what they store then lies in 8 different bank groups
     const int dt = tid - 256;
     const int cc = D == 128 ? (dt & 3) | ((dt >> 1) & 4) : dt & 3;
