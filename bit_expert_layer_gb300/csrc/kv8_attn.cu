@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     fence_mbar_init();
   }
   if (tid < 2 * KA_WARPS) meta[tid].b = -1;
+  grid_dep_wait();                          // what follows reads and writes what earlier kernels wrote
   Kv8Runs runs;
   runs.total = kv8_line<KA_U, KA_COST, KA_THREADS>(p, prefix, s_warp);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x) * KA_WARPS));
@@ -700,8 +701,7 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const Kv
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  k<<<grid, ka_warps(R) * 32, ka_smem(D, R, p.b.n_seqs), s>>>(tk, tv, p, box);
-  return cudaGetLastError();
+  return launch_pdl(k, dim3(grid), dim3(ka_warps(R) * 32), ka_smem(D, R, p.b.n_seqs), s, tk, tv, p, box);
 }
 
 }  // namespace

@@ -36,6 +36,7 @@ struct Kv8Block {
 };
 
 __device__ __forceinline__ Kv8Block kv8_block(const Kv8RowsParams& p) {
+  grid_dep_wait();
   Kv8Block k;
   k.live = false;
   // consecutive warps take the keys and values of all heads of a unit, then the next unit
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
       }
     }
   };
+  grid_dep_wait();
   load(threadIdx.x);                     // on their way while the sines are computed
   for (int i = threadIdx.x; i < nt * p.half; i += RP_THREADS) {
     const int t = i / p.half, j = i - t * p.half;
@@ -373,8 +375,7 @@ moe_status_t kv8_rows_launch(const gqa_kv8_cache_t* cache, const Kv8RowsParams& 
   else
     k = d128 ? (e4 ? kv8_gather_kernel<128, GQA_KV8_E4M3> : kv8_gather_kernel<128, GQA_KV8_INT8>)
              : (e4 ? kv8_gather_kernel<64, GQA_KV8_E4M3> : kv8_gather_kernel<64, GQA_KV8_INT8>);
-  k<<<grid, block, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(k, grid, block, 0, s, p);
   if (e != cudaSuccess) {
     set_error_detail(APPEND ? "gqa_kv8_append: launch" : "gqa_kv8_gather: launch", e);
     return MOE_ERR_CUDA;
@@ -525,11 +526,7 @@ extern "C" moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, lon
   const dim3 grid((T + p.tokens - 1) / p.tokens);
   const size_t smem = 2ull * p.tokens * p.half * sizeof(float);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 128)
-    rope_kernel<128><<<grid, RP_THREADS, smem, s>>>(p);
-  else
-    rope_kernel<64><<<grid, RP_THREADS, smem, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(D == 128 ? rope_kernel<128> : rope_kernel<64>, grid, dim3(RP_THREADS), smem, s, p);
   if (e != cudaSuccess) {
     set_error_detail("gqa_rope: launch", e);
     return MOE_ERR_CUDA;

@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     *abort_flag = 0;
     fence_mbar_init();
   }
+  grid_dep_wait();                              // what follows reads and writes what earlier kernels wrote
   Kv8Runs runs;
   runs.total = kv8_line<KP_U, KP_COST, KP_THREADS>(p, prefix, s_warp);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x)));
@@ -817,8 +818,7 @@ cudaError_t launch_prompt(const Kv8AttnParams& p, int nblk, int grid, int dev, c
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  k<<<grid, KP_THREADS, kp_smem(D, p.b.n_seqs), s>>>(p, nblk);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(k, dim3(grid), dim3(KP_THREADS), kp_smem(D, p.b.n_seqs), s, p, nblk);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv8_prompt_join_kernel<D>, dim3(grid, nblk * KP_ROWS / 8), dim3(256), 0, s, p, nblk);
 }
