@@ -1,8 +1,8 @@
 // kv8_cache.cu -- the 8-bit key/value cache's write and read back, and rotary positions.
 // All three are bound by memory: each reads its rows once and writes them once.  Measured on 2
-// key/value and 16 query heads of 128: the write of 16 thousand tokens (int8, 23 MB) 6.2 us
-// (3.5 at the copy rate), 60 thousand rows read back (e4m3, 92 MB) 15.6 us (13.8), 16384 tokens
-// rotated (151 MB) 28.7 us (22.6).
+// key/value and 16 query heads of 128: the write of 16 thousand tokens (int8, 23 MB) 5.9 us
+// (3.5 at the copy rate), 60 thousand rows read back (e4m3, 92 MB) 15.1 us (13.8), 16384 tokens
+// rotated (151 MB) 28.0 us (22.6).
 #include <cmath>
 #include <cstring>
 

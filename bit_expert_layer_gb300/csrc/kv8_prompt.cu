@@ -1,6 +1,6 @@
 // kv8_prompt.cu -- attention over the 8-bit key/value cache for many query rows per
-// key/value head (prompts, pieces of one, more drafted tokens than the decode kernel's 16
-// rows hold), on tcgen05.
+// key/value head (prompts, pieces of one, more drafted tokens than the decode kernel takes),
+// on tcgen05.
 //
 // A CTA works on one or two blocks of 128 query rows (TQ tokens x G heads each) that share
 // their keys, in tiles of 128 positions; its 14 warps (128 registers each; with more than 16
@@ -13,9 +13,10 @@
 // Per tile and row block, TMEM lane = query row:
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
-//   softmax      in base 2 with the value block's scale folded in, as in the decode kernel:
-//                w_i = 2^(s_i + e_i - m), normaliser sum w_i 2^-e_i in fp32.  The reference m
-//                moves only when the maximum has grown by more than 2^8: until then weights
+//   softmax      in base 2 with the scale 2^e of the tile's values folded in, as in the decode
+//                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^-e in fp32.  (Dequantising
+//                brings a tile's blocks to one scale for the keys and one for the values, so that
+//                no score needs a factor of its own block's.)  The reference m moves only when the maximum has grown by more than 2^8: until then weights
 //                up to 2^8 fit fp16 as exactly as smaller ones, and O in TMEM needs no
 //                rescaling.  fp16(w) goes back to TMEM over S.
 //   O += w V     w from TMEM, V from shared memory, its rows as they are (N-major operand)
@@ -27,7 +28,7 @@
 // 16 query and 2 key/value heads of 128, in 390 us, 1.29 PFLOP/s, 0.65 of the measured bf16 rate;
 // the tensor pipe is active 56 % of the time, and what is left is a block's chain from scores
 // through weights to the next scores, which the other block's covers only in part.  A prompt of
-// 2048 tokens from the start takes 43 us: 128 tiles of 1 to 16 units each, where a tile's start
+// 2048 tokens from the start takes 41 us: 128 tiles of 1 to 16 units each, where a tile's start
 // and end (queries in, result out, some 10 thousand cycles) weigh as much as its units.
 #include <cstring>
 #include <type_traits>

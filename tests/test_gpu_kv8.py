@@ -313,6 +313,17 @@ def test_attention_extreme_scales(kv8):
     s.check_attention(c.attention(s.batch, s.q))
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("new", [1, 3, 90])
+def test_attention_uneven_scales(kv8, new, fmt):
+    """Blocks side by side whose scales differ by up to 2^20, for keys and values alike."""
+    s = Setup(kv8, [500, 90], [new, new], (16, 2, 128), 32, fmt, seed=33, q_gain=1.0)
+    c = s.cache
+    for x, lo in ((c.k_scale, -26), (c.v_scale, -18)):
+        x[:] = torch.exp2(torch.randint(lo, lo + 21, x.shape, generator=s.g, device="cuda").float())
+    s.check_attention(c.attention(s.batch, s.q))
+
+
 def test_attention_not_finite_queries_stay_in_their_rows(kv8):
     s = Setup(kv8, [100, 70, 40], [1, 3, 1], seed=12)
     a = s.cache.attention(s.batch, s.q)
@@ -321,6 +332,18 @@ def test_attention_not_finite_queries_stay_in_their_rows(kv8):
     b = s.cache.attention(s.batch, s.q)
     keep = torch.ones(5, 16, dtype=torch.bool, device="cuda")
     keep[0, 3] = keep[2, 8] = False
+    assert torch.equal(a[keep], b[keep]) and torch.isnan(b[~keep]).all()
+
+
+def test_prompt_queries_that_are_not_finite_stay_in_their_rows(kv8):
+    s = Setup(kv8, [700, 200], [60, 200], seed=34)
+    a = s.cache.attention(s.batch, s.q)
+    s.q[5, 3, 5] = math.nan
+    s.q[61, 8, 0] = math.nan
+    s.q[150, 15] = math.inf
+    b = s.cache.attention(s.batch, s.q)
+    keep = torch.ones(260, 16, dtype=torch.bool, device="cuda")
+    keep[5, 3] = keep[61, 8] = keep[150, 15] = False
     assert torch.equal(a[keep], b[keep]) and torch.isnan(b[~keep]).all()
 
 
