@@ -302,11 +302,10 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 2));
       const uint32_t big = max(big2 >> 16, big2 & 0xFFFFu);
       // the row's largest magnitude lands in [2^13, 2^14): bf16's 8 bits stay exact in fp16
-      // down to 2^-28 of it
-      const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, -100), 100);
-      const float f = pow2i(-e);
-      // the factor stays below 2^62, so that its product with a K scale is finite
-      const float rf = fminf(pow2i(e) * p.scale_log2, 0x1p62f);
+      // down to 2^-28 of it.  What is not finite makes the whole row NaN.
+      const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, KV8_Q_MIN_EXP), KV8_Q_MAX_EXP);
+      const float f = big >= 0x7F80u ? NAN : pow2i(-e);
+      const float rf = fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint32_t* x = &v[j >> 1].x + (j & 1) * 2;
@@ -349,7 +348,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         ksc[k] = __shfl_sync(0xffffffffu, sc, k);
         const float vs = __shfl_sync(0xffffffffu, sc, NK + k);
         live[k] = ksc[k] >= 0.0f;
-        ksc[k] = fminf(fmaxf(ksc[k], 0.0f), 0x1p62f);
+        ksc[k] = fmaxf(ksc[k], 0.0f);
         ve[k] = static_cast<float>(max(scale_exp(vs), KV8_MIN_EXP));
 #pragma unroll
         for (int b = 0; b < NB; ++b) x[b][k][0] = x[b][k][1] = x[b][k][2] = x[b][k][3] = 0.0f;
@@ -373,6 +372,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       const bool masked = u * KA_U + KA_U > least || !live[0] || !live[NK - 1];
       bool grow = false;
       float y[NB][NK][4];
+      const auto factor = [&](int b, int k, int i) { return fminf(rs[b][i] * ksc[k], KV8_MAX_FACTOR); };
       const auto hidden = [&](int b, int k, int h, int i) {
         return !live[k] || u * KA_U + 16 * k + 8 * h + g4 >= see[b][i];
       };
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         for (int k = 0; k < NK; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f = rs[b][i] * ksc[k], add = ve[k] - m[b][i];
+            const float f = factor(b, k, i), add = ve[k] - m[b][i];
 #pragma unroll
             for (int h = 0; h < 2; ++h) y[b][k][2 * h + i] = fmaf(x[b][k][2 * h + i], f, add);
           }
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
             for (int k = 0; k < NK; ++k)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (!hidden(b, k, h, i)) mx = fmaxf(mx, fmaf(x[b][k][2 * h + i], rs[b][i] * ksc[k], ve[k]));
+                if (!hidden(b, k, h, i)) mx = fmaxf(mx, fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k]));
 #pragma unroll
             for (int s = 4; s <= 16; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
             const float corr = ex2(m[b][i] - mx);    // from no reference: 0
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
             for (int k = 0; k < NK; ++k)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                y[b][k][2 * h + i] = hidden(b, k, h, i) ? -INFINITY : fmaf(x[b][k][2 * h + i], rs[b][i] * ksc[k], ve[k] - mx);
+                y[b][k][2 * h + i] = hidden(b, k, h, i) ? -INFINITY : fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k] - mx);
           }
       }
       uint32_t pb[NB][NK][2];         // weights as B: keys 16 k + 8 h + 2 c4 and + 1 of row g4

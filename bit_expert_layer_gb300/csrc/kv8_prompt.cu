@@ -16,9 +16,10 @@
 //   softmax      in base 2 with the scale 2^e of the tile's values folded in, as in the decode
 //                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^-e in fp32.  (Dequantising
 //                brings a tile's blocks to one scale for the keys and one for the values, so that
-//                no score needs a factor of its own block's.)  The reference m moves only when the maximum has grown by more than 2^8: until then weights
-//                up to 2^8 fit fp16 as exactly as smaller ones, and O in TMEM needs no
-//                rescaling.  fp16(w) goes back to TMEM over S.
+//                no score needs a factor of its own block's.)  The reference m moves only when the
+//                maximum has grown by more than 2^8: until then weights up to 2^8 fit fp16 as
+//                exactly as smaller ones, and O in TMEM needs no rescaling.  fp16(w) goes back to
+//                TMEM over S.
 //   O += w V     w from TMEM, V from shared memory, its rows as they are (N-major operand)
 // The two row blocks alternate: while one is in its softmax the tensor cores work for the
 // other (order of issue: PV of block 0, next QK of block 0, PV of block 1, next QK of block 1).
@@ -324,13 +325,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll
               for (int m = LPR / 2; m >= 1; m >>= 1) big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, m));
               const uint32_t big = max(big2 >> 16, big2 & 0xFFFFu);
-              const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, -100), 100);
-              const float f = pow2i(-e);
+              const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, KV8_Q_MIN_EXP), KV8_Q_MAX_EXP);
+              const float f = big >= 0x7F80u ? NAN : pow2i(-e);
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[j] = pack2h(bf16lo(x[j]) * f, bf16hi(x[j]) * f);
               *reinterpret_cast<uint4*>(s_q + blk * TILE + (qc >> 3) * BOX + r2 * 128 + (((qc & 7) ^ (r2 & 7)) << 4)) = v[i];
-              // the factor stays below 2^62, so that its product with a K scale is finite
-              if (qc == 0) s_rs[blk * KP_ROWS + r2] = fminf(pow2i(e) * p.scale_log2, 0x1p62f);
+              if (qc == 0) s_rs[blk * KP_ROWS + r2] = fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
             }
           }
         }
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           if (dead) continue;
           tc_fence_after();
           const float4 sc4 = s_scale[it & (KP_SLOTS - 1)];
-          const float f = fmaxf(rs * sc4.x, 1e-37f), e = sc4.y;  // positive, so that -inf stays -inf
+          const float f = fminf(fmaxf(rs * sc4.x, 1e-37f), KV8_MAX_FACTOR), e = sc4.y;  // positive: -inf stays -inf
           const uint32_t bad = __float_as_uint(sc4.w);
           const int left = see - u * KP_U;                       // positions of the tile that the row sees
           uint32_t sc[2][32];
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           } else if (lane == 16) {
             plan->valid = valid;
             s_scale[it & (KP_SLOTS - 1)] =
-                make_float4(pow2i(min(kt - HEAD, 62)), static_cast<float>(vt - HEAD), pow2i(HEAD - vt), __uint_as_float(bads));
+                make_float4(pow2i(kt - HEAD), static_cast<float>(vt - HEAD), pow2i(HEAD - vt), __uint_as_float(bads));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_LF + slot));

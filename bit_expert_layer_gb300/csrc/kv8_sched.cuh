@@ -29,6 +29,12 @@ namespace moe {
 constexpr int KV8_MAX_CTAS = 160;
 constexpr int KV8_MAX_DEVICES = 64;
 constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one ticket per CTA
+// A query row is brought to [2^13, 2^14) by 2^-e, e within these bounds (any finite bf16 row fits
+// fp16 then, and 2^e times a score scale of ordinary size is a normal number).  The factor
+// of its scores, 2^e times the score scale times the keys' scale, ends at the last: past it the
+// scores themselves leave fp32, and a score of zero stays one.
+constexpr int KV8_Q_MIN_EXP = -120, KV8_Q_MAX_EXP = 115;
+constexpr float KV8_MAX_FACTOR = 0x1p126f;
 
 struct Kv8AttnParams {
   Kv8Cache c;

@@ -347,6 +347,32 @@ def test_prompt_queries_that_are_not_finite_stay_in_their_rows(kv8):
     assert torch.equal(a[keep], b[keep]) and torch.isnan(b[~keep]).all()
 
 
+@pytest.mark.parametrize("new", [1, 4, 90])
+def test_query_of_infinity_makes_its_row_nan_whatever_the_keys(kv8, new):
+    """All scores minus infinity (one sign of keys in the query's infinite dim) are no row of zeros."""
+    s = Setup(kv8, [150], [new], seed=35)
+    s.cache.k[..., 5] = 0x38                     # 1.0 in every key
+    a = s.cache.attention(s.batch, s.q)
+    s.q[new - 1, 3] = 0
+    s.q[new - 1, 3, 5] = -math.inf
+    b = s.cache.attention(s.batch, s.q)
+    keep = torch.ones(new, 16, dtype=torch.bool, device="cuda")
+    keep[new - 1, 3] = False
+    assert torch.equal(a[keep], b[keep]) and torch.isnan(b[~keep]).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 90])
+@pytest.mark.parametrize("gain, key", [(116, -100), (90, -95), (-100, 95), (-126, 118)])
+def test_queries_and_keys_at_opposite_ends_of_the_range(kv8, new, gain, key):
+    """The scores are of ordinary size although neither factor is."""
+    s = Setup(kv8, [150, 90], [new, new], seed=36)
+    s.cache.k_scale[:] = 2.0 ** key
+    s.q[:] = (s.q.double() * 2.0 ** gain).to(torch.bfloat16)
+    scale = 2.0 ** (-8 - gain - key)
+    assert torch.isfinite(s.q).all() and 1e-30 < scale < 1e30
+    s.check_attention(s.cache.attention(s.batch, s.q, scale=scale), scale=scale)
+
+
 @pytest.mark.parametrize("scale", [0.02, 1.5])
 def test_attention_scale(kv8, scale):
     s = Setup(kv8, [300, 33], [1, 1], seed=13, q_gain=0.5)
