@@ -68,7 +68,16 @@ def _ints(x: torch.Tensor, name: str, dim: int, device=None) -> torch.Tensor:
     return x
 
 
-class KV8Batch:
+class _Fixed:
+    """Attributes are set once: the C description made from them would not follow."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{name} is fixed; make a new {type(self).__name__}, or change its tensor in place")
+        self.__dict__[name] = value
+
+
+class KV8Batch(_Fixed):
     """The sequences of a call: ``page_table`` int32 [n_seqs, max_pages], ``lens`` int32
     [n_seqs] (cached positions, the call's tokens among them), ``offsets`` int32
     [n_seqs + 1] (sequence b's tokens are rows offsets[b] .. offsets[b + 1] - 1), and
@@ -93,11 +102,12 @@ class KV8Batch:
             c = GqaKv8Batch(self.page_table.data_ptr(), self.lens.data_ptr(), self.offsets.data_ptr(),
                             self.page_table.shape[0], self.page_table.shape[1], n_tokens, self.max_new)
             ref = ctypes.byref(c)
-            self._c = {n_tokens: ref}
+            self._c.clear()
+            self._c[n_tokens] = ref
         return ref
 
 
-class KV8Cache:
+class KV8Cache(_Fixed):
     """A paged 8-bit cache over caller-owned tensors: ``k``, ``v`` one byte per number
     [n_pages, n_kv_heads, page_size, head_size], ``k_scale``, ``v_scale`` float32
     [n_pages, n_kv_heads, page_size / 16]."""
@@ -210,7 +220,7 @@ class KV8Cache:
             return _abi.gqa_kv8_get_error(self._c)
 
 
-class Rope:
+class Rope(_Fixed):
     """Rotary positions: pair j (elements j and j + rotary / 2 of a head) turns by
     pos[axis(j)] * inv_freq[j].  ``sections`` gives each axis its number of pairs (one axis
     by default); ``cyclic`` deals the pairs out to the axes in turn instead of in runs."""

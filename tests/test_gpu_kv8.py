@@ -593,6 +593,22 @@ def test_refusals(kv8):
 
 
 # ----------------------------------------------------------------------------- together
+def test_what_a_call_describes_cannot_be_replaced(kv8):
+    """A new tensor under an old name would leave the library with the old one's address."""
+    s = Setup(kv8, [20], [1])
+    out = s.cache.attention(s.batch, s.q)
+    for obj, names in ((s.batch, ("page_table", "lens", "offsets", "max_new")), (s.cache, ("k", "v_scale", "error", "fmt")),
+                       (kv8.Rope(), ("plan", "head_size"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(obj, name, getattr(obj, name))
+    s.batch.lens.fill_(10)                       # in place is how they change
+    assert not torch.equal(s.cache.attention(s.batch, s.q), out)
+    s.cache.attention(s.batch, s.q[:0])          # another number of rows, and back
+    s.batch.lens.fill_(20)
+    assert torch.equal(s.cache.attention(s.batch, s.q), out)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_prompt_then_decode(kv8, fmt):
     """As a model uses them: rotary positions, cache write and attention, first two prompts of
