@@ -165,7 +165,7 @@ struct __align__(16) KpPlan {
   int rows[8];           // first code row of each 16-position block (negative: none)
   uint32_t kfac[8];      // factor of each block to the tile's scale, an fp16 pair
   uint32_t vfac[8];
-  int valid;             // positions before the tile's last token's; negative: no more tiles
+  int valid;             // positions up to the tile's last token's, 0 at least; negative: no more tiles
   int pad[7];
 };
 static_assert(sizeof(KpPlan) == 128, "one line of shared memory");
@@ -587,7 +587,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             row = ((pid * p.c.hkv + sg.g) << p.c.page_shift) + (pos & ((1 << p.c.page_shift) - 1));   // below 2^31
             scale = __ldg(p.c.scales[(lane >> 3) & 1] + row / KV8_BLOCK);
           }
-          const int valid = more ? end - u * KP_U : -1;
+          // A sequence with fewer positions than new tokens has units past its end: nothing valid
+          // in them, which is not the mark of the end.
+          const int valid = more ? max(end - u * KP_U, 0) : -1;
           ++u;
           look();                                      // the next tile's pages meanwhile
           const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xFFu;

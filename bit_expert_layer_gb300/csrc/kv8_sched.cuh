@@ -117,7 +117,8 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
-    if (s.bad && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+    // (fewer positions than new tokens: the tokens without one get zeros)
+    if ((s.bad || (s.n > 0 && s.first < 0)) && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
     sum += kv8_units_seq<U, C>(s, p.tq_shift) * p.c.hkv;
     prefix[b] = sum;                       // inside this thread's run for now
   }
@@ -229,7 +230,9 @@ __device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, cons
   kv8_seg_close<C>(g, 0, kv8_units_tile<U, C>(g.s, p.tq_shift, g.t), w, w_end);
 }
 
-// Positions that the tile's last token sees.
+// Positions that the tile's last token sees.  (The tile's units are counted as if the sequence
+// began at position 0 at the latest, so that with fewer positions than new tokens, first < 0, the
+// last units lie past this.)
 __device__ __forceinline__ int kv8_seg_end(const Kv8Seg& g, int tq_shift) {
   return max(g.s.first + min((g.t + 1) << tq_shift, g.s.n), 0);
 }

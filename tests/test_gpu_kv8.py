@@ -677,3 +677,19 @@ def test_captured_decode_step_follows_its_inputs(kv8):
         want, bound = ref.attention(s.table, s.lens, s.offsets, q.double())
         assert ((out.double() - want).abs() <= bound).all()
     assert s.cache.get_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("layout", [(16, 2, 128), (16, 1, 128), (7, 7, 64)], ids=str)
+@pytest.mark.parametrize("n, new", [(100, 400), (0, 2048), (126, 129), (0, 129), (3, 4), (0, 1)])
+def test_fewer_positions_than_new_tokens(kv8, n, new, layout, fmt):
+    """The tokens that stand before position 0 get zeros, the others theirs, the sequences beside
+    them all of theirs, and the length is recorded."""
+    from bit_expert_layer_gb300 import _abi
+    s = Setup(kv8, [300, n, 1000], [new % 40 + 1, new, 70 if new > 8 else 1], layout, 32, fmt, seed=n + new)
+    out = torch.full(s.q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    s.cache.attention(s.batch, s.q, out=out)
+    assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    s.check_attention(out)
+    r0 = int(s.offsets[1])
+    assert (out[r0:r0 + new - n] == 0).all() and (out[r0 + new - n:] != 0).any(-1).all()
