@@ -14,10 +14,11 @@
 //                 consecutive dims of a key, two 16-byte loads.
 //   weights       in base 2, with the value block's scale folded in: w_i = 2^(s_i + e_i - m)
 //                 for values of scale 2^e_i.  The value product takes fp16(w_i) and the bare
-//                 codes, the normaliser sums w_i 2^-e_i in fp32; so the scales cost nothing
-//                 per score.  The reference m moves only when some s_i + e_i outgrows it by
-//                 more than 8: fp16 holds weights up to 2^8 as exactly as smaller ones, and a
-//                 piece that does not move it needs no exchange between lanes.
+//                 codes, the normaliser sums w_i 2^-e_i in fp32 (against a reference of its
+//                 own); so the scales cost nothing per score.  The reference m moves only when
+//                 some s_i + e_i outgrows it by more than 8: fp16 holds weights up to 2^8 as
+//                 exactly as smaller ones, and a piece that does not move it needs no exchange
+//                 between lanes.
 //   O^T += V^T w  a lane takes 16 consecutive dims of 4 keys and interleaves their bytes, so
 //                 that a pair of codes of one dim becomes an fp16 pair; the weights change
 //                 from S's layout to B's by a transposing move.
@@ -48,7 +49,7 @@ __host__ __device__ constexpr int ka_stages(int R) { return R == 8 ? KA_ST8 : KA
 constexpr int KA_COST = 2;                     // a tile's start, in pieces
 __host__ __device__ constexpr int ka_half(int D, int R) { return ka_u(R) * D; }       // bytes of a piece's keys (or values)
 __host__ __device__ constexpr int ka_own(int D, int R) { return ka_stages(R) * 2 * ka_half(D, R); }   // a warp's ring
-__host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, max, sum
+__host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, m, ms, normaliser
 // shared memory: rings (1024-aligned), a part per warp (the tile that began before its run;
 // the tile that goes on after it takes the warp's own ring, which is done by then), the line,
 // what the parts belong to, barriers and words
@@ -108,7 +109,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 
 // One 16-position block of a piece: bad or past the tile's end when scale < 0.
 constexpr float KA_NO_BLOCK = -1.0f;
-constexpr float KA_NO_REF = -1e30f;
 constexpr float KA_GROW = 8.0f;
 
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
@@ -319,12 +319,12 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       }
     }
     const int least = sg.s.first + tok0 + 1;       // positions that every row sees
-    // m: reference of a row's weights (-1e30: none yet); l: this lane's share of the normaliser
-    float m[NB][2], l[NB][2];
+    // references of a row's weights and normaliser; l: this lane's share of the normaliser
+    float m[NB][2], ms[NB][2], l[NB][2];
     float o[NB][NM][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      m[b][0] = m[b][1] = KA_NO_REF;
+      m[b][0] = m[b][1] = ms[b][0] = ms[b][1] = KV8_NO_REF;
       l[b][0] = l[b][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
@@ -370,8 +370,10 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       }
       // ---- s + e - m, masked where a row may not see the whole piece
       const bool masked = u * KA_U + KA_U > least || !live[0] || !live[NK - 1];
-      bool grow = false;
-      float y[NB][NK][4];
+      bool move = false;
+      float y[NB][NK][4], least_e = ve[0];
+#pragma unroll
+      for (int k = 1; k < NK; ++k) least_e = fminf(least_e, ve[k]);
       const auto factor = [&](int b, int k, int i) { return fminf(rs[b][i] * ksc[k], KV8_MAX_FACTOR); };
       const auto hidden = [&](int b, int k, int h, int i) {
         return !live[k] || u * KA_U + 16 * k + 8 * h + g4 >= see[b][i];
@@ -396,27 +398,37 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
               if (hidden(b, k, j >> 1, j & 1)) y[b][k][j] = -INFINITY;
       }
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        move |= fmaxf(m[b][0] - ms[b][0], m[b][1] - ms[b][1]) - least_e > KV8_SUM_TOP;
 #pragma unroll
         for (int k = 0; k < NK; ++k)
-          grow |= fmaxf(fmaxf(y[b][k][0], y[b][k][1]), fmaxf(y[b][k][2], y[b][k][3])) > KA_GROW;
-      if (__any_sync(0xffffffffu, grow)) {
+          move |= fmaxf(fmaxf(y[b][k][0], y[b][k][1]), fmaxf(y[b][k][2], y[b][k][3])) > KA_GROW;
+      }
+      move = __any_sync(0xffffffffu, move);
+      if (move) {
         // the references move to the rows' maxima; what was summed so far follows
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float mx = m[b][i];
+            float mx = m[b][i], bare = ms[b][i];
 #pragma unroll
             for (int k = 0; k < NK; ++k)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (!hidden(b, k, h, i)) mx = fmaxf(mx, fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k]));
+                if (!hidden(b, k, h, i)) {
+                  mx = fmaxf(mx, fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k]));
+                  bare = fmaxf(bare, x[b][k][2 * h + i] * factor(b, k, i));
+                }
 #pragma unroll
-            for (int s = 4; s <= 16; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            for (int s = 4; s <= 16; s <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+              bare = fmaxf(bare, __shfl_xor_sync(0xffffffffu, bare, s));
+            }
             const float corr = ex2(m[b][i] - mx);    // from no reference: 0
+            l[b][i] *= ex2(ms[b][i] - bare);
             m[b][i] = mx;
-            l[b][i] *= corr;
+            ms[b][i] = bare;
 #pragma unroll
             for (int t = 0; t < NM; ++t) {
               o[b][t][i] *= corr;
@@ -425,8 +437,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
 #pragma unroll
             for (int k = 0; k < NK; ++k)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                y[b][k][2 * h + i] = hidden(b, k, h, i) ? -INFINITY : fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k] - mx);
+              for (int h = 0; h < 2; ++h) {
+                float& v = y[b][k][2 * h + i];
+                v = hidden(b, k, h, i) ? -INFINITY : fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k] - mx);
+                l[b][i] += ex2(v + (mx - bare - ve[k]));
+              }
           }
       }
       uint32_t pb[NB][NK][2];         // weights as B: keys 16 k + 8 h + 2 c4 and + 1 of row g4
@@ -437,9 +452,10 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
           float w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = ex2(y[b][k][j]);
-          const float inv = pow2i(-static_cast<int>(ve[k]));
-          l[b][0] = fmaf(w[0] + w[2], inv, l[b][0]);
-          l[b][1] = fmaf(w[1] + w[3], inv, l[b][1]);
+          if (!move) {
+            l[b][0] = fmaf(w[0] + w[2], ex2(m[b][0] - ms[b][0] - ve[k]), l[b][0]);
+            l[b][1] = fmaf(w[1] + w[3], ex2(m[b][1] - ms[b][1] - ve[k]), l[b][1]);
+          }
           pb[b][k][0] = transpose8x8(pack2_f16(w[0], w[1]));
           pb[b][k][1] = transpose8x8(pack2_f16(w[2], w[3]));
         }
@@ -508,6 +524,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         if (whole) {
           if (r < nrows) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw no key: zeros
+            const float unit = ex2(m[b][i] - ms[b][i]);          // of the weights, in the normaliser's
             const int tok = r / p.G, hh = r - tok * p.G;
             __nv_bfloat16* dst =
                 p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + VD * g4;
@@ -516,17 +533,15 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
               uint32_t v[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                v[k] = pack_bf16x2(__float_as_uint(o[b][t + k][i] * inv), __float_as_uint(o[b][t + k][2 + i] * inv));
+                v[k] = pack_bf16x2(__float_as_uint(o[b][t + k][i] * inv * unit),
+                                   __float_as_uint(o[b][t + k][2 + i] * inv * unit));
               *reinterpret_cast<uint4*>(dst + 2 * t) = make_uint4(v[0], v[1], v[2], v[3]);
             }
           }
         } else {
           float* row = (sg.u0 ? heads + warp * R * PS
                               : reinterpret_cast<float*>(smem + warp * OWN)) + r * PS;
-          if (g4 == 0) {
-            row[D] = m[b][i] == KA_NO_REF ? -INFINITY : m[b][i];
-            row[D + 1] = sum;
-          }
+          if (g4 == 0) *reinterpret_cast<float4*>(row + D) = make_float4(m[b][i], ms[b][i], sum, 0.0f);
 #pragma unroll
           for (int t = 0; t < NM; t += 2)
             *reinterpret_cast<float4*>(row + VD * g4 + 2 * t) =
@@ -562,28 +577,29 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       return (i == i0 ? reinterpret_cast<const float*>(smem + i * OWN) : heads + i * R * PS) + row * PS;
     };
     const int i1 = max(i0, 0);
-    float M = -INFINITY, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    float M = KV8_NO_REF, Ms = KV8_NO_REF, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (tid < ACT) {
       // unrolled over all warps, so that the loads do not wait for one another
-      float mw[KA_WARPS], lw2[KA_WARPS];
+      float mw[KA_WARPS], msw[KA_WARPS], lw2[KA_WARPS];
 #pragma unroll
       for (int i = 0; i < KA_WARPS; ++i) {
-        mw[i] = -INFINITY;
+        mw[i] = msw[i] = KV8_NO_REF;
         lw2[i] = 0.0f;
         if (i >= i1 && i <= last) {
-          const float2 v = *reinterpret_cast<const float2*>(part(i) + D);
+          const float4 v = *reinterpret_cast<const float4*>(part(i) + D);
           mw[i] = v.x;
-          lw2[i] = v.y;
+          msw[i] = v.y;
+          lw2[i] = v.z;
         }
         M = fmaxf(M, mw[i]);
+        Ms = fmaxf(Ms, msw[i]);
       }
-      const float at = M == -INFINITY ? 0.0f : M;
 #pragma unroll
       for (int i = 0; i < KA_WARPS; ++i) {
         if (i < i1 || i > last) continue;
         const float4 v0 = *reinterpret_cast<const float4*>(part(i) + d0), v1 = *reinterpret_cast<const float4*>(part(i) + d0 + 4);
-        const float f = ex2(mw[i] - at);
-        L = fmaf(f, lw2[i], L);
+        const float f = ex2(mw[i] - M);
+        L = fmaf(ex2(msw[i] - Ms), lw2[i], L);
         O[0] = fmaf(f, v0.x, O[0]), O[1] = fmaf(f, v0.y, O[1]), O[2] = fmaf(f, v0.z, O[2]), O[3] = fmaf(f, v0.w, O[3]);
         O[4] = fmaf(f, v1.x, O[4]), O[5] = fmaf(f, v1.y, O[5]), O[6] = fmaf(f, v1.z, O[6]), O[7] = fmaf(f, v1.w, O[7]);
       }
@@ -595,7 +611,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         float* dst = slot(cta);
         *reinterpret_cast<float4*>(dst + d0) = make_float4(O[0], O[1], O[2], O[3]);
         *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(O[4], O[5], O[6], O[7]);
-        if (d0 == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, L);
+        if (d0 == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(M, Ms, L, 0.0f);
       }
       __syncthreads();
       const int ns = c_last - c_first + 1;
@@ -614,24 +630,32 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         if (tid < ACT) {
           const int j0 = tid % TPR;
           constexpr int PER = (KV8_MAX_CTAS + TPR - 1) / TPR;
-          float2 ml[PER];
-          M = -INFINITY;
+          float ml[PER], msl[PER], ll[PER];
+          M = Ms = KV8_NO_REF;
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             const int i = j0 + k * TPR;
-            ml[k] = i < ns ? __ldcg(reinterpret_cast<const float2*>(slot(c_first + i) + D)) : make_float2(-INFINITY, 0.0f);
+            ml[k] = msl[k] = KV8_NO_REF;
+            ll[k] = 0.0f;
+            if (i < ns) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(c_first + i) + D));
+              ml[k] = v.x;
+              msl[k] = v.y;
+              ll[k] = v.z;
+            }
           }
 #pragma unroll
-          for (int k = 0; k < PER; ++k) M = fmaxf(M, ml[k].x);
+          for (int k = 0; k < PER; ++k) M = fmaxf(M, ml[k]), Ms = fmaxf(Ms, msl[k]);
 #pragma unroll
-          for (int s = TPR / 2; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-          const float at = M == -INFINITY ? 0.0f : M;
+          for (int s = TPR / 2; s >= 1; s >>= 1) {
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+            Ms = fmaxf(Ms, __shfl_xor_sync(0xffffffffu, Ms, s));
+          }
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             const int i = j0 + k * TPR;
-            const float f = ex2(ml[k].x - at);
-            L = fmaf(f, ml[k].y, L);
-            if (i < ns) fs[row * ns + i] = f;
+            L = fmaf(ex2(msl[k] - Ms), ll[k], L);
+            if (i < ns) fs[row * ns + i] = ex2(ml[k] - M);
           }
 #pragma unroll
           for (int s = TPR / 2; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
@@ -654,12 +678,13 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     const int tok0 = pt.t << p.tq_shift;
     if (write && tid < ACT && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
+      const float unit = ex2(M - Ms);
       const int tok = row / p.G, hh = row - tok * p.G;
       uint4 r;
-      r.x = pack_bf16x2(__float_as_uint(O[0] * inv), __float_as_uint(O[1] * inv));
-      r.y = pack_bf16x2(__float_as_uint(O[2] * inv), __float_as_uint(O[3] * inv));
-      r.z = pack_bf16x2(__float_as_uint(O[4] * inv), __float_as_uint(O[5] * inv));
-      r.w = pack_bf16x2(__float_as_uint(O[6] * inv), __float_as_uint(O[7] * inv));
+      r.x = pack_bf16x2(__float_as_uint(O[0] * inv * unit), __float_as_uint(O[1] * inv * unit));
+      r.y = pack_bf16x2(__float_as_uint(O[2] * inv * unit), __float_as_uint(O[3] * inv * unit));
+      r.z = pack_bf16x2(__float_as_uint(O[4] * inv * unit), __float_as_uint(O[5] * inv * unit));
+      r.w = pack_bf16x2(__float_as_uint(O[6] * inv * unit), __float_as_uint(O[7] * inv * unit));
       *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(pt.off + tok0 + tok) * p.hq + pt.g * p.G + hh) * D + d0) = r;
     }
   }

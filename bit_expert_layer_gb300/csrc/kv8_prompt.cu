@@ -14,9 +14,9 @@
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
 //   softmax      in base 2 with the scale 2^e of the tile's values folded in, as in the decode
-//                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^-e in fp32.  (Dequantising
-//                brings a tile's blocks to one scale for the keys and one for the values, so that
-//                no score needs a factor of its own block's.)  The reference m moves only when the
+//                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^(m - ms - e) in fp32.
+//                (Dequantising brings a tile's blocks to one scale for the keys and one for the
+//                values, so that no score needs a factor of its own block's.)  m moves only when the
 //                maximum has grown by more than 2^8: until then weights up to 2^8 fit fp16 as
 //                exactly as smaller ones, and O in TMEM needs no rescaling.  fp16(w) goes back to
 //                TMEM over S.
@@ -118,6 +118,12 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+// Four columns.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -128,6 +134,22 @@ __device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// A row's normaliser terms of one tile by themselves, in units of 2^ms.  (Rarely needed, and a
+// function of its own with few instructions: with its loop in the softmax's, the compiler's
+// registers for that one moved, and a piece of 2048 tokens over 31000 positions took 430 to
+// 470 us instead of 392.)
+__device__ __noinline__ float kp_bare_sum(uint32_t t_s, float f, float ms) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < KP_U; c += 4) {
+    uint32_t x[4];
+    tmem_ld4(t_s + c, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += ex2(fmaf(__uint_as_float(x[j]), f, -ms));
+  }
+  return sum;
 }
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
@@ -197,7 +219,7 @@ struct __align__(16) KpTile {
   int pad[3];
 };
 
-// Workspace of a part: floats of a row (O, reference, normaliser), the rows of CTA c's part of
+// Workspace of a part: floats of a row (O, references, normaliser), the rows of CTA c's part of
 // a tile that began in CTA c_first, and the tiles to join, one entry per CTA.
 __host__ __device__ constexpr int kp_ps(int D) { return D + 8; }      // 32-byte rows
 constexpr size_t KP_TILES_BYTES = KV8_MAX_CTAS * sizeof(KpTile);
@@ -220,7 +242,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   uint8_t* s_q = smem;
   uint8_t* s_k = smem + 2 * TILE;
   uint8_t* s_v = smem + 4 * TILE;
-  // per tile {K scale, e, 2^-e of its V scale 2^e, blocks without a page (bits)}
+  // per tile {K scale, e of its V scale 2^e, nothing, blocks without a page (bits)}
   float4* s_scale = reinterpret_cast<float4*>(smem + 6 * TILE);
   KpPlan* s_plan = reinterpret_cast<KpPlan*>(s_scale + KP_SLOTS);
   float* s_rs = reinterpret_cast<float*>(s_plan + KP_PLANS);       // [256] factor of a query row's scores
@@ -340,7 +362,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
         const float rs = s_rs[blk * KP_ROWS + r];
 
-        float m_ref = -INFINITY, l = 0.0f;
+        float m_ref = KV8_NO_REF, ms_ref = KV8_NO_REF, l = 0.0f;   // references of the weights and of the normaliser
 #pragma unroll 1
         for (int u = sg.u0; u < sg.u1; ++u, ++it) {
           wait(BAR_S + blk, it);
@@ -391,14 +413,23 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             for (int j = 0; j < 3; ++j) m[j] = max3(m[j], m[3 + j], m[6 + j]);
             mx = max3(mx, max3(m[0], m[1], m[2]), m[9]);
           }
-          mx = fmaf(mx, f, e);
-          // ---- the reference moves: O and the normaliser follow
-          const bool grow = mx > m_ref + KP_GROW;                // also the first finite maximum
-          if (__any_sync(0xffffffffu, grow)) {
-            const float m_new = grow ? mx : m_ref;
-            const float corr = grow ? ex2(m_ref - m_new) : 1.0f;   // -inf - finite: 0
+          // ---- the references move: O and the normaliser follow
+          const bool move = fmaf(mx, f, e) > m_ref + KP_GROW || m_ref - ms_ref - e > KV8_SUM_TOP;
+          bool wide = false;
+          if (__any_sync(0xffffffffu, move)) {
+            tmem_ld_wait();                                      // sc[0], pass 2's first
+            const float m_new = move ? fmaxf(m_ref, fmaf(mx, f, e)) : m_ref;
+            const float ms_new = move ? fmaxf(ms_ref, mx * f) : ms_ref;
+            const float corr = ex2(m_ref - m_new);               // from no reference: 0
+            l *= ex2(ms_ref - ms_new);
             m_ref = m_new;
-            l *= corr;
+            ms_ref = ms_new;
+            wide = m_ref - ms_ref - e > KV8_SUM_TOP;
+            if (__any_sync(0xffffffffu, wide)) {
+              // the normaliser's terms by themselves
+              const float sum = kp_bare_sum(t_s, f, ms_ref);
+              if (wide) l += sum;
+            }
             if (u > sg.u0) {
               wait(BAR_PV + blk, it - 1);
               if (dead) continue;
@@ -414,10 +445,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
               }
             }
           }
-          const float m_at = m_ref == -INFINITY ? 0.0f : m_ref;
           // ---- pass 2: weights, over the scores that were read
           {
-            const float add = e - m_at;
+            const float add = e - m_ref, to_sum = wide ? 0.0f : ex2(m_ref - ms_ref - e);
             const uint64_t f2 = f32x2(f, f), a2 = f32x2(add, add);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -436,7 +466,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
               tmem_st16(t_s + 16 * c, w16);
             }
             const float2 t = f32x2_get(add2(sum[0], sum[1]));
-            l = fmaf(t.x + t.y, sc4.z, l);
+            l = fmaf(t.x + t.y, to_sum, l);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -448,6 +478,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         tc_fence_after();
         const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // a row that saw no key: zeros
+        const float unit = ex2(m_ref - ms_ref);                  // of the weights, in the normaliser's
         __nv_bfloat16* dst =
             live ? p.out + (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh) * D : nullptr;
         const int2 own = whole ? make_int2(cta, cta) : kv8_owners<KP_COST>(sg, w - sg.len, runs);
@@ -465,8 +496,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                   x[k] = l == 0.0f ? 0u
-                                   : pack_bf16x2(__float_as_uint(__uint_as_float(o[j + 2 * k]) * inv),
-                                                 __float_as_uint(__uint_as_float(o[j + 2 * k + 1]) * inv));
+                                   : pack_bf16x2(__float_as_uint(__uint_as_float(o[j + 2 * k]) * inv * unit),
+                                                 __float_as_uint(__uint_as_float(o[j + 2 * k + 1]) * inv * unit));
                 if (p.out_wide) {
                   st_global_v8(dst + 32 * c + j, x);
                 } else {
@@ -481,7 +512,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         }
         tc_fence_before();
         if (!whole) {
-          *reinterpret_cast<float2*>(part + D) = make_float2(m_ref, l);
+          *reinterpret_cast<float4*>(part + D) = make_float4(m_ref, ms_ref, l, 0.0f);
           if (tid == 0 && own.x == cta)
             kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
@@ -613,7 +644,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           } else if (lane == 16) {
             plan->valid = valid;
             s_scale[it & (KP_SLOTS - 1)] =
-                make_float4(pow2i(kt - HEAD), static_cast<float>(vt - HEAD), pow2i(HEAD - vt), __uint_as_float(bads));
+                make_float4(pow2i(kt - HEAD), static_cast<float>(vt - HEAD), 0.0f, __uint_as_float(bads));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_LF + slot));
@@ -732,7 +763,7 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
   if (tb >= blk_tokens || tok >= tl.n) return;
   constexpr int PL = D / 32;                    // dims per lane
   const auto slot = [&](int i) { return kp_slot<D>(p.part, c0 + i, c0, row); };
-  float M = -INFINITY, L = 0.0f, O[PL];
+  float M = KV8_NO_REF, Ms = KV8_NO_REF, L = 0.0f, O[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) O[k] = 0.0f;
   const auto fetch = [&](int i, float (&v)[PL]) {
@@ -744,44 +775,56 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
   };
   if (tl.ns <= KP_FEW) {
     // few parts (tiles of a long prompt): all loads at once
-    float2 ml[KP_FEW];
+    float ml[KP_FEW], msl[KP_FEW], ll[KP_FEW];
     float v[KP_FEW][PL];
 #pragma unroll
     for (int i = 0; i < KP_FEW; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.0f);
+      ml[i] = msl[i] = KV8_NO_REF;
       if (i < tl.ns) {
-        ml[i] = *reinterpret_cast<const float2*>(slot(i) + D);
+        const float4 r = *reinterpret_cast<const float4*>(slot(i) + D);
+        ml[i] = r.x;
+        msl[i] = r.y;
+        ll[i] = r.z;
         fetch(i, v[i]);
       }
-      M = fmaxf(M, ml[i].x);
+      M = fmaxf(M, ml[i]);
+      Ms = fmaxf(Ms, msl[i]);
     }
-    const float at = M == -INFINITY ? 0.0f : M;
 #pragma unroll
     for (int i = 0; i < KP_FEW; ++i) {
       if (i >= tl.ns) break;
-      const float f = ex2(ml[i].x - at);
-      L = fmaf(f, ml[i].y, L);
+      const float f = ex2(ml[i] - M);
+      L = fmaf(ex2(msl[i] - Ms), ll[i], L);
 #pragma unroll
       for (int k = 0; k < PL; ++k) O[k] = fmaf(f, v[i][k], O[k]);
     }
   } else {
     // many (few query rows over a long cache): lane i keeps the weights of parts i, i + 32, ...
     constexpr int PER = (KV8_MAX_CTAS + 31) / 32;
-    float2 ml[PER];
-    float wt[PER];
+    float wt[PER], msl[PER], ll[PER];             // wt: references until they are weights
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int i = lane + 32 * k;
-      ml[k] = i < tl.ns ? *reinterpret_cast<const float2*>(slot(i) + D) : make_float2(-INFINITY, 0.0f);
-      M = fmaxf(M, ml[k].x);
+      wt[k] = msl[k] = KV8_NO_REF;
+      ll[k] = 0.0f;
+      if (i < tl.ns) {
+        const float4 r = *reinterpret_cast<const float4*>(slot(i) + D);
+        wt[k] = r.x;
+        msl[k] = r.y;
+        ll[k] = r.z;
+      }
+      M = fmaxf(M, wt[k]);
+      Ms = fmaxf(Ms, msl[k]);
     }
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-    const float at = M == -INFINITY ? 0.0f : M;
+    for (int s = 16; s >= 1; s >>= 1) {
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+      Ms = fmaxf(Ms, __shfl_xor_sync(0xffffffffu, Ms, s));
+    }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      wt[k] = ex2(ml[k].x - at);
-      L = fmaf(wt[k], ml[k].y, L);
+      wt[k] = ex2(wt[k] - M);
+      L = fmaf(ex2(msl[k] - Ms), ll[k], L);
     }
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
@@ -799,10 +842,12 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
     }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
+  const float unit = ex2(M - Ms);
   __nv_bfloat16* dst = p.out + (static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G) * D + PL * lane;
 #pragma unroll
   for (int k = 0; k < PL; k += 2)
-    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2(__float_as_uint(O[k] * inv), __float_as_uint(O[k + 1] * inv));
+    *reinterpret_cast<uint32_t*>(dst + k) =
+        pack_bf16x2(__float_as_uint(O[k] * inv * unit), __float_as_uint(O[k + 1] * inv * unit));
 }
 
 // ---------------------------------------------------------------- host side

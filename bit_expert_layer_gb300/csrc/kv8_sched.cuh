@@ -35,6 +35,15 @@ constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one tic
 // scores themselves leave fp32, and a score of zero stays one.
 constexpr int KV8_Q_MIN_EXP = -120, KV8_Q_MAX_EXP = 115;
 constexpr float KV8_MAX_FACTOR = 0x1p126f;
+// A row keeps two references: m for its weights w_i = 2^(s_i + e_i - m), which carry the scale
+// 2^e_i of the value's block, and ms for its normaliser sum_i 2^(s_i - ms), which must not:
+// blocks of zeros have the smallest scale there is, 2^-100, and in units of the weights their
+// share of the normaliser passes fp32 after some thousand positions.  A term of the normaliser
+// is w_i 2^(m - ms - e_i) as long as that factor's exponent is at most KV8_SUM_TOP, so that terms
+// stay under 2^72 and 2^24 of them in range; else the references move first, and the terms are
+// exponentials of their own.
+constexpr float KV8_SUM_TOP = 64.0f;
+constexpr float KV8_NO_REF = -1e30f;       // no score so far
 
 struct Kv8AttnParams {
   Kv8Cache c;

@@ -693,3 +693,81 @@ def test_fewer_positions_than_new_tokens(kv8, n, new, layout, fmt):
     s.check_attention(out)
     r0 = int(s.offsets[1])
     assert (out[r0:r0 + new - n] == 0).all() and (out[r0 + new - n:] != 0).any(-1).all()
+
+
+def one_row(s, b, h, q, scale=None):
+    """(p, v, e) float64: weights, values and value-scale exponents of query q [d] of head h over all
+    positions of sequence b, by the definition."""
+    n = s.lens[b]
+    k, v, vs = s.ref().values(s.table[b], n)
+    g = h // (s.hq // s.hkv)
+    return torch.softmax(k[:, g] @ q.double() * (scale or 1 / math.sqrt(s.d)), 0), v[:, g], vs[:, g].log2()
+
+
+def shared_pages(kv8, n, seqs, new, layout, fmt, seed, page=64):
+    """One cached sequence of n positions, read by `seqs` sequences of `new` new tokens each: so many
+    tiles that a single run of work holds (nearly) all positions of a row."""
+    one = Setup(kv8, [n], [1], layout, page, fmt, seed=seed)
+    s = Setup(kv8, [n] * 2, [new] * 2, layout, page, fmt, seed=seed, n_pages=2 * -(-n // page))
+    s.cache, s.n_pages = one.cache, one.n_pages
+    s.lens, s.new = [n] * seqs, [new] * seqs
+    s.table = np.tile(one.table, (seqs, 1))
+    s.offsets = np.arange(seqs + 1) * new
+    s.t = seqs * new
+    s.q = torch.randn(s.t, s.hq, s.d, generator=s.g, device="cuda").to(torch.bfloat16)
+    s.batch = kv8.KV8Batch(ints(s.table), ints(s.lens), ints(s.offsets), max_new=new)
+    return s
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("seqs, new, layout", [(152, 5, (8, 1, 128)), (608, 1, (16, 2, 128)), (608, 2, (16, 2, 64)),
+                                               (1, 1, (16, 2, 128)), (1, 90, (16, 2, 64))])
+def test_long_runs_of_zero_values(kv8, seqs, new, layout, fmt):
+    """36 thousand positions whose values are all zero (the smallest scale there is), scored 2^7.9
+    above the first ones, and 500 others after them with as high a score: the rows' sums of weights
+    pass no range.  Of sum_i p_i |v_i|: 2^-11 for the weights, the scores' 2^-22 (8 + 128) twice,
+    2^-21 twice for the exponential, 2^-23 (36500 / 128 + 64) for fp32 sums, all under 2^-10; and one
+    rounding."""
+    n, last = 36500, 500
+    s = shared_pages(kv8, n, seqs, new, layout, fmt, 40)
+    c = s.cache
+    pos = torch.arange(n, device="cuda")
+    pg, at = torch.tensor(s.table[0], device="cuda").long()[pos // 64], pos % 64
+    c.k.zero_()
+    c.k[pg[128:], :, at[128:], 0] = 0x38 if fmt == "e4m3" else 1          # 1
+    c.k_scale.fill_(1)
+    zero = (n - last) // 16 * 16
+    c.v[pg[:zero], :, at[:zero]] = 0
+    c.v_scale[pg[:zero:16], :, at[:zero:16] // 16] = 2.0 ** -100
+    s.q.zero_()
+    s.q[:, :, 0] = 1
+    scale = 7.9 * math.log(2)
+    out = c.attention(s.batch, s.q, scale=scale).double()
+    for g in range(s.hkv):
+        h = g * s.hq // s.hkv
+        p, v, _ = one_row(s, 0, h, s.q[0, h], scale)
+        for i in range(new):
+            w = p.clone()
+            w[n - new + i + 1:] = 0
+            w /= w.sum()
+            want, mag = w @ v, w @ v.abs()
+            assert ((out[i::new, h] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag).all()
+    assert c.get_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("new", [1, 4, 90])
+@pytest.mark.parametrize("unit", [16, 128])
+@pytest.mark.parametrize("low, high", [(-100, 60), (-100, 115), (-60, 20), (-100, 0)])
+def test_zero_values_beside_large_ones(kv8, new, low, high, unit, fmt):
+    """Every second 16 (or 128) positions have values of zero and the smallest scales, the others
+    large ones: the zeros' weights count in full."""
+    s = Setup(kv8, [700, 130], [new, new], (16, 2, 128), 16, fmt, seed=41, q_gain=1.0)
+    c = s.cache
+    c.v_scale[:] = 2.0 ** high
+    for b, n in enumerate(s.lens):
+        for i in range(0, n, 16):
+            if i // unit % 2 == 0:
+                c.v[int(s.table[b, i // 16])] = 0
+                c.v_scale[int(s.table[b, i // 16])] = 2.0 ** low
+    s.check_attention(c.attention(s.batch, s.q))
