@@ -13,12 +13,11 @@
 //                 of two to fit.  The order of the contraction is free, so a lane takes 32
 //                 consecutive dims of a key, two 16-byte loads.
 //   weights       in base 2, with the value block's scale folded in: w_i = 2^(s_i + e_i - m)
-//                 for values of scale 2^e_i.  The value product takes fp16(w_i) and the bare
-//                 codes, the normaliser sums w_i 2^-e_i in fp32 (against a reference of its
-//                 own); so the scales cost nothing per score.  The reference m moves only when
-//                 some s_i + e_i outgrows it by more than 8: fp16 holds weights up to 2^8 as
-//                 exactly as smaller ones, and a piece that does not move it needs no exchange
-//                 between lanes.
+//                 for values of scale 2^e_i, m = ms + d.  The value product takes fp16(w_i) and
+//                 the bare codes, the normaliser sums w_i 2^(d - e_i) in fp32; so the scales
+//                 cost nothing per score.  The references move only when some s_i + e_i
+//                 outgrows m by more than 8: fp16 holds weights up to 2^8 as exactly as smaller
+//                 ones, and a piece that does not move them needs no exchange between lanes.
 //   O^T += V^T w  a lane takes 16 consecutive dims of 4 keys and interleaves their bytes, so
 //                 that a pair of codes of one dim becomes an fp16 pair; the weights change
 //                 from S's layout to B's by a transposing move.
@@ -49,7 +48,7 @@ __host__ __device__ constexpr int ka_stages(int R) { return R == 8 ? KA_ST8 : KA
 constexpr int KA_COST = 2;                     // a tile's start, in pieces
 __host__ __device__ constexpr int ka_half(int D, int R) { return ka_u(R) * D; }       // bytes of a piece's keys (or values)
 __host__ __device__ constexpr int ka_own(int D, int R) { return ka_stages(R) * 2 * ka_half(D, R); }   // a warp's ring
-__host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, m, ms, normaliser
+__host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // floats of a partial row: O, references, normaliser
 // shared memory: rings (1024-aligned), a part per warp (the tile that began before its run;
 // the tile that goes on after it takes the warp's own ring, which is done by then), the line,
 // what the parts belong to, barriers and words
@@ -290,7 +289,9 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     for (int b = 0; b < NB; ++b) {
       const int r = g4 + 8 * b;
       const uint4* v = qv[b];
-      const int sees = r < nrows ? sg.s.first + tok0 + r / p.G + 1 : 0;
+      // (a row without a token has zeros for a query and sees all there is, so that it gets references
+      // with the others; with none to see, it would have moved them at every piece)
+      const int sees = r < nrows ? sg.s.first + tok0 + r / p.G + 1 : end;
       uint32_t big2 = 0;
 #pragma unroll
       for (int i = 0; i < LD / 8; ++i) {
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       // down to 2^-28 of it.  What is not finite makes the whole row NaN.
       const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, KV8_Q_MIN_EXP), KV8_Q_MAX_EXP);
       const float f = big >= 0x7F80u ? NAN : pow2i(-e);
-      const float rf = fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
+      const float rf = big >= 0x7F80u ? NAN : fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const uint32_t* x = &v[j >> 1].x + (j & 1) * 2;
@@ -320,12 +321,15 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     }
     const int least = sg.s.first + tok0 + 1;       // positions that every row sees
     // references of a row's weights and normaliser; l: this lane's share of the normaliser
-    float m[NB][2], ms[NB][2], l[NB][2];
+    float d[NB][2], ms[NB][2], l[NB][2];
     float o[NB][NM][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      m[b][0] = m[b][1] = ms[b][0] = ms[b][1] = KV8_NO_REF;
-      l[b][0] = l[b][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ms[b][i] = rs[b][i] == rs[b][i] ? KV8_NO_REF : 0.0f;   // a row of NaN moves no references
+        d[b][i] = l[b][i] = 0.0f;
+      }
 #pragma unroll
       for (int i = 0; i < NM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
     }
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         for (int k = 0; k < NK; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float f = factor(b, k, i), add = ve[k] - m[b][i];
+            const float f = factor(b, k, i), add = ve[k] - (ms[b][i] + d[b][i]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) y[b][k][2 * h + i] = fmaf(x[b][k][2 * h + i], f, add);
           }
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        move |= fmaxf(m[b][0] - ms[b][0], m[b][1] - ms[b][1]) - least_e > KV8_SUM_TOP;
+        move |= fmaxf(d[b][0], d[b][1]) - least_e > KV8_SUM_TOP || fmaxf(fabsf(ms[b][0]), fabsf(ms[b][1])) >= KV8_FAR;
 #pragma unroll
         for (int k = 0; k < NK; ++k)
           move |= fmaxf(fmaxf(y[b][k][0], y[b][k][1]), fmaxf(y[b][k][2], y[b][k][3])) > KA_GROW;
@@ -411,24 +415,25 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float mx = m[b][i], bare = ms[b][i];
+            float sv[NK][2], at = ms[b][i], top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < NK; ++k)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (!hidden(b, k, h, i)) {
-                  mx = fmaxf(mx, fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k]));
-                  bare = fmaxf(bare, x[b][k][2 * h + i] * factor(b, k, i));
-                }
+              for (int h = 0; h < 2; ++h) {
+                sv[k][h] = hidden(b, k, h, i) ? -INFINITY : kv8_end(x[b][k][2 * h + i] * factor(b, k, i));
+                at = fmaxf(at, sv[k][h]);
+              }
 #pragma unroll
-            for (int s = 4; s <= 16; s <<= 1) {
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-              bare = fmaxf(bare, __shfl_xor_sync(0xffffffffu, bare, s));
-            }
-            const float corr = ex2(m[b][i] - mx);    // from no reference: 0
-            l[b][i] *= ex2(ms[b][i] - bare);
-            m[b][i] = mx;
-            ms[b][i] = bare;
+            for (int s = 4; s <= 16; s <<= 1) at = fmaxf(at, __shfl_xor_sync(0xffffffffu, at, s));
+#pragma unroll
+            for (int k = 0; k < NK; ++k) top = fmaxf(top, fmaxf(sv[k][0], sv[k][1]) - at + ve[k]);
+#pragma unroll
+            for (int s = 4; s <= 16; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            const float was = d[b][i] + (ms[b][i] - at);     // d in units of the new ms
+            const float to = fmaxf(was, top), corr = ex2(was - to);    // from no reference: 0
+            l[b][i] *= ex2(ms[b][i] - at);
+            ms[b][i] = at;
+            d[b][i] = to;
 #pragma unroll
             for (int t = 0; t < NM; ++t) {
               o[b][t][i] *= corr;
@@ -438,27 +443,31 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
             for (int k = 0; k < NK; ++k)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                float& v = y[b][k][2 * h + i];
-                v = hidden(b, k, h, i) ? -INFINITY : fmaf(x[b][k][2 * h + i], factor(b, k, i), ve[k] - mx);
-                l[b][i] += ex2(v + (mx - bare - ve[k]));
+                y[b][k][2 * h + i] = sv[k][h] - at + (ve[k] - to);
+                l[b][i] += ex2(sv[k][h] - at);
               }
           }
       }
       uint32_t pb[NB][NK][2];         // weights as B: keys 16 k + 8 h + 2 c4 and + 1 of row g4
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        float sum[2] = {0.0f, 0.0f};    // of this piece, as if d were 0
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
           float w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = ex2(y[b][k][j]);
-          if (!move) {
-            l[b][0] = fmaf(w[0] + w[2], ex2(m[b][0] - ms[b][0] - ve[k]), l[b][0]);
-            l[b][1] = fmaf(w[1] + w[3], ex2(m[b][1] - ms[b][1] - ve[k]), l[b][1]);
-          }
+          const float inv = pow2i(-static_cast<int>(ve[k]));
+          sum[0] = fmaf(w[0] + w[2], inv, sum[0]);
+          sum[1] = fmaf(w[1] + w[3], inv, sum[1]);
           pb[b][k][0] = transpose8x8(pack2_f16(w[0], w[1]));
           pb[b][k][1] = transpose8x8(pack2_f16(w[2], w[3]));
         }
+        if (!move) {
+          l[b][0] = fmaf(sum[0], ex2(d[b][0]), l[b][0]);
+          l[b][1] = fmaf(sum[1], ex2(d[b][1]), l[b][1]);
+        }
+      }
       // ---- O^T += V^T w, 16 keys a step; rows past the tile's end are not looked at
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         if (whole) {
           if (r < nrows) {
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw no key: zeros
-            const float unit = ex2(m[b][i] - ms[b][i]);          // of the weights, in the normaliser's
+            const float unit = ex2(d[b][i]);                     // of the weights, in the normaliser's
             const int tok = r / p.G, hh = r - tok * p.G;
             __nv_bfloat16* dst =
                 p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + VD * g4;
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         } else {
           float* row = (sg.u0 ? heads + warp * R * PS
                               : reinterpret_cast<float*>(smem + warp * OWN)) + r * PS;
-          if (g4 == 0) *reinterpret_cast<float4*>(row + D) = make_float4(m[b][i], ms[b][i], sum, 0.0f);
+          if (g4 == 0) *reinterpret_cast<float4*>(row + D) = make_float4(ms[b][i], d[b][i], sum, 0.0f);
 #pragma unroll
           for (int t = 0; t < NM; t += 2)
             *reinterpret_cast<float4*>(row + VD * g4 + 2 * t) =
@@ -577,29 +586,31 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       return (i == i0 ? reinterpret_cast<const float*>(smem + i * OWN) : heads + i * R * PS) + row * PS;
     };
     const int i1 = max(i0, 0);
-    float M = KV8_NO_REF, Ms = KV8_NO_REF, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    float M = KV8_NO_REF, top = -INFINITY, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};   // references ms and d
     if (tid < ACT) {
       // unrolled over all warps, so that the loads do not wait for one another
-      float mw[KA_WARPS], msw[KA_WARPS], lw2[KA_WARPS];
+      float mw[KA_WARPS], dw[KA_WARPS], lw2[KA_WARPS];
 #pragma unroll
       for (int i = 0; i < KA_WARPS; ++i) {
-        mw[i] = msw[i] = KV8_NO_REF;
-        lw2[i] = 0.0f;
+        mw[i] = KV8_NO_REF;
+        dw[i] = lw2[i] = 0.0f;
         if (i >= i1 && i <= last) {
           const float4 v = *reinterpret_cast<const float4*>(part(i) + D);
           mw[i] = v.x;
-          msw[i] = v.y;
+          dw[i] = v.y;
           lw2[i] = v.z;
         }
         M = fmaxf(M, mw[i]);
-        Ms = fmaxf(Ms, msw[i]);
       }
+#pragma unroll
+      for (int i = 0; i < KA_WARPS; ++i)
+        if (i >= i1 && i <= last) top = fmaxf(top, mw[i] - M + dw[i]);
 #pragma unroll
       for (int i = 0; i < KA_WARPS; ++i) {
         if (i < i1 || i > last) continue;
         const float4 v0 = *reinterpret_cast<const float4*>(part(i) + d0), v1 = *reinterpret_cast<const float4*>(part(i) + d0 + 4);
-        const float f = ex2(mw[i] - M);
-        L = fmaf(ex2(msw[i] - Ms), lw2[i], L);
+        const float f = ex2(mw[i] - M + dw[i] - top);
+        L = fmaf(ex2(mw[i] - M), lw2[i], L);
         O[0] = fmaf(f, v0.x, O[0]), O[1] = fmaf(f, v0.y, O[1]), O[2] = fmaf(f, v0.z, O[2]), O[3] = fmaf(f, v0.w, O[3]);
         O[4] = fmaf(f, v1.x, O[4]), O[5] = fmaf(f, v1.y, O[5]), O[6] = fmaf(f, v1.z, O[6]), O[7] = fmaf(f, v1.w, O[7]);
       }
@@ -611,7 +622,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         float* dst = slot(cta);
         *reinterpret_cast<float4*>(dst + d0) = make_float4(O[0], O[1], O[2], O[3]);
         *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(O[4], O[5], O[6], O[7]);
-        if (d0 == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(M, Ms, L, 0.0f);
+        if (d0 == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(M, top, L, 0.0f);
       }
       __syncthreads();
       const int ns = c_last - c_first + 1;
@@ -630,32 +641,38 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         if (tid < ACT) {
           const int j0 = tid % TPR;
           constexpr int PER = (KV8_MAX_CTAS + TPR - 1) / TPR;
-          float ml[PER], msl[PER], ll[PER];
-          M = Ms = KV8_NO_REF;
+          float ml[PER], dl[PER], ll[PER];
+          M = KV8_NO_REF;
+          top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             const int i = j0 + k * TPR;
-            ml[k] = msl[k] = KV8_NO_REF;
+            ml[k] = KV8_NO_REF;
+            dl[k] = -INFINITY;
             ll[k] = 0.0f;
             if (i < ns) {
               const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(c_first + i) + D));
               ml[k] = v.x;
-              msl[k] = v.y;
+              dl[k] = v.y;
               ll[k] = v.z;
             }
           }
 #pragma unroll
-          for (int k = 0; k < PER; ++k) M = fmaxf(M, ml[k]), Ms = fmaxf(Ms, msl[k]);
+          for (int k = 0; k < PER; ++k) M = fmaxf(M, ml[k]);
 #pragma unroll
-          for (int s = TPR / 2; s >= 1; s >>= 1) {
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-            Ms = fmaxf(Ms, __shfl_xor_sync(0xffffffffu, Ms, s));
+          for (int s = TPR / 2; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            L = fmaf(ex2(ml[k] - M), ll[k], L);
+            dl[k] += ml[k] - M;
+            top = fmaxf(top, dl[k]);
           }
+#pragma unroll
+          for (int s = TPR / 2; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
             const int i = j0 + k * TPR;
-            L = fmaf(ex2(msl[k] - Ms), ll[k], L);
-            if (i < ns) fs[row * ns + i] = ex2(ml[k] - M);
+            if (i < ns) fs[row * ns + i] = ex2(dl[k] - top);
           }
 #pragma unroll
           for (int s = TPR / 2; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
@@ -678,7 +695,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     const int tok0 = pt.t << p.tq_shift;
     if (write && tid < ACT && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
-      const float unit = ex2(M - Ms);
+      const float unit = ex2(top);
       const int tok = row / p.G, hh = row - tok * p.G;
       uint4 r;
       r.x = pack_bf16x2(__float_as_uint(O[0] * inv * unit), __float_as_uint(O[1] * inv * unit));

@@ -14,7 +14,7 @@
 //   S = Q K^T    both operands in shared memory.  fp16 holds every code exactly, and a query
 //                row is scaled by a power of two to fit, so the products are exact.
 //   softmax      in base 2 with the scale 2^e of the tile's values folded in, as in the decode
-//                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^(m - ms - e) in fp32.
+//                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^(d - e) in fp32 (m = ms + d).
 //                (Dequantising brings a tile's blocks to one scale for the keys and one for the
 //                values, so that no score needs a factor of its own block's.)  m moves only when the
 //                maximum has grown by more than 2^8: until then weights up to 2^8 fit fp16 as
@@ -59,7 +59,7 @@ __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 4 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128;
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 8 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128;
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
 
@@ -124,6 +124,11 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -134,22 +139,6 @@ __device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-// A row's normaliser terms of one tile by themselves, in units of 2^ms.  (Rarely needed, and a
-// function of its own with few instructions: with its loop in the softmax's, the compiler's
-// registers for that one moved, and a piece of 2048 tokens over 31000 positions took 430 to
-// 470 us instead of 392.)
-__device__ __noinline__ float kp_bare_sum(uint32_t t_s, float f, float ms) {
-  float sum = 0.0f;
-#pragma unroll 1
-  for (int c = 0; c < KP_U; c += 4) {
-    uint32_t x[4];
-    tmem_ld4(t_s + c, x);
-    tmem_ld_wait();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum += ex2(fmaf(__uint_as_float(x[j]), f, -ms));
-  }
-  return sum;
 }
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
@@ -181,6 +170,37 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// Two steps that few tiles need, functions of their own with few instructions (with the first's
+// loop inside the softmax's, the compiler's registers for that one moved, and a piece of 2048
+// tokens over 31000 positions took 430 to 470 us instead of 392).
+// The sum of a row's terms 2^(f x + add) of one tile.
+__device__ __noinline__ float kp_bare_sum(uint32_t t_s, float f, float add) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < KP_U; c += 4) {
+    uint32_t x[4];
+    tmem_ld4(t_s + c, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += ex2(fmaf(__uint_as_float(x[j]), f, add));
+  }
+  return sum;
+}
+// The rows whose scores lie past KV8_FAR: in the scores' place what f makes of them rounded and
+// relative to `ms`.  What a row does not see stays -inf.
+__device__ __noinline__ void kp_far_scores(uint32_t t_s, float f, float ms, bool far) {
+#pragma unroll 1
+  for (int c = 0; c < KP_U; c += 4) {
+    uint32_t x[4];
+    tmem_ld4(t_s + c, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (far && x[j] != 0xFF800000u) x[j] = __float_as_uint((kv8_end(__uint_as_float(x[j]) * f) - ms) / f);
+    tmem_st4(t_s + c, x);
+  }
+  tmem_st_wait();
 }
 // A tile's codes, as the dequantising warps need to know them.
 struct __align__(16) KpPlan {
@@ -246,7 +266,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   float4* s_scale = reinterpret_cast<float4*>(smem + 6 * TILE);
   KpPlan* s_plan = reinterpret_cast<KpPlan*>(s_scale + KP_SLOTS);
   float* s_rs = reinterpret_cast<float*>(s_plan + KP_PLANS);       // [256] factor of a query row's scores
-  long long* prefix = reinterpret_cast<long long*>(s_rs + 2 * KP_ROWS);
+  float* s_ms = s_rs + 2 * KP_ROWS;                                // [256] a row's reference, while it is far or none
+  long long* prefix = reinterpret_cast<long long*>(s_ms + 2 * KP_ROWS);
   long long* s_warp = prefix + p.b.n_seqs + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
@@ -352,7 +373,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll
               for (int j = 0; j < 4; ++j) x[j] = pack2h(bf16lo(x[j]) * f, bf16hi(x[j]) * f);
               *reinterpret_cast<uint4*>(s_q + blk * TILE + (qc >> 3) * BOX + r2 * 128 + (((qc & 7) ^ (r2 & 7)) << 4)) = v[i];
-              if (qc == 0) s_rs[blk * KP_ROWS + r2] = fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
+              if (qc == 0) s_rs[blk * KP_ROWS + r2] = big >= 0x7F80u ? NAN : fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
             }
           }
         }
@@ -362,7 +383,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
         const float rs = s_rs[blk * KP_ROWS + r];
 
-        float m_ref = KV8_NO_REF, ms_ref = KV8_NO_REF, l = 0.0f;   // references of the weights and of the normaliser
+        // m_ref is ms + d.  Where the scores are far, or none has been seen, it is d alone; ms lies in
+        // s_ms then, and in its place minus infinity, which no tile passes by.
+        float m_ref = 0.0f, ms_ref = rs == rs ? -INFINITY : 0.0f, l = 0.0f;   // a row of NaN moves nothing
+        s_ms[tid] = KV8_NO_REF;
 #pragma unroll 1
         for (int u = sg.u0; u < sg.u1; ++u, ++it) {
           wait(BAR_S + blk, it);
@@ -414,21 +438,25 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             mx = max3(mx, max3(m[0], m[1], m[2]), m[9]);
           }
           // ---- the references move: O and the normaliser follow
-          const bool move = fmaf(mx, f, e) > m_ref + KP_GROW || m_ref - ms_ref - e > KV8_SUM_TOP;
+          const bool move = fmaf(mx, f, e - m_ref) > KP_GROW || m_ref - ms_ref - e > KV8_SUM_TOP;
           bool wide = false;
           if (__any_sync(0xffffffffu, move)) {
-            tmem_ld_wait();                                      // sc[0], pass 2's first
-            const float m_new = move ? fmaxf(m_ref, fmaf(mx, f, e)) : m_ref;
-            const float ms_new = move ? fmaxf(ms_ref, mx * f) : ms_ref;
-            const float corr = ex2(m_ref - m_new);               // from no reference: 0
-            l *= ex2(ms_ref - ms_new);
-            m_ref = m_new;
-            ms_ref = ms_new;
-            wide = m_ref - ms_ref - e > KV8_SUM_TOP;
+            tmem_ld_wait();                                      // no load is under way across the calls below
+            const float s_max = move ? kv8_end(mx * f) : KV8_NO_REF;
+            const float ms = ms_ref == -INFINITY ? s_ms[tid] : ms_ref, ms_new = fmaxf(ms, s_max);
+            const float was = (ms_ref == -INFINITY ? m_ref : m_ref - ms) + (ms - ms_new);     // d in units of the new ms
+            const float d = move ? fmaxf(was, s_max - ms_new + e) : was, corr = ex2(was - d);   // from no reference: 0
+            l *= ex2(ms - ms_new);
+            const bool far = fabsf(ms_new) >= KV8_FAR;
+            m_ref = far ? d : move ? ms_new + d : m_ref;
+            ms_ref = far ? -INFINITY : ms_new;
+            s_ms[tid] = ms_new;
+            wide = d - e > KV8_SUM_TOP || far;
             if (__any_sync(0xffffffffu, wide)) {
-              // the normaliser's terms by themselves
-              const float sum = kp_bare_sum(t_s, f, ms_ref);
+              kp_far_scores(t_s, f, ms_new, far);
+              const float sum = kp_bare_sum(t_s, f, far ? 0.0f : -ms_new);
               if (wide) l += sum;
+              tmem_ld32(t_s, sc[0]);                             // pass 2's first, again
             }
             if (u > sg.u0) {
               wait(BAR_PV + blk, it - 1);
@@ -478,7 +506,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         tc_fence_after();
         const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // a row that saw no key: zeros
-        const float unit = ex2(m_ref - ms_ref);                  // of the weights, in the normaliser's
+        const float ms = ms_ref == -INFINITY ? s_ms[tid] : ms_ref;
+        const float d = ms_ref == -INFINITY ? m_ref : m_ref - ms;
+        const float unit = ex2(d);                               // of the weights, in the normaliser's
         __nv_bfloat16* dst =
             live ? p.out + (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh) * D : nullptr;
         const int2 own = whole ? make_int2(cta, cta) : kv8_owners<KP_COST>(sg, w - sg.len, runs);
@@ -512,7 +542,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         }
         tc_fence_before();
         if (!whole) {
-          *reinterpret_cast<float4*>(part + D) = make_float4(m_ref, ms_ref, l, 0.0f);
+          *reinterpret_cast<float4*>(part + D) = make_float4(ms, d, l, 0.0f);
           if (tid == 0 && own.x == cta)
             kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
         }
@@ -763,7 +793,7 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
   if (tb >= blk_tokens || tok >= tl.n) return;
   constexpr int PL = D / 32;                    // dims per lane
   const auto slot = [&](int i) { return kp_slot<D>(p.part, c0 + i, c0, row); };
-  float M = KV8_NO_REF, Ms = KV8_NO_REF, L = 0.0f, O[PL];
+  float M = KV8_NO_REF, top = -INFINITY, L = 0.0f, O[PL];           // references ms and d of the whole
 #pragma unroll
   for (int k = 0; k < PL; ++k) O[k] = 0.0f;
   const auto fetch = [&](int i, float (&v)[PL]) {
@@ -775,57 +805,61 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
   };
   if (tl.ns <= KP_FEW) {
     // few parts (tiles of a long prompt): all loads at once
-    float ml[KP_FEW], msl[KP_FEW], ll[KP_FEW];
+    float ml[KP_FEW], dl[KP_FEW], ll[KP_FEW];
     float v[KP_FEW][PL];
 #pragma unroll
     for (int i = 0; i < KP_FEW; ++i) {
-      ml[i] = msl[i] = KV8_NO_REF;
+      ml[i] = KV8_NO_REF;
+      dl[i] = -INFINITY;
       if (i < tl.ns) {
         const float4 r = *reinterpret_cast<const float4*>(slot(i) + D);
         ml[i] = r.x;
-        msl[i] = r.y;
+        dl[i] = r.y;
         ll[i] = r.z;
         fetch(i, v[i]);
       }
       M = fmaxf(M, ml[i]);
-      Ms = fmaxf(Ms, msl[i]);
     }
+#pragma unroll
+    for (int i = 0; i < KP_FEW; ++i) top = fmaxf(top, ml[i] - M + dl[i]);
 #pragma unroll
     for (int i = 0; i < KP_FEW; ++i) {
       if (i >= tl.ns) break;
-      const float f = ex2(ml[i] - M);
-      L = fmaf(ex2(msl[i] - Ms), ll[i], L);
+      const float f = ex2(ml[i] - M + dl[i] - top);
+      L = fmaf(ex2(ml[i] - M), ll[i], L);
 #pragma unroll
       for (int k = 0; k < PL; ++k) O[k] = fmaf(f, v[i][k], O[k]);
     }
   } else {
     // many (few query rows over a long cache): lane i keeps the weights of parts i, i + 32, ...
     constexpr int PER = (KV8_MAX_CTAS + 31) / 32;
-    float wt[PER], msl[PER], ll[PER];             // wt: references until they are weights
+    float wt[PER], ml[PER], ll[PER];              // wt: d until it is the weight
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int i = lane + 32 * k;
-      wt[k] = msl[k] = KV8_NO_REF;
+      ml[k] = KV8_NO_REF;
+      wt[k] = -INFINITY;
       ll[k] = 0.0f;
       if (i < tl.ns) {
         const float4 r = *reinterpret_cast<const float4*>(slot(i) + D);
-        wt[k] = r.x;
-        msl[k] = r.y;
+        ml[k] = r.x;
+        wt[k] = r.y;
         ll[k] = r.z;
       }
-      M = fmaxf(M, wt[k]);
-      Ms = fmaxf(Ms, msl[k]);
+      M = fmaxf(M, ml[k]);
     }
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) {
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-      Ms = fmaxf(Ms, __shfl_xor_sync(0xffffffffu, Ms, s));
-    }
+    for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      wt[k] = ex2(wt[k] - M);
-      L = fmaf(ex2(msl[k] - Ms), ll[k], L);
+      L = fmaf(ex2(ml[k] - M), ll[k], L);
+      wt[k] += ml[k] - M;
+      top = fmaxf(top, wt[k]);
     }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+#pragma unroll
+    for (int k = 0; k < PER; ++k) wt[k] = ex2(wt[k] - top);
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
 #pragma unroll
@@ -842,7 +876,7 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
     }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
-  const float unit = ex2(M - Ms);
+  const float unit = ex2(top);
   __nv_bfloat16* dst = p.out + (static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G) * D + PL * lane;
 #pragma unroll
   for (int k = 0; k < PL; k += 2)

@@ -35,15 +35,27 @@ constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one tic
 // scores themselves leave fp32, and a score of zero stays one.
 constexpr int KV8_Q_MIN_EXP = -120, KV8_Q_MAX_EXP = 115;
 constexpr float KV8_MAX_FACTOR = 0x1p126f;
-// A row keeps two references: m for its weights w_i = 2^(s_i + e_i - m), which carry the scale
-// 2^e_i of the value's block, and ms for its normaliser sum_i 2^(s_i - ms), which must not:
-// blocks of zeros have the smallest scale there is, 2^-100, and in units of the weights their
-// share of the normaliser passes fp32 after some thousand positions.  A term of the normaliser
-// is w_i 2^(m - ms - e_i) as long as that factor's exponent is at most KV8_SUM_TOP, so that terms
-// stay under 2^72 and 2^24 of them in range; else the references move first, and the terms are
+// A row's references: ms, the largest score so far, and d.  Its weights are
+//   w_i = 2^(s_i - ms + e_i - d), 2^e_i being the scale of the value's block,
+// and its normaliser is sum_i 2^(s_i - ms), which must not carry the scales: blocks of zeros
+// have the smallest one there is, 2^-100, and in units of the weights their share of the
+// normaliser passes fp32 after some thousand positions.  A term of the normaliser is
+// w_i 2^(d - e_i) as long as that exponent is at most KV8_SUM_TOP, so that terms stay under
+// 2^72 and 2^24 of them in range; else the references move first, and the terms are
 // exponentials of their own.
 constexpr float KV8_SUM_TOP = 64.0f;
-constexpr float KV8_NO_REF = -1e30f;       // no score so far
+// Scores are products rounded once with the references in one multiply-add.  Past KV8_FAR the
+// part of the product that rounding would have cut off is itself worth powers of two, so that
+// there, and where no score has been seen yet, the score is rounded first.  One past fp32's
+// range counts as its largest number.
+constexpr float KV8_FAR = 0x1p20f;
+constexpr float KV8_NO_REF = -0x1.fffffep127f;
+__device__ __forceinline__ float kv8_end(float s) {      // NaN stays
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(s), "f"(KV8_NO_REF));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-KV8_NO_REF));
+  return r;
+}
 
 struct Kv8AttnParams {
   Kv8Cache c;

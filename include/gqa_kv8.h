@@ -107,14 +107,15 @@ size_t gqa_kv8_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int 
  *   workspace  256-byte aligned; two calls that overlap in time need two
  * The products are exact, sums, maxima and the softmax are fp32, its weights are rounded to
  * fp16 for the value product only, and o is rounded once.  The normaliser counts every
- * weight in full, whatever the scale of its values.  Exactness ends where scales lie very
- * far apart: among 128 consecutive positions a block whose scale is under 2^-21 of the
- * largest loses low bits of its codes.  A token that sees no position (its sequence has
- * fewer positions than new tokens, which is recorded as a bad length) gets
- * zeros; a query that is not finite makes its own row NaN and no other.  Between 1 and 16
- * query heads per key/value head.  Results do not depend on timing: the same call gives the
- * same bits.  max_new decides the kernel (one for at most 32 query rows per key/value head,
- * one for more), so a bound that is far too large is right but slow.
+ * weight in full, whatever the scale of its values.  Scores may have any size; one that is
+ * past fp32's range (in units of log2) counts as its largest number.  Exactness ends where
+ * scales lie very far apart: among 128 consecutive positions a block whose scale is under
+ * 2^-21 of the largest loses low bits of its codes.  A token that sees no position (its
+ * sequence has fewer positions than new tokens, which is recorded as a bad length) gets
+ * zeros; a query that is not finite makes its own row NaN and no other.
+ * Between 1 and 16 query heads per key/value head.  Results do not depend on timing: the
+ * same call gives the same bits.  max_new decides the kernel (one for at most 32 query rows
+ * per key/value head, one for more), so a bound that is far too large is right but slow.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED (heads), CUDA. */
 moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch, const void* q,
                                long long q_stride, int n_q_heads, float scale, void* out, void* workspace,

@@ -771,3 +771,36 @@ def test_zero_values_beside_large_ones(kv8, new, low, high, unit, fmt):
                 c.v[int(s.table[b, i // 16])] = 0
                 c.v_scale[int(s.table[b, i // 16])] = 2.0 ** low
     s.check_attention(c.attention(s.batch, s.q))
+
+
+@pytest.mark.parametrize("new", [1, 4, 90])
+@pytest.mark.parametrize("score", [2.0 ** 20, 2.0 ** 28, 1e31, 3e38, 1e45, -2.0 ** 20, -2.0 ** 28, -1e31, -3e38, -1e45])
+def test_scores_of_any_size(kv8, new, score):
+    """Equal scores of any size, past fp32's range too, are equal weights; one that is larger by an
+    eighth has all the weight.  2^-10 of sum_i p_i |v_i| and one rounding, as for ordinary scores."""
+    s = Setup(kv8, [1000, 200, new], [new] * 3, seed=42)
+    c = s.cache
+    c.k.zero_()
+    c.k[..., 0] = 0x38                                   # 1, next: 1.125
+    e = 0 if abs(score) < 1e30 else 60
+    c.k_scale.fill_(2.0 ** e)
+    s.q.zero_()
+    s.q[:, :, 0] = math.copysign(2.0 ** e, score)
+    scale = float(np.float32(abs(score) / 4.0 ** e))
+    a = c.attention(s.batch, s.q, scale=scale).double()
+    at = 64 + 37                                         # of the second sequence
+    c.k[int(s.table[1, 1]), :, 37, 0] = 0x39 if score > 0 else 0x37
+    b = c.attention(s.batch, s.q, scale=scale).double()
+    for j in range(3):
+        v = s.ref().values(s.table[j], s.lens[j])[1]
+        for i in range(new):
+            see = s.lens[j] - new + i + 1
+            r = int(s.offsets[j]) + i
+            for h in (0, 9):
+                x = v[:see, h // 8]
+                want, mag = x.mean(0), x.abs().mean(0)
+                assert ((a[r, h] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag).all()
+                if j == 1 and see > at and abs(score) < 3e38:
+                    want, mag = x[at], x[at].abs()
+                assert ((b[r, h] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag).all()
+    assert c.get_error() == 0
