@@ -15,9 +15,9 @@
 //   weights       in base 2, with the value block's scale folded in: w_i = 2^(s_i + e_i - m)
 //                 for values of scale 2^e_i, m = ms + d.  The value product takes fp16(w_i) and
 //                 the bare codes, the normaliser sums w_i 2^(d - e_i) in fp32; so the scales
-//                 cost nothing per score.  The references move only when some s_i + e_i
-//                 outgrows m by more than 8: fp16 holds weights up to 2^8 as exactly as smaller
-//                 ones, and a piece that does not move them needs no exchange between lanes.
+//                 cost nothing per score.  The references move only when a row's weights pass
+//                 fp16's range at either end, and a piece that does not move them needs little
+//                 exchange between lanes.
 //   O^T += V^T w  a lane takes 16 consecutive dims of 4 keys and interleaves their bytes, so
 //                 that a pair of codes of one dim becomes an fp16 pair; the weights change
 //                 from S's layout to B's by a transposing move.
@@ -56,7 +56,7 @@ __host__ __device__ constexpr int ka_parts(int D, int R) { return ka_warps(R) * 
 __host__ __device__ constexpr int ka_wsum(int R) { return R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
 __host__ __device__ constexpr int ka_smem(int D, int R, int B) {
   return 1024 + ka_warps(R) * ka_own(D, R) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 +
-         ka_warps(R) * (8 + ka_stages(R) * 8 + 2 * 32) + 64;
+         ka_warps(R) * (8 + ka_stages(R) * 8 + 2 * 32 + R * 4) + 64;
 }
 static_assert(ka_smem(128, 16, KV8_MAX_SEQS) <= 232448 && ka_smem(128, 8, KV8_MAX_SEQS) <= 232448,
               "shared memory per CTA exceeds 227 KB");
@@ -108,7 +108,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 
 // One 16-position block of a piece: bad or past the tile's end when scale < 0.
 constexpr float KA_NO_BLOCK = -1.0f;
-constexpr float KA_GROW = 8.0f;
+constexpr float KA_LOW = -9.0f;                // 32 positions: 32 * 2^-25 = 2^-11 2^-9
 
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   uint64_t p;
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(meta + 2 * KA_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + KA_WARPS * KA_STAGES);
   int* s_last = const_cast<int*>(abort_flag) + 1;
+  float* s_peak = reinterpret_cast<float*>(s_last + 1) + (threadIdx.x >> 5) * R;   // [R] the highest ms + d of a row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * OWN;
@@ -323,12 +324,15 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     // references of a row's weights and normaliser; l: this lane's share of the normaliser
     float d[NB][2], ms[NB][2], l[NB][2];
     float o[NB][NM][4];
+    float reach = -INFINITY;          // the largest d of the lane's rows; infinite where scores are far or none was seen
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         ms[b][i] = rs[b][i] == rs[b][i] ? KV8_NO_REF : 0.0f;   // a row of NaN moves no references
+        if (rs[b][i] == rs[b][i]) reach = INFINITY;
         d[b][i] = l[b][i] = 0.0f;
+        s_peak[8 * b + 2 * c4 + i] = KV8_NO_REF;               // by each lane for itself
       }
 #pragma unroll
       for (int i = 0; i < NM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
@@ -374,7 +378,6 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       }
       // ---- s + e - m, masked where a row may not see the whole piece
       const bool masked = u * KA_U + KA_U > least || !live[0] || !live[NK - 1];
-      bool move = false;
       float y[NB][NK][4], least_e = ve[0];
 #pragma unroll
       for (int k = 1; k < NK; ++k) least_e = fminf(least_e, ve[k]);
@@ -401,15 +404,22 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
             for (int j = 0; j < 4; ++j)
               if (hidden(b, k, j >> 1, j & 1)) y[b][k][j] = -INFINITY;
       }
+      bool move = reach - least_e > KV8_SUM_TOP;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        move |= fmaxf(d[b][0], d[b][1]) - least_e > KV8_SUM_TOP || fmaxf(fabsf(ms[b][0]), fabsf(ms[b][1])) >= KV8_FAR;
 #pragma unroll
-        for (int k = 0; k < NK; ++k)
-          move |= fmaxf(fmaxf(y[b][k][0], y[b][k][1]), fmaxf(y[b][k][2], y[b][k][3])) > KA_GROW;
+        for (int i = 0; i < 2; ++i) {
+          float mx = fmaxf(y[b][0][i], y[b][0][2 + i]);
+#pragma unroll
+          for (int k = 1; k < NK; ++k) mx = fmaxf(mx, fmaxf(y[b][k][i], y[b][k][2 + i]));
+          // too large for fp16, or too small in all lanes of the row
+          const bool low = (__ballot_sync(0xffffffffu, mx >= KA_LOW) & (0x11111111u << c4)) == 0;
+          move |= mx > KV8_W_TOP || (low && mx > KV8_W_LOST);
+        }
       }
       move = __any_sync(0xffffffffu, move);
       if (move) {
+        reach = -INFINITY;
         // the references move to the rows' maxima; what was summed so far follows
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -430,7 +440,12 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
 #pragma unroll
             for (int s = 4; s <= 16; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             const float was = d[b][i] + (ms[b][i] - at);     // d in units of the new ms
-            const float to = fmaxf(was, top), corr = ex2(was - to);    // from no reference: 0
+            float& peak = s_peak[8 * b + 2 * c4 + i];
+            float to = fmaxf(was, top - KV8_W_FIRST);
+            if (kv8_down(top, was, KA_LOW, at, peak)) to = top - KV8_W_FIRST;
+            peak = fmaxf(peak, at + to);
+            reach = fmaxf(reach, fabsf(at) < KV8_FAR ? to : INFINITY);
+            const float corr = ex2(was - to);                // from no reference: 0
             l[b][i] *= ex2(ms[b][i] - at);
             ms[b][i] = at;
             d[b][i] = to;

@@ -16,10 +16,9 @@
 //   softmax      in base 2 with the scale 2^e of the tile's values folded in, as in the decode
 //                kernel: w_i = 2^(s_i + e - m), normaliser sum w_i 2^(d - e) in fp32 (m = ms + d).
 //                (Dequantising brings a tile's blocks to one scale for the keys and one for the
-//                values, so that no score needs a factor of its own block's.)  m moves only when the
-//                maximum has grown by more than 2^8: until then weights up to 2^8 fit fp16 as
-//                exactly as smaller ones, and O in TMEM needs no rescaling.  fp16(w) goes back to
-//                TMEM over S.
+//                values, so that no score needs a factor of its own block's.)  m moves only when a
+//                row's weights pass fp16's range at either end; until then O in TMEM needs no
+//                rescaling.  fp16(w) goes back to TMEM over S.
 //   O += w V     w from TMEM, V from shared memory, its rows as they are (N-major operand)
 // The two row blocks alternate: while one is in its softmax the tensor cores work for the
 // other (order of issue: PV of block 0, next QK of block 0, PV of block 1, next QK of block 1).
@@ -50,7 +49,7 @@ constexpr int KP_ROWS = 128;                      // query rows per block
 constexpr int KP_SLOTS = 8;                       // tiles whose scales the softmax can ask for
 constexpr int KP_PLANS = 4;                       // tiles planned ahead
 constexpr int KP_FEW = 4;                         // parts of a tile that a join loads at once
-constexpr float KP_GROW = 8.0f;                   // the maximum may outgrow the reference by 2^8
+constexpr float KP_LOW = -7.0f;                   // 128 positions: 128 * 2^-25 = 2^-11 2^-7
 // Blocks of a tile are brought to the tile's largest scale in fp16, 2^head on top of it: the
 // largest code (448; for int8 the offset 1152 of its conversion) lands just under fp16's
 // largest number, and a block whose scale is down to 2^-21 of the tile's largest keeps every
@@ -59,7 +58,7 @@ __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 8 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128;
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 12 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128;
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
 
@@ -171,9 +170,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// Two steps that few tiles need, functions of their own with few instructions (with the first's
-// loop inside the softmax's, the compiler's registers for that one moved, and a piece of 2048
-// tokens over 31000 positions took 430 to 470 us instead of 392).
+// The softmax's steps that few tiles need are functions of their own: with them inside its loop a
+// piece of 2048 tokens over 31000 positions took between 392 and 475 us, as the compiler's
+// registers for the loop fell out, with changing inputs up to 486; now 395 and 402.
+//
+// What a row does not see of a tile becomes -inf: positions from `left` on, blocks of `bad`.
+__device__ __noinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad) {
+  uint32_t x[32];
+#pragma unroll 1
+  for (int c = 0; c < KP_U / 32; ++c) {
+    tmem_ld32(t_s + 32 * c, x);
+    const int n = left - 32 * c;
+    uint32_t seen = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+    if ((bad >> (2 * c)) & 1) seen &= 0xFFFF0000u;
+    if ((bad >> (2 * c + 1)) & 1) seen &= 0x0000FFFFu;
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!(seen & (1u << j))) x[j] = 0xFF800000u;
+    tmem_st32(t_s + 32 * c, x);
+  }
+  tmem_st_wait();
+}
 // The sum of a row's terms 2^(f x + add) of one tile.
 __device__ __noinline__ float kp_bare_sum(uint32_t t_s, float f, float add) {
   float sum = 0.0f;
@@ -201,6 +219,31 @@ __device__ __noinline__ void kp_far_scores(uint32_t t_s, float f, float ms, bool
     tmem_st4(t_s + c, x);
   }
   tmem_st_wait();
+}
+// The references move in the rows with `move` (m_ref and ms_ref as the softmax keeps them, ms and
+// the peak in shared memory), and a tile whose weights give no terms of the normaliser adds those
+// by themselves.  Returns m_ref, ms_ref, the normaliser, and what O is to be multiplied by.
+__device__ __noinline__ float4 kp_refs(uint32_t t_s, float mx, float f, float e, float m_ref, float ms_ref, float l,
+                                       float* s_ms, float* s_peak, bool move) {
+  const float s_max = move ? kv8_end(mx * f) : KV8_NO_REF;
+  const float ms = ms_ref == -INFINITY ? *s_ms : ms_ref, ms_new = fmaxf(ms, s_max);
+  const float was = (ms_ref == -INFINITY ? m_ref : m_ref - ms) + (ms - ms_new);     // d in units of the new ms
+  const float top = s_max - ms_new + e;
+  const bool far = fabsf(ms_new) >= KV8_FAR;
+  float d = was;
+  if (move) d = kv8_down(top, was, KP_LOW, ms_new, *s_peak) ? top - KV8_W_FIRST : fmaxf(was, top - KV8_W_FIRST);
+  *s_peak = fmaxf(*s_peak, ms_new + d);
+  l *= ex2(ms - ms_new);
+  m_ref = far ? d : move ? ms_new + d : m_ref;
+  ms_ref = far ? -INFINITY : ms_new;
+  *s_ms = ms_new;
+  const bool wide = d - e > KV8_SUM_TOP || far;
+  if (__any_sync(0xffffffffu, wide)) {
+    kp_far_scores(t_s, f, ms_new, far);
+    const float sum = kp_bare_sum(t_s, f, far ? 0.0f : -ms_new);
+    if (wide) l += sum;
+  }
+  return make_float4(m_ref, ms_ref, l, ex2(was - d));   // from no reference: 0
 }
 // A tile's codes, as the dequantising warps need to know them.
 struct __align__(16) KpPlan {
@@ -267,7 +310,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   KpPlan* s_plan = reinterpret_cast<KpPlan*>(s_scale + KP_SLOTS);
   float* s_rs = reinterpret_cast<float*>(s_plan + KP_PLANS);       // [256] factor of a query row's scores
   float* s_ms = s_rs + 2 * KP_ROWS;                                // [256] a row's reference, while it is far or none
-  long long* prefix = reinterpret_cast<long long*>(s_ms + 2 * KP_ROWS);
+  float* s_peak = s_ms + 2 * KP_ROWS;                              // [256] the highest ms + d of a row
+  long long* prefix = reinterpret_cast<long long*>(s_peak + 2 * KP_ROWS);
   long long* s_warp = prefix + p.b.n_seqs + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
@@ -386,7 +430,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         // m_ref is ms + d.  Where the scores are far, or none has been seen, it is d alone; ms lies in
         // s_ms then, and in its place minus infinity, which no tile passes by.
         float m_ref = 0.0f, ms_ref = rs == rs ? -INFINITY : 0.0f, l = 0.0f;   // a row of NaN moves nothing
-        s_ms[tid] = KV8_NO_REF;
+        s_ms[tid] = s_peak[tid] = KV8_NO_REF;
 #pragma unroll 1
         for (int u = sg.u0; u < sg.u1; ++u, ++it) {
           wait(BAR_S + blk, it);
@@ -400,22 +444,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           // A tile at the causal edge, or with a page missing: what the row does not see becomes
           // -inf in TMEM first, so that the passes below carry no mask (with it in them, the
           // compiler masked every tile: 767 us against 557).
-          if (__any_sync(0xffffffffu, left < KP_U) || bad) {
-#pragma unroll 1
-            for (int c = 0; c < KP_U / 32; ++c) {
-              tmem_ld32(t_s + 32 * c, sc[0]);
-              const int n = left - 32 * c;
-              uint32_t seen = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
-              if ((bad >> (2 * c)) & 1) seen &= 0xFFFF0000u;
-              if ((bad >> (2 * c + 1)) & 1) seen &= 0x0000FFFFu;
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(seen & (1u << j))) sc[0][j] = 0xFF800000u;
-              tmem_st32(t_s + 32 * c, sc[0]);
-            }
-            tmem_st_wait();
-          }
+          if (__any_sync(0xffffffffu, left < KP_U) || bad) kp_mask(t_s, left, bad);
           // The scores are read twice, 32 columns at a time, the next ones while these are worked
           // on: 128 of them in registers do not fit beside the rest.  (One pass against the
           // reference of the tiles before, the weights waiting in registers until all scores are
@@ -438,26 +467,17 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
             mx = max3(mx, max3(m[0], m[1], m[2]), m[9]);
           }
           // ---- the references move: O and the normaliser follow
-          const bool move = fmaf(mx, f, e - m_ref) > KP_GROW || m_ref - ms_ref - e > KV8_SUM_TOP;
-          bool wide = false;
+          const float w_max = fmaf(mx, f, e - m_ref);            // the largest weight's exponent
+          const bool move = w_max > KV8_W_TOP || (w_max < KP_LOW && w_max > KV8_W_LOST) ||
+                            m_ref - ms_ref - e > KV8_SUM_TOP;
           if (__any_sync(0xffffffffu, move)) {
             tmem_ld_wait();                                      // no load is under way across the calls below
-            const float s_max = move ? kv8_end(mx * f) : KV8_NO_REF;
-            const float ms = ms_ref == -INFINITY ? s_ms[tid] : ms_ref, ms_new = fmaxf(ms, s_max);
-            const float was = (ms_ref == -INFINITY ? m_ref : m_ref - ms) + (ms - ms_new);     // d in units of the new ms
-            const float d = move ? fmaxf(was, s_max - ms_new + e) : was, corr = ex2(was - d);   // from no reference: 0
-            l *= ex2(ms - ms_new);
-            const bool far = fabsf(ms_new) >= KV8_FAR;
-            m_ref = far ? d : move ? ms_new + d : m_ref;
-            ms_ref = far ? -INFINITY : ms_new;
-            s_ms[tid] = ms_new;
-            wide = d - e > KV8_SUM_TOP || far;
-            if (__any_sync(0xffffffffu, wide)) {
-              kp_far_scores(t_s, f, ms_new, far);
-              const float sum = kp_bare_sum(t_s, f, far ? 0.0f : -ms_new);
-              if (wide) l += sum;
-              tmem_ld32(t_s, sc[0]);                             // pass 2's first, again
-            }
+            const float4 r = kp_refs(t_s, mx, f, e, m_ref, ms_ref, l, s_ms + tid, s_peak + tid, move);
+            m_ref = r.x;
+            ms_ref = r.y;
+            l = r.z;
+            const float corr = r.w;
+            tmem_ld32(t_s, sc[0]);                               // pass 2's first, again
             if (u > sg.u0) {
               wait(BAR_PV + blk, it - 1);
               if (dead) continue;
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           }
           // ---- pass 2: weights, over the scores that were read
           {
-            const float add = e - m_ref, to_sum = wide ? 0.0f : ex2(m_ref - ms_ref - e);
+            const float add = e - m_ref;
             const uint64_t f2 = f32x2(f, f), a2 = f32x2(add, add);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -494,7 +514,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
               tmem_st16(t_s + 16 * c, w16);
             }
             const float2 t = f32x2_get(add2(sum[0], sum[1]));
-            l = fmaf(t.x + t.y, to_sum, l);
+            const float unit = m_ref - ms_ref - e;               // of the weights, in the terms'
+            if (unit <= KV8_SUM_TOP)                             // else kp_refs has added them
+              l = fmaf(t.x + t.y, ex2(unit), l);
           }
           tmem_st_wait();
           tc_fence_before();

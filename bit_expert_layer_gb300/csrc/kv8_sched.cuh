@@ -41,7 +41,7 @@ constexpr float KV8_MAX_FACTOR = 0x1p126f;
 // have the smallest one there is, 2^-100, and in units of the weights their share of the
 // normaliser passes fp32 after some thousand positions.  A term of the normaliser is
 // w_i 2^(d - e_i) as long as that exponent is at most KV8_SUM_TOP, so that terms stay under
-// 2^72 and 2^24 of them in range; else the references move first, and the terms are
+// 2^80 and 2^24 of them in range; else the references move first, and the terms are
 // exponentials of their own.
 constexpr float KV8_SUM_TOP = 64.0f;
 // Scores are products rounded once with the references in one multiply-add.  Past KV8_FAR the
@@ -55,6 +55,23 @@ __device__ __forceinline__ float kv8_end(float s) {      // NaN stays
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(s), "f"(KV8_NO_REF));
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-KV8_NO_REF));
   return r;
+}
+// The value product takes the weights in fp16, which holds 11 bits of them from 2^-14 to 2^16.
+// Where the references move, the largest weight of the positions at hand becomes 2^KV8_W_FIRST; they
+// move again when one passes 2^KV8_W_TOP, and also when the largest is below a bound (LOW: chosen
+// by the kernels, so that what subnormal weights lose, 2^-25 each, is under 2^-11 of the largest
+// one of theirs).  Without the latter a single position with nearly all the weight (and, as such
+// positions have it, a value near zero) would cost the others their bits: 32 thousand positions
+// with 0.1 % of the weight came out 33 % off.  A row's unit comes no further down than
+// 2^-KV8_W_SPAN of its highest, which keeps sums in fp32's range, so that weights under that of
+// the largest are lost, nor under 2^KV8_W_LEAST.  (First 9 or 11: 470 and 475 us for a piece of a
+// prompt that takes 408 with 7, from the moves.)
+constexpr float KV8_W_FIRST = 7.0f, KV8_W_TOP = 15.0f, KV8_W_SPAN = 40.0f, KV8_W_LEAST = -118.0f;
+constexpr float KV8_W_LOST = KV8_W_FIRST - KV8_W_SPAN;
+// Whether d comes down from `was`, for positions whose largest weight is 2^top in units of ms.
+__device__ __forceinline__ bool kv8_down(float top, float was, float low, float ms, float peak) {
+  const float to = top - KV8_W_FIRST;
+  return top < was + low && to > fmaxf(peak - ms - KV8_W_SPAN, KV8_W_LEAST) && fabsf(ms) < KV8_FAR;
 }
 
 struct Kv8AttnParams {

@@ -106,13 +106,17 @@ size_t gqa_kv8_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int 
  *   scale    multiplies the scores; 0 means 1 / sqrt(head_size)
  *   workspace  256-byte aligned; two calls that overlap in time need two
  * The products are exact, sums, maxima and the softmax are fp32, its weights are rounded to
- * fp16 for the value product only, and o is rounded once.  The normaliser counts every
- * weight in full, whatever the scale of its values.  Scores may have any size; one that is
- * past fp32's range (in units of log2) counts as its largest number.  Exactness ends where
- * scales lie very far apart: among 128 consecutive positions a block whose scale is under
- * 2^-21 of the largest loses low bits of its codes.  A token that sees no position (its
- * sequence has fewer positions than new tokens, which is recorded as a bad length) gets
- * zeros; a query that is not finite makes its own row NaN and no other.
+ * fp16 for the value product only, and o is rounded once.  A weight counts there with its
+ * value's scale.  It is off by at most 2^-11 of itself, and the 32 (in prompts 128) positions
+ * that are multiplied together by 2^-11 of the largest of them in all; how small they are
+ * beside the row's other positions does not matter down to 2^-40 of the largest, under which
+ * they may be lost.  The normaliser counts every weight in full, whatever the scale of its
+ * value.  Scores may have any size; one that is past fp32's range (in units of log2) counts
+ * as its largest number.  Exactness ends where scales lie very far apart: among 128
+ * consecutive positions a block whose scale is under 2^-21 of the largest loses low bits of
+ * its codes.  A token that sees no position (its sequence has fewer positions than new
+ * tokens, which is recorded as a bad length) gets zeros; a query that is not finite makes
+ * its own row NaN and no other.
  * Between 1 and 16 query heads per key/value head.  Results do not depend on timing: the
  * same call gives the same bits.  max_new decides the kernel (one for at most 32 query rows
  * per key/value head, one for more), so a bound that is far too large is right but slow.

@@ -804,3 +804,79 @@ def test_scores_of_any_size(kv8, new, score):
                     want, mag = x[at], x[at].abs()
                 assert ((b[r, h] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag).all()
     assert c.get_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n, share", [(32768, 0.99), (32768, 0.999), (131072, 0.99), (131072, 0.999), (8192, 0.9999),
+                                      (8192, 0.9999999)])
+@pytest.mark.parametrize("zeros", [0, 4096])
+@pytest.mark.parametrize("seqs, new, layout", [(152, 5, (8, 1, 128)), (608, 1, (16, 2, 128)), (608, 2, (16, 2, 64)),
+                                               (1, 1, (16, 2, 128)), (1, 40, (8, 1, 64))])
+def test_a_position_that_takes_nearly_all_the_weight(kv8, seqs, new, layout, zeros, n, share, fmt):
+    """A sink: the first position has nearly all the weight and a value of zero, so that the row is
+    what the many small weights make of theirs, the first of which may be zeros, too, of the smallest
+    scale there is.  The row's error is under 2^-7 of the row, by the
+    Euclidean norm: one rounding to bf16 is at most 2^-8 of each element, the rest is small beside it."""
+    s = shared_pages(kv8, n, seqs, new, layout, fmt, 43)
+    c = s.cache
+    c.k[..., 0] = 0
+    first = int(s.table[0, 0])
+    c.k[first, :, 0] = 0
+    c.k[first, :, 0, 0] = 0x7E if fmt == "e4m3" else 127
+    c.v[first, :, 0] = 0
+    pages = torch.tensor(s.table[0], device="cuda").long()[:zeros // 64]
+    c.v[pages] = 0
+    c.v_scale[pages] = 2.0 ** -100
+    s.q[:, :, 0] = 0
+    k, v, _ = s.ref().values(s.table[0], n)
+    rows = sorted({0, 1, s.t // 2, s.t - 1} & set(range(s.t)))
+    scale = 1 / math.sqrt(s.d)
+    for h in range(s.hq):                                # each row's own share, the other rows 1 / 2
+        g = h // (s.hq // s.hkv)
+        lse = torch.logsumexp(k[1:, g] @ s.q[rows, h].double().T * scale, 0)
+        t = (lse + math.log(share / (1 - share))) / (k[0, g, 0] * scale)
+        s.q[:, h, 0] = float(t.median())
+        s.q[rows, h, 0] = t.to(torch.bfloat16)
+    out = c.attention(s.batch, s.q).double()
+    for r in rows:
+        see = n - new + r % new + 1
+        for h in (0, s.hq - 1):
+            g = h // (s.hq // s.hkv)
+            p = torch.softmax(k[:see, g] @ s.q[r, h].double() * scale, 0)
+            want, lost = p @ v[:see, g], 0.0
+            assert abs(math.log((1 - float(p[0])) / (1 - share))) < 0.3
+            if (1 - share) / n < 2.0 ** -32:
+                # The 128 positions of the sink's own tile meet it in one product, in which it is
+                # 2^7: theirs are under 2^(7 - 32) = 2^-25 there, what fp16 rounds to zero or to
+                # 2^-24, and are off by up to 2^-25, or 2^-32 of the sink's weight, times the scales'
+                # ratio of at most 2^3.
+                lost = (p[1:128].clamp_max(2.0 ** -29) @ v[1:128, g].abs()).norm()
+            err = (out[r, h] - want).norm()
+            assert err <= 2.0 ** -7 * want.norm() + lost, (r, h, float(err / want.norm()))
+    assert c.get_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("seqs, new, layout", [(152, 5, (8, 1, 128)), (608, 1, (16, 2, 128)), (1, 1, (16, 2, 128))])
+def test_one_block_of_large_values(kv8, seqs, new, layout, fmt):
+    """A block whose scale is 2^10 times the others', all of it in one dim: the other dims keep
+    their bits."""
+    n = 32768
+    s = shared_pages(kv8, n, seqs, new, layout, fmt, 44)
+    c = s.cache
+    c.v_scale.fill_(2.0 ** -9)
+    pg = int(s.table[0, 2])
+    c.v[pg, :, 16:32] = 0
+    c.v[pg, :, 16:32, 7] = 0x7E if fmt == "e4m3" else 127
+    c.v_scale[pg, :, 1] = 2.0
+    out = c.attention(s.batch, s.q).double()
+    keep = torch.arange(s.d, device="cuda") != 7
+    for r in sorted({0, s.t - 1}):
+        for h in (0, s.hq - 1):
+            see = n - new + r % new + 1
+            k, v, _ = s.ref().values(s.table[0], see)
+            g = h // (s.hq // s.hkv)
+            p = torch.softmax(k[:, g] @ s.q[r, h].double() / math.sqrt(s.d), 0)
+            want = p @ v[:, g]
+            assert (out[r, h] - want)[keep].norm() <= 2.0 ** -7 * want[keep].norm()
+            assert (out[r, h] - want)[7].abs() <= 2.0 ** -7 * want[7].abs()
