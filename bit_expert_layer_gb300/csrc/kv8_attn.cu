@@ -82,12 +82,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Shared-memory offset of 16-byte chunk c of row r (rows of D bytes, the tensor map's swizzle).
 template <int D>
 __device__ __forceinline__ uint32_t code_off(int r, int c) {
@@ -208,7 +202,9 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     if (loader && pos < l_end)
       pid = __ldg(p.b.page_table + static_cast<size_t>(ls.b) * p.b.max_pages + (pos >> p.c.page_shift));
   };
-  // codes that one tile alone reads need no place in L2
+  // Codes that one tile alone reads need no place in L2 (8 x 32768 positions: 31.0 us, 31.9 with the
+  // usual policy; which one the codes of several tiles get made no difference).  Pages that
+  // sequences share are taken for read once, too.
   const uint64_t pol = p.b.max_new <= (1 << p.tq_shift) ? l2_policy_evict_first() : l2_policy_evict_normal();
   int issued = 0;
   // Issue the cursor's piece into its stage; returns this lane's block scale (the loaders).
@@ -733,10 +729,12 @@ int floor_log2(int n) {
 }
 
 // Query rows of a tile, or 0 for the prompt kernel.  Up to 32 rows go through the decode
-// kernel in tiles of 16, which read the codes twice, the second time mostly from L2: 4 new
-// tokens of 8 query heads each took 28 us that way over 16 sequences of 8 thousand positions and
-// 18 over one, and 36 and 25 in one block of 128 rows, three quarters empty.  With 64 rows it was
-// 53 and 17 against 36 and 25.
+// kernel in tiles of 16, each of which reads the codes again, mostly from L2: 4 new tokens of 8
+// query heads each, two tiles, took 28 us that way over 16 sequences of 8 thousand positions and
+// 18 over one, and 36 and 25 in one block of 128 rows, three quarters empty.  With 64 rows, four
+// tiles, it was 53 and 17 against 36 and 25.  A tile holds a power of two of tokens, so that
+// other numbers of query heads make three tiles of up to 32 rows (5 heads, 6 tokens: 2 a tile);
+// those were not measured.
 int ka_rows(int G, int max_new) {
   const long long n = static_cast<long long>(G) * max_new;
   return n <= 8 ? 8 : n <= 32 ? 16 : 0;

@@ -25,10 +25,11 @@
 // Bound: the tensor cores' 16.8 MFLOP per tile and two row blocks, 2048 cycles at the nominal
 // rate (2400 at the 75 cycles that an M128 N128 K16 instruction takes in a chain), 32768
 // exponentials (1024 cycles) beside them.  Measured: 2048 tokens over 31000 positions of int8,
-// 16 query and 2 key/value heads of 128, in 390 us, 1.29 PFLOP/s, 0.65 of the measured bf16 rate;
-// the tensor pipe is active 56 % of the time, and what is left is a block's chain from scores
+// 16 query and 2 key/value heads of 128, in 396 us (404 with inputs that change from call to call),
+// 1.27 PFLOP/s, 0.64 of the measured bf16 rate; the tensor pipe is active 56 % of the time, and what
+// is left is a block's chain from scores
 // through weights to the next scores, which the other block's covers only in part.  A prompt of
-// 2048 tokens from the start takes 41 us: 128 tiles of 1 to 16 units each, where a tile's start
+// 2048 tokens from the start takes 42 us: 128 tiles of 1 to 16 units each, where a tile's start
 // and end (queries in, result out, some 10 thousand cycles) weigh as much as its units.
 #include <cstring>
 #include <type_traits>
@@ -51,9 +52,9 @@ constexpr int KP_PLANS = 4;                       // tiles planned ahead
 constexpr int KP_FEW = 4;                         // parts of a tile that a join loads at once
 constexpr float KP_LOW = -7.0f;                   // 128 positions: 128 * 2^-25 = 2^-11 2^-7
 // Blocks of a tile are brought to the tile's largest scale in fp16, 2^head on top of it: the
-// largest code (448; for int8 the offset 1152 of its conversion) lands just under fp16's
-// largest number, and a block whose scale is down to 2^-21 of the tile's largest keeps every
-// bit of its codes.
+// largest code (448; for int8 the offset 1152 of its conversion) stays under fp16's largest number
+// (28672 and 36864 of 65504), and a block whose scale is down to 2^-21 of the tile's largest
+// keeps every bit of its codes (e4m3's smallest is 2^-9: 2^(-9 + 6 - 21) = 2^-24).
 __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 ? 6 : 5; }
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B) {
@@ -134,11 +135,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -172,10 +168,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 // The softmax's steps that few tiles need are functions of their own: with them inside its loop a
 // piece of 2048 tokens over 31000 positions took between 392 and 475 us, as the compiler's
-// registers for the loop fell out, with changing inputs up to 486; now 395 and 402.
+// registers for the loop fell out, with changing inputs up to 486; now 396 and 404.  (Heads of 64
+// are better off with the mask inside: 16 prompts of 512 tokens 43.6 us, 45.7 without.)
 //
 // What a row does not see of a tile becomes -inf: positions from `left` on, blocks of `bad`.
-__device__ __noinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad) {
+__device__ __forceinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad) {
   uint32_t x[32];
 #pragma unroll 1
   for (int c = 0; c < KP_U / 32; ++c) {
@@ -192,6 +189,7 @@ __device__ __noinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad) {
   }
   tmem_st_wait();
 }
+__device__ __noinline__ void kp_mask_apart(uint32_t t_s, int left, uint32_t bad) { kp_mask(t_s, left, bad); }
 // The sum of a row's terms 2^(f x + add) of one tile.
 __device__ __noinline__ float kp_bare_sum(uint32_t t_s, float f, float add) {
   float sum = 0.0f;
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
               const int e = min(max(static_cast<int>(big >> 7) - 127 - 13, KV8_Q_MIN_EXP), KV8_Q_MAX_EXP);
               const float f = big >= 0x7F80u ? NAN : pow2i(-e);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = pack2h(bf16lo(x[j]) * f, bf16hi(x[j]) * f);
+              for (int j = 0; j < 4; ++j) x[j] = pack2_f16(bf16lo(x[j]) * f, bf16hi(x[j]) * f);
               *reinterpret_cast<uint4*>(s_q + blk * TILE + (qc >> 3) * BOX + r2 * 128 + (((qc & 7) ^ (r2 & 7)) << 4)) = v[i];
               if (qc == 0) s_rs[blk * KP_ROWS + r2] = big >= 0x7F80u ? NAN : fminf(pow2i(e) * p.scale_log2, KV8_MAX_FACTOR);
             }
@@ -444,7 +442,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           // A tile at the causal edge, or with a page missing: what the row does not see becomes
           // -inf in TMEM first, so that the passes below carry no mask (with it in them, the
           // compiler masked every tile: 767 us against 557).
-          if (__any_sync(0xffffffffu, left < KP_U) || bad) kp_mask(t_s, left, bad);
+          if (__any_sync(0xffffffffu, left < KP_U) || bad) {
+            if constexpr (D == 64)
+              kp_mask(t_s, left, bad);
+            else
+              kp_mask_apart(t_s, left, bad);
+          }
           // The scores are read twice, 32 columns at a time, the next ones while these are worked
           // on: 128 of them in registers do not fit beside the rest.  (One pass against the
           // reference of the tiles before, the weights waiting in registers until all scores are
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
                 const float2 y = f32x2_get(fma2(f32x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2, a2));
                 const float w0 = ex2(y.x), w1 = ex2(y.y);
                 sum[j & 1] = add2(sum[j & 1], f32x2(w0, w1));
-                w16[j] = pack2h(w0, w1);
+                w16[j] = pack2_f16(w0, w1);
               }
               tmem_st16(t_s + 16 * c, w16);
             }
@@ -690,9 +693,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           KpPlan* plan = s_plan + slot;
           if (lane < 8) {
             plan->rows[lane] = row;
-            plan->kfac[lane] = pack2h(f, f);
+            plan->kfac[lane] = pack2_f16(f, f);
           } else if (lane < 16) {
-            plan->vfac[lane - 8] = pack2h(f, f);
+            plan->vfac[lane - 8] = pack2_f16(f, f);
           } else if (lane == 16) {
             plan->valid = valid;
             s_scale[it & (KP_SLOTS - 1)] =

@@ -8,8 +8,9 @@
 // whole tiles and at most one part at either end.  The parts of a tile meet first inside
 // the CTA, then through the workspace: each CTA leaves its unnormalised sums in a slot of
 // its own (2 per CTA: a tile that began before the CTA's runs, a tile that goes on after
-// them), and the last CTA to arrive, by a ticket that belongs to the tile's first CTA, adds
-// them up in the order of the line.  Nothing waits.
+// them), to be added up in the order of the line: in the decode kernel by the last CTA to
+// arrive, by a ticket that belongs to the tile's first CTA, for prompts by a second kernel.
+// Nothing waits.
 //
 // Nothing is tabulated per tile: a sequence's units up to tile t have a closed form.  With
 // TQ a power of two that divides U, r = U / TQ, `a` the first new token's position and
