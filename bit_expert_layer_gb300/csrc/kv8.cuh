@@ -40,9 +40,10 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Batch& p, int page_shift, int
   const int cap = p.max_pages << page_shift;
   s.off = min(max(o0, 0), p.n_tokens);
   const int end = min(max(o1, s.off), p.n_tokens);
-  s.n = min(end - s.off, p.max_new);
   s.len = min(max(len, 0), cap);
-  s.first = s.len - (end - s.off);
+  // a length past the page table moves no token: those past its end are left out
+  s.first = max(len, 0) - (end - s.off);
+  s.n = max(min(min(end - s.off, p.max_new), cap - s.first), 0);
   s.bad = s.off != o0 || end != o1 || s.n != end - s.off || s.len != len;
   return s;
 }

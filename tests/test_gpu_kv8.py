@@ -880,3 +880,38 @@ def test_one_block_of_large_values(kv8, seqs, new, layout, fmt):
             want = p @ v[:, g]
             assert (out[r, h] - want)[keep].norm() <= 2.0 ** -7 * want[keep].norm()
             assert (out[r, h] - want)[7].abs() <= 2.0 ** -7 * want[7].abs()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("over, new", [(1, 1), (3, 5), (5, 5), (40, 60), (2 ** 31 - 1 - 128, 60)])
+def test_lengths_past_the_page_table_move_no_token(kv8, over, new, fmt):
+    """A sequence with more positions than its row of the page table: the tokens past its end are
+    left out, the others stand where they would have, and no cached position changes."""
+    from bit_expert_layer_gb300 import _abi
+    cap = 128
+    s = Setup(kv8, [200, cap, 90], [3, new, 20], page=64, fmt=fmt, seed=45)
+    table = s.table[:, :2].copy()
+    lens = [100, cap + over, 90]
+    b = kv8.KV8Batch(ints(table), ints(lens), s.batch.offsets, s.batch.max_new)
+    ref = s.ref()
+    r = [int(x) for x in s.offsets]
+    fit = max(new - over, 0)                                     # tokens before the end
+    rows = list(range(r[0], r[1])) + list(range(r[1], r[1] + fit)) + list(range(r[2], r[3]))
+    off = [0, 3, 3 + fit, 23 + fit]
+    ref.append(table, [100, cap, 90], off, s.k[rows].double(), s.v[rows].double())
+    s.cache.append(b, s.k, s.v)
+    assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    s.check_cache(ref)
+    k, v = (torch.full((s.t, s.hkv, s.d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    s.cache.gather(b, s.t, out=(k, v))
+    assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert (k[r[1] + fit:r[2]] == 7).all() and (v[r[1] + fit:r[2]] == 7).all()
+    for i, n, w, row in ((0, 100, 3, r[0]), (1, cap, fit, r[1]), (2, 90, 20, r[2])):
+        kk, vv, _ = ref.values(table[i], n)
+        assert torch.equal(k[row:row + w].double(), kk[n - w:]) and torch.equal(v[row:row + w].double(), vv[n - w:])
+    out = torch.full(s.q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    s.cache.attention(b, s.q, out=out)
+    assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert (out[r[1] + fit:r[2]] == 5).all()
+    want, bound = ref.attention(table, [100, cap, 90], off, s.q[rows].double())
+    assert ((out[rows].double() - want).abs() <= bound).all()
