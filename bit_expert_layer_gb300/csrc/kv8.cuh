@@ -44,6 +44,8 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Batch& p, int page_shift, int
   // a length past the page table moves no token: those past its end are left out
   s.first = max(len, 0) - (end - s.off);
   s.n = max(min(min(end - s.off, p.max_new), cap - s.first), 0);
+  // offsets that contradict the call's rows do not say which row stands where
+  if (s.off != o0 || end != o1) s.n = 0;
   s.bad = s.off != o0 || end != o1 || s.n != end - s.off || s.len != len;
   return s;
 }

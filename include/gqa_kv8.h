@@ -29,9 +29,9 @@
  * synchronisation, no allocation inside the library, calls asynchronous on `stream` of the
  * current device.  What only the device can see (a page outside the cache, a length past the
  * page table, offsets out of order, values that are not finite) never faults: the kernels
- * leave out what it concerns and record it in the cache's error word.  Tokens that a length
- * places past the end of the page table are left out by every call (no other position or
- * row stands for them).
+ * leave out what it concerns and record it in the cache's error word.  Every call leaves
+ * out the tokens that a length places past the end of the page table, and a sequence whose
+ * offsets are out of order or past the rows; no other position or row stands for them.
  */
 #ifndef GQA_KV8_H
 #define GQA_KV8_H

@@ -915,3 +915,28 @@ def test_lengths_past_the_page_table_move_no_token(kv8, over, new, fmt):
     assert (out[r[1] + fit:r[2]] == 5).all()
     want, bound = ref.attention(table, [100, cap, 90], off, s.q[rows].double())
     assert ((out[rows].double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("offsets", [[0, 4, 2, 9], [0, 3, 6, 40], [-2, 3, 6, 9], [0, 2 ** 30, 6, 9]])
+def test_offsets_out_of_range_write_nothing(kv8, offsets):
+    """A sequence whose offsets contradict the call's rows: none of its positions is written, and no
+    row of its own in the outputs."""
+    from bit_expert_layer_gb300 import _abi
+    s = Setup(kv8, [100, 80, 90], [3, 3, 3], seed=46)
+    good = [0 <= a <= b <= s.t for a, b in zip(offsets, offsets[1:])]
+    b = kv8.KV8Batch(s.batch.page_table, s.batch.lens, ints(offsets), 9)
+    before = s.ref()
+    s.cache.append(b, s.k, s.v)
+    assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    out = torch.full(s.q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    s.cache.attention(b, s.q, out=out)
+    assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    mine = torch.zeros(s.t, dtype=torch.bool, device="cuda")
+    for i, ok in enumerate(good):
+        pages = torch.tensor(s.table[i][s.table[i] >= 0], device="cuda").long()
+        if ok:
+            mine[offsets[i]:offsets[i + 1]] = True
+        else:
+            assert torch.equal(s.cache.k[pages], before.codes["k"][pages])
+            assert torch.equal(s.cache.v_scale[pages].double(), before.scales["v"][pages])
+    assert (out[~mine] == 5).all()
