@@ -25,8 +25,8 @@
 // Bound: the tensor cores' 16.8 MFLOP per tile and two row blocks, 2048 cycles at the nominal
 // rate (2400 at the 75 cycles that an M128 N128 K16 instruction takes in a chain), 32768
 // exponentials (1024 cycles) beside them.  Measured: 2048 tokens over 31000 positions of int8,
-// 16 query and 2 key/value heads of 128, in 396 us (404 with inputs that change from call to call),
-// 1.27 PFLOP/s, 0.64 of the measured bf16 rate; the tensor pipe is active 56 % of the time, and what
+// 16 query and 2 key/value heads of 128, in 401 us (409 with inputs that change from call to call),
+// 1.25 PFLOP/s, 0.64 of the measured bf16 rate; the tensor pipe is active 56 % of the time, and what
 // is left is a block's chain from scores
 // through weights to the next scores, which the other block's covers only in part.  A prompt of
 // 2048 tokens from the start takes 42 us: 128 tiles of 1 to 16 units each, where a tile's start
@@ -168,7 +168,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 // The softmax's steps that few tiles need are functions of their own: with them inside its loop a
 // piece of 2048 tokens over 31000 positions took between 392 and 475 us, as the compiler's
-// registers for the loop fell out, with changing inputs up to 486; now 396 and 404.  (Heads of 64
+// registers for the loop fell out, with changing inputs up to 486; now 401 and 409.  (Heads of 64
 // are better off with the mask inside: 16 prompts of 512 tokens 43.6 us, 45.7 without.)
 //
 // What a row does not see of a tile becomes -inf: positions from `left` on, blocks of `bad`.
@@ -235,7 +235,7 @@ __device__ __noinline__ float4 kp_refs(uint32_t t_s, float mx, float f, float e,
   m_ref = far ? d : move ? ms_new + d : m_ref;
   ms_ref = far ? -INFINITY : ms_new;
   *s_ms = ms_new;
-  const bool wide = d - e > KV8_SUM_TOP || far;
+  const bool wide = move && (d - e > KV8_SUM_TOP || far);
   if (__any_sync(0xffffffffu, wide)) {
     kp_far_scores(t_s, f, ms_new, far);
     const float sum = kp_bare_sum(t_s, f, far ? 0.0f : -ms_new);
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         const float rs = s_rs[blk * KP_ROWS + r];
 
         // m_ref is ms + d.  Where the scores are far, or none has been seen, it is d alone; ms lies in
-        // s_ms then, and in its place minus infinity, which no tile passes by.
+        // s_ms then, and in its place minus infinity, which no tile passes by that the row sees.
         float m_ref = 0.0f, ms_ref = rs == rs ? -INFINITY : 0.0f, l = 0.0f;   // a row of NaN moves nothing
         s_ms[tid] = s_peak[tid] = KV8_NO_REF;
 #pragma unroll 1
@@ -471,8 +471,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           }
           // ---- the references move: O and the normaliser follow
           const float w_max = fmaf(mx, f, e - m_ref);            // the largest weight's exponent
+          // (a row that sees nothing here has mx = -inf, which makes the last sum NaN: it waits; moving
+          // it cost runs that begin at a tile's edge 10 us of 44)
           const bool move = w_max > KV8_W_TOP || (w_max < KP_LOW && w_max > KV8_W_LOST) ||
-                            m_ref - ms_ref - e > KV8_SUM_TOP;
+                            fmaf(mx, 0.0f, m_ref - ms_ref - e) > KV8_SUM_TOP;
           if (__any_sync(0xffffffffu, move)) {
             tmem_ld_wait();                                      // no load is under way across the calls below
             const float4 r = kp_refs(t_s, mx, f, e, m_ref, ms_ref, l, s_ms + tid, s_peak + tid, move);
