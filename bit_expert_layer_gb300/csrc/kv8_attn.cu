@@ -325,9 +325,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        ms[b][i] = rs[b][i] == rs[b][i] ? KV8_NO_REF : 0.0f;   // a row of NaN moves no references
-        if (rs[b][i] == rs[b][i]) reach = INFINITY;
-        d[b][i] = l[b][i] = 0.0f;
+        const bool nan = rs[b][i] != rs[b][i];                 // a row of NaN moves no references
+        ms[b][i] = nan ? 0.0f : KV8_NO_REF;
+        d[b][i] = nan ? KV8_W_LEAST : 0.0f;
+        if (!nan) reach = INFINITY;
+        l[b][i] = 0.0f;
         s_peak[8 * b + 2 * c4 + i] = KV8_NO_REF;               // by each lane for itself
       }
 #pragma unroll
@@ -453,11 +455,18 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
 #pragma unroll
             for (int k = 0; k < NK; ++k)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                y[b][k][2 * h + i] = sv[k][h] - at + (ve[k] - to);
-                l[b][i] += ex2(sv[k][h] - at);
-              }
+              for (int h = 0; h < 2; ++h) y[b][k][2 * h + i] = sv[k][h] - at + (ve[k] - to);
           }
+      }
+      // the normaliser's terms by themselves, where the weights do not give them
+      const bool apart = move && __any_sync(0xffffffffu, reach - least_e > KV8_SUM_TOP);
+      if (apart) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[b][j & 1] += ex2(y[b][k][j] + (d[b][j & 1] - ve[k]));
       }
       uint32_t pb[NB][NK][2];         // weights as B: keys 16 k + 8 h + 2 c4 and + 1 of row g4
 #pragma unroll
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
           pb[b][k][0] = transpose8x8(pack2_f16(w[0], w[1]));
           pb[b][k][1] = transpose8x8(pack2_f16(w[2], w[3]));
         }
-        if (!move) {
+        if (!apart) {
           l[b][0] = fmaf(sum[0], ex2(d[b][0]), l[b][0]);
           l[b][1] = fmaf(sum[1], ex2(d[b][1]), l[b][1]);
         }

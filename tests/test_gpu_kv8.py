@@ -940,3 +940,22 @@ def test_offsets_out_of_range_write_nothing(kv8, offsets):
             assert torch.equal(s.cache.k[pages], before.codes["k"][pages])
             assert torch.equal(s.cache.v_scale[pages].double(), before.scales["v"][pages])
     assert (out[~mine] == 5).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 90])
+def test_not_finite_queries_beside_zero_values(kv8, new):
+    """Zero blocks of values among others, of small and of large scales: the other rows keep their bits."""
+    s = Setup(kv8, [200, 130], [new, new], seed=47)
+    c = s.cache
+    c.v[:, :, 16:32] = 0
+    c.v_scale[:, :, 1] = 2.0 ** -100
+    for high in (-9, 20):
+        c.v_scale[:, :, 0] = 2.0 ** high
+        a = c.attention(s.batch, s.q)
+        q = s.q.clone()
+        q[new - 1, 3, 5] = math.nan
+        q[2 * new - 1, 8, 0] = -math.inf
+        b = c.attention(s.batch, q)
+        keep = torch.ones(2 * new, 16, dtype=torch.bool, device="cuda")
+        keep[new - 1, 3] = keep[2 * new - 1, 8] = False
+        assert torch.equal(a[keep], b[keep]) and torch.isnan(b[~keep]).all()
