@@ -68,6 +68,24 @@ class GqaKv8Batch(C.Structure):
                [(n, C.c_int) for n in ("n_seqs", "max_pages", "n_tokens", "max_new")]
 
 
+class GqaKv8Prefix(C.Structure):
+    _fields_ = [("groups", C.c_void_p), ("shared", C.c_void_p), ("n_groups", C.c_int)]
+
+
+class GqaKv8Pages(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("page_table", "free_pages", "control")] + \
+               [(n, C.c_int) for n in ("n_seqs", "max_pages", "n_pages", "page_size")]
+
+
+class GqaKv8PagesState(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("lens", "held", "n_free")]
+
+
+class GqaNorm(C.Structure):
+    _fields_ = [("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("weight_f32", C.c_int), ("eps", C.c_float),
+                ("offset", C.c_float)]
+
+
 class GqaRopePlan(C.Structure):
     _fields_ = [("turn", C.c_uint64 * GQA_ROPE_MAX_PAIRS), ("axis", C.c_uint8 * GQA_ROPE_MAX_PAIRS),
                 ("head_size", C.c_int), ("rotary", C.c_int), ("n_axes", C.c_int)]
@@ -128,12 +146,25 @@ def lib() -> C.CDLL:
         L.gqa_kv8_workspace_bytes.restype = C.c_size_t
         L.gqa_kv8_attention.argtypes = [PC, PB, P, LL, I, C.c_float, P, P, C.c_size_t, P]
         L.gqa_kv8_attention.restype = S
+        L.gqa_kv8_window_attention.argtypes = [PC, PB, P, LL, I, C.c_float, I, I, P, P, C.c_size_t, P]
+        L.gqa_kv8_window_attention.restype = S
+        L.gqa_kv8_prefix_workspace_bytes.argtypes = [PC, I, I, I]
+        L.gqa_kv8_prefix_workspace_bytes.restype = C.c_size_t
+        L.gqa_kv8_prefix_attention.argtypes = [PC, PB, C.POINTER(GqaKv8Prefix), P, LL, I, C.c_float, P, P, C.c_size_t, P]
+        L.gqa_kv8_prefix_attention.restype = S
+        PG, PS = C.POINTER(GqaKv8Pages), C.POINTER(GqaKv8PagesState)
+        L.gqa_kv8_pages_step.argtypes = [PG, PS, PS, P, P, P, P, P, P, I, P]
+        L.gqa_kv8_pages_step.restype = S
+        L.gqa_kv8_pages_get_error.argtypes = [PG]
+        L.gqa_kv8_pages_get_error.restype = S
         L.gqa_kv8_get_error.argtypes = [PC]
         L.gqa_kv8_get_error.restype = S
         L.gqa_rope_plan_init.argtypes = [PR, I, I, C.c_double, P, P, I, I]
         L.gqa_rope_plan_init.restype = S
         L.gqa_rope.argtypes = [PR, P, LL, I, P, LL, I, P, I, P, LL, P, LL, P]
         L.gqa_rope.restype = S
+        L.gqa_norm_rope.argtypes = [PR, C.POINTER(GqaNorm), P, LL, I, P, LL, I, P, I, P, LL, P, LL, P]
+        L.gqa_norm_rope.restype = S
         L.moe_decode_trace.argtypes = [P, P, C.c_size_t]
         L.moe_decode_trace.restype = S
         L.moe_set_wait_limit_ns.argtypes = [C.c_ulonglong]
@@ -308,6 +339,34 @@ def gqa_kv8_attention(cache: GqaKv8Cache, batch: GqaKv8Batch, q: int, q_stride: 
                                    stream or None), "gqa_kv8_attention")
 
 
+def gqa_kv8_window_attention(cache: GqaKv8Cache, batch: GqaKv8Batch, q: int, q_stride: int, n_q_heads: int, scale: float,
+                             window: int, sinks: int, out: int, workspace: int, workspace_bytes: int,
+                             stream: int = 0) -> None:
+    _check(lib().gqa_kv8_window_attention(cache, batch, q, q_stride, n_q_heads, scale, window, sinks, out, workspace,
+                                          workspace_bytes, stream or None), "gqa_kv8_window_attention")
+
+
+def gqa_kv8_prefix_workspace_bytes(cache: GqaKv8Cache, n_q_heads: int, max_new: int, n_tokens: int) -> int:
+    return int(lib().gqa_kv8_prefix_workspace_bytes(cache, n_q_heads, max_new, n_tokens))
+
+
+def gqa_kv8_prefix_attention(cache: GqaKv8Cache, batch: GqaKv8Batch, prefix: GqaKv8Prefix, q: int, q_stride: int,
+                             n_q_heads: int, scale: float, out: int, workspace: int, workspace_bytes: int,
+                             stream: int = 0) -> None:
+    _check(lib().gqa_kv8_prefix_attention(cache, batch, prefix, q, q_stride, n_q_heads, scale, out, workspace,
+                                          workspace_bytes, stream or None), "gqa_kv8_prefix_attention")
+
+
+def gqa_kv8_pages_step(pages: GqaKv8Pages, state: GqaKv8PagesState, to: GqaKv8PagesState, keep: int, n_new: int,
+                       borrowed: int, offsets: int, positions: int, slots: int, n_tokens: int, stream: int = 0) -> None:
+    _check(lib().gqa_kv8_pages_step(pages, state, to, keep or None, n_new, borrowed or None, offsets, positions or None,
+                                    slots or None, n_tokens, stream or None), "gqa_kv8_pages_step")
+
+
+def gqa_kv8_pages_get_error(pages: GqaKv8Pages) -> int:
+    return int(lib().gqa_kv8_pages_get_error(pages))
+
+
 def gqa_kv8_get_error(cache: GqaKv8Cache) -> int:
     return int(lib().gqa_kv8_get_error(cache))
 
@@ -330,6 +389,13 @@ def gqa_rope(plan: GqaRopePlan, q: int, q_stride: int, n_q_heads: int, k: int, k
              pos: int, T: int, q_out: int, q_out_stride: int, k_out: int, k_out_stride: int, stream: int = 0) -> None:
     _check(lib().gqa_rope(plan, q, q_stride, n_q_heads, k or None, k_stride, n_k_heads, pos, T, q_out, q_out_stride,
                           k_out or None, k_out_stride, stream or None), "gqa_rope")
+
+
+def gqa_norm_rope(plan: GqaRopePlan, norm: GqaNorm, q: int, q_stride: int, n_q_heads: int, k: int, k_stride: int,
+                  n_k_heads: int, pos: int, T: int, q_out: int, q_out_stride: int, k_out: int, k_out_stride: int,
+                  stream: int = 0) -> None:
+    _check(lib().gqa_norm_rope(plan, norm, q, q_stride, n_q_heads, k or None, k_stride, n_k_heads, pos, T, q_out,
+                               q_out_stride, k_out or None, k_out_stride, stream or None), "gqa_norm_rope")
 
 
 def declared_functions() -> list[str]:

@@ -31,6 +31,7 @@ struct Kv8Batch {
 struct Kv8Seq {
   int off, n, len;   // first row, new tokens, cached positions
   int first;         // position of the first new token (negative: the length is too short for it)
+  int base;          // attention: first positions that another pass sees to (a multiple of every unit)
   bool bad;
 };
 

@@ -54,11 +54,11 @@ __host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // f
 // what the parts belong to, barriers and words
 __host__ __device__ constexpr int ka_parts(int D, int R) { return ka_warps(R) * R * ka_ps(D) * 4; }
 __host__ __device__ constexpr int ka_wsum(int R) { return R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
-__host__ __device__ constexpr int ka_smem(int D, int R, int B) {
+__host__ __device__ constexpr int ka_smem(int D, int R, int B, bool suffix) {
   return 1024 + ka_warps(R) * ka_own(D, R) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 +
-         ka_warps(R) * (8 + ka_stages(R) * 8 + 2 * 32 + R * 4) + 64;
+         ka_warps(R) * (8 + ka_stages(R) * 8 + 2 * 32 + R * 4) + 64 + (suffix ? B * 4 : 0);
 }
-static_assert(ka_smem(128, 16, KV8_MAX_SEQS) <= 232448 && ka_smem(128, 8, KV8_MAX_SEQS) <= 232448,
+static_assert(ka_smem(128, 16, KV8_MAX_SEQS, true) <= 232448 && ka_smem(128, 8, KV8_MAX_SEQS, true) <= 232448,
               "shared memory per CTA exceeds 227 KB");
 static_assert(ka_warps(8) * ka_stages(8) <= 32 && ka_warps(16) * ka_stages(16) <= 32, "one lane per barrier");
 static_assert(16 * ka_ps(128) * 4 <= ka_own(128, 16) && 16 * ka_ps(64) * 4 <= ka_own(64, 16) &&
@@ -70,7 +70,7 @@ struct __align__(16) KaPart {
   int b, g, t;           // sequence, key/value head, tile; b < 0: no part
   int off, n;            // the sequence's first row and new tokens
   int r_first, r_last;   // the runs of the tile's first and last unit
-  int pad;
+  int base;              // positions that the prefix pass has seen to
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }  // namespace
 
 // box: rows of the tensor maps' box, 16 (pages of 16 positions) or 32.
-template <int D, int R, int FMT>
+template <int D, int R, int FMT, int MODE>
 __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Kv8AttnParams p, int box) {
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + KA_WARPS * KA_STAGES);
   int* s_last = const_cast<int*>(abort_flag) + 1;
   float* s_peak = reinterpret_cast<float*>(s_last + 1) + (threadIdx.x >> 5) * R;   // [R] the highest ms + d of a row
+  int* base = reinterpret_cast<int*>(s_last + 1) + KA_WARPS * R;      // suffix mode: [n_seqs]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * OWN;
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   if (tid < 2 * KA_WARPS) meta[tid].b = -1;
   grid_dep_wait();                          // what follows reads and writes what earlier kernels wrote
   Kv8Runs runs;
-  runs.total = kv8_line<KA_U, KA_COST, KA_THREADS>(p, prefix, s_warp);
+  runs.total = kv8_line<KA_U, KA_COST, KA_THREADS, MODE>(p, prefix, s_warp, base);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x) * KA_WARPS));
   const int cta = blockIdx.x, run = cta * KA_WARPS + warp;
   if (cta * KA_WARPS >= runs.n) return;
@@ -179,9 +180,9 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   int lu = 0, l_end = 0, pid = -1;
   bool more = w_beg < w_end;
   if (more) {
-    ls = kv8_seg<KA_U, KA_COST>(p, prefix, lw, w_end);
+    ls = kv8_seg<KA_U, KA_COST, MODE>(p, prefix, base, lw, w_end);
     lu = ls.u0;
-    l_end = kv8_seg_end(ls, p.tq_shift);
+    l_end = kv8_seg_end<MODE>(ls, p.tq_shift);
   }
   const Kv8Seg first_seg = ls;
   auto settle = [&] {                 // the cursor's next piece: its segment and its pages
@@ -193,11 +194,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         more = false;
         return;
       }
-      kv8_next<KA_U, KA_COST>(ls, p, prefix, lw, w_end);
+      kv8_next<KA_U, KA_COST, MODE>(ls, p, prefix, base, lw, w_end);
       lu = ls.u0;
-      l_end = kv8_seg_end(ls, p.tq_shift);
+      l_end = kv8_seg_end<MODE>(ls, p.tq_shift);
     }
-    const int pos = lu * KA_U + block * KV8_BLOCK;
+    const int pos = kv8_unit<KA_U, MODE>(ls, lu) * KA_U + block * KV8_BLOCK;
     pid = -1;
     if (loader && pos < l_end)
       pid = __ldg(p.b.page_table + static_cast<size_t>(ls.b) * p.b.max_pages + (pos >> p.c.page_shift));
@@ -212,8 +213,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     float sc = KA_NO_BLOCK;
     if (!more) return sc;
     const int st = issued % KA_STAGES;
-    const int pos = lu * KA_U + block * KV8_BLOCK;
+    const int pos = kv8_unit<KA_U, MODE>(ls, lu) * KA_U + block * KV8_BLOCK;
     bool live = loader && pos < l_end;
+    // a block that no token of the tile sees (its page may be gone); one of a box of 32 rows shares
+    // its page with one that is seen
+    if (MODE == KV8_WINDOW && box == KV8_BLOCK) live &= pos < p.sinks || pos + KV8_BLOCK > ls.low;
     if (live && (pid < 0 || pid >= p.c.n_pages)) {
       atomicOr(p.c.err, ERRBIT_BOUNDS);
       live = false;
@@ -267,12 +271,12 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
 #pragma unroll 1
   for (long long w = w_beg; w < w_end;) {
     if (w > w_beg) {
-      kv8_next<KA_U, KA_COST>(sg, p, prefix, w, w_end);
+      kv8_next<KA_U, KA_COST, MODE>(sg, p, prefix, base, w, w_end);
       fetched = false;
     }
     w += sg.len;
     if (sg.u1 <= sg.u0) continue;     // the run ends before the tile's first piece
-    const int end = kv8_seg_end(sg, p.tq_shift);
+    const int end = kv8_seg_end<MODE>(sg, p.tq_shift);
     const int tok0 = sg.t << p.tq_shift;
     const int ntok = min(1 << p.tq_shift, sg.s.n - tok0);
     const int nrows = ntok * p.G;
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     if (!fetched) fetch_q(sg);
     float rs[NB][2];                  // factor of the row's scores
     int see[NB][2];                   // positions that the row's token sees
+    int low[NB][2];                   // window mode: the first position of its window
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int r = g4 + 8 * b;
@@ -314,9 +319,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       for (int i = 0; i < 2; ++i) {
         rs[b][i] = __shfl_sync(0xffffffffu, rf, 4 * (2 * c4 + i));
         see[b][i] = __shfl_sync(0xffffffffu, sees, 4 * (2 * c4 + i));
+        low[b][i] = MODE == KV8_WINDOW && 8 * b + 2 * c4 + i < nrows ? see[b][i] - p.window : 0;
       }
     }
     const int least = sg.s.first + tok0 + 1;       // positions that every row sees
+    const int most = least + ntok - 1 - p.window;  // window mode: the last row's window begins here
     // references of a row's weights and normaliser; l: this lane's share of the normaliser
     float d[NB][2], ms[NB][2], l[NB][2];
     float o[NB][NM][4];
@@ -375,13 +382,16 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         }
       }
       // ---- s + e - m, masked where a row may not see the whole piece
-      const bool masked = u * KA_U + KA_U > least || !live[0] || !live[NK - 1];
+      const int at_u = kv8_unit<KA_U, MODE>(sg, u) * KA_U;
+      const bool masked = at_u + KA_U > least || !live[0] || !live[NK - 1] ||
+                          (MODE == KV8_WINDOW && at_u < most && at_u + KA_U > p.sinks);
       float y[NB][NK][4], least_e = ve[0];
 #pragma unroll
       for (int k = 1; k < NK; ++k) least_e = fminf(least_e, ve[k]);
       const auto factor = [&](int b, int k, int i) { return fminf(rs[b][i] * ksc[k], KV8_MAX_FACTOR); };
       const auto hidden = [&](int b, int k, int h, int i) {
-        return !live[k] || u * KA_U + 16 * k + 8 * h + g4 >= see[b][i];
+        const int at = at_u + 16 * k + 8 * h + g4;
+        return !live[k] || at >= see[b][i] || (MODE == KV8_WINDOW && at < low[b][i] && at >= p.sinks);
       };
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -506,11 +516,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
             rw[i][0] = v.x, rw[i][1] = v.y;
           }
         }
-        const int base = u * KA_U + 16 * k;
-        if (base + 16 > end) {
+        const int at = at_u + 16 * k;
+        if (at + 16 > end) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (base + 2 * c4 + (i & 1) + (i >> 1) * 8 >= end)
+            if (at + 2 * c4 + (i & 1) + (i >> 1) * 8 >= end)
 #pragma unroll
               for (int j = 0; j < W; ++j) rw[i][j] = 0;
         }
@@ -552,11 +562,25 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         const int r = 8 * b + 2 * c4 + i;
         if (whole) {
           if (r < nrows) {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw no key: zeros
-            const float unit = ex2(d[b][i]);                     // of the weights, in the normaliser's
             const int tok = r / p.G, hh = r - tok * p.G;
-            __nv_bfloat16* dst =
-                p.out + (static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh) * D + VD * g4;
+            const size_t at = static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh;
+            float unit = ex2(d[b][i]);                           // of the weights, in the normaliser's
+            if (MODE == KV8_SUFFIX && sg.s.base) {               // the row's shared positions
+              const float* row = p.rows + at * kv8_row_floats(D);
+              const Kv8Join j = kv8_join(make_float4(ms[b][i], d[b][i], sum, 0.0f), *reinterpret_cast<const float4*>(row + D));
+              sum = j.sum;
+              unit = j.unit;
+#pragma unroll
+              for (int t = 0; t < NM; t += 2) {
+                const float4 v = *reinterpret_cast<const float4*>(row + VD * g4 + 2 * t);
+                o[b][t][i] = fmaf(j.f[0], o[b][t][i], j.f[1] * v.x);
+                o[b][t][2 + i] = fmaf(j.f[0], o[b][t][2 + i], j.f[1] * v.y);
+                o[b][t + 1][i] = fmaf(j.f[0], o[b][t + 1][i], j.f[1] * v.z);
+                o[b][t + 1][2 + i] = fmaf(j.f[0], o[b][t + 1][2 + i], j.f[1] * v.w);
+              }
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw no key: zeros
+            __nv_bfloat16* dst = p.out + at * D + VD * g4;
 #pragma unroll
             for (int t = 0; t < NM; t += 4) {
               uint32_t v[4];
@@ -579,7 +603,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       }
     if (!whole) {
       const int2 own = kv8_owners<KA_COST>(sg, w - sg.len, runs);
-      if (lane == 0) meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, own.x, own.y, 0};
+      if (lane == 0) meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, own.x, own.y, sg.s.base};
     }
   }
   // a warp that gave up: copies still in flight land before the shared memory goes away
@@ -714,15 +738,26 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     }
     const int tok0 = pt.t << p.tq_shift;
     if (write && tid < ACT && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
-      const float unit = ex2(top);
       const int tok = row / p.G, hh = row - tok * p.G;
+      const size_t at = static_cast<size_t>(pt.off + tok0 + tok) * p.hq + pt.g * p.G + hh;
+      float unit = ex2(top);
+      if (MODE == KV8_SUFFIX && pt.base) {               // the row's shared positions
+        const float* src = p.rows + at * kv8_row_floats(D);
+        const Kv8Join j = kv8_join(make_float4(M, top, L, 0.0f), *reinterpret_cast<const float4*>(src + D));
+        const float4 v0 = *reinterpret_cast<const float4*>(src + d0), v1 = *reinterpret_cast<const float4*>(src + d0 + 4);
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) O[k] = fmaf(j.f[0], O[k], j.f[1] * v[k]);
+        L = j.sum;
+        unit = j.unit;
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
       uint4 r;
       r.x = pack_bf16x2(__float_as_uint(O[0] * inv * unit), __float_as_uint(O[1] * inv * unit));
       r.y = pack_bf16x2(__float_as_uint(O[2] * inv * unit), __float_as_uint(O[3] * inv * unit));
       r.z = pack_bf16x2(__float_as_uint(O[4] * inv * unit), __float_as_uint(O[5] * inv * unit));
       r.w = pack_bf16x2(__float_as_uint(O[6] * inv * unit), __float_as_uint(O[7] * inv * unit));
-      *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(pt.off + tok0 + tok) * p.hq + pt.g * p.G + hh) * D + d0) = r;
+      *reinterpret_cast<uint4*>(p.out + at * D + d0) = r;
     }
   }
 }
@@ -754,35 +789,64 @@ size_t kv8_ws_bytes(int D, int rows) {
   return KV8_TICKET_BYTES + static_cast<size_t>(KV8_MAX_CTAS) * 2 * rows * ka_ps(D) * sizeof(float);
 }
 
-template <int D, int R, int FMT>
+template <int D, int R, int FMT, int MODE>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8AttnParams& p, int box, int grid, int dev,
                           cudaStream_t s) {
   static bool set[KV8_MAX_DEVICES] = {};
-  auto* k = kv8_decode_kernel<D, R, FMT>;
+  constexpr bool suffix = MODE == KV8_SUFFIX;
+  auto* k = kv8_decode_kernel<D, R, FMT, MODE>;
   if (!set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ka_smem(D, R, KV8_MAX_SEQS));
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ka_smem(D, R, KV8_MAX_SEQS, suffix));
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  return launch_pdl(k, dim3(grid), dim3(ka_warps(R) * 32), ka_smem(D, R, p.b.n_seqs), s, tk, tv, p, box);
+  return launch_pdl(k, dim3(grid), dim3(ka_warps(R) * 32), ka_smem(D, R, p.b.n_seqs, suffix), s, tk, tv, p, box);
 }
 
-}  // namespace
-}  // namespace moe
-
-using namespace moe;
-
-extern "C" size_t gqa_kv8_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new) {
-  if (!cache || (cache->head_size != 64 && cache->head_size != 128) || cache->n_kv_heads < 1 || max_new < 1 ||
-      max_new > (1 << 20) || n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_q_heads / cache->n_kv_heads > 16)
-    return 0;
-  return kv8_ws_bytes(cache->head_size, ka_rows(n_q_heads / cache->n_kv_heads, max_new));
+// One pass of attention over the batch's sequences, by the kernel that suits R.
+template <int MODE>
+moe_status_t attend(const gqa_kv8_cache_t* cache, Kv8AttnParams p, int R, int grid, int dev, cudaStream_t s) {
+  const int D = cache->head_size;
+  cudaError_t e;
+  if (!R) {
+    e = launch_kv8_prompt<MODE>(p, D, cache->format, grid, dev, s);
+  } else {
+    p.tq_shift = floor_log2(R / p.G);
+    if (MODE == KV8_WINDOW) p.win_units = kv8_win_units(ka_u(R), 1 << p.tq_shift, p.window, p.sinks);
+    CUtensorMap tk, tv;
+    const uint64_t rows = static_cast<uint64_t>(cache->n_pages) * cache->n_kv_heads * cache->page_size;
+    const int box = cache->page_size >= ka_u(R) ? ka_u(R) : KV8_BLOCK;
+    if (!encode_u8_rows(&tk, cache->k_codes, D, rows, box) || !encode_u8_rows(&tv, cache->v_codes, D, rows, box))
+      return MOE_ERR_CUDA;
+    const bool e4 = cache->format == GQA_KV8_E4M3;
+    if (D == 128 && R == 8)
+      e = e4 ? launch_decode<128, 8, GQA_KV8_E4M3, MODE>(tk, tv, p, box, grid, dev, s)
+             : launch_decode<128, 8, GQA_KV8_INT8, MODE>(tk, tv, p, box, grid, dev, s);
+    else if (D == 128)
+      e = e4 ? launch_decode<128, 16, GQA_KV8_E4M3, MODE>(tk, tv, p, box, grid, dev, s)
+             : launch_decode<128, 16, GQA_KV8_INT8, MODE>(tk, tv, p, box, grid, dev, s);
+    else if (R == 8)
+      e = e4 ? launch_decode<64, 8, GQA_KV8_E4M3, MODE>(tk, tv, p, box, grid, dev, s)
+             : launch_decode<64, 8, GQA_KV8_INT8, MODE>(tk, tv, p, box, grid, dev, s);
+    else
+      e = e4 ? launch_decode<64, 16, GQA_KV8_E4M3, MODE>(tk, tv, p, box, grid, dev, s)
+             : launch_decode<64, 16, GQA_KV8_INT8, MODE>(tk, tv, p, box, grid, dev, s);
+  }
+  if (e != cudaSuccess) {
+    set_error_detail("attention over the 8-bit cache: launch", e);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
-extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch, const void* q,
-                                          long long q_stride, int n_q_heads, float scale, void* out, void* workspace,
-                                          size_t workspace_bytes, moe_stream_t stream) {
+// What the attention entries have in common: their checks, and the kernels' parameters.
+struct Kv8Call {
+  Kv8AttnParams p;
+  int R, grid, dev;
+};
+moe_status_t prepare(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch, const void* q, long long q_stride,
+                     int n_q_heads, float scale, void* out, void* workspace, Kv8Call* call) {
   moe_status_t st;
   if (!kv8_cache_ok(cache, &st) || !kv8_batch_ok(cache, batch, &st)) return st;
   if (n_q_heads < 1 || !workspace || !(scale >= 0.0f && scale <= 1e30f)) return MOE_ERR_INVALID_ARG;
@@ -795,24 +859,7 @@ extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gq
   const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
   const uintptr_t qn = 2 * (static_cast<uintptr_t>(batch->n_tokens - 1) * q_stride + width);
   if (q0 < o0 + 2 * static_cast<uintptr_t>(batch->n_tokens) * width && o0 < q0 + qn) return MOE_ERR_INVALID_ARG;
-  const int G = n_q_heads / cache->n_kv_heads, R = ka_rows(G, batch->max_new);
-  if (workspace_bytes < kv8_ws_bytes(D, R)) return MOE_ERR_WORKSPACE;
-
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev < 0 || dev >= KV8_MAX_DEVICES)) e = cudaErrorInvalidDevice;
-  static int sm_count[KV8_MAX_DEVICES] = {};
-  if (e == cudaSuccess && !sm_count[dev]) {
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) sm_count[dev] = sms;
-  }
-  if (e != cudaSuccess) {
-    set_error_detail("gqa_kv8_attention: device", e);
-    return MOE_ERR_CUDA;
-  }
-  const int grid = sm_count[dev] < KV8_MAX_CTAS ? sm_count[dev] : KV8_MAX_CTAS;
-
-  Kv8AttnParams p;
+  Kv8AttnParams& p = call->p;
   std::memset(&p, 0, sizeof p);
   p.c = kv8_cache(cache);
   p.b = kv8_batch(batch);
@@ -821,43 +868,113 @@ extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gq
   p.out = static_cast<__nv_bfloat16*>(out);
   p.out_wide = (o0 & 31u) == 0;
   p.hq = n_q_heads;
-  p.G = G;
-  p.tq_shift = R ? floor_log2(R / G) : 0;
+  p.G = n_q_heads / cache->n_kv_heads;
   p.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(D))) * 1.4426950408889634f;
   p.tickets = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KV8_TICKET_BYTES);
   p.wait_ns = wait_limit_ns();
-
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!R) {
-    e = launch_kv8_prompt(p, D, cache->format, grid, dev, s);
-    if (e != cudaSuccess) {
-      set_error_detail("gqa_kv8_attention: launch", e);
-      return MOE_ERR_CUDA;
-    }
-    return MOE_OK;
-  }
-  CUtensorMap tk, tv;
-  const uint64_t rows = static_cast<uint64_t>(cache->n_pages) * cache->n_kv_heads * cache->page_size;
-  const int box = cache->page_size >= ka_u(R) ? ka_u(R) : KV8_BLOCK;
-  if (!encode_u8_rows(&tk, cache->k_codes, D, rows, box) || !encode_u8_rows(&tv, cache->v_codes, D, rows, box))
-    return MOE_ERR_CUDA;
-  const bool e4 = cache->format == GQA_KV8_E4M3;
-  if (D == 128 && R == 8)
-    e = e4 ? launch_decode<128, 8, GQA_KV8_E4M3>(tk, tv, p, box, grid, dev, s)
-           : launch_decode<128, 8, GQA_KV8_INT8>(tk, tv, p, box, grid, dev, s);
-  else if (D == 128)
-    e = e4 ? launch_decode<128, 16, GQA_KV8_E4M3>(tk, tv, p, box, grid, dev, s)
-           : launch_decode<128, 16, GQA_KV8_INT8>(tk, tv, p, box, grid, dev, s);
-  else if (R == 8)
-    e = e4 ? launch_decode<64, 8, GQA_KV8_E4M3>(tk, tv, p, box, grid, dev, s)
-           : launch_decode<64, 8, GQA_KV8_INT8>(tk, tv, p, box, grid, dev, s);
-  else
-    e = e4 ? launch_decode<64, 16, GQA_KV8_E4M3>(tk, tv, p, box, grid, dev, s)
-           : launch_decode<64, 16, GQA_KV8_INT8>(tk, tv, p, box, grid, dev, s);
-  if (e != cudaSuccess) {
-    set_error_detail("gqa_kv8_attention: launch", e);
-    return MOE_ERR_CUDA;
-  }
+  call->R = ka_rows(p.G, batch->max_new);
   return MOE_OK;
+}
+moe_status_t find_device(Kv8Call* call) {
+  int sms = 0;
+  cudaError_t e = cudaGetDevice(&call->dev);
+  if (e == cudaSuccess && (call->dev < 0 || call->dev >= KV8_MAX_DEVICES)) e = cudaErrorInvalidDevice;
+  static int sm_count[KV8_MAX_DEVICES] = {};
+  if (e == cudaSuccess && !sm_count[call->dev]) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, call->dev);
+    if (e == cudaSuccess) sm_count[call->dev] = sms;
+  }
+  if (e != cudaSuccess) {
+    set_error_detail("attention over the 8-bit cache: device", e);
+    return MOE_ERR_CUDA;
+  }
+  call->grid = sm_count[call->dev] < KV8_MAX_CTAS ? sm_count[call->dev] : KV8_MAX_CTAS;
+  return MOE_OK;
+}
+
+bool heads_ok(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new) {
+  return cache && (cache->head_size == 64 || cache->head_size == 128) && cache->n_kv_heads >= 1 && max_new >= 1 &&
+         max_new <= (1 << 20) && n_q_heads >= 1 && n_q_heads % cache->n_kv_heads == 0 && n_q_heads / cache->n_kv_heads <= 16;
+}
+
+// Whether groups that hold `tokens` new tokens in all are worth a pass of their own over what they
+// share: with more than 32 query rows per key/value head and group in the mean.
+bool kv8_share(int G, int tokens, int groups) { return static_cast<long long>(G) * tokens > 32ll * groups; }
+
+// The workspace of attention with shared prefixes: that of either pass, then the prefix pass's rows.
+size_t kv8_prefix_rows_at(int D, int R) {
+  const size_t a = kv8_ws_bytes(D, R), b = kv8_prompt_ws_bytes(D);
+  return ((a > b ? a : b) + 255) / 256 * 256;
+}
+size_t kv8_prefix_ws_bytes(int D, int R, int hq, int tokens) {
+  return kv8_prefix_rows_at(D, R) + static_cast<size_t>(tokens) * hq * kv8_row_floats(D) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t gqa_kv8_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new) {
+  if (!heads_ok(cache, n_q_heads, max_new)) return 0;
+  return kv8_ws_bytes(cache->head_size, ka_rows(n_q_heads / cache->n_kv_heads, max_new));
+}
+
+extern "C" moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch, const void* q,
+                                          long long q_stride, int n_q_heads, float scale, void* out, void* workspace,
+                                          size_t workspace_bytes, moe_stream_t stream) {
+  Kv8Call c;
+  moe_status_t st = prepare(cache, batch, q, q_stride, n_q_heads, scale, out, workspace, &c);
+  if (st != MOE_OK || batch->n_tokens == 0) return st;
+  if (workspace_bytes < kv8_ws_bytes(cache->head_size, c.R)) return MOE_ERR_WORKSPACE;
+  if ((st = find_device(&c)) != MOE_OK) return st;
+  return attend<KV8_CAUSAL>(cache, c.p, c.R, c.grid, c.dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status_t gqa_kv8_window_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch, const void* q,
+                                                 long long q_stride, int n_q_heads, float scale, int window, int sinks,
+                                                 void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  Kv8Call c;
+  if (window < 1 || window > (1 << 24) || sinks < 0 || sinks > (1 << 24)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = prepare(cache, batch, q, q_stride, n_q_heads, scale, out, workspace, &c);
+  if (st != MOE_OK || batch->n_tokens == 0) return st;
+  if (workspace_bytes < kv8_ws_bytes(cache->head_size, c.R)) return MOE_ERR_WORKSPACE;
+  if ((st = find_device(&c)) != MOE_OK) return st;
+  c.p.window = window;
+  c.p.sinks = sinks;
+  return attend<KV8_WINDOW>(cache, c.p, c.R, c.grid, c.dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t gqa_kv8_prefix_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new, int n_tokens) {
+  if (!heads_ok(cache, n_q_heads, max_new) || n_tokens < 1 || n_tokens > (1 << 20)) return 0;
+  return kv8_prefix_ws_bytes(cache->head_size, ka_rows(n_q_heads / cache->n_kv_heads, max_new), n_q_heads, n_tokens);
+}
+
+extern "C" moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch,
+                                                 const gqa_kv8_prefix_t* prefix, const void* q, long long q_stride,
+                                                 int n_q_heads, float scale, void* out, void* workspace,
+                                                 size_t workspace_bytes, moe_stream_t stream) {
+  Kv8Call c;
+  if (!prefix || !prefix->groups || !prefix->shared || prefix->n_groups < 1 || prefix->n_groups > KV8_MAX_SEQS)
+    return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(prefix->groups) | reinterpret_cast<uintptr_t>(prefix->shared)) & 3u)
+    return MOE_ERR_ALIGNMENT;
+  moe_status_t st = prepare(cache, batch, q, q_stride, n_q_heads, scale, out, workspace, &c);
+  if (st != MOE_OK || batch->n_tokens == 0) return st;
+  const int D = cache->head_size;
+  if (workspace_bytes < kv8_prefix_ws_bytes(D, c.R, n_q_heads, batch->n_tokens)) return MOE_ERR_WORKSPACE;
+  if ((st = find_device(&c)) != MOE_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!kv8_share(c.p.G, batch->n_tokens, prefix->n_groups)) return attend<KV8_CAUSAL>(cache, c.p, c.R, c.grid, c.dev, s);
+  c.p.groups = prefix->groups;
+  c.p.shared = prefix->shared;
+  c.p.n_groups = prefix->n_groups;
+  c.p.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv8_prefix_rows_at(D, c.R));
+  const cudaError_t e = launch_kv8_prompt<KV8_PREFIX>(c.p, D, cache->format, c.grid, c.dev, s);
+  if (e != cudaSuccess) {
+    set_error_detail("gqa_kv8_prefix_attention: launch", e);
+    return MOE_ERR_CUDA;
+  }
+  return attend<KV8_SUFFIX>(cache, c.p, c.R, c.grid, c.dev, s);
 }

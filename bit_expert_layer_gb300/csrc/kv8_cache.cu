@@ -213,7 +213,35 @@ struct RopeParams {
   uint32_t inv_heads;            // th / heads = th inv_heads >> 21 for th < 4 heads, heads <= 512
   uint64_t turn[GQA_ROPE_MAX_PAIRS];
   uint8_t axis[GQA_ROPE_MAX_PAIRS];
+  const void* weight[2];         // norms: of the q heads, the k heads (null: ones)
+  int weight_f32;
+  float eps, offset;
 };
+
+// Sums of squares between these need no care: none of their terms that matter left fp32's range.
+constexpr float NORM_LEAST = 0x1p-80f;
+constexpr float NORM_LEAST_EPS = 0x1p-60f;       // beside it, smaller sums do not matter
+
+// A head whose squares leave fp32 (magnitudes over 2^60 or under 2^-45): the norm in 64 bits, on
+// the head's 2^D8 lanes.  Infinities make the others zeros and themselves NaN, as the formula does.
+template <int IPH>
+__device__ __noinline__ void norm_far(uint4& a, uint4& b, float (&x)[16], uint32_t mask, float eps, int D) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double lo = bf16lo(w[j]), hi = bf16hi(w[j]);
+    sum += lo * lo + hi * hi;
+  }
+#pragma unroll
+  for (int m = IPH / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
+  const double root = sqrt(sum / D + eps), r = root == 0.0 ? 0.0 : 1.0 / root;     // zeros with eps 0 stay zeros
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[2 * j] = static_cast<float>(bf16lo(w[j]) * r);
+    x[2 * j + 1] = static_cast<float>(bf16hi(w[j]) * r);
+  }
+}
 
 }  // namespace
 
@@ -222,12 +250,17 @@ struct RopeParams {
 // tokens once into shared memory and turns all heads with them.  Its work items are two
 // 16-byte chunks of a head: chunk i with chunk i + half / 8 of the rotated part, or two
 // chunks of the part that passes through.
-template <int D>
+//
+// With NORM every head is first divided by its root mean square and multiplied by its weights, in
+// fp32 and without a rounding between: the D / 16 threads of a head, neighbours in a warp, add
+// their squares by shuffles.
+template <int D, bool NORM>
 __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ float s_cs[];        // [tokens][half] cosines, then sines
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
   float* s_cos = s_cs;
   float* s_sin = s_cs + p.tokens * p.half;
+  float* s_w = s_sin + p.tokens * p.half;                // [2][D] weights, as factors
   constexpr int IPH = D / 16;            // items per head
   constexpr int NB = 3;                  // items of a thread in flight: 4 tokens of 18 heads of 128
   const int rot_items = p.half / 8, nh = p.heads[0] + p.heads[1], n = nt * nh * IPH;
@@ -235,6 +268,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     const __nv_bfloat16* src;
     __nv_bfloat16* dst;
     int ca, cb, at;                      // its chunks' first elements; of its sines, or -1
+    int which;                           // q, k
   };
   const auto item = [&](int i) {
     Item r;
@@ -242,6 +276,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     const int t = static_cast<int>((static_cast<uint32_t>(th) * p.inv_heads) >> 21), hh = th - t * nh;
     const int which = hh >= p.heads[0];
     const int h = which ? hh - p.heads[0] : hh;
+    r.which = which;
     r.src = p.in[which] + static_cast<size_t>(t0 + t) * p.in_stride[which] + h * D;
     r.dst = p.out[which] + static_cast<size_t>(t0 + t) * p.out_stride[which] + h * D;
     const bool rot = part < rot_items;
@@ -273,6 +308,15 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     s_cos[i] = c;
     s_sin[i] = s;
   }
+  if constexpr (NORM) {
+    for (int i = threadIdx.x; i < 2 * D; i += RP_THREADS) {
+      const void* w = p.weight[i / D];
+      float v = 1.0f;
+      if (w) v = (p.weight_f32 ? __ldg(static_cast<const float*>(w) + i % D)
+                               : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i % D))) + p.offset;
+      s_w[i] = v;
+    }
+  }
   __syncthreads();
   for (int i0 = threadIdx.x; i0 < n; i0 += NB * RP_THREADS) {
     if (i0 != threadIdx.x) load(i0);
@@ -281,7 +325,49 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
       const int i = i0 + k * RP_THREADS;
       if (i >= n) break;
       const Item r = item(i);
-      if (r.at >= 0) {
+      if constexpr (NORM) {
+        const uint32_t w[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
+        float x[16];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[2 * j] = bf16lo(w[j]);
+          x[2 * j + 1] = bf16hi(w[j]);
+          sum = fmaf(x[2 * j], x[2 * j], fmaf(x[2 * j + 1], x[2 * j + 1], sum));
+        }
+        // the head's threads only: others of the warp may be past the end
+        const uint32_t mask = ((1u << IPH) - 1) << (threadIdx.x & 31 & ~(IPH - 1));
+#pragma unroll
+        for (int m = IPH / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
+        if (sum <= 0x1p120f && (sum >= NORM_LEAST || p.eps >= NORM_LEAST_EPS)) {
+          const float f = rsqrtf(fmaf(sum, 1.0f / D, p.eps));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] *= f;
+        } else {
+          norm_far<IPH>(a[k], b[k], x, mask, p.eps, D);
+        }
+        const float* wt = s_w + r.which * D;
+        const float *wa = wt + r.ca, *wb = wt + r.cb;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float4 va = *reinterpret_cast<const float4*>(wa + j), vb = *reinterpret_cast<const float4*>(wb + j);
+          x[j] *= va.x, x[j + 1] *= va.y, x[j + 2] *= va.z, x[j + 3] *= va.w;
+          x[8 + j] *= vb.x, x[9 + j] *= vb.y, x[10 + j] *= vb.z, x[11 + j] *= vb.w;
+        }
+        if (r.at >= 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float c = s_cos[r.at + j], s = s_sin[r.at + j], u = x[j], v = x[8 + j];
+            x[j] = u * c - v * s;
+            x[8 + j] = v * c + u * s;
+          }
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(__float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]));
+        a[k] = make_uint4(o[0], o[1], o[2], o[3]);
+        b[k] = make_uint4(o[4], o[5], o[6], o[7]);
+      } else if (r.at >= 0) {
         uint32_t *wa = &a[k].x, *wb = &b[k].x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -481,10 +567,11 @@ extern "C" moe_status_t gqa_rope_plan_init(gqa_rope_plan_t* plan, int head_size,
   return MOE_OK;
 }
 
-extern "C" moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, long long q_stride, int n_q_heads,
-                                 const void* k, long long k_stride, int n_k_heads, const int32_t* pos, int T,
-                                 void* q_out, long long q_out_stride, void* k_out, long long k_out_stride,
-                                 moe_stream_t stream) {
+namespace {
+
+moe_status_t rope_launch(const gqa_rope_plan_t* plan, const gqa_norm_t* norm, const void* q, long long q_stride, int n_q_heads,
+                         const void* k, long long k_stride, int n_k_heads, const int32_t* pos, int T, void* q_out,
+                         long long q_out_stride, void* k_out, long long k_out_stride, moe_stream_t stream) {
   if (!plan || T < 0 || T > (1 << 20) || n_q_heads < 1 || n_q_heads > 256 || n_k_heads < 0 || n_k_heads > 256)
     return MOE_ERR_INVALID_ARG;
   const int D = plan->head_size;
@@ -498,6 +585,16 @@ extern "C" moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, lon
     if (plan->axis[j] >= plan->n_axes) return MOE_ERR_INVALID_ARG;
     p.turn[j] = plan->turn[j];
     p.axis[j] = plan->axis[j];
+  }
+  if (norm) {
+    if (!(norm->eps >= 0.0f && norm->eps <= 1e30f) || !(std::fabs(norm->offset) <= 1e30f)) return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(norm->q_weight) | reinterpret_cast<uintptr_t>(norm->k_weight)) & (norm->weight_f32 ? 3u : 1u))
+      return MOE_ERR_ALIGNMENT;
+    p.weight[0] = norm->q_weight;
+    p.weight[1] = norm->k_weight;
+    p.weight_f32 = norm->weight_f32;
+    p.eps = norm->eps;
+    p.offset = norm->offset;
   }
   if (T == 0) return MOE_OK;
   if (!pos) return MOE_ERR_INVALID_ARG;
@@ -527,12 +624,33 @@ extern "C" moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, lon
   p.tokens = T >= 1024 ? 4 : 1;
   p.inv_heads = ((1u << 21) + n_q_heads + n_k_heads - 1) / (n_q_heads + n_k_heads);
   const dim3 grid((T + p.tokens - 1) / p.tokens);
-  const size_t smem = 2ull * p.tokens * p.half * sizeof(float);
+  const size_t smem = (2ull * p.tokens * p.half + (norm ? 2 * D : 0)) * sizeof(float);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_pdl(D == 128 ? rope_kernel<128> : rope_kernel<64>, grid, dim3(RP_THREADS), smem, s, p);
+  auto* kernel = norm ? (D == 128 ? rope_kernel<128, true> : rope_kernel<64, true>)
+                      : (D == 128 ? rope_kernel<128, false> : rope_kernel<64, false>);
+  const cudaError_t e = launch_pdl(kernel, grid, dim3(RP_THREADS), smem, s, p);
   if (e != cudaSuccess) {
-    set_error_detail("gqa_rope: launch", e);
+    set_error_detail(norm ? "gqa_norm_rope: launch" : "gqa_rope: launch", e);
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, long long q_stride, int n_q_heads,
+                                 const void* k, long long k_stride, int n_k_heads, const int32_t* pos, int T,
+                                 void* q_out, long long q_out_stride, void* k_out, long long k_out_stride,
+                                 moe_stream_t stream) {
+  return rope_launch(plan, nullptr, q, q_stride, n_q_heads, k, k_stride, n_k_heads, pos, T, q_out, q_out_stride, k_out,
+                     k_out_stride, stream);
+}
+
+extern "C" moe_status_t gqa_norm_rope(const gqa_rope_plan_t* plan, const gqa_norm_t* norm, const void* q, long long q_stride,
+                                      int n_q_heads, const void* k, long long k_stride, int n_k_heads, const int32_t* pos,
+                                      int T, void* q_out, long long q_out_stride, void* k_out, long long k_out_stride,
+                                      moe_stream_t stream) {
+  if (!norm) return MOE_ERR_INVALID_ARG;
+  return rope_launch(plan, norm, q, q_stride, n_q_heads, k, k_stride, n_k_heads, pos, T, q_out, q_out_stride, k_out,
+                     k_out_stride, stream);
 }

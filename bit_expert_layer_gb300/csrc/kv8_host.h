@@ -19,6 +19,7 @@ Kv8Batch kv8_batch(const gqa_kv8_batch_t* b);
 // Attention with many query rows per key/value head (kv8_prompt.cu): its workspace, and its
 // launch on `grid` CTAs of device `dev` (sets p.tq_shift itself).
 size_t kv8_prompt_ws_bytes(int D);
+template <int MODE>
 cudaError_t launch_kv8_prompt(Kv8AttnParams p, int D, int format, int grid, int dev, cudaStream_t s);
 
 }  // namespace moe

@@ -57,11 +57,12 @@ constexpr float KP_LOW = -7.0f;                   // 128 positions: 128 * 2^-25 
 // keeps every bit of its codes (e4m3's smallest is 2^-9: 2^(-9 + 6 - 21) = 2^-24).
 __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 ? 6 : 5; }
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
-__host__ __device__ constexpr int kp_smem(int D, int B) {
+__host__ __device__ constexpr int kp_smem(int D, int B, bool suffix) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 12 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128;
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 12 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128 +
+         (suffix ? B * 4 : 0);
 }
-static_assert(kp_smem(128, KV8_MAX_SEQS) <= 232448, "shared memory per CTA exceeds 227 KB");
+static_assert(kp_smem(128, KV8_MAX_SEQS, true) <= 232448, "shared memory per CTA exceeds 227 KB");
 
 // barriers: two each of the K and V buffers (full, empty) and of the row blocks, the end, and one
 // per plan slot (full, empty)
@@ -171,14 +172,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // registers for the loop fell out, with changing inputs up to 486; now 401 and 409.  (Heads of 64
 // are better off with the mask inside: 16 prompts of 512 tokens 43.6 us, 45.7 without.)
 //
-// What a row does not see of a tile becomes -inf: positions from `left` on, blocks of `bad`.
-__device__ __forceinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad) {
+// What a row does not see of a tile becomes -inf: positions from `left` on, blocks of `bad`, in
+// window mode those under `before` that are not under `sinks`.
+__device__ __forceinline__ uint32_t kp_under(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+template <int MODE>
+__device__ __forceinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad, int before, int sinks) {
   uint32_t x[32];
 #pragma unroll 1
   for (int c = 0; c < KP_U / 32; ++c) {
     tmem_ld32(t_s + 32 * c, x);
-    const int n = left - 32 * c;
-    uint32_t seen = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+    uint32_t seen = kp_under(left - 32 * c);
+    if (MODE == KV8_WINDOW) seen &= ~kp_under(before - 32 * c) | kp_under(sinks - 32 * c);
     if ((bad >> (2 * c)) & 1) seen &= 0xFFFF0000u;
     if ((bad >> (2 * c + 1)) & 1) seen &= 0x0000FFFFu;
     tmem_ld_wait();
@@ -189,7 +193,10 @@ __device__ __forceinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad) {
   }
   tmem_st_wait();
 }
-__device__ __noinline__ void kp_mask_apart(uint32_t t_s, int left, uint32_t bad) { kp_mask(t_s, left, bad); }
+template <int MODE>
+__device__ __noinline__ void kp_mask_apart(uint32_t t_s, int left, uint32_t bad, int before, int sinks) {
+  kp_mask<MODE>(t_s, left, bad, before, sinks);
+}
 // The sum of a row's terms 2^(f x + add) of one tile.
 __device__ __noinline__ float kp_bare_sum(uint32_t t_s, float f, float add) {
   float sum = 0.0f;
@@ -277,12 +284,13 @@ __device__ __forceinline__ uint32_t kv8_half2_scaled(uint32_t w, int hi, uint32_
 struct __align__(16) KpTile {
   int ns;                // CTAs (0: no such tile)
   int t, g, off, n;      // tile, key/value head, the sequence's first row and new tokens
-  int pad[3];
+  int base;              // positions that the prefix pass has seen to
+  int pad[2];
 };
 
 // Workspace of a part: floats of a row (O, references, normaliser), the rows of CTA c's part of
 // a tile that began in CTA c_first, and the tiles to join, one entry per CTA.
-__host__ __device__ constexpr int kp_ps(int D) { return D + 8; }      // 32-byte rows
+__host__ __device__ constexpr int kp_ps(int D) { return kv8_row_floats(D); }
 constexpr size_t KP_TILES_BYTES = KV8_MAX_CTAS * sizeof(KpTile);
 __device__ __forceinline__ KpTile* kp_tiles(float* part) { return reinterpret_cast<KpTile*>(part); }
 template <int D>
@@ -294,7 +302,7 @@ __device__ __forceinline__ float* kp_slot(float* part, int c, int c_first, int r
 }  // namespace
 
 // nblk: row blocks per CTA tile (1 or 2); p.tq_shift counts the tokens of all of them.
-template <int D, int FMT>
+template <int D, int FMT, int MODE>
 __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_constant__ Kv8AttnParams p, int nblk) {
   constexpr int TILE = kp_tile(D);
   constexpr int BOX = KP_U * 128;               // bytes of 64 dims of a tile
@@ -310,11 +318,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   float* s_ms = s_rs + 2 * KP_ROWS;                                // [256] a row's reference, while it is far or none
   float* s_peak = s_ms + 2 * KP_ROWS;                              // [256] the highest ms + d of a row
   long long* prefix = reinterpret_cast<long long*>(s_peak + 2 * KP_ROWS);
-  long long* s_warp = prefix + p.b.n_seqs + 1;
+  long long* s_warp = prefix + kv8_items<MODE>(p) + 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(abort_flag) + 1);
   volatile int* s_n = reinterpret_cast<volatile int*>(s_tmem + 1);    // [2]
+  int* base = reinterpret_cast<int*>(s_tmem + 3);                     // suffix mode: [n_seqs]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * i; };
@@ -340,7 +349,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   }
   grid_dep_wait();                              // what follows reads and writes what earlier kernels wrote
   Kv8Runs runs;
-  runs.total = kv8_line<KP_U, KP_COST, KP_THREADS>(p, prefix, s_warp);
+  runs.total = kv8_line<KP_U, KP_COST, KP_THREADS, MODE>(p, prefix, s_warp, base);
   runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x)));
   const int cta = blockIdx.x;
   if (cta >= runs.n) {                          // the whole CTA, before any TMEM is held
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     return;
   }
   const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
-  const Kv8Seg first = kv8_seg<KP_U, KP_COST>(p, prefix, w_beg, w_end);   // where every role begins
+  const Kv8Seg first = kv8_seg<KP_U, KP_COST, MODE>(p, prefix, base, w_beg, w_end);   // where every role begins
   if (warp == 8 + KP_DEQ) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
@@ -375,14 +384,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       Kv8Seg sg = first;
 #pragma unroll 1
       for (long long w = w_beg; w < w_end;) {
-        if (w > w_beg) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
+        if (w > w_beg) kv8_next<KP_U, KP_COST, MODE>(sg, p, prefix, base, w, w_end);
         w += sg.len;
         if (sg.u1 <= sg.u0) continue;      // the run ends before the tile's first positions
         const int tok0 = (sg.t << p.tq_shift) + blk * blk_tokens;
         const int tr = (r * inv_g) >> 16, tok = tok0 + tr, hh = r - tr * p.G;
         const bool live = tr < blk_tokens && tok < sg.s.n;
         // positions that the row sees; a row without a token (zeros) needs no mask
-        const int see = live ? sg.s.first + tok + 1 : 1 << 30;
+        const int see = live && MODE != KV8_PREFIX ? sg.s.first + tok + 1 : 1 << 30;
         // ---- the warp's 32 query rows, scaled into fp16, into the swizzled tile: a row per
         // D / 8 lanes, so that loads and stores are whole lines
         {
@@ -437,16 +446,19 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           const float4 sc4 = s_scale[it & (KP_SLOTS - 1)];
           const float f = fminf(fmaxf(rs * sc4.x, 1e-37f), KV8_MAX_FACTOR), e = sc4.y;  // positive: -inf stays -inf
           const uint32_t bad = __float_as_uint(sc4.w);
-          const int left = see - u * KP_U;                       // positions of the tile that the row sees
+          const int at_u = kv8_unit<KP_U, MODE>(sg, u) * KP_U;
+          const int left = see - at_u;                           // positions of the tile that the row sees
+          // window mode: those of the tile before the window, and those of the sinks
+          const int before = MODE == KV8_WINDOW && live ? left - p.window : 0, sinks = MODE == KV8_WINDOW ? p.sinks - at_u : 0;
           uint32_t sc[2][32];
           // A tile at the causal edge, or with a page missing: what the row does not see becomes
           // -inf in TMEM first, so that the passes below carry no mask (with it in them, the
           // compiler masked every tile: 767 us against 557).
-          if (__any_sync(0xffffffffu, left < KP_U) || bad) {
+          if (__any_sync(0xffffffffu, left < KP_U || (MODE == KV8_WINDOW && max(sinks, 0) < min(before, KP_U))) || bad) {
             if constexpr (D == 64)
-              kp_mask(t_s, left, bad);
+              kp_mask<MODE>(t_s, left, bad, before, sinks);
             else
-              kp_mask_apart(t_s, left, bad);
+              kp_mask_apart<MODE>(t_s, left, bad, before, sinks);
           }
           // The scores are read twice, 32 columns at a time, the next ones while these are worked
           // on: 128 of them in registers do not fit beside the rest.  (One pass against the
@@ -532,12 +544,19 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         wait(BAR_PV + blk, it - 1);
         tc_fence_after();
         const bool whole = sg.u0 == 0 && sg.u1 == sg.units;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // a row that saw no key: zeros
         const float ms = ms_ref == -INFINITY ? s_ms[tid] : ms_ref;
         const float d = ms_ref == -INFINITY ? m_ref : m_ref - ms;
-        const float unit = ex2(d);                               // of the weights, in the normaliser's
-        __nv_bfloat16* dst =
-            live ? p.out + (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh) * D : nullptr;
+        float unit = ex2(d);                                     // of the weights, in the normaliser's
+        const size_t at = (static_cast<size_t>(sg.s.off + tok) * p.hq + sg.g * p.G + hh);
+        __nv_bfloat16* dst = live ? p.out + at * D : nullptr;
+        // the row's shared positions: where the prefix pass leaves them, and where the suffix pass finds them
+        float* const row = MODE == KV8_PREFIX || MODE == KV8_SUFFIX ? p.rows + at * kv8_row_floats(D) : nullptr;
+        Kv8Join jn = {l, {1.0f, 0.0f}, unit};
+        if (MODE == KV8_SUFFIX && sg.s.base && live) {
+          jn = kv8_join(make_float4(ms, d, l, 0.0f), *reinterpret_cast<const float4*>(row + D));
+          unit = jn.unit;
+        }
+        const float inv = jn.sum == 0.0f ? 0.0f : 1.0f / jn.sum; // a row that saw no key: zeros
         const int2 own = whole ? make_int2(cta, cta) : kv8_owners<KP_COST>(sg, w - sg.len, runs);
         float* part = kp_slot<D>(p.part, cta, own.x, blk * KP_ROWS + r);
 #pragma unroll 1
@@ -545,14 +564,27 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           uint32_t o[32];
           tmem_ld32(t_o + 32 * c, o);
           tmem_ld_wait();
-          if (whole) {
+          if (whole && MODE == KV8_PREFIX) {
+            if (dst && !dead)
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) st_global_v8(row + 32 * c + j, o + j);
+          } else if (whole) {
+            if (MODE == KV8_SUFFIX && sg.s.base && live)
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(row + 32 * c + j);
+                o[j] = __float_as_uint(fmaf(jn.f[0], __uint_as_float(o[j]), jn.f[1] * v.x));
+                o[j + 1] = __float_as_uint(fmaf(jn.f[0], __uint_as_float(o[j + 1]), jn.f[1] * v.y));
+                o[j + 2] = __float_as_uint(fmaf(jn.f[0], __uint_as_float(o[j + 2]), jn.f[1] * v.z));
+                o[j + 3] = __float_as_uint(fmaf(jn.f[0], __uint_as_float(o[j + 3]), jn.f[1] * v.w));
+              }
             if (dst && !dead)
 #pragma unroll
               for (int j = 0; j < 32; j += 16) {
                 uint32_t x[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                  x[k] = l == 0.0f ? 0u
+                  x[k] = jn.sum == 0.0f ? 0u
                                    : pack_bf16x2(__float_as_uint(__uint_as_float(o[j + 2 * k]) * inv * unit),
                                                  __float_as_uint(__uint_as_float(o[j + 2 * k + 1]) * inv * unit));
                 if (p.out_wide) {
@@ -571,7 +603,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!whole) {
           *reinterpret_cast<float4*>(part + D) = make_float4(ms, d, l, 0.0f);
           if (tid == 0 && own.x == cta)
-            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, {0, 0, 0}};
+            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, sg.s.base, {0, 0}};
+        } else if (MODE == KV8_PREFIX && live && !dead) {
+          *reinterpret_cast<float4*>(row + D) = make_float4(ms, d, l, 0.0f);
         }
         ++seg;
       }
@@ -653,22 +687,24 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       int it = 0;
 #pragma unroll 1
       for (long long w = w_beg; ok; w += sg.len) {
-        if (w > w_beg && w < w_end) kv8_next<KP_U, KP_COST>(sg, p, prefix, w, w_end);
+        if (w > w_beg && w < w_end) kv8_next<KP_U, KP_COST, MODE>(sg, p, prefix, base, w, w_end);
         const bool more = w < w_end;
-        const int end = kv8_seg_end(sg, p.tq_shift);
-        const int* table = p.b.page_table + static_cast<size_t>(sg.b) * p.b.max_pages;
+        const int end = kv8_seg_end<MODE>(sg, p.tq_shift);
+        const int* table = kv8_table<MODE>(p, sg.b);
         int u = more ? sg.u0 : 0;
         const int u1 = more ? sg.u1 : 1;               // at the end one more plan: no more tiles
         int pid = -1;
         const auto look = [&] {
-          const int pos = u * KP_U + lb * KV8_BLOCK;
+          const int pos = kv8_unit<KP_U, MODE>(sg, u) * KP_U + lb * KV8_BLOCK;
           pid = more && u < u1 && pos < end ? __ldg(table + (pos >> p.c.page_shift)) : -1;
         };
         look();
 #pragma unroll 1
         while (u < u1) {
-          const int pos = u * KP_U + lb * KV8_BLOCK;
-          const bool exists = more && pos < end, bad = exists && (pid < 0 || pid >= p.c.n_pages);
+          const int at_u = kv8_unit<KP_U, MODE>(sg, u) * KP_U, pos = at_u + lb * KV8_BLOCK;
+          // (a block that no token of the tile sees is left out: its page may be gone)
+          const bool exists = more && pos < end && (MODE != KV8_WINDOW || pos < p.sinks || pos + KV8_BLOCK > sg.low);
+          const bool bad = exists && (pid < 0 || pid >= p.c.n_pages);
           int row = -1;
           float scale = 0.0f;
           if (exists && !bad) {
@@ -677,7 +713,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           }
           // A sequence with fewer positions than new tokens has units past its end: nothing valid
           // in them, which is not the mark of the end.
-          const int valid = more ? max(end - u * KP_U, 0) : -1;
+          const int valid = more ? max(end - at_u, 0) : -1;
           ++u;
           look();                                      // the next tile's pages meanwhile
           const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xFFu;
@@ -808,7 +844,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 // Joins the parts of the tiles that lie in several CTAs: a block per tile (by its first CTA)
 // and 8 rows, a warp per row, the parts in the order of the line.  (The last CTA of a tile
 // joining them itself took over 60 us of a 150 us prompt: 256 rows by one CTA's 8 warps.)
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk) {
   grid_dep_wait();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
@@ -902,9 +938,25 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
       }
     }
   }
+  float unit = ex2(top);
+  const size_t at = static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G;
+  if constexpr (MODE == KV8_PREFIX) {
+    float* to = p.rows + at * kv8_row_floats(D);
+#pragma unroll
+    for (int k = 0; k < PL; ++k) to[PL * lane + k] = O[k];
+    if (lane == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, top, L, 0.0f);
+    return;
+  }
+  if (MODE == KV8_SUFFIX && tl.base) {             // the row's shared positions
+    const float* src = p.rows + at * kv8_row_floats(D);
+    const Kv8Join j = kv8_join(make_float4(M, top, L, 0.0f), *reinterpret_cast<const float4*>(src + D));
+#pragma unroll
+    for (int k = 0; k < PL; ++k) O[k] = fmaf(j.f[0], O[k], j.f[1] * src[PL * lane + k]);
+    L = j.sum;
+    unit = j.unit;
+  }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
-  const float unit = ex2(top);
-  __nv_bfloat16* dst = p.out + (static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G) * D + PL * lane;
+  __nv_bfloat16* dst = p.out + at * D + PL * lane;
 #pragma unroll
   for (int k = 0; k < PL; k += 2)
     *reinterpret_cast<uint32_t*>(dst + k) =
@@ -918,31 +970,42 @@ size_t kv8_prompt_ws_bytes(int D) {
 }
 
 namespace {
-template <int D, int FMT>
+template <int D, int FMT, int MODE>
 cudaError_t launch_prompt(const Kv8AttnParams& p, int nblk, int grid, int dev, cudaStream_t s) {
   static bool set[KV8_MAX_DEVICES] = {};
-  auto* k = kv8_prompt_kernel<D, FMT>;
+  auto* k = kv8_prompt_kernel<D, FMT, MODE>;
   if (!set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kp_smem(D, KV8_MAX_SEQS));
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kp_smem(D, KV8_MAX_SEQS, MODE == KV8_SUFFIX));
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  const cudaError_t e = launch_pdl(k, dim3(grid), dim3(KP_THREADS), kp_smem(D, p.b.n_seqs), s, p, nblk);
+  const cudaError_t e = launch_pdl(k, dim3(grid), dim3(KP_THREADS),
+                                   kp_smem(D, MODE == KV8_PREFIX ? p.n_groups : p.b.n_seqs, MODE == KV8_SUFFIX), s, p, nblk);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_prompt_join_kernel<D>, dim3(grid, nblk * KP_ROWS / 8), dim3(256), 0, s, p, nblk);
+  return launch_pdl(kv8_prompt_join_kernel<D, MODE == KV8_WINDOW ? KV8_CAUSAL : MODE>, dim3(grid, nblk * KP_ROWS / 8), dim3(256),
+                    0, s, p, nblk);
 }
 }  // namespace
 
+template <int MODE>
 cudaError_t launch_kv8_prompt(Kv8AttnParams p, int D, int format, int grid, int dev, cudaStream_t s) {
   // tokens of a row block: the largest power of two whose rows fit
   int shift = 0;
   while ((2 << shift) * p.G <= KP_ROWS) ++shift;
-  const int nblk = p.b.max_new <= (1 << shift) ? 1 : 2;
+  const int nblk = (MODE == KV8_PREFIX ? p.b.n_tokens : p.b.max_new) <= (1 << shift) ? 1 : 2;
   p.tq_shift = shift + nblk - 1;
+  if (MODE == KV8_WINDOW) p.win_units = kv8_win_units(KP_U, 1 << p.tq_shift, p.window, p.sinks);
   const bool e4 = format == GQA_KV8_E4M3;
   if (D == 128)
-    return e4 ? launch_prompt<128, GQA_KV8_E4M3>(p, nblk, grid, dev, s) : launch_prompt<128, GQA_KV8_INT8>(p, nblk, grid, dev, s);
-  return e4 ? launch_prompt<64, GQA_KV8_E4M3>(p, nblk, grid, dev, s) : launch_prompt<64, GQA_KV8_INT8>(p, nblk, grid, dev, s);
+    return e4 ? launch_prompt<128, GQA_KV8_E4M3, MODE>(p, nblk, grid, dev, s)
+              : launch_prompt<128, GQA_KV8_INT8, MODE>(p, nblk, grid, dev, s);
+  return e4 ? launch_prompt<64, GQA_KV8_E4M3, MODE>(p, nblk, grid, dev, s)
+            : launch_prompt<64, GQA_KV8_INT8, MODE>(p, nblk, grid, dev, s);
 }
+template cudaError_t launch_kv8_prompt<KV8_CAUSAL>(Kv8AttnParams, int, int, int, int, cudaStream_t);
+template cudaError_t launch_kv8_prompt<KV8_WINDOW>(Kv8AttnParams, int, int, int, int, cudaStream_t);
+template cudaError_t launch_kv8_prompt<KV8_PREFIX>(Kv8AttnParams, int, int, int, int, cudaStream_t);
+template cudaError_t launch_kv8_prompt<KV8_SUFFIX>(Kv8AttnParams, int, int, int, int, cudaStream_t);
 
 }  // namespace moe

@@ -21,6 +21,17 @@
 // Starting a tile costs as much as some units (its queries are fetched, its result written),
 // so each has C more units in the line than positions to see; they come first, and a run
 // that ends inside them leaves the tile to the next.
+//
+// The four modes differ in the positions that a tile's units stand for:
+//   causal   0 up to the tile's last token
+//   window   those of a sliding window and the first `sinks`, as whole units: the sinks' come first,
+//            then the window's.  The line counts a tile's units by a bound that needs no search,
+//            the causal count or K = ceil((W + TQ - 1 + U - 1) / U) + ceil(sinks / U), whichever is
+//            less; what a tile has less than that are units without positions at its end, which
+//            no run works on.
+//   prefix   the line's items are groups of sequences, an item's tokens those of all of the group's
+//            sequences, and every token sees all of the group's shared positions
+//   suffix   causal, from the first position on that the prefix pass left
 #pragma once
 
 #include "kv8.cuh"
@@ -30,6 +41,9 @@ namespace moe {
 constexpr int KV8_MAX_CTAS = 160;
 constexpr int KV8_MAX_DEVICES = 64;
 constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one ticket per CTA
+enum Kv8Mode { KV8_CAUSAL, KV8_WINDOW, KV8_PREFIX, KV8_SUFFIX };
+// Shared positions are worked on in whole units of either kernel; a sequence sees to the rest itself.
+constexpr int KV8_SHARED_UNIT = 128;
 // A query row is brought to [2^13, 2^14) by 2^-e, e within these bounds (any finite bf16 row fits
 // fp16 then, and 2^e times a score scale of ordinary size is a normal number).  The factor
 // of its scores, 2^e times the score scale times the keys' scale, ends at the last: past it the
@@ -87,7 +101,37 @@ struct Kv8AttnParams {
   unsigned* tickets;     // [KV8_MAX_CTAS], zero between calls
   float* part;           // [CTA][2][rows][row floats]
   unsigned long long wait_ns;
+  int window, sinks;     // window mode: positions of a window, first positions that stay visible
+  int win_units;         // and the most units that a tile has there
+  const int* groups;     // prefix and suffix modes: first sequence of each group, the end
+  const int* shared;     // positions that each group shares
+  int n_groups;
+  float* rows;           // what the prefix pass leaves: [token][query head][kv8_row_floats(D)]
 };
+
+// Workspace of a query row's sums (O, references ms and d, normaliser): 32-byte rows.
+__host__ __device__ constexpr int kv8_row_floats(int D) { return D + 8; }
+
+// Two sums of one row with references of their own become one: its normaliser, the factors of the
+// two O, and the unit of the result's weights in the normaliser's.
+struct Kv8Join {
+  float sum, f[2], unit;
+};
+__device__ __forceinline__ Kv8Join kv8_join(const float4& a, const float4& b) {    // each {ms, d, normaliser}
+  Kv8Join j;
+  const float m = fmaxf(a.x, b.x), da = a.x - m + a.y, db = b.x - m + b.y, top = fmaxf(da, db);
+  j.sum = fmaf(ex2(a.x - m), a.z, ex2(b.x - m) * b.z);
+  j.f[0] = ex2(da - top);
+  j.f[1] = ex2(db - top);
+  j.unit = ex2(top);
+  return j;
+}
+
+// Window mode: the most units of a tile, those that W + TQ - 1 consecutive positions can touch and the
+// sinks'.
+__host__ __device__ constexpr int kv8_win_units(int U, int tq, int window, int sinks) {
+  return (window + tq - 1 + 2 * U - 2) / U + (sinks + U - 1) / U;
+}
 
 // A run of units inside one tile.
 struct Kv8Seg {
@@ -96,7 +140,16 @@ struct Kv8Seg {
   int u0, u1, units;     // this run's units of positions (none: u1 <= u0), the tile's
   int len;               // units of the line that the segment takes
   int x;                 // units of the line before it in its tile
+  int su, skip;          // window mode: the tile's units of sinks, and the units between them and the window
+  int low;               // and the first position of the window of its first token
 };
+// The unit of positions that unit u of a segment's tile stands for.
+template <int U, int MODE>
+__device__ __forceinline__ int kv8_unit(const Kv8Seg& g, int u) {
+  if constexpr (MODE == KV8_WINDOW) return u < g.su ? u : u + g.skip;
+  if constexpr (MODE == KV8_SUFFIX) return u + g.s.base / U;
+  return u;
+}
 
 // The line cut into n runs: run i is units i total / n up to (i + 1) total / n, and unit w
 // belongs to run ((w + 1) n - 1) / total (whole divisions).
@@ -121,44 +174,130 @@ __device__ __forceinline__ long long kv8_upto(long long x, int r_shift) {
   return ((q * (q - 1)) << r_shift) / 2 + q * (m + 1);
 }
 
+// The position that the tiles' units are counted from: the first new token's, less what a prefix
+// pass has done.
+template <int MODE>
+__device__ __forceinline__ int kv8_from(const Kv8Seq& s) {
+  return max(s.first, 0) - (MODE == KV8_SUFFIX ? s.base : 0);
+}
 // Units of tiles 0 .. t - 1 of a sequence (t at most its last tile).
-template <int U, int C>
-__device__ __forceinline__ long long kv8_units_before(const Kv8Seq& s, int tq_shift, int t) {
+template <int U, int C, int MODE>
+__device__ __forceinline__ long long kv8_units_before(const Kv8AttnParams& p, const Kv8Seq& s, int t) {
   constexpr int US = U == 16 ? 4 : U == 32 ? 5 : U == 64 ? 6 : 7;
   static_assert((1 << US) == U, "U is 16 to 128");
-  const long long n = t;
-  if (tq_shift > US) return n * ((max(s.first, 0) + U - 1) / U + C) + ((n * (n + 1) / 2) << (tq_shift - US));
+  const int from = kv8_from<MODE>(s), tq_shift = p.tq_shift;
+  long long n = t, rest = 0;
+  if constexpr (MODE == KV8_PREFIX) return n * (s.len / U + C);
+  if constexpr (MODE == KV8_WINDOW) {
+    // tile i has K = win_units or more by the causal count from i + 1 >= ((K - 1) U + 1 - from) / TQ on
+    const int full = max(((p.win_units - 1) * U - from) >> tq_shift, 0);
+    if (t > full) {
+      rest = static_cast<long long>(t - full) * (p.win_units + C);
+      n = full;
+    }
+  }
+  if (tq_shift > US) return rest + n * ((from + U - 1) / U + C) + ((n * (n + 1) / 2) << (tq_shift - US));
   const int rs = US - tq_shift;
-  const long long A = (max(s.first, 0) + U - 1) >> tq_shift;
-  return kv8_upto(A + t, rs) - kv8_upto(A, rs) + C * n;
+  const long long A = (from + U - 1) >> tq_shift;
+  return rest + kv8_upto(A + n, rs) - kv8_upto(A, rs) + C * n;
 }
 // Units of one tile: what its last token sees, one at least, and C.
-template <int U, int C>
-__device__ __forceinline__ int kv8_units_tile(const Kv8Seq& s, int tq_shift, int t) {
-  return (max(s.first, 0) + min((t + 1) << tq_shift, s.n) + U - 1) / U + C;
+template <int U, int C, int MODE>
+__device__ __forceinline__ int kv8_units_tile(const Kv8AttnParams& p, const Kv8Seq& s, int t) {
+  if constexpr (MODE == KV8_PREFIX) return s.len / U + C;
+  const int n = (kv8_from<MODE>(s) + min((t + 1) << p.tq_shift, s.n) + U - 1) / U;
+  return (MODE == KV8_WINDOW ? min(n, p.win_units) : n) + C;
 }
-template <int U, int C>
-__device__ __forceinline__ long long kv8_units_seq(const Kv8Seq& s, int tq_shift) {
+template <int U, int C, int MODE>
+__device__ __forceinline__ long long kv8_units_seq(const Kv8AttnParams& p, const Kv8Seq& s) {
   if (s.n <= 0) return 0;
-  if (s.n <= (1 << tq_shift)) return kv8_units_tile<U, C>(s, tq_shift, 0);
-  const int tiles = (s.n + (1 << tq_shift) - 1) >> tq_shift;
-  return kv8_units_before<U, C>(s, tq_shift, tiles - 1) + kv8_units_tile<U, C>(s, tq_shift, tiles - 1);
+  if (s.n <= (1 << p.tq_shift)) return kv8_units_tile<U, C, MODE>(p, s, 0);
+  const int tiles = (s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
+  return kv8_units_before<U, C, MODE>(p, s, tiles - 1) + kv8_units_tile<U, C, MODE>(p, s, tiles - 1);
 }
 
-// The line: prefix[b] = units before sequence b (all heads), in shared memory, filled by
-// the whole CTA (THREADS threads, s_warp: THREADS / 32 words); returns its length.
-template <int U, int C, int THREADS>
-__device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long* prefix, long long* s_warp) {
-  const int tid = threadIdx.x, B = p.b.n_seqs;
+// A group of sequences with a shared prefix as an item of the line: the tokens of all of them,
+// each seeing `len` positions (whole units).  `bad` when something was out of range.
+__device__ __forceinline__ Kv8Seq kv8_group(const Kv8AttnParams& p, int i) {
+  Kv8Seq s;
+  const int b0 = __ldg(p.groups + i), b1 = __ldg(p.groups + i + 1), shared = __ldg(p.shared + i);
+  const int o0 = __ldg(p.b.offsets + b0), o1 = __ldg(p.b.offsets + b1);
+  const int len = min(max(shared, 0), p.b.max_pages << p.c.page_shift);
+  const bool rows = o0 >= 0 && o0 <= o1 && o1 <= p.b.n_tokens;
+  s.off = rows ? o0 : 0;
+  s.len = len / KV8_SHARED_UNIT * KV8_SHARED_UNIT;
+  s.n = rows && s.len > 0 ? o1 - o0 : 0;
+  s.first = 0;
+  s.base = 0;
+  s.bad = !rows || len != shared;
+  return s;
+}
+// The positions of sequence b that the prefix pass sees to: those of its group, if all of its new
+// tokens come after them.
+__device__ __forceinline__ int kv8_base(const Kv8AttnParams& p, const Kv8Seq& s, int b) {
+  int lo = 0, hi = p.n_groups;           // the last group that begins at b or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.groups + mid) <= b) lo = mid;
+    else hi = mid;
+  }
+  if (s.n <= 0 || b < __ldg(p.groups + lo) || b >= __ldg(p.groups + lo + 1)) return 0;
+  const Kv8Seq g = kv8_group(p, lo);
+  return s.first >= g.len && s.off >= g.off && s.off + s.n <= g.off + g.n ? g.len : 0;
+}
+// Item i of the line: a sequence, or in prefix mode a group.  (base: filled by kv8_line.)
+template <int MODE>
+__device__ __forceinline__ Kv8Seq kv8_item(const Kv8AttnParams& p, const int* base, int i) {
+  if constexpr (MODE == KV8_PREFIX) {
+    return kv8_group(p, i);
+  } else {
+    Kv8Seq s = kv8_seq(p.b, p.c.page_shift, i);
+    s.base = MODE == KV8_SUFFIX ? base[i] : 0;
+    return s;
+  }
+}
+template <int MODE>
+__device__ __forceinline__ int kv8_items(const Kv8AttnParams& p) { return MODE == KV8_PREFIX ? p.n_groups : p.b.n_seqs; }
+// The page-table row of item i.
+template <int MODE>
+__device__ __forceinline__ const int* kv8_table(const Kv8AttnParams& p, int i) {
+  const int b = MODE == KV8_PREFIX ? __ldg(p.groups + i) : i;
+  return p.b.page_table + static_cast<size_t>(b) * p.b.max_pages;
+}
+
+// The line: prefix[b] = units before item b (all heads), in shared memory, filled by the whole
+// CTA (THREADS threads, s_warp: THREADS / 32 words); returns its length.  In suffix mode base[b]
+// becomes what the prefix pass has seen to of sequence b.
+template <int U, int C, int THREADS, int MODE>
+__device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long* prefix, long long* s_warp, int* base) {
+  const int tid = threadIdx.x, B = kv8_items<MODE>(p);
   const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long sum = 0;
+  bool groups = true;                      // out of order or range: nothing is shared
+  if constexpr (MODE == KV8_PREFIX || MODE == KV8_SUFFIX) {
+#pragma unroll 1
+    for (int i = tid; i <= p.n_groups; i += THREADS) {
+      const int b = __ldg(p.groups + i);
+      groups &= b >= 0 && b <= p.b.n_seqs && (i == 0 || __ldg(p.groups + i - 1) <= b);
+    }
+    groups = __syncthreads_and(groups) != 0;
+    if (!groups && tid == 0 && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+  }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
+    Kv8Seq s;
+    if constexpr (MODE == KV8_PREFIX) {
+      s.n = 0;
+      s.bad = false;
+      if (groups) s = kv8_group(p, b);
+    } else {
+      s = kv8_seq(p.b, p.c.page_shift, b);
+      if constexpr (MODE == KV8_SUFFIX) base[b] = s.base = groups ? kv8_base(p, s, b) : 0;
+    }
     // (fewer positions than new tokens: the tokens without one get zeros)
     if ((s.bad || (s.n > 0 && s.first < 0)) && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
-    sum += kv8_units_seq<U, C>(s, p.tq_shift) * p.c.hkv;
+    sum += kv8_units_seq<U, C, MODE>(p, s) * p.c.hkv;
     prefix[b] = sum;                       // inside this thread's run for now
   }
   long long incl = sum;
@@ -189,10 +328,20 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
   return total;
 }
 
-// Ends the segment that starts at unit w, x units into its tile of `all` units, with the tile or
-// at w_end.
-template <int C>
-__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, int x, int all, long long w, long long w_end) {
+// Positions that the tile's last token sees.  (The tile's units are counted as if the sequence
+// began at position 0 at the latest, so that with fewer positions than new tokens, first < 0, the
+// last units lie past this.)
+template <int MODE>
+__device__ __forceinline__ int kv8_seg_end(const Kv8Seg& g, int tq_shift) {
+  if constexpr (MODE == KV8_PREFIX) return g.s.len;
+  return max(g.s.first + min((g.t + 1) << tq_shift, g.s.n), 0);
+}
+
+// Ends the segment that starts at unit w, x units into its tile of `all` units of the line, with
+// the tile or at w_end.
+template <int U, int C, int MODE>
+__device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, const Kv8AttnParams& p, int x, int all, long long w,
+                                              long long w_end) {
   const long long left = w_end - w;
   const int end = all - x <= left ? all : x + static_cast<int>(left);
   g.x = x;
@@ -200,6 +349,13 @@ __device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, int x, int all, long lo
   g.units = all - C;
   g.u0 = max(x - C, 0);
   g.u1 = end - C;
+  if constexpr (MODE == KV8_WINDOW) {
+    g.low = max(g.s.first + (g.t << p.tq_shift) + 1 - p.window, 0);
+    g.su = min((p.sinks + U - 1) / U, g.low / U);
+    g.skip = g.low / U - g.su;
+    g.units = max((kv8_seg_end<MODE>(g, p.tq_shift) + U - 1) / U - g.skip, 1);
+    g.u1 = min(g.u1, g.units);
+  }
 }
 // The runs that hold the first and the last unit of positions of the segment's tile (the
 // segment starts at unit w).
@@ -227,15 +383,15 @@ __device__ __forceinline__ int kv8_last_of(int n, F ok) {
 }
 
 // The segment that starts at unit w of the line (asked for by whole warps).
-template <int U, int C>
-__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, long long w,
+template <int U, int C, int MODE>
+__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, const int* base, long long w,
                                           long long w_end) {
   Kv8Seg g;
-  const int lo = kv8_last_of(p.b.n_seqs, [&](int i) { return prefix[i] <= w; });
+  const int lo = kv8_last_of(kv8_items<MODE>(p), [&](int i) { return prefix[i] <= w; });
   g.b = lo;
-  g.s = kv8_seq(p.b, p.c.page_shift, lo);
+  g.s = kv8_item<MODE>(p, base, lo);
   long long x = w - prefix[lo];
-  const long long per_head = kv8_units_seq<U, C>(g.s, p.tq_shift);
+  const long long per_head = kv8_units_seq<U, C, MODE>(p, g.s);
   g.g = 0;
   if (p.c.hkv > 4) {
     g.g = static_cast<int>(kv8_div(x, per_head));
@@ -245,35 +401,28 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
     for (; x >= per_head; x -= per_head) ++g.g;
   }
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
-  const int tl = kv8_last_of(tiles, [&](int t) { return kv8_units_before<U, C>(g.s, p.tq_shift, t) <= x; });
+  const int tl = kv8_last_of(tiles, [&](int t) { return kv8_units_before<U, C, MODE>(p, g.s, t) <= x; });
   g.t = tl;
-  const int in_tile = static_cast<int>(tl ? x - kv8_units_before<U, C>(g.s, p.tq_shift, tl) : x);
-  kv8_seg_close<C>(g, in_tile, kv8_units_tile<U, C>(g.s, p.tq_shift, tl), w, w_end);
+  const int in_tile = static_cast<int>(tl ? x - kv8_units_before<U, C, MODE>(p, g.s, tl) : x);
+  kv8_seg_close<U, C, MODE>(g, p, in_tile, kv8_units_tile<U, C, MODE>(p, g.s, tl), w, w_end);
   return g;
 }
 
 // The segment after `g`, at unit w of the line (g was not the run's last): it begins a tile,
 // the sequence's next one, or the first of the next head or sequence.
-template <int U, int C>
-__device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const long long* prefix, long long w,
-                                         long long w_end) {
+template <int U, int C, int MODE>
+__device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const long long* prefix, const int* base,
+                                         long long w, long long w_end) {
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
   if (++g.t >= tiles) {
     g.t = 0;
     if (++g.g >= p.c.hkv) {
       g.g = 0;
       do ++g.b; while (prefix[g.b + 1] <= w);      // sequences without new tokens have no units
-      g.s = kv8_seq(p.b, p.c.page_shift, g.b);
+      g.s = kv8_item<MODE>(p, base, g.b);
     }
   }
-  kv8_seg_close<C>(g, 0, kv8_units_tile<U, C>(g.s, p.tq_shift, g.t), w, w_end);
-}
-
-// Positions that the tile's last token sees.  (The tile's units are counted as if the sequence
-// began at position 0 at the latest, so that with fewer positions than new tokens, first < 0, the
-// last units lie past this.)
-__device__ __forceinline__ int kv8_seg_end(const Kv8Seg& g, int tq_shift) {
-  return max(g.s.first + min((g.t + 1) << tq_shift, g.s.n), 0);
+  kv8_seg_close<U, C, MODE>(g, p, 0, kv8_units_tile<U, C, MODE>(p, g.s, g.t), w, w_end);
 }
 
 }  // namespace moe

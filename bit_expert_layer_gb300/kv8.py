@@ -1,5 +1,6 @@
 """Torch-facing wrappers of the 8-bit key/value cache (``include/gqa_kv8.h``): the paged
-cache, the batch that every call describes its sequences with, and rotary positions.
+cache, the batch that every call describes its sequences with, page tables built on the
+device, and rotary positions with or without norms of the heads.
 
 One decode step of a model's attention::
 
@@ -10,6 +11,13 @@ One decode step of a model's attention::
     q, k = rope(q, k, positions)
     cache.append(batch, k, v)
     out = cache.attention(batch, q, workspace=ws)
+
+with ``window=`` and ``sinks=`` for a sliding window, or ``prefix=KV8Prefix(groups, shared)``
+where sequences begin alike.  A server's step begins with its page tables::
+
+    pages = kv8.KV8Pages.all_free(n_pages, page_size=64, n_seqs=64, max_pages=512)
+    offsets, positions, slots = pages.step(new, n_tokens)        # new: int32 [n_seqs], on the device
+    batch = kv8.KV8Batch(pages.table, pages.lens, offsets, max_new)
 
 PyTorch supplies device memory and streams only; each method is one C call on the current
 stream of the tensors' device.  Tensors are checked here for type, shape, layout and device,
@@ -23,12 +31,13 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import GqaKv8Batch, GqaKv8Cache
+from ._abi import GqaKv8Batch, GqaKv8Cache, GqaKv8Pages, GqaKv8PagesState, GqaKv8Prefix, GqaNorm
 
 BLOCK = 16                                   # positions that share a scale
 FORMATS = {"e4m3": _abi.GQA_KV8_E4M3, "int8": _abi.GQA_KV8_INT8}
 _BF16 = torch.bfloat16
 _empty, _current_device = torch.empty, torch.cuda.current_device
+_INT = torch.int32
 
 
 def _elsewhere(device: torch.device, stream):
@@ -107,6 +116,96 @@ class KV8Batch(_Fixed):
         return ref
 
 
+class KV8Prefix(_Fixed):
+    """Sequences that begin alike: sequences ``groups[i]`` .. ``groups[i + 1] - 1`` share their first
+    ``shared[i]`` positions (int32 [n_groups + 1] and [n_groups], on the device; they may be
+    changed in place between calls, also under a captured graph)."""
+
+    def __init__(self, groups: torch.Tensor, shared: torch.Tensor):
+        self.groups = _ints(groups, "groups", 1)
+        self.device = groups.device
+        self.shared = _ints(shared, "shared", 1, self.device)
+        n = shared.shape[0]
+        if n < 1 or groups.shape[0] != n + 1:
+            raise ValueError(f"shared has {n} entries: one at least is wanted, and groups has to have {n + 1}")
+        self._c = ctypes.byref(GqaKv8Prefix(groups.data_ptr(), shared.data_ptr(), n))
+
+
+class KV8Pages(_Fixed):
+    """Which pages of a pool each sequence holds, kept on the device: ``table`` int32 [n_seqs,
+    max_pages], ``free`` int32 [n_pages] (a stack), and the state that a step changes: ``lens``
+    int32 [n_seqs] (cached positions), ``held`` int32 [n_seqs] (pages in the sequence's row)
+    and ``n_free`` int32 [1].  Sequences that begin with pages of another one's (a shared
+    prefix) say how many in ``borrowed`` int32 [n_seqs]; those are not given back."""
+
+    def __init__(self, table: torch.Tensor, free: torch.Tensor, page_size: int, lens: torch.Tensor, held: torch.Tensor,
+                 n_free: torch.Tensor, borrowed: torch.Tensor | None = None, control: torch.Tensor | None = None):
+        self.table = _ints(table, "table", 2)
+        self.device = dev = table.device
+        n = table.shape[0]
+        self.free, self.lens, self.held = _ints(free, "free", 1, dev), _ints(lens, "lens", 1, dev), _ints(held, "held", 1, dev)
+        self.n_free = _ints(n_free, "n_free", 1, dev)
+        self.borrowed = None if borrowed is None else _ints(borrowed, "borrowed", 1, dev)
+        for name, x, m in (("lens", lens, n), ("held", held, n), ("n_free", n_free, 1), ("borrowed", borrowed, n)):
+            if x is not None and x.shape[0] != m:
+                raise ValueError(f"{name}: {m} entries are wanted, got {x.shape[0]}")
+        self.page_size = int(page_size)
+        self.control = torch.zeros(2, dtype=_INT, device=dev) if control is None else control
+        self._pages = ctypes.byref(GqaKv8Pages(table.data_ptr(), free.data_ptr(), self.control.data_ptr(), n, table.shape[1],
+                                               free.shape[0], self.page_size))
+        self._state = ctypes.byref(GqaKv8PagesState(lens.data_ptr(), held.data_ptr(), n_free.data_ptr()))
+
+    @classmethod
+    def all_free(cls, n_pages: int, page_size: int = 64, n_seqs: int = 64, max_pages: int = 512, device="cuda") -> "KV8Pages":
+        """A pool of which no page is held; the first to be taken is page 0."""
+        zeros = lambda *s: torch.zeros(s, dtype=_INT, device=device)  # noqa: E731
+        free = torch.arange(n_pages - 1, -1, -1, dtype=_INT, device=device)
+        return cls(zeros(n_seqs, max_pages), free, page_size, zeros(n_seqs), zeros(n_seqs), zeros(1) + n_pages)
+
+    def fork(self) -> "KV8Pages":
+        """Another state over the same table and free list, equal to this one for now: for
+        ``step(into=...)``.  Only steps from one of them may follow once it has been stepped in place."""
+        return KV8Pages(self.table, self.free, self.page_size, self.lens.clone(), self.held.clone(), self.n_free.clone(),
+                        self.borrowed, self.control)
+
+    def step(self, new: torch.Tensor, n_tokens: int, keep: torch.Tensor | None = None, out=None,
+             into: "KV8Pages | None" = None, stream=None):
+        """Every sequence keeps its first ``keep`` positions (int32 [n_seqs]; None: all; 0: it is
+        done, and gives its pages back), adds ``new`` tokens (int32 [n_seqs]) and gets the pages
+        for them.  Writes the state after it into ``into`` (None: in place) and returns
+        (offsets [n_seqs + 1], positions [n_tokens], slots [n_tokens]), int32; rows at or past
+        offsets[n_seqs] are left as they were.  A slot is page * page_size + place in the page,
+        -1 for a token without a page (the free list ran out, which ``get_error`` tells)."""
+        dev = self.device
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return self.step(new, n_tokens, keep, out, into)
+        n = self.table.shape[0]
+        if _ints(new, "new", 1, dev).shape[0] != n or (keep is not None and _ints(keep, "keep", 1, dev).shape[0] != n):
+            raise ValueError(f"new, keep: {n} entries are wanted")
+        if into is None:
+            into = self
+        elif into.table is not self.table or into.free is not self.free:
+            raise ValueError("into: a fork of these pages is wanted")
+        if out is None:
+            out = (_empty(n + 1, dtype=_INT, device=dev), _empty(n_tokens, dtype=_INT, device=dev),
+                   _empty(n_tokens, dtype=_INT, device=dev))
+        else:
+            for name, x, m in zip(("offsets", "positions", "slots"), out, (n + 1, n_tokens, n_tokens)):
+                if _ints(x, name, 1, dev).shape[0] != m:
+                    raise ValueError(f"{name}: {m} entries are wanted")
+        _abi.gqa_kv8_pages_step(self._pages, self._state, into._state, 0 if keep is None else keep.data_ptr(),
+                                new.data_ptr(), 0 if self.borrowed is None else self.borrowed.data_ptr(), out[0].data_ptr(),
+                                out[1].data_ptr(), out[2].data_ptr(), n_tokens, _handle(dev.index))
+        return out
+
+    def get_error(self) -> int:
+        """Synchronises, then reads and clears the pool's error word (a status of ``_abi.STATUS``)."""
+        with torch.cuda.device(self.device):
+            return _abi.gqa_kv8_pages_get_error(self._pages)
+
+
 class KV8Cache(_Fixed):
     """A paged 8-bit cache over caller-owned tensors: ``k``, ``v`` one byte per number
     [n_pages, n_kv_heads, page_size, head_size], ``k_scale``, ``v_scale`` float32
@@ -182,23 +281,33 @@ class KV8Cache(_Fixed):
                             _handle(dev.index))
         return out
 
-    def new_workspace(self, n_q_heads: int, max_new: int) -> torch.Tensor:
-        """A zero-filled workspace for attention calls of up to max_new new tokens per sequence."""
-        n = _abi.gqa_kv8_workspace_bytes(self._c, n_q_heads, max_new)
+    def new_workspace(self, n_q_heads: int, max_new: int, prefix_tokens: int = 0) -> torch.Tensor:
+        """A zero-filled workspace for attention calls of up to max_new new tokens per sequence; for calls
+        with a prefix, of up to prefix_tokens tokens in all."""
+        n = _abi.gqa_kv8_prefix_workspace_bytes(self._c, n_q_heads, max_new, prefix_tokens) if prefix_tokens else \
+            _abi.gqa_kv8_workspace_bytes(self._c, n_q_heads, max_new)
         if n == 0:
             raise ValueError("configuration refused")
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
 
     def attention(self, batch: KV8Batch, q: torch.Tensor, scale: float = 0.0, out: torch.Tensor | None = None,
-                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                  workspace: torch.Tensor | None = None, stream=None, *, window: int | None = None, sinks: int = 0,
+                  prefix: KV8Prefix | None = None) -> torch.Tensor:
         """Causal attention of the new tokens' queries (bf16 [T, n_q_heads, head_size]) over
         the cache, their own positions among it; scale 0 means 1 / sqrt(head_size).  The
-        workspace is allocated for the call if none is given."""
+        workspace is allocated for the call if none is given.
+
+        With ``window`` a token sees the last `window` positions, its own among them, and its
+        sequence's first ``sinks``.  With ``prefix`` the positions that sequences share are
+        worked on once for all of them (see ``KV8Prefix``; the workspace is then one for
+        ``prefix_tokens``); not together with a window."""
         dev = self.device
         there = _elsewhere(dev, stream)
         if there is not None:
             with there:
-                return self.attention(batch, q, scale, out, workspace)
+                return self.attention(batch, q, scale, out, workspace, window=window, sinks=sinks, prefix=prefix)
+        if window is None and sinks or window is not None and prefix is not None:
+            raise ValueError("sinks go with a window, and a prefix without one")
         shape = q.shape
         heads = shape[1] if len(shape) == 3 else 0
         qs = _rows(q, "q", heads, self.head_size, dev)
@@ -207,11 +316,18 @@ class KV8Cache(_Fixed):
         elif out.shape != shape or out.dtype is not _BF16 or out.device != dev or not out.is_contiguous():
             raise ValueError("out: a contiguous bfloat16 tensor of q's shape is wanted")
         if workspace is None:
-            workspace = self.new_workspace(heads, batch.max_new)
+            workspace = self.new_workspace(heads, batch.max_new, 0 if prefix is None else shape[0])
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: a contiguous tensor on {dev} is wanted")
-        _abi.gqa_kv8_attention(self._c, self._batch(batch, shape[0]), q.data_ptr(), qs, heads, scale, out.data_ptr(),
-                               workspace.data_ptr(), workspace.nbytes, _handle(dev.index))
+        c, where = self._batch(batch, shape[0]), (out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _handle(dev.index))
+        if window is not None:
+            _abi.gqa_kv8_window_attention(self._c, c, q.data_ptr(), qs, heads, scale, window, sinks, *where)
+        elif prefix is not None:
+            if prefix.device != dev:
+                raise ValueError(f"the prefix is on {prefix.device}, the cache on {dev}")
+            _abi.gqa_kv8_prefix_attention(self._c, c, prefix._c, q.data_ptr(), qs, heads, scale, *where)
+        else:
+            _abi.gqa_kv8_attention(self._c, c, q.data_ptr(), qs, heads, scale, *where)
         return out
 
     def get_error(self) -> int:
@@ -224,6 +340,8 @@ class Rope(_Fixed):
     """Rotary positions: pair j (elements j and j + rotary / 2 of a head) turns by
     pos[axis(j)] * inv_freq[j].  ``sections`` gives each axis its number of pairs (one axis
     by default); ``cyclic`` deals the pairs out to the axes in turn instead of in runs."""
+
+    _norm = None
 
     def __init__(self, head_size: int = 128, rotary: int | None = None, theta: float = 10000.0, inv_freq=None,
                  sections=None, cyclic: bool = False):
@@ -266,6 +384,34 @@ class Rope(_Fixed):
             qos = _rows(qo, "q_out", hq, d, dev)
             if ko is not None:
                 kos = _rows(ko, "k_out", hk, d, dev)
-        _abi.gqa_rope(self._plan, q.data_ptr(), qs, hq, kp, ks, hk, pos.data_ptr(), t, qo.data_ptr(), qos,
-                      0 if ko is None else ko.data_ptr(), kos, _handle(dev.index))
+        args = (q.data_ptr(), qs, hq, kp, ks, hk, pos.data_ptr(), t, qo.data_ptr(), qos, 0 if ko is None else ko.data_ptr(),
+                kos, _handle(dev.index))
+        if self._norm is None:
+            _abi.gqa_rope(self._plan, *args)
+        else:
+            if self._norm_device is not None and self._norm_device != dev:
+                raise ValueError(f"the weights are on {self._norm_device}, q on {dev}")
+            _abi.gqa_norm_rope(self._plan, self._norm, *args)
         return qo, ko
+
+
+class NormRope(Rope):
+    """Norms of the heads and rotary positions in one pass: every head x of q and k becomes
+    x / sqrt(mean(x^2) + eps) * (weight + offset), with q's and k's own weights ([head_size], both
+    bf16 or both fp32; None: ones), and turns as ``rope`` has it.  Called as a Rope."""
+
+    def __init__(self, rope: Rope, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 eps: float = 1e-6, offset: float = 0.0):
+        given = [w for w in (q_weight, k_weight) if w is not None]
+        for w in given:
+            if w.dtype not in (_BF16, torch.float32) or w.dtype != given[0].dtype or w.device != given[0].device or \
+                    not w.is_cuda or w.shape != (rope.head_size,) or not w.is_contiguous():
+                raise ValueError(f"weights: contiguous bfloat16 or float32 CUDA tensors of [{rope.head_size}], alike, are wanted")
+        if not 0.0 <= eps <= 1e30 or not abs(offset) <= 1e30:
+            raise ValueError(f"eps {eps}, offset {offset}: finite numbers are wanted, eps 0 at least")
+        self.plan, self._plan, self.head_size, self.n_axes = rope.plan, rope._plan, rope.head_size, rope.n_axes
+        self.q_weight, self.k_weight, self.eps, self.offset = q_weight, k_weight, float(eps), float(offset)
+        self._norm_device = given[0].device if given else None
+        self._norm = ctypes.byref(GqaNorm(0 if q_weight is None else q_weight.data_ptr(),
+                                          0 if k_weight is None else k_weight.data_ptr(),
+                                          1 if given and given[0].dtype is torch.float32 else 0, eps, offset))

@@ -127,6 +127,94 @@ moe_status_t gqa_kv8_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch
                                long long q_stride, int n_q_heads, float scale, void* out, void* workspace,
                                size_t workspace_bytes, moe_stream_t stream);
 
+/* The same with a sliding window: a token at position p sees the positions i <= p with
+ * i > p - window or i < sinks, that is the last `window` positions, its own among them, and
+ * the first `sinks` of its sequence (window 1 .. 2^24, sinks 0 .. 2^24; a window that
+ * reaches back to position 0 leaves ordinary causal attention).  Blocks of 16 positions that
+ * no token of the call sees are not read, nor are their page-table entries looked at, but
+ * where they share a page with positions that are: pages that only hold such positions may
+ * have been given back.  Workspace, errors and precision as gqa_kv8_attention. */
+moe_status_t gqa_kv8_window_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch, const void* q,
+                                      long long q_stride, int n_q_heads, float scale, int window, int sinks, void* out,
+                                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Sequences that begin alike.  Sequences groups[i] .. groups[i + 1] - 1 have the same first
+ * shared[i] positions: page-table rows whose entries for them are equal, or pages of equal
+ * contents (a prompt's last, partly filled page may be copied).  Sequences outside every
+ * group share nothing.  Both arrays are in device memory and read when the kernels run. */
+typedef struct {
+    const int32_t* groups;      /* [n_groups + 1] non-decreasing, 0 .. n_seqs */
+    const int32_t* shared;      /* [n_groups] positions, 0 at least */
+    int n_groups;               /* 1 .. 1024 */
+} gqa_kv8_prefix_t;
+
+/* Bytes of device workspace of gqa_kv8_prefix_attention for calls of at most n_tokens rows
+ * (0 if refused).  Zero-fill it before its first use. */
+size_t gqa_kv8_prefix_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new, int n_tokens);
+
+/* gqa_kv8_attention for sequences that share their beginnings.  The shared positions, as many
+ * whole 128s of them as there are, are attended to by all of a group's queries together, read
+ * from the pages of the group's first sequence, whose row has to hold them even if it has no
+ * new tokens; each sequence then adds the rest of its own.  The result is that of
+ * gqa_kv8_attention to within its error.  A sequence whose new tokens do not all lie behind the
+ * shared positions is attended to by itself, and so is every one where the mean group has at
+ * most 32 query rows per key/value head.  Groups out of order or range are recorded in the
+ * error word and nothing is shared; a shared length past the page table is recorded and cut.
+ * Errors: as gqa_kv8_attention. */
+moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch,
+                                      const gqa_kv8_prefix_t* prefix, const void* q, long long q_stride, int n_q_heads,
+                                      float scale, void* out, void* workspace, size_t workspace_bytes,
+                                      moe_stream_t stream);
+
+/* Page tables built on the GPU.  A pool's pages are either held, by the entries
+ * page_table[b][0 .. held[b] - 1], or on its free list, free_pages[0 .. n_free - 1], a stack.
+ * What changes from step to step is a state of its own, so that a step can write another one
+ * than it reads: the old state stays good until a step from the new one (a draft that is
+ * not taken costs nothing). */
+typedef struct {
+    int32_t* page_table;        /* [n_seqs][max_pages] */
+    int32_t* free_pages;        /* [n_pages] */
+    uint32_t* control;          /* two device words, zero before the first call */
+    int n_seqs;                 /* 1 .. 1024 */
+    int max_pages;              /* max_pages * page_size <= 2^24 */
+    int n_pages;                /* of the pool; n_pages * page_size < 2^31 */
+    int page_size;              /* a power of two, 16 .. 1024 */
+} gqa_kv8_pages_t;
+
+typedef struct {
+    int32_t* lens;              /* [n_seqs] cached positions */
+    int32_t* held;              /* [n_seqs] pages held */
+    int32_t* n_free;            /* one word: pages on the free list */
+} gqa_kv8_pages_state_t;
+
+/* One step of every sequence: it keeps its first keep[b] positions (NULL: all it has; 0: it is
+ * done), adds n_new[b] tokens, and holds ceil((keep + n_new) / page_size) pages after it.
+ * First the pages that are no longer wanted go on the free list, in order of sequence and
+ * page, then every sequence that wants more takes them from the list's end, in the same
+ * order.  (A page can change hands within a call; list entries at or past the count stay as
+ * they are.)
+ *   to         the state after the step: arrays of from's own, or others that do not overlap
+ *   borrowed   [n_seqs] or NULL: a sequence's first pages that are not its own (a shared
+ *              prefix's); it does not give them back
+ *   offsets    [n_seqs + 1] tokens before each sequence
+ *   positions  [n_tokens] or NULL: position of every token
+ *   slots      [n_tokens] or NULL: page * page_size + position % page_size, where the token
+ *              is kept among all positions of the pool; -1 where it has no page
+ * with `to->lens`, `offsets` and the page table this is a batch for the calls above.
+ * n_tokens (0 .. 2^20) is the rows of positions and slots; rows from offsets[n_seqs] on stay
+ * as they are.  Recorded in control[0]: a free list that runs out (entries without a page
+ * become -1, and the sequence asks for them again at its next step), and lengths, counts or
+ * pages out of range, which are cut to it.  Two calls on one pool must not overlap in time.
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+moe_status_t gqa_kv8_pages_step(const gqa_kv8_pages_t* pages, const gqa_kv8_pages_state_t* from,
+                                const gqa_kv8_pages_state_t* to, const int32_t* keep, const int32_t* n_new,
+                                const int32_t* borrowed, int32_t* offsets, int32_t* positions, int32_t* slots,
+                                int n_tokens, moe_stream_t stream);
+
+/* Synchronise the current device, then read and clear control[0]: MOE_OK or
+ * MOE_ERR_DEVICE_BOUNDS. */
+moe_status_t gqa_kv8_pages_get_error(const gqa_kv8_pages_t* pages);
+
 /* Synchronise the current device, then read and clear the cache's error word: MOE_OK,
  * MOE_ERR_DEVICE_BOUNDS (a page, length or offset out of range), MOE_ERR_NONFINITE or
  * MOE_ERR_TIMEOUT (a bounded wait gave up). */
@@ -164,6 +252,20 @@ moe_status_t gqa_rope_plan_init(gqa_rope_plan_t* plan, int head_size, int rotary
 moe_status_t gqa_rope(const gqa_rope_plan_t* plan, const void* q, long long q_stride, int n_q_heads, const void* k,
                       long long k_stride, int n_k_heads, const int32_t* pos, int T, void* q_out,
                       long long q_out_stride, void* k_out, long long k_out_stride, moe_stream_t stream);
+
+/* The same with each head normed first: y = x / sqrt(mean(x^2) + eps) * (weight + offset) over
+ * the head's elements, then turned.  Everything is fp32 (64 bits where squares leave its
+ * range) and rounded once at the end.  A head of zeros stays zeros, also with eps 0. */
+typedef struct {
+    const void* q_weight;       /* [head_size] device memory, or NULL: all ones, no offset */
+    const void* k_weight;
+    int weight_f32;             /* 0: bf16, 1: fp32 */
+    float eps;                  /* 0 .. 1e30 */
+    float offset;               /* added to every weight (1 where a checkpoint stores weight - 1) */
+} gqa_norm_t;
+moe_status_t gqa_norm_rope(const gqa_rope_plan_t* plan, const gqa_norm_t* norm, const void* q, long long q_stride,
+                           int n_q_heads, const void* k, long long k_stride, int n_k_heads, const int32_t* pos, int T,
+                           void* q_out, long long q_out_stride, void* k_out, long long k_out_stride, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
