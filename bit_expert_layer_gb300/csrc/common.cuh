@@ -158,6 +158,9 @@ __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 // that wait on SMs while this one runs measured slower than letting them in at exit.)
 // Launched without the attribute, the wait does nothing.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel of the stream may start once every CTA has called this or left (the exception to
+// the rule above: it must touch nothing that this kernel writes before it waits itself).
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ----------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -56,7 +56,7 @@ __host__ __device__ constexpr int ka_parts(int D, int R) { return ka_warps(R) * 
 __host__ __device__ constexpr int ka_wsum(int R) { return R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
 __host__ __device__ constexpr int ka_smem(int D, int R, int B, bool suffix) {
   return 1024 + ka_warps(R) * ka_own(D, R) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 +
-         ka_warps(R) * (8 + ka_stages(R) * 8 + 2 * 32 + R * 4) + 64 + (suffix ? B * 4 : 0);
+         ka_warps(R) * (3 * 8 + ka_stages(R) * 8 + 2 * 32 + R * 4) + 64 + (suffix ? B * 4 : 0);
 }
 static_assert(ka_smem(128, 16, KV8_MAX_SEQS, true) <= 232448 && ka_smem(128, 8, KV8_MAX_SEQS, true) <= 232448,
               "shared memory per CTA exceeds 227 KB");
@@ -144,12 +144,12 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   float* wsum = heads + ka_parts(D, R) / 4;
   long long* prefix = reinterpret_cast<long long*>(wsum + ka_wsum(R) / 4);
   long long* s_warp = prefix + p.b.n_seqs + 1 + ((p.b.n_seqs + 1) & 1);      // 16-byte aligned
-  KaPart* meta = reinterpret_cast<KaPart*>(s_warp + KA_WARPS);             // [warp][began before, goes on]
+  KaPart* meta = reinterpret_cast<KaPart*>(s_warp + 3 * KA_WARPS);         // [warp][began before, goes on]
   uint64_t* bars = reinterpret_cast<uint64_t*>(meta + 2 * KA_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + KA_WARPS * KA_STAGES);
   int* s_last = const_cast<int*>(abort_flag) + 1;
   float* s_peak = reinterpret_cast<float*>(s_last + 1) + (threadIdx.x >> 5) * R;   // [R] the highest ms + d of a row
-  int* base = reinterpret_cast<int*>(s_last + 1) + KA_WARPS * R;      // suffix mode: [n_seqs]
+  Kv8Line line = {prefix, reinterpret_cast<int*>(s_last + 1) + KA_WARPS * R, 0, false};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * OWN;
@@ -162,14 +162,21 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     fence_mbar_init();
   }
   if (tid < 2 * KA_WARPS) meta[tid].b = -1;
-  grid_dep_wait();                          // what follows reads and writes what earlier kernels wrote
-  Kv8Runs runs;
-  runs.total = kv8_line<KA_U, KA_COST, KA_THREADS, MODE>(p, prefix, s_warp, base);
-  runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x) * KA_WARPS));
+  // What follows reads and writes what earlier kernels wrote.  (The suffix pass starts beside the prefix
+  // pass, whose CTAs have waited for those kernels before they let it; its last CTA waits for the
+  // prefix pass, so that what comes after finds both done.)
+  if (MODE != KV8_SUFFIX) grid_dep_wait();
+  const auto leave = [] {
+    if (MODE == KV8_SUFFIX && blockIdx.x == gridDim.x - 1) grid_dep_wait();
+  };
+  const Kv8Runs runs = kv8_line<KA_U, KA_COST, KA_THREADS, KA_WARPS, 0, MODE>(p, line, s_warp, gridDim.x);
   const int cta = blockIdx.x, run = cta * KA_WARPS + warp;
-  if (cta * KA_WARPS >= runs.n) return;
-  const long long w_beg = run < runs.n ? kv8_run_begin(runs, run) : 0;
-  const long long w_end = run < runs.n ? kv8_run_begin(runs, run + 1) : 0;
+  if (cta * KA_WARPS >= runs.n) {
+    leave();
+    return;
+  }
+  const long long w_beg = run < runs.n ? kv8_run_begin<KA_U, MODE>(runs, run) : 0;
+  const long long w_end = run < runs.n ? kv8_run_begin<KA_U, MODE>(runs, run + 1) : 0;
 
   // ---- this warp's load cursor: its next piece, and in the first lanes the page of one of the
   // piece's blocks each (first those of the keys, then those of the values)
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   int lu = 0, l_end = 0, pid = -1;
   bool more = w_beg < w_end;
   if (more) {
-    ls = kv8_seg<KA_U, KA_COST, MODE>(p, prefix, base, lw, w_end);
+    ls = kv8_seg<KA_U, KA_COST, MODE>(p, line, lw, w_end);
     lu = ls.u0;
     l_end = kv8_seg_end<MODE>(ls, p.tq_shift);
   }
@@ -194,11 +201,11 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         more = false;
         return;
       }
-      kv8_next<KA_U, KA_COST, MODE>(ls, p, prefix, base, lw, w_end);
+      kv8_next<KA_U, KA_COST, MODE>(ls, p, line, lw, w_end);
       lu = ls.u0;
       l_end = kv8_seg_end<MODE>(ls, p.tq_shift);
     }
-    const int pos = kv8_unit<KA_U, MODE>(ls, lu) * KA_U + block * KV8_BLOCK;
+    const int pos = lu * KA_U + kv8_skip<MODE>(ls, lu * KA_U) + block * KV8_BLOCK;
     pid = -1;
     if (loader && pos < l_end)
       pid = __ldg(p.b.page_table + static_cast<size_t>(ls.b) * p.b.max_pages + (pos >> p.c.page_shift));
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     float sc = KA_NO_BLOCK;
     if (!more) return sc;
     const int st = issued % KA_STAGES;
-    const int pos = kv8_unit<KA_U, MODE>(ls, lu) * KA_U + block * KV8_BLOCK;
+    const int pos = lu * KA_U + kv8_skip<MODE>(ls, lu * KA_U) + block * KV8_BLOCK;
     bool live = loader && pos < l_end;
     // a block that no token of the tile sees (its page may be gone); one of a box of 32 rows shares
     // its page with one that is seen
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
 #pragma unroll 1
   for (long long w = w_beg; w < w_end;) {
     if (w > w_beg) {
-      kv8_next<KA_U, KA_COST, MODE>(sg, p, prefix, base, w, w_end);
+      kv8_next<KA_U, KA_COST, MODE>(sg, p, line, w, w_end);
       fetched = false;
     }
     w += sg.len;
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         }
       }
       // ---- s + e - m, masked where a row may not see the whole piece
-      const int at_u = kv8_unit<KA_U, MODE>(sg, u) * KA_U;
+      const int at_u = u * KA_U + kv8_skip<MODE>(sg, u * KA_U);
       const bool masked = at_u + KA_U > least || !live[0] || !live[NK - 1] ||
                           (MODE == KV8_WINDOW && at_u < most && at_u + KA_U > p.sinks);
       float y[NB][NK][4], least_e = ve[0];
@@ -564,21 +571,18 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
           if (r < nrows) {
             const int tok = r / p.G, hh = r - tok * p.G;
             const size_t at = static_cast<size_t>(sg.s.off + tok0 + tok) * p.hq + sg.g * p.G + hh;
-            float unit = ex2(d[b][i]);                           // of the weights, in the normaliser's
-            if (MODE == KV8_SUFFIX && sg.s.base) {               // the row's shared positions
-              const float* row = p.rows + at * kv8_row_floats(D);
-              const Kv8Join j = kv8_join(make_float4(ms[b][i], d[b][i], sum, 0.0f), *reinterpret_cast<const float4*>(row + D));
-              sum = j.sum;
-              unit = j.unit;
+            if (MODE == KV8_SUFFIX) {                            // sums that wait for those of the shared positions
+              float* row = p.own + at * kv8_row_floats(D);
+              if (g4 == 0) *reinterpret_cast<float4*>(row + D) = make_float4(ms[b][i], d[b][i], sum, sg.s.base ? 1.0f : 0.0f);
+              if (sg.s.base) {
 #pragma unroll
-              for (int t = 0; t < NM; t += 2) {
-                const float4 v = *reinterpret_cast<const float4*>(row + VD * g4 + 2 * t);
-                o[b][t][i] = fmaf(j.f[0], o[b][t][i], j.f[1] * v.x);
-                o[b][t][2 + i] = fmaf(j.f[0], o[b][t][2 + i], j.f[1] * v.y);
-                o[b][t + 1][i] = fmaf(j.f[0], o[b][t + 1][i], j.f[1] * v.z);
-                o[b][t + 1][2 + i] = fmaf(j.f[0], o[b][t + 1][2 + i], j.f[1] * v.w);
+                for (int t = 0; t < NM; t += 2)
+                  *reinterpret_cast<float4*>(row + VD * g4 + 2 * t) =
+                      make_float4(o[b][t][i], o[b][t][2 + i], o[b][t + 1][i], o[b][t + 1][2 + i]);
+                continue;
               }
             }
+            const float unit = ex2(d[b][i]);                     // of the weights, in the normaliser's
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // a row that saw no key: zeros
             __nv_bfloat16* dst = p.out + at * D + VD * g4;
 #pragma unroll
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
         }
       }
     if (!whole) {
-      const int2 own = kv8_owners<KA_COST>(sg, w - sg.len, runs);
+      const int2 own = kv8_owners<KA_U, KA_COST, MODE>(sg, w - sg.len, runs);
       if (lane == 0) meta[2 * warp + (sg.u0 == 0)] = KaPart{sg.b, sg.g, sg.t, sg.s.off, sg.s.n, own.x, own.y, sg.s.base};
     }
   }
@@ -740,17 +744,16 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     if (write && tid < ACT && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
       const int tok = row / p.G, hh = row - tok * p.G;
       const size_t at = static_cast<size_t>(pt.off + tok0 + tok) * p.hq + pt.g * p.G + hh;
-      float unit = ex2(top);
-      if (MODE == KV8_SUFFIX && pt.base) {               // the row's shared positions
-        const float* src = p.rows + at * kv8_row_floats(D);
-        const Kv8Join j = kv8_join(make_float4(M, top, L, 0.0f), *reinterpret_cast<const float4*>(src + D));
-        const float4 v0 = *reinterpret_cast<const float4*>(src + d0), v1 = *reinterpret_cast<const float4*>(src + d0 + 4);
-        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) O[k] = fmaf(j.f[0], O[k], j.f[1] * v[k]);
-        L = j.sum;
-        unit = j.unit;
+      if (MODE == KV8_SUFFIX) {                          // as above
+        float* to = p.own + at * kv8_row_floats(D);
+        if (d0 == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, top, L, pt.base ? 1.0f : 0.0f);
+        if (pt.base) {
+          *reinterpret_cast<float4*>(to + d0) = make_float4(O[0], O[1], O[2], O[3]);
+          *reinterpret_cast<float4*>(to + d0 + 4) = make_float4(O[4], O[5], O[6], O[7]);
+          continue;
+        }
       }
+      const float unit = ex2(top);
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
       uint4 r;
       r.x = pack_bf16x2(__float_as_uint(O[0] * inv * unit), __float_as_uint(O[1] * inv * unit));
@@ -760,6 +763,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       *reinterpret_cast<uint4*>(p.out + at * D + d0) = r;
     }
   }
+  leave();
 }
 
 // ============================================================================ C ABI
@@ -902,13 +906,16 @@ bool heads_ok(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new) {
 // share: with more than 32 query rows per key/value head and group in the mean.
 bool kv8_share(int G, int tokens, int groups) { return static_cast<long long>(G) * tokens > 32ll * groups; }
 
-// The workspace of attention with shared prefixes: that of either pass, then the prefix pass's rows.
-size_t kv8_prefix_rows_at(int D, int R) {
-  const size_t a = kv8_ws_bytes(D, R), b = kv8_prompt_ws_bytes(D);
-  return ((a > b ? a : b) + 255) / 256 * 256;
+// The workspace of attention with shared prefixes: the suffix pass's, the prefix pass's (each has the
+// tickets' bytes before it), then the rows of sums of the one and of the other.
+size_t kv8_align(size_t n) { return (n + 255) / 256 * 256; }
+size_t kv8_prefix_part_at(int D, int R) { return kv8_align(kv8_ws_bytes(D, R)); }
+size_t kv8_prefix_rows_at(int D, int R) { return kv8_prefix_part_at(D, R) + kv8_align(kv8_prompt_ws_bytes(D)); }
+size_t kv8_prefix_rows(int D, int hq, int tokens) {
+  return kv8_align(static_cast<size_t>(tokens) * hq * kv8_row_floats(D) * sizeof(float));
 }
 size_t kv8_prefix_ws_bytes(int D, int R, int hq, int tokens) {
-  return kv8_prefix_rows_at(D, R) + static_cast<size_t>(tokens) * hq * kv8_row_floats(D) * sizeof(float);
+  return kv8_prefix_rows_at(D, R) + (R ? 2 : 1) * kv8_prefix_rows(D, hq, tokens);
 }
 
 }  // namespace
@@ -970,11 +977,30 @@ extern "C" moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, c
   c.p.groups = prefix->groups;
   c.p.shared = prefix->shared;
   c.p.n_groups = prefix->n_groups;
-  c.p.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv8_prefix_rows_at(D, c.R));
-  const cudaError_t e = launch_kv8_prompt<KV8_PREFIX>(c.p, D, cache->format, c.grid, c.dev, s);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  c.p.rows = reinterpret_cast<float*>(ws + kv8_prefix_rows_at(D, c.R));
+  // Few new tokens: the passes run side by side, each on some of the SMs, and a third kernel joins what
+  // they leave.  Prompts: one after the other, and the second takes up what the first has left.
+  Kv8AttnParams first = c.p;
+  first.part = reinterpret_cast<float*>(ws + kv8_prefix_part_at(D, c.R) + KV8_TICKET_BYTES);
+  if (c.R) {
+    c.p.own = reinterpret_cast<float*>(ws + kv8_prefix_rows_at(D, c.R) + kv8_prefix_rows(D, n_q_heads, batch->n_tokens));
+    c.p.shift_prefix = kv8_prompt_shift(c.p.G, batch->n_tokens);
+    c.p.shift_suffix = floor_log2(c.R / c.p.G);
+    first.own = c.p.own;
+    first.shift_prefix = c.p.shift_prefix;
+    first.shift_suffix = c.p.shift_suffix;
+  }
+  cudaError_t e = launch_kv8_prompt<KV8_PREFIX>(first, D, cache->format, c.grid, c.dev, s);
+  if (e == cudaSuccess && !c.R) e = launch_kv8_join<KV8_PREFIX>(first, D, c.grid, s);
+  if (e == cudaSuccess) {
+    st = attend<KV8_SUFFIX>(cache, c.p, c.R, c.grid, c.dev, s);
+    if (st != MOE_OK) return st;
+    if (c.R) e = launch_kv8_join<KV8_PREFIX>(first, D, c.grid, s);
+  }
   if (e != cudaSuccess) {
     set_error_detail("gqa_kv8_prefix_attention: launch", e);
     return MOE_ERR_CUDA;
   }
-  return attend<KV8_SUFFIX>(cache, c.p, c.R, c.grid, c.dev, s);
+  return MOE_OK;
 }

@@ -3,6 +3,7 @@
 // key/value and 16 query heads of 128: the write of 16 thousand tokens (int8, 23 MB) 5.9 us
 // (3.5 at the copy rate), 60 thousand rows read back (e4m3, 92 MB) 15.1 us (13.8), 16384 tokens
 // rotated (151 MB) 28.0 us (22.6).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -218,31 +219,6 @@ struct RopeParams {
   float eps, offset;
 };
 
-// Sums of squares between these need no care: none of their terms that matter left fp32's range.
-constexpr float NORM_LEAST = 0x1p-80f;
-constexpr float NORM_LEAST_EPS = 0x1p-60f;       // beside it, smaller sums do not matter
-
-// A head whose squares leave fp32 (magnitudes over 2^60 or under 2^-45): the norm in 64 bits, on
-// the head's 2^D8 lanes.  Infinities make the others zeros and themselves NaN, as the formula does.
-template <int IPH>
-__device__ __noinline__ void norm_far(uint4& a, uint4& b, float (&x)[16], uint32_t mask, float eps, int D) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  double sum = 0.0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const double lo = bf16lo(w[j]), hi = bf16hi(w[j]);
-    sum += lo * lo + hi * hi;
-  }
-#pragma unroll
-  for (int m = IPH / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
-  const double root = sqrt(sum / D + eps), r = root == 0.0 ? 0.0 : 1.0 / root;     // zeros with eps 0 stay zeros
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[2 * j] = static_cast<float>(bf16lo(w[j]) * r);
-    x[2 * j + 1] = static_cast<float>(bf16hi(w[j]) * r);
-  }
-}
-
 }  // namespace
 
 // Rotary positions.  pos * turn is exact modulo one turn in 64-bit arithmetic, its top bits
@@ -250,17 +226,12 @@ __device__ __noinline__ void norm_far(uint4& a, uint4& b, float (&x)[16], uint32
 // tokens once into shared memory and turns all heads with them.  Its work items are two
 // 16-byte chunks of a head: chunk i with chunk i + half / 8 of the rotated part, or two
 // chunks of the part that passes through.
-//
-// With NORM every head is first divided by its root mean square and multiplied by its weights, in
-// fp32 and without a rounding between: the D / 16 threads of a head, neighbours in a warp, add
-// their squares by shuffles.
-template <int D, bool NORM>
+template <int D>
 __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ float s_cs[];        // [tokens][half] cosines, then sines
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
   float* s_cos = s_cs;
   float* s_sin = s_cs + p.tokens * p.half;
-  float* s_w = s_sin + p.tokens * p.half;                // [2][D] weights, as factors
   constexpr int IPH = D / 16;            // items per head
   constexpr int NB = 3;                  // items of a thread in flight: 4 tokens of 18 heads of 128
   const int rot_items = p.half / 8, nh = p.heads[0] + p.heads[1], n = nt * nh * IPH;
@@ -268,7 +239,6 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     const __nv_bfloat16* src;
     __nv_bfloat16* dst;
     int ca, cb, at;                      // its chunks' first elements; of its sines, or -1
-    int which;                           // q, k
   };
   const auto item = [&](int i) {
     Item r;
@@ -276,7 +246,6 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     const int t = static_cast<int>((static_cast<uint32_t>(th) * p.inv_heads) >> 21), hh = th - t * nh;
     const int which = hh >= p.heads[0];
     const int h = which ? hh - p.heads[0] : hh;
-    r.which = which;
     r.src = p.in[which] + static_cast<size_t>(t0 + t) * p.in_stride[which] + h * D;
     r.dst = p.out[which] + static_cast<size_t>(t0 + t) * p.out_stride[which] + h * D;
     const bool rot = part < rot_items;
@@ -308,15 +277,6 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
     s_cos[i] = c;
     s_sin[i] = s;
   }
-  if constexpr (NORM) {
-    for (int i = threadIdx.x; i < 2 * D; i += RP_THREADS) {
-      const void* w = p.weight[i / D];
-      float v = 1.0f;
-      if (w) v = (p.weight_f32 ? __ldg(static_cast<const float*>(w) + i % D)
-                               : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i % D))) + p.offset;
-      s_w[i] = v;
-    }
-  }
   __syncthreads();
   for (int i0 = threadIdx.x; i0 < n; i0 += NB * RP_THREADS) {
     if (i0 != threadIdx.x) load(i0);
@@ -325,49 +285,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
       const int i = i0 + k * RP_THREADS;
       if (i >= n) break;
       const Item r = item(i);
-      if constexpr (NORM) {
-        const uint32_t w[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
-        float x[16];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[2 * j] = bf16lo(w[j]);
-          x[2 * j + 1] = bf16hi(w[j]);
-          sum = fmaf(x[2 * j], x[2 * j], fmaf(x[2 * j + 1], x[2 * j + 1], sum));
-        }
-        // the head's threads only: others of the warp may be past the end
-        const uint32_t mask = ((1u << IPH) - 1) << (threadIdx.x & 31 & ~(IPH - 1));
-#pragma unroll
-        for (int m = IPH / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
-        if (sum <= 0x1p120f && (sum >= NORM_LEAST || p.eps >= NORM_LEAST_EPS)) {
-          const float f = rsqrtf(fmaf(sum, 1.0f / D, p.eps));
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] *= f;
-        } else {
-          norm_far<IPH>(a[k], b[k], x, mask, p.eps, D);
-        }
-        const float* wt = s_w + r.which * D;
-        const float *wa = wt + r.ca, *wb = wt + r.cb;
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          const float4 va = *reinterpret_cast<const float4*>(wa + j), vb = *reinterpret_cast<const float4*>(wb + j);
-          x[j] *= va.x, x[j + 1] *= va.y, x[j + 2] *= va.z, x[j + 3] *= va.w;
-          x[8 + j] *= vb.x, x[9 + j] *= vb.y, x[10 + j] *= vb.z, x[11 + j] *= vb.w;
-        }
-        if (r.at >= 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float c = s_cos[r.at + j], s = s_sin[r.at + j], u = x[j], v = x[8 + j];
-            x[j] = u * c - v * s;
-            x[8 + j] = v * c + u * s;
-          }
-        }
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(__float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]));
-        a[k] = make_uint4(o[0], o[1], o[2], o[3]);
-        b[k] = make_uint4(o[4], o[5], o[6], o[7]);
-      } else if (r.at >= 0) {
+      if (r.at >= 0) {
         uint32_t *wa = &a[k].x, *wb = &b[k].x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -380,6 +298,184 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
       }
       *reinterpret_cast<uint4*>(r.dst + r.ca) = a[k];
       *reinterpret_cast<uint4*>(r.dst + r.cb) = b[k];
+    }
+  }
+}
+
+// ============================================================================ norms and rotary positions
+namespace {
+
+constexpr int NR_TOKENS = 8;               // tokens of a CTA at most
+constexpr int NR_CTAS = 4;                 // resident CTAs per SM (64 registers)
+
+// Sums of squares between these need no care: none of their terms that matter left fp32's range.
+constexpr float NORM_LEAST = 0x1p-80f;
+constexpr float NORM_LEAST_EPS = 0x1p-60f;       // beside it, smaller sums do not matter
+
+// A head whose squares leave fp32 (magnitudes over 2^60 or under 2^-45): its root mean square in
+// 64 bits, by the head's IPH threads.  Returns a power of two next to its reciprocal and the rest
+// of it, so that neither product leaves fp32.  Infinities make the others zeros and themselves NaN,
+// as the formula does.  (By value: a thread's elements stay in registers on the ordinary way.)
+template <int IPH>
+__device__ __noinline__ float2 norm_far(uint4 a, uint4 b, uint32_t mask, float eps) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double lo = bf16lo(w[j]), hi = bf16hi(w[j]);
+    sum += lo * lo + hi * hi;
+  }
+#pragma unroll
+  for (int m = IPH / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(mask, sum, m);
+  const double root = sqrt(sum / (16 * IPH) + eps);
+  if (root == 0.0) return make_float2(1.0f, 0.0f);       // zeros with eps 0 stay zeros
+  const int e = isfinite(root) ? min(max(ilogb(root), -126), 126) : 0;
+  return make_float2(pow2i(-e), static_cast<float>(1.0 / (root * pow2i(-e))));
+}
+
+}  // namespace
+
+// Norms of the heads with the rotary positions.  A CTA has some tokens and computes their sines once.
+// D / 16 neighbouring lanes share a head (two 16-byte chunks each, as in rope_kernel) and add
+// their squares by shuffles, so a step of a warp is 512 / D heads of q or of k of one token, and a
+// lane keeps its place in the head from step to step.  Arithmetic goes two elements at a time;
+// sines and weights (as factors) lie in shared memory with the halves of the 8-element chunks
+// apart, so that neighbours' 16-byte loads lie side by side.
+template <int D>
+__global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float s_cs[];          // [tokens][half] cosines, then sines, then [2][D] weights
+  __shared__ uint64_t s_turn[GQA_ROPE_MAX_PAIRS];
+  __shared__ const int* s_pos[GQA_ROPE_MAX_PAIRS];
+  const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0), half = p.half;
+  float* s_cos = s_cs;
+  float* s_sin = s_cs + p.tokens * half;
+  float* s_w = s_sin + p.tokens * half;
+  constexpr int IPH = D / 16, NG = 32 / IPH, WARPS = RP_THREADS / 32;      // lanes of a head, heads of a step
+  constexpr int NB = 2;                  // steps of a warp in flight
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, part = lane % IPH, grp = lane / IPH;
+  const bool rot = part < half / 8;
+  const int ca = rot ? part * 8 : 2 * half + (part - half / 8) * 16, gap = rot ? half : 8, own = grp * D + ca;
+  const int nq = (p.heads[0] + NG - 1) / NG, per = nq + (p.heads[1] + NG - 1) / NG, n = nt * per;
+  struct Step {
+    int t, head, which;                  // token, first head, q or k
+    bool live;                           // the lane's head exists
+  };
+  const auto step = [&](int i) {
+    Step r;
+    r.t = (static_cast<uint32_t>(i) * p.inv_heads) >> 21;
+    const int st = i - r.t * per;
+    r.which = st >= nq;
+    r.head = (r.which ? st - nq : st) * NG;
+    r.live = r.head + grp < (r.which ? p.heads[1] : p.heads[0]);
+    return r;
+  };
+  uint4 a[NB], b[NB];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      a[k] = b[k] = make_uint4(0, 0, 0, 0);
+      const int i = i0 + k * WARPS;
+      if (i >= n) break;
+      const Step r = step(i);
+      const __nv_bfloat16* src =
+          (r.which ? p.in[1] : p.in[0]) + (t0 + r.t) * (r.which ? p.in_stride[1] : p.in_stride[0]) + r.head * D;
+      if (r.live) {
+        a[k] = *reinterpret_cast<const uint4*>(src + own);
+        b[k] = *reinterpret_cast<const uint4*>(src + own + gap);
+      }
+    }
+  };
+  if (threadIdx.x < half) {
+    s_turn[threadIdx.x] = p.turn[threadIdx.x];
+    s_pos[threadIdx.x] = p.pos + static_cast<size_t>(p.axis[threadIdx.x]) * p.T + t0;
+  }
+  grid_dep_wait();
+  load(warp);                            // on their way while the sines are computed
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += RP_THREADS) {
+    const int t = i / half, j = i - t * half;
+    const long long pos = __ldg(s_pos[j] + t);
+    const long long frac = static_cast<long long>(static_cast<unsigned long long>(pos) * s_turn[j]);
+    float s, c;
+    sincospif(static_cast<float>(frac) * 1.0842021724855044e-19f /* 2^-63 */, &s, &c);
+    const int at = t * half + (j >> 2 & 1) * (half / 2) + (j >> 3) * 4 + (j & 3);
+    s_cos[at] = c;
+    s_sin[at] = s;
+  }
+  for (int i = threadIdx.x; i < 2 * D; i += RP_THREADS) {
+    const int which = i / D, e = i % D;
+    const void* w = which ? p.weight[1] : p.weight[0];
+    float v = 1.0f;
+    if (w) v = (p.weight_f32 ? __ldg(static_cast<const float*>(w) + e) : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + e))) + p.offset;
+    s_w[which * D + (e >> 2 & 1) * (D / 2) + (e >> 3) * 4 + (e & 3)] = v;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i0 = warp; i0 < n; i0 += NB * WARPS) {
+    if (i0 != warp) load(i0);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int i = i0 + k * WARPS;
+      if (i >= n) break;
+      const uint32_t w[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
+      uint64_t x[8], sum2[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = f32x2(bf16lo(w[j]), bf16hi(w[j]));
+        sum2[j & 1] = fma2(x[j], x[j], sum2[j & 1]);
+      }
+      const float2 both = f32x2_get(add2(sum2[0], sum2[1]));
+      float sum = both.x + both.y;
+#pragma unroll
+      for (int m = IPH / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      float f;
+      if (sum <= 0x1p120f && (sum >= NORM_LEAST || p.eps >= NORM_LEAST_EPS)) {
+        f = rsqrtf(fmaf(sum, 1.0f / D, p.eps));
+      } else {
+        // by the head's lanes: other heads of the step may be ordinary ones
+        const float2 r2 = norm_far<IPH>(a[k], b[k], ((1u << IPH) - 1) << (grp * IPH), p.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], f32x2(r2.x, r2.x));
+        f = r2.y;
+      }
+      const Step r = step(i);
+      const float* wt = s_w + r.which * D + ca / 2;
+      const float *cs = s_cos + r.t * half + part * 4, *sn = s_sin + r.t * half + part * 4;
+      const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const ulonglong2 wa = *reinterpret_cast<const ulonglong2*>(wt + q * (D / 2));
+        const ulonglong2 wb = *reinterpret_cast<const ulonglong2*>(wt + gap / 2 + q * (D / 2));
+        const uint64_t u[2] = {wa.x, wa.y}, v[2] = {wb.x, wb.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[2 * q + j] = mul2(mul2(x[2 * q + j], f2), u[j]);
+          x[4 + 2 * q + j] = mul2(mul2(x[4 + 2 * q + j], f2), v[j]);
+        }
+        if (rot) {
+          const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(cs + q * (half / 2));
+          const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(sn + q * (half / 2));
+          const uint64_t c[2] = {c2.x, c2.y}, s[2] = {s2.x, s2.y};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint64_t a0 = x[2 * q + j], b0 = x[4 + 2 * q + j];
+            x[2 * q + j] = fma2(b0, s[j] ^ 0x8000000080000000ull, mul2(a0, c[j]));
+            x[4 + 2 * q + j] = fma2(a0, s[j], mul2(b0, c[j]));
+          }
+        }
+      }
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 y = f32x2_get(x[j]);
+        o[j] = pack_bf16x2(__float_as_uint(y.x), __float_as_uint(y.y));
+      }
+      __nv_bfloat16* dst =
+          (r.which ? p.out[1] : p.out[0]) + (t0 + r.t) * (r.which ? p.out_stride[1] : p.out_stride[0]) + r.head * D;
+      if (r.live) {
+        *reinterpret_cast<uint4*>(dst + own) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + own + gap) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
@@ -618,17 +714,21 @@ moe_status_t rope_launch(const gqa_rope_plan_t* plan, const gqa_norm_t* norm, co
   p.pos = pos;
   p.T = T;
   p.n_axes = plan->n_axes;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
   // One token per CTA spreads few tokens over more SMs, four share the launch of a CTA and its wait
   // for the sines (18 heads of 128): 64 tokens 2.1 us one by one and 2.7 by four, 512 2.6 and 2.8,
   // 1024 4.1 and 3.7, 2048 5.8 and 5.2, 16384 43.6 and 28.3.
   p.tokens = T >= 1024 ? 4 : 1;
-  p.inv_heads = ((1u << 21) + n_q_heads + n_k_heads - 1) / (n_q_heads + n_k_heads);
+  // With norms, as many as make one wave of CTAs.
+  if (norm) p.tokens = std::min(NR_TOKENS, std::max(1, (T - 1) / (152 * NR_CTAS) + 1));
+  const int ng = 512 / D, per = norm ? (n_q_heads + ng - 1) / ng + (n_k_heads + ng - 1) / ng : n_q_heads + n_k_heads;
+  p.inv_heads = ((1u << 21) + per - 1) / per;
   const dim3 grid((T + p.tokens - 1) / p.tokens);
   const size_t smem = (2ull * p.tokens * p.half + (norm ? 2 * D : 0)) * sizeof(float);
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto* kernel = norm ? (D == 128 ? rope_kernel<128, true> : rope_kernel<64, true>)
-                      : (D == 128 ? rope_kernel<128, false> : rope_kernel<64, false>);
-  const cudaError_t e = launch_pdl(kernel, grid, dim3(RP_THREADS), smem, s, p);
+  auto* kernel = norm ? (D == 128 ? norm_rope_kernel<128> : norm_rope_kernel<64>)
+                      : (D == 128 ? rope_kernel<128> : rope_kernel<64>);
+  e = launch_pdl(kernel, grid, dim3(RP_THREADS), smem, s, p);
   if (e != cudaSuccess) {
     set_error_detail(norm ? "gqa_norm_rope: launch" : "gqa_rope: launch", e);
     return MOE_ERR_CUDA;

@@ -16,10 +16,15 @@ bool kv8_rows_ok(const void* p, long long stride, long long width, moe_status_t*
 Kv8Cache kv8_cache(const gqa_kv8_cache_t* c);
 Kv8Batch kv8_batch(const gqa_kv8_batch_t* b);
 
-// Attention with many query rows per key/value head (kv8_prompt.cu): its workspace, and its
-// launch on `grid` CTAs of device `dev` (sets p.tq_shift itself).
+// Attention with many query rows per key/value head (kv8_prompt.cu): its workspace, the tokens of
+// a tile (as a shift) with at most `tokens` to a sequence or group, and its launch on `grid` CTAs of
+// device `dev` (sets p.tq_shift itself), which leaves the parts of divided tiles to the join in
+// prefix mode and joins them in the others.
 size_t kv8_prompt_ws_bytes(int D);
+int kv8_prompt_shift(int G, int tokens);
 template <int MODE>
 cudaError_t launch_kv8_prompt(Kv8AttnParams p, int D, int format, int grid, int dev, cudaStream_t s);
+template <int MODE>
+cudaError_t launch_kv8_join(Kv8AttnParams p, int D, int grid, cudaStream_t s);
 
 }  // namespace moe

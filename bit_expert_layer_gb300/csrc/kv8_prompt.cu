@@ -46,6 +46,10 @@ constexpr int KP_DEQ = 4;                         // dequantising warps
 constexpr int KP_THREADS = (8 + KP_DEQ + 2) * 32;
 constexpr int KP_U = 128;                         // positions per tile
 constexpr int KP_COST = 2;                        // a tile's start, in units
+#ifndef XKP
+#define XKP 6
+#endif
+constexpr int KP_JOIN = XKP;                      // parts of a tile meeting through the workspace, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
 constexpr int KP_SLOTS = 8;                       // tiles whose scales the softmax can ask for
 constexpr int KP_PLANS = 4;                       // tiles planned ahead
@@ -59,7 +63,7 @@ __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
 __host__ __device__ constexpr int kp_smem(int D, int B, bool suffix) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
-  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 12 + (B + 2) * 8 + KP_THREADS / 32 * 8 + 25 * 8 + 64 + KP_PLANS * 128 +
+  return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 12 + (B + 2) * 8 + KP_THREADS / 32 * 3 * 8 + 25 * 8 + 64 + KP_PLANS * 128 +
          (suffix ? B * 4 : 0);
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS, true) <= 232448, "shared memory per CTA exceeds 227 KB");
@@ -146,27 +150,6 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
-// Two fp32 fused multiply-adds / additions in one instruction.
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f32x2_get(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // The softmax's steps that few tiles need are functions of their own: with them inside its loop a
 // piece of 2048 tokens over 31000 positions took between 392 and 475 us, as the compiler's
 // registers for the loop fell out, with changing inputs up to 486; now 401 and 409.  (Heads of 64
@@ -180,11 +163,16 @@ __device__ __forceinline__ void kp_mask(uint32_t t_s, int left, uint32_t bad, in
   uint32_t x[32];
 #pragma unroll 1
   for (int c = 0; c < KP_U / 32; ++c) {
-    tmem_ld32(t_s + 32 * c, x);
+    if (MODE != KV8_WINDOW) tmem_ld32(t_s + 32 * c, x);
     uint32_t seen = kp_under(left - 32 * c);
     if (MODE == KV8_WINDOW) seen &= ~kp_under(before - 32 * c) | kp_under(sinks - 32 * c);
     if ((bad >> (2 * c)) & 1) seen &= 0xFFFF0000u;
     if ((bad >> (2 * c + 1)) & 1) seen &= 0x0000FFFFu;
+    if (MODE == KV8_WINDOW) {
+      // most tiles of a window have two edges, which most of their columns lie clear of
+      if (__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) continue;
+      tmem_ld32(t_s + 32 * c, x);
+    }
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -285,8 +273,11 @@ struct __align__(16) KpTile {
   int ns;                // CTAs (0: no such tile)
   int t, g, off, n;      // tile, key/value head, the sequence's first row and new tokens
   int base;              // positions that the prefix pass has seen to
-  int pad[2];
+  int whole;             // prefix mode: whether the CTA has tiles of its own (set apart from the others)
+  int pad;
 };
+constexpr int KP_SHARES = KV8_TICKET_BYTES / 4 - 1;      // prefix mode: the word of the tickets' that tells whether anything is shared
+static_assert(KP_SHARES >= KV8_MAX_CTAS, "behind the tickets");
 
 // Workspace of a part: floats of a row (O, references, normaliser), the rows of CTA c's part of
 // a tile that began in CTA c_first, and the tiles to join, one entry per CTA.
@@ -319,11 +310,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   float* s_peak = s_ms + 2 * KP_ROWS;                              // [256] the highest ms + d of a row
   long long* prefix = reinterpret_cast<long long*>(s_peak + 2 * KP_ROWS);
   long long* s_warp = prefix + kv8_items<MODE>(p) + 1;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_warp + KP_THREADS / 32 * 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(abort_flag) + 1);
   volatile int* s_n = reinterpret_cast<volatile int*>(s_tmem + 1);    // [2]
-  int* base = reinterpret_cast<int*>(s_tmem + 3);                     // suffix mode: [n_seqs]
+  Kv8Line line = {prefix, reinterpret_cast<int*>(s_tmem + 3), 0, false};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * i; };
@@ -348,16 +339,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
     fence_mbar_init();
   }
   grid_dep_wait();                              // what follows reads and writes what earlier kernels wrote
-  Kv8Runs runs;
-  runs.total = kv8_line<KP_U, KP_COST, KP_THREADS, MODE>(p, prefix, s_warp, base);
-  runs.n = static_cast<int>(min(runs.total, static_cast<long long>(gridDim.x)));
+  if (MODE == KV8_PREFIX && p.own) grid_dep_launch();
+  const Kv8Runs runs = kv8_line<KP_U, KP_COST, KP_THREADS, 1, KP_JOIN, MODE>(p, line, s_warp, gridDim.x);
   const int cta = blockIdx.x;
+  if (MODE == KV8_PREFIX && tid == 0 && cta == 0) p.tickets[KP_SHARES] = line.shares;
   if (cta >= runs.n) {                          // the whole CTA, before any TMEM is held
-    if (tid == 0) kp_tiles(p.part)[cta].ns = 0;
+    if (tid == 0) kp_tiles(p.part)[cta].ns = kp_tiles(p.part)[cta].whole = 0;
     return;
   }
-  const long long w_beg = kv8_run_begin(runs, cta), w_end = kv8_run_begin(runs, cta + 1);
-  const Kv8Seg first = kv8_seg<KP_U, KP_COST, MODE>(p, prefix, base, w_beg, w_end);   // where every role begins
+  const long long w_beg = kv8_run_begin<KP_U, MODE>(runs, cta), w_end = kv8_run_begin<KP_U, MODE>(runs, cta + 1);
+  const Kv8Seg first = kv8_seg<KP_U, KP_COST, MODE>(p, line, w_beg, w_end);   // where every role begins
   if (warp == 8 + KP_DEQ) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
@@ -379,12 +370,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns))) dead = true;
       };
       const uint32_t inv_g = (65535u + p.G) / p.G;       // r / G = r inv_g >> 16 for r < 128, G <= 16
-      int it = 0, seg = 0;
-      if (tid == 0) kp_tiles(p.part)[cta].ns = 0;        // unless a tile that begins here goes on
+      int it = 0, seg = 0, any_whole = 0;
+      if (tid == 0) kp_tiles(p.part)[cta].ns = kp_tiles(p.part)[cta].whole = 0;   // unless a tile that begins here goes on
       Kv8Seg sg = first;
 #pragma unroll 1
       for (long long w = w_beg; w < w_end;) {
-        if (w > w_beg) kv8_next<KP_U, KP_COST, MODE>(sg, p, prefix, base, w, w_end);
+        if (w > w_beg) kv8_next<KP_U, KP_COST, MODE>(sg, p, line, w, w_end);
         w += sg.len;
         if (sg.u1 <= sg.u0) continue;      // the run ends before the tile's first positions
         const int tok0 = (sg.t << p.tq_shift) + blk * blk_tokens;
@@ -446,10 +437,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           const float4 sc4 = s_scale[it & (KP_SLOTS - 1)];
           const float f = fminf(fmaxf(rs * sc4.x, 1e-37f), KV8_MAX_FACTOR), e = sc4.y;  // positive: -inf stays -inf
           const uint32_t bad = __float_as_uint(sc4.w);
-          const int at_u = kv8_unit<KP_U, MODE>(sg, u) * KP_U;
-          const int left = see - at_u;                           // positions of the tile that the row sees
-          // window mode: those of the tile before the window, and those of the sinks
-          const int before = MODE == KV8_WINDOW && live ? left - p.window : 0, sinks = MODE == KV8_WINDOW ? p.sinks - at_u : 0;
+          // places of the unit that the row sees
+          const int left = see - kv8_skip<MODE>(sg, 1 << 30) - u * KP_U;
+          // window mode: those before its window, and those of the sinks
+          const int before = MODE == KV8_WINDOW && live ? left - p.window : 0;
+          const int sinks = MODE == KV8_WINDOW ? p.sinks - u * KP_U : 0;
           uint32_t sc[2][32];
           // A tile at the causal edge, or with a page missing: what the row does not see becomes
           // -inf in TMEM first, so that the passes below carry no mask (with it in them, the
@@ -557,7 +549,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           unit = jn.unit;
         }
         const float inv = jn.sum == 0.0f ? 0.0f : 1.0f / jn.sum; // a row that saw no key: zeros
-        const int2 own = whole ? make_int2(cta, cta) : kv8_owners<KP_COST>(sg, w - sg.len, runs);
+        const int2 own = whole ? make_int2(cta, cta) : kv8_owners<KP_U, KP_COST, MODE>(sg, w - sg.len, runs);
         float* part = kp_slot<D>(p.part, cta, own.x, blk * KP_ROWS + r);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -565,7 +557,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           tmem_ld32(t_o + 32 * c, o);
           tmem_ld_wait();
           if (whole && MODE == KV8_PREFIX) {
-            if (dst && !dead)
+            if (live && !dead)
 #pragma unroll
               for (int j = 0; j < 32; j += 8) st_global_v8(row + 32 * c + j, o + j);
           } else if (whole) {
@@ -603,9 +595,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!whole) {
           *reinterpret_cast<float4*>(part + D) = make_float4(ms, d, l, 0.0f);
           if (tid == 0 && own.x == cta)
-            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, sg.s.base, {0, 0}};
-        } else if (MODE == KV8_PREFIX && live && !dead) {
-          *reinterpret_cast<float4*>(row + D) = make_float4(ms, d, l, 0.0f);
+            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, sg.s.base, any_whole, 0};
+          // (a row whose parts are joined first says so)
+          if (MODE == KV8_PREFIX && own.x == cta && live) row[D + 3] = 0.0f;
+        } else if (MODE == KV8_PREFIX && live) {
+          *reinterpret_cast<float4*>(row + D) = make_float4(ms, d, l, dead ? 0.0f : 1.0f);
+          any_whole = 1;
+          if (r == 0 && blk == 0) kp_tiles(p.part)[cta].whole = 1;
         }
         ++seg;
       }
@@ -687,24 +683,26 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
       int it = 0;
 #pragma unroll 1
       for (long long w = w_beg; ok; w += sg.len) {
-        if (w > w_beg && w < w_end) kv8_next<KP_U, KP_COST, MODE>(sg, p, prefix, base, w, w_end);
+        if (w > w_beg && w < w_end) kv8_next<KP_U, KP_COST, MODE>(sg, p, line, w, w_end);
         const bool more = w < w_end;
         const int end = kv8_seg_end<MODE>(sg, p.tq_shift);
         const int* table = kv8_table<MODE>(p, sg.b);
         int u = more ? sg.u0 : 0;
         const int u1 = more ? sg.u1 : 1;               // at the end one more plan: no more tiles
         int pid = -1;
+        const auto place = [&](int u) {                // where the lane's block of unit u begins
+          const int i = u * KP_U + lb * KV8_BLOCK;
+          return i + kv8_skip<MODE>(sg, i);
+        };
         const auto look = [&] {
-          const int pos = kv8_unit<KP_U, MODE>(sg, u) * KP_U + lb * KV8_BLOCK;
+          const int pos = place(u);
           pid = more && u < u1 && pos < end ? __ldg(table + (pos >> p.c.page_shift)) : -1;
         };
         look();
 #pragma unroll 1
         while (u < u1) {
-          const int at_u = kv8_unit<KP_U, MODE>(sg, u) * KP_U, pos = at_u + lb * KV8_BLOCK;
-          // (a block that no token of the tile sees is left out: its page may be gone)
-          const bool exists = more && pos < end && (MODE != KV8_WINDOW || pos < p.sinks || pos + KV8_BLOCK > sg.low);
-          const bool bad = exists && (pid < 0 || pid >= p.c.n_pages);
+          const int pos = place(u);
+          const bool exists = more && pos < end, bad = exists && (pid < 0 || pid >= p.c.n_pages);
           int row = -1;
           float scale = 0.0f;
           if (exists && !bad) {
@@ -713,7 +711,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
           }
           // A sequence with fewer positions than new tokens has units past its end: nothing valid
           // in them, which is not the mark of the end.
-          const int valid = more ? max(end - at_u, 0) : -1;
+          const int valid = more ? max(end - kv8_skip<MODE>(sg, 1 << 30) - u * KP_U, 0) : -1;
           ++u;
           look();                                      // the next tile's pages meanwhile
           const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xFFu;
@@ -844,7 +842,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
 // Joins the parts of the tiles that lie in several CTAs: a block per tile (by its first CTA)
 // and 8 rows, a warp per row, the parts in the order of the line.  (The last CTA of a tile
 // joining them itself took over 60 us of a 150 us prompt: 256 rows by one CTA's 8 warps.)
-template <int D, int MODE>
+template <int D>
 __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk) {
   grid_dep_wait();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
@@ -938,29 +936,202 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
       }
     }
   }
-  float unit = ex2(top);
-  const size_t at = static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G;
-  if constexpr (MODE == KV8_PREFIX) {
-    float* to = p.rows + at * kv8_row_floats(D);
-#pragma unroll
-    for (int k = 0; k < PL; ++k) to[PL * lane + k] = O[k];
-    if (lane == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, top, L, 0.0f);
-    return;
-  }
-  if (MODE == KV8_SUFFIX && tl.base) {             // the row's shared positions
-    const float* src = p.rows + at * kv8_row_floats(D);
-    const Kv8Join j = kv8_join(make_float4(M, top, L, 0.0f), *reinterpret_cast<const float4*>(src + D));
-#pragma unroll
-    for (int k = 0; k < PL; ++k) O[k] = fmaf(j.f[0], O[k], j.f[1] * src[PL * lane + k]);
-    L = j.sum;
-    unit = j.unit;
-  }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // a row that saw no key: zeros
-  __nv_bfloat16* dst = p.out + at * D + PL * lane;
+  const float unit = ex2(top);
+  __nv_bfloat16* dst = p.out + (static_cast<size_t>(tl.off + tok) * p.hq + tl.g * p.G + r - tb * p.G) * D + PL * lane;
 #pragma unroll
   for (int k = 0; k < PL; k += 2)
     *reinterpret_cast<uint32_t*>(dst + k) =
         pack_bf16x2(__float_as_uint(O[k] * inv * unit), __float_as_uint(O[k + 1] * inv * unit));
+}
+
+// The same for the other modes, whose tiles are few or have many parts.  Every block makes the list of
+// tiles to join, as chunks of work of the same size, and takes its share of them, so no block is
+// launched for a tile that is not there (4864 of them cost 6 us).  A row's parts are divided among 1, 2, 4
+// or 8 warps, each of which has its loads under way together, and the warps' sums meet in shared
+// memory in order.  In prefix mode the result stays in sums, for the suffix pass to take up; or, where
+// that pass ran beside it, meets that pass's sums, as those of rows do whose tile was whole.
+constexpr int KJ_WARPS = 8, KJ_PER_SM = 4;  // and blocks of a launch per SM
+constexpr int KJ_FLIGHT = 6;                // parts of a warp whose loads are under way together
+__device__ __forceinline__ int kj_split(int ns) {          // warps of a row
+  return ns <= KJ_FLIGHT ? 1 : ns <= 2 * KJ_FLIGHT ? 2 : ns <= 4 * KJ_FLIGHT ? 4 : 8;
+}
+template <int D, int MODE>
+__global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk, int ctas) {
+  constexpr int PL = D / 32;                    // dims per lane
+  __shared__ int s_start[KV8_MAX_CTAS + 1], s_sum[KJ_WARPS];
+  __shared__ float s_o[KJ_WARPS][D];
+  __shared__ float4 s_ref[KJ_WARPS];
+  static_assert(KV8_MAX_CTAS <= KJ_WARPS * 32, "a thread per tile");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tq = 1 << p.tq_shift, blk_tokens = tq / nblk;
+  const auto rows_of = [&](const KpTile& t) { return min(tq, t.n - (t.t << p.tq_shift)) * p.G; };
+  grid_dep_wait();
+  const bool both = MODE == KV8_PREFIX && p.own;         // the two passes ran side by side
+  int chunks = 0, whole = 0;
+  if (tid < ctas && !(both && !p.tickets[KP_SHARES])) {
+    const KpTile t = kp_tiles(p.part)[tid];
+    whole = t.whole;
+    if (t.ns > 0) chunks = (rows_of(t) * kj_split(t.ns) + KJ_WARPS - 1) / KJ_WARPS;
+  }
+  int incl = chunks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < KJ_WARPS; ++w) {
+    if (w < warp) incl += s_sum[w];
+    total += s_sum[w];
+  }
+  if (tid < KV8_MAX_CTAS) s_start[tid] = incl - chunks;
+  whole = __syncthreads_or(whole);
+  // a row's two sums, meeting: that of its shared positions (m, d, l, O) and its own
+  const auto meet = [&](size_t at, const float4& shared, float (&O)[PL]) {
+    const float* src = p.own + at * kv8_row_floats(D);
+    const float4 own = *reinterpret_cast<const float4*>(src + D);
+    if (own.w == 0.0f) return;                   // the sequence did without the prefix pass
+    const Kv8Join jn = kv8_join(own, shared);
+    const float inv = jn.sum == 0.0f ? 0.0f : 1.0f / jn.sum;
+    __nv_bfloat16* dst = p.out + at * D + PL * lane;
+#pragma unroll
+    for (int q = 0; q < PL; q += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + PL * lane + q);
+      *reinterpret_cast<uint32_t*>(dst + q) =
+          pack_bf16x2(__float_as_uint(fmaf(jn.f[0], v.x, jn.f[1] * O[q]) * inv * jn.unit),
+                      __float_as_uint(fmaf(jn.f[0], v.y, jn.f[1] * O[q + 1]) * inv * jn.unit));
+    }
+  };
+  const int off0 = both && whole ? __ldg(p.b.offsets) : 0;
+  const int rows = both && whole ? (__ldg(p.b.offsets + p.b.n_seqs) - off0) * p.hq : 0;
+#pragma unroll 1
+  for (int item = blockIdx.x; item < total + (rows + KJ_WARPS - 1) / KJ_WARPS; item += gridDim.x) {
+    if (item >= total) {
+      // a row of the batch, if its tile was whole
+      const int i = (item - total) * KJ_WARPS + warp;
+      if (i >= rows) continue;
+      const size_t at = static_cast<size_t>(off0) * p.hq + i;
+      if (p.own[at * kv8_row_floats(D) + D + 3] == 0.0f) continue;
+      const float* src = p.rows + at * kv8_row_floats(D);
+      const float4 ref = *reinterpret_cast<const float4*>(src + D);
+      if (ref.w == 0.0f) continue;
+      float O[PL];
+#pragma unroll
+      for (int q = 0; q < PL; ++q) O[q] = src[PL * lane + q];
+      meet(at, ref, O);
+      continue;
+    }
+    const int c0 = kv8_last_of(ctas, [&](int i) { return s_start[i] <= item; });
+    const KpTile tl = kp_tiles(p.part)[c0];
+    const int S = kj_split(tl.ns), sub = warp & (S - 1);
+    const int j = ((item - s_start[c0]) * KJ_WARPS + warp) / S;         // the row among the tile's
+    const bool live = j < rows_of(tl);
+    const int tok = j / p.G, hh = j - tok * p.G, blk = tok >= blk_tokens;
+    const int row = blk * KP_ROWS + (tok - blk * blk_tokens) * p.G + hh;
+    const auto slot = [&](int i) { return kp_slot<D>(p.part, c0 + i, c0, row); };
+    float m = KV8_NO_REF, d = -INFINITY, l = 0.0f, v[KJ_FLIGHT][PL];
+    const int i = sub + lane * S;                                       // this lane's part
+    const int n = live ? (tl.ns - sub + S - 1) / S : 0;                 // the warp's parts, at most 20
+    const auto fetch = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < KJ_FLIGHT; ++k)
+        if (k0 + k < n) {
+          const float* src = slot(sub + (k0 + k) * S) + PL * lane;
+          if constexpr (PL == 4)
+            *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+          else
+            *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+        }
+    };
+    if (lane < n) {
+      const float4 r = *reinterpret_cast<const float4*>(slot(i) + D);
+      m = r.x;
+      d = r.y;
+      l = r.z;
+    }
+    fetch(0);
+    float M = m;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = ex2(m - M) * l;
+    d += m - M;
+    float top = d;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      L += __shfl_xor_sync(0xffffffffu, L, o);
+    }
+    const float wt = ex2(d - top);
+    float O[PL];
+#pragma unroll
+    for (int k = 0; k < PL; ++k) O[k] = 0.0f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += KJ_FLIGHT) {
+      if (k0) fetch(k0);
+#pragma unroll
+      for (int k = 0; k < KJ_FLIGHT; ++k) {
+        const float f = __shfl_sync(0xffffffffu, wt, (k0 + k) & 31);
+        if (k0 + k < n)
+#pragma unroll
+          for (int q = 0; q < PL; ++q) O[q] = fmaf(f, v[k][q], O[q]);
+      }
+    }
+    if (S > 1) {
+#pragma unroll
+      for (int q = 0; q < PL; ++q) s_o[warp][PL * lane + q] = O[q];
+      if (lane == 0) s_ref[warp] = make_float4(M, top, L, 0.0f);
+      __syncthreads();
+      if (sub == 0) {
+        M = KV8_NO_REF;
+        for (int w = 0; w < S; ++w) M = fmaxf(M, s_ref[warp + w].x);
+        top = -INFINITY;
+        for (int w = 0; w < S; ++w) top = fmaxf(top, s_ref[warp + w].x - M + s_ref[warp + w].y);
+        L = 0.0f;
+#pragma unroll
+        for (int q = 0; q < PL; ++q) O[q] = 0.0f;
+        for (int w = 0; w < S; ++w) {
+          const float4 r = s_ref[warp + w];
+          L = fmaf(ex2(r.x - M), r.z, L);
+          const float f = ex2(r.x - M + r.y - top);
+#pragma unroll
+          for (int q = 0; q < PL; ++q) O[q] = fmaf(f, s_o[warp + w][PL * lane + q], O[q]);
+        }
+      }
+      __syncthreads();
+    }
+    if (sub != 0 || !live) continue;
+    const size_t at = static_cast<size_t>(tl.off + (tl.t << p.tq_shift) + tok) * p.hq + tl.g * p.G + hh;
+    if (both) {
+      meet(at, make_float4(M, top, L, 0.0f), O);
+      continue;
+    }
+    if constexpr (MODE == KV8_PREFIX) {
+      float* to = p.rows + at * kv8_row_floats(D);
+#pragma unroll
+      for (int q = 0; q < PL; ++q) to[PL * lane + q] = O[q];
+      if (lane == 0) *reinterpret_cast<float4*>(to + D) = make_float4(M, top, L, 0.0f);
+      continue;
+    }
+    float unit = ex2(top);
+    if (MODE == KV8_SUFFIX && tl.base) {           // the row's shared positions
+      const float* src = p.rows + at * kv8_row_floats(D);
+      const Kv8Join jn = kv8_join(make_float4(M, top, L, 0.0f), *reinterpret_cast<const float4*>(src + D));
+#pragma unroll
+      for (int q = 0; q < PL; ++q) O[q] = fmaf(jn.f[0], O[q], jn.f[1] * src[PL * lane + q]);
+      L = jn.sum;
+      unit = jn.unit;
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L; // a row that saw no key: zeros
+    __nv_bfloat16* dst = p.out + at * D + PL * lane;
+#pragma unroll
+    for (int q = 0; q < PL; q += 2)
+      *reinterpret_cast<uint32_t*>(dst + q) =
+          pack_bf16x2(__float_as_uint(O[q] * inv * unit), __float_as_uint(O[q + 1] * inv * unit));
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -983,26 +1154,49 @@ cudaError_t launch_prompt(const Kv8AttnParams& p, int nblk, int grid, int dev, c
   const cudaError_t e = launch_pdl(k, dim3(grid), dim3(KP_THREADS),
                                    kp_smem(D, MODE == KV8_PREFIX ? p.n_groups : p.b.n_seqs, MODE == KV8_SUFFIX), s, p, nblk);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_prompt_join_kernel<D, MODE == KV8_WINDOW ? KV8_CAUSAL : MODE>, dim3(grid, nblk * KP_ROWS / 8), dim3(256),
-                    0, s, p, nblk);
+  if constexpr (MODE == KV8_CAUSAL)
+    return launch_pdl(kv8_prompt_join_kernel<D>, dim3(grid, nblk * KP_ROWS / 8), dim3(256), 0, s, p, nblk);
+  return cudaSuccess;
+}
+// Tokens of a row block: the largest power of two whose rows fit.
+int kp_block_shift(int G) {
+  int shift = 0;
+  while ((2 << shift) * G <= KP_ROWS) ++shift;
+  return shift;
 }
 }  // namespace
 
+int kv8_prompt_shift(int G, int tokens) {
+  const int shift = kp_block_shift(G);
+  return shift + (tokens > (1 << shift));
+}
+
+template <int MODE>
+cudaError_t launch_kv8_join(Kv8AttnParams p, int D, int grid, cudaStream_t s) {
+  p.tq_shift = kv8_prompt_shift(p.G, MODE == KV8_PREFIX ? p.b.n_tokens : p.b.max_new);
+  const int nblk = 1 + p.tq_shift - kp_block_shift(p.G);
+  return launch_pdl(D == 128 ? kv8_parts_join_kernel<128, MODE> : kv8_parts_join_kernel<64, MODE>, dim3(grid * KJ_PER_SM),
+                    dim3(KJ_WARPS * 32), 0, s, p, nblk, grid);
+}
+
 template <int MODE>
 cudaError_t launch_kv8_prompt(Kv8AttnParams p, int D, int format, int grid, int dev, cudaStream_t s) {
-  // tokens of a row block: the largest power of two whose rows fit
-  int shift = 0;
-  while ((2 << shift) * p.G <= KP_ROWS) ++shift;
-  const int nblk = (MODE == KV8_PREFIX ? p.b.n_tokens : p.b.max_new) <= (1 << shift) ? 1 : 2;
-  p.tq_shift = shift + nblk - 1;
+  p.tq_shift = kv8_prompt_shift(p.G, MODE == KV8_PREFIX ? p.b.n_tokens : p.b.max_new);
+  const int nblk = 1 + p.tq_shift - kp_block_shift(p.G);
   if (MODE == KV8_WINDOW) p.win_units = kv8_win_units(KP_U, 1 << p.tq_shift, p.window, p.sinks);
   const bool e4 = format == GQA_KV8_E4M3;
+  cudaError_t e;
   if (D == 128)
-    return e4 ? launch_prompt<128, GQA_KV8_E4M3, MODE>(p, nblk, grid, dev, s)
-              : launch_prompt<128, GQA_KV8_INT8, MODE>(p, nblk, grid, dev, s);
-  return e4 ? launch_prompt<64, GQA_KV8_E4M3, MODE>(p, nblk, grid, dev, s)
-            : launch_prompt<64, GQA_KV8_INT8, MODE>(p, nblk, grid, dev, s);
+    e = e4 ? launch_prompt<128, GQA_KV8_E4M3, MODE>(p, nblk, grid, dev, s)
+           : launch_prompt<128, GQA_KV8_INT8, MODE>(p, nblk, grid, dev, s);
+  else
+    e = e4 ? launch_prompt<64, GQA_KV8_E4M3, MODE>(p, nblk, grid, dev, s)
+           : launch_prompt<64, GQA_KV8_INT8, MODE>(p, nblk, grid, dev, s);
+  if constexpr (MODE == KV8_WINDOW || MODE == KV8_SUFFIX)
+    if (e == cudaSuccess) e = launch_kv8_join<MODE>(p, D, grid, s);
+  return e;
 }
+template cudaError_t launch_kv8_join<KV8_PREFIX>(Kv8AttnParams, int, int, cudaStream_t);
 template cudaError_t launch_kv8_prompt<KV8_CAUSAL>(Kv8AttnParams, int, int, int, int, cudaStream_t);
 template cudaError_t launch_kv8_prompt<KV8_WINDOW>(Kv8AttnParams, int, int, int, int, cudaStream_t);
 template cudaError_t launch_kv8_prompt<KV8_PREFIX>(Kv8AttnParams, int, int, int, int, cudaStream_t);

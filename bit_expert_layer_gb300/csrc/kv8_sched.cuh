@@ -24,11 +24,12 @@
 //
 // The four modes differ in the positions that a tile's units stand for:
 //   causal   0 up to the tile's last token
-//   window   those of a sliding window and the first `sinks`, as whole units: the sinks' come first,
-//            then the window's.  The line counts a tile's units by a bound that needs no search,
-//            the causal count or K = ceil((W + TQ - 1 + U - 1) / U) + ceil(sinks / U), whichever is
-//            less; what a tile has less than that are units without positions at its end, which
-//            no run works on.
+//   window   the granules (of 16 positions for prompts, 32 for decode) that the first `sinks` touch,
+//            then those of the windows of the tile's tokens, one after the other as if the ones
+//            between them were not there; units are cut from that row.  The line counts a tile's
+//            units by a bound that needs no search, the causal count or K = kv8_win_units(),
+//            whichever is less; what a tile has less than that are units without positions at its
+//            end, which no run works on.
 //   prefix   the line's items are groups of sequences, an item's tokens those of all of the group's
 //            sequences, and every token sees all of the group's shared positions
 //   suffix   causal, from the first position on that the prefix pass left
@@ -42,6 +43,9 @@ constexpr int KV8_MAX_CTAS = 160;
 constexpr int KV8_MAX_DEVICES = 64;
 constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one ticket per CTA
 enum Kv8Mode { KV8_CAUSAL, KV8_WINDOW, KV8_PREFIX, KV8_SUFFIX };
+// Whether a kernel's runs may be aligned to tiles (see kv8_line): prompts, in these modes.
+__host__ __device__ constexpr bool kv8_aligns(int U, int mode) { return U == 128 && (mode == KV8_WINDOW || mode == KV8_SUFFIX); }
+__host__ __device__ constexpr int kv8_granule(int U) { return U == 128 ? 16 : U; }
 // Shared positions are worked on in whole units of either kernel; a sequence sees to the rest itself.
 constexpr int KV8_SHARED_UNIT = 128;
 // A query row is brought to [2^13, 2^14) by 2^-e, e within these bounds (any finite bf16 row fits
@@ -106,7 +110,9 @@ struct Kv8AttnParams {
   const int* groups;     // prefix and suffix modes: first sequence of each group, the end
   const int* shared;     // positions that each group shares
   int n_groups;
-  float* rows;           // what the prefix pass leaves: [token][query head][kv8_row_floats(D)]
+  float* rows;           // sums of the query rows, [token][query head][kv8_row_floats(D)]: what the prefix pass leaves,
+  float* own;            // and in side-by-side passes what the suffix pass leaves (else null)
+  int shift_prefix, shift_suffix;   // side by side: tokens of the two passes' tiles, as shifts
 };
 
 // Workspace of a query row's sums (O, references ms and d, normaliser): 32-byte rows.
@@ -127,10 +133,11 @@ __device__ __forceinline__ Kv8Join kv8_join(const float4& a, const float4& b) { 
   return j;
 }
 
-// Window mode: the most units of a tile, those that W + TQ - 1 consecutive positions can touch and the
-// sinks'.
+// Window mode: the most units of a tile, by the granules that W + TQ - 1 consecutive positions can
+// touch and the sinks'.
 __host__ __device__ constexpr int kv8_win_units(int U, int tq, int window, int sinks) {
-  return (window + tq - 1 + 2 * U - 2) / U + (sinks + U - 1) / U;
+  const int g = kv8_granule(U);
+  return (((window + tq - 1 + 2 * g - 2) / g + (sinks + g - 1) / g) * g + U - 1) / U;
 }
 
 // A run of units inside one tile.
@@ -140,22 +147,32 @@ struct Kv8Seg {
   int u0, u1, units;     // this run's units of positions (none: u1 <= u0), the tile's
   int len;               // units of the line that the segment takes
   int x;                 // units of the line before it in its tile
-  int su, skip;          // window mode: the tile's units of sinks, and the units between them and the window
-  int low;               // and the first position of the window of its first token
+  int sunk, skip;        // window mode: positions of the sinks' granules, and positions left out after them
+  int low;               // and the first position of the window of the tile's first token
 };
-// The unit of positions that unit u of a segment's tile stands for.
-template <int U, int MODE>
-__device__ __forceinline__ int kv8_unit(const Kv8Seg& g, int u) {
-  if constexpr (MODE == KV8_WINDOW) return u < g.su ? u : u + g.skip;
-  if constexpr (MODE == KV8_SUFFIX) return u + g.s.base / U;
-  return u;
+// Where positions of a segment's tile stand: place i of its row (unit u begins at place u U) is position
+// i + kv8_skip(i).
+template <int MODE>
+__device__ __forceinline__ int kv8_skip(const Kv8Seg& g, int i) {
+  if constexpr (MODE == KV8_WINDOW) return i < g.sunk ? 0 : g.skip;
+  if constexpr (MODE == KV8_SUFFIX) return g.s.base;
+  return 0;
 }
 
-// The line cut into n runs: run i is units i total / n up to (i + 1) total / n, and unit w
-// belongs to run ((w + 1) n - 1) / total (whole divisions).
+// The line cut into n runs: run i is units i span / n up to (i + 1) span / n, and unit w
+// belongs to run ((w + 1) n - 1) / span (whole divisions).  The span is the line's length, or in
+// window and suffix mode a little more, so that runs begin where tiles do: see kv8_line.
 struct Kv8Runs {
-  long long total;
+  long long total, span;
   int n;
+};
+// The line as it lies in shared memory: units before each item; in suffix mode what the prefix pass
+// has seen to of each sequence; and the length that every tile counts with, where it is one.
+struct Kv8Line {
+  long long* prefix;
+  int* base;
+  int uni;
+  bool shares;           // prefix and suffix mode: groups and sequences are in order
 };
 // Code that is fetched once per launch costs more than its arithmetic (some 250 cycles per 8
 // instructions that come from L2), so the rare long division is a function of its own.
@@ -164,9 +181,14 @@ __device__ __forceinline__ long long kv8_div(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return kv8_div_long(a, b);
 }
-__device__ __forceinline__ long long kv8_run_begin(const Kv8Runs& r, int i) { return kv8_div(i * r.total, r.n); }
+template <int U, int MODE>
+__device__ __forceinline__ long long kv8_run_begin(const Kv8Runs& r, int i) {
+  if constexpr (kv8_aligns(U, MODE)) return min(kv8_div(i * r.span, r.n), r.total);
+  return kv8_div(i * r.total, r.n);
+}
+template <int U, int MODE>
 __device__ __forceinline__ int kv8_run_of(const Kv8Runs& r, long long w) {
-  return static_cast<int>(kv8_div((w + 1) * r.n - 1, r.total));
+  return static_cast<int>(kv8_div((w + 1) * r.n - 1, kv8_aligns(U, MODE) ? r.span : r.total));
 }
 
 __device__ __forceinline__ long long kv8_upto(long long x, int r_shift) {
@@ -182,7 +204,8 @@ __device__ __forceinline__ int kv8_from(const Kv8Seq& s) {
 }
 // Units of tiles 0 .. t - 1 of a sequence (t at most its last tile).
 template <int U, int C, int MODE>
-__device__ __forceinline__ long long kv8_units_before(const Kv8AttnParams& p, const Kv8Seq& s, int t) {
+__device__ __forceinline__ long long kv8_units_before(const Kv8AttnParams& p, int uni, const Kv8Seq& s, int t) {
+  if (kv8_aligns(U, MODE) && uni) return static_cast<long long>(t) * uni;
   constexpr int US = U == 16 ? 4 : U == 32 ? 5 : U == 64 ? 6 : 7;
   static_assert((1 << US) == U, "U is 16 to 128");
   const int from = kv8_from<MODE>(s), tq_shift = p.tq_shift;
@@ -203,17 +226,18 @@ __device__ __forceinline__ long long kv8_units_before(const Kv8AttnParams& p, co
 }
 // Units of one tile: what its last token sees, one at least, and C.
 template <int U, int C, int MODE>
-__device__ __forceinline__ int kv8_units_tile(const Kv8AttnParams& p, const Kv8Seq& s, int t) {
+__device__ __forceinline__ int kv8_units_tile(const Kv8AttnParams& p, int uni, const Kv8Seq& s, int t) {
+  if (kv8_aligns(U, MODE) && uni) return uni;
   if constexpr (MODE == KV8_PREFIX) return s.len / U + C;
   const int n = (kv8_from<MODE>(s) + min((t + 1) << p.tq_shift, s.n) + U - 1) / U;
   return (MODE == KV8_WINDOW ? min(n, p.win_units) : n) + C;
 }
 template <int U, int C, int MODE>
-__device__ __forceinline__ long long kv8_units_seq(const Kv8AttnParams& p, const Kv8Seq& s) {
+__device__ __forceinline__ long long kv8_units_seq(const Kv8AttnParams& p, int uni, const Kv8Seq& s) {
   if (s.n <= 0) return 0;
-  if (s.n <= (1 << p.tq_shift)) return kv8_units_tile<U, C, MODE>(p, s, 0);
+  if (s.n <= (1 << p.tq_shift)) return kv8_units_tile<U, C, MODE>(p, uni, s, 0);
   const int tiles = (s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
-  return kv8_units_before<U, C, MODE>(p, s, tiles - 1) + kv8_units_tile<U, C, MODE>(p, s, tiles - 1);
+  return kv8_units_before<U, C, MODE>(p, uni, s, tiles - 1) + kv8_units_tile<U, C, MODE>(p, uni, s, tiles - 1);
 }
 
 // A group of sequences with a shared prefix as an item of the line: the tokens of all of them,
@@ -265,24 +289,103 @@ __device__ __forceinline__ const int* kv8_table(const Kv8AttnParams& p, int i) {
   return p.b.page_table + static_cast<size_t>(b) * p.b.max_pages;
 }
 
+// How many of `grid` CTAs the suffix pass gets where the two passes run side by side: those under
+// which the longer of the two is shortest.  units, pieces: CTA-times of the prefix pass's units
+// (one or two row blocks) and of the suffix pass's pieces; the constants are microseconds
+// measured with 128 sequences over 32768 shared positions (2.3 us a unit of two blocks, 0.33 a
+// piece) and what either pass takes before and after its work.
+__device__ __forceinline__ int kv8_split(long long units, long long pieces, bool one_block, int grid) {
+  if (units == 0) return grid;
+  const float u = static_cast<float>(units) * (one_block ? 1.4f : 2.3f), s = static_cast<float>(pieces) * 0.33f;
+  float best = INFINITY;
+  int at = 1;
+  for (int i = lane_id() + 1; i < grid; i += 32) {
+    const float t = fmaxf(7.0f + s / i, 5.0f + u / (grid - i));
+    if (t < best) {
+      best = t;
+      at = i;
+    }
+  }
+  // the least time, then the fewest CTAs: the same in every warp of both passes
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, best, o);
+    const int i = __shfl_xor_sync(0xffffffffu, at, o);
+    if (t < best || (t == best && i < at)) {
+      best = t;
+      at = i;
+    }
+  }
+  return at;
+}
+
 // The line: prefix[b] = units before item b (all heads), in shared memory, filled by the whole
-// CTA (THREADS threads, s_warp: THREADS / 32 words); returns its length.  In suffix mode base[b]
-// becomes what the prefix pass has seen to of sequence b.
-template <int U, int C, int THREADS, int MODE>
-__device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long* prefix, long long* s_warp, int* base) {
+// CTA (THREADS threads, s_warp: kv8_scan_words(THREADS)), and its runs, PER of them a CTA of `grid`.
+// In suffix mode base[b] becomes what the prefix pass has seen to of sequence b.
+//
+// In window and suffix mode prompts have tiles of much the same size, and often about as many as there
+// are CTAs.  Then every tile counts as long as the longest, and a CTA gets whole tiles, the same
+// number each: the longest run may grow, but no tile's parts meet through the workspace, which
+// costs about JOIN units of a run.  (Decode loses by it: a warp's pieces come one after the other,
+// 1 us each; one sequence of 33 pieces took 12.8 us in one CTA and 10.7 in five.)
+__host__ __device__ constexpr int kv8_scan_words(int threads) { return threads / 32 * 3; }
+template <int U, int C, int THREADS, int PER, int JOIN, int MODE>
+__device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& line, long long* s_warp, int grid) {
   const int tid = threadIdx.x, B = kv8_items<MODE>(p);
   const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  long long* const prefix = line.prefix;
+  line.uni = 0;
+  line.shares = false;
   long long sum = 0;
-  bool groups = true;                      // out of order or range: nothing is shared
+  int tiles = 0, top = 0;
   if constexpr (MODE == KV8_PREFIX || MODE == KV8_SUFFIX) {
+    // with groups out of order or range, or a sequence that contradicts the call, nothing is shared
+    bool fine = true;
 #pragma unroll 1
     for (int i = tid; i <= p.n_groups; i += THREADS) {
       const int b = __ldg(p.groups + i);
-      groups &= b >= 0 && b <= p.b.n_seqs && (i == 0 || __ldg(p.groups + i - 1) <= b);
+      fine &= b >= 0 && b <= p.b.n_seqs && (i == 0 || __ldg(p.groups + i - 1) <= b);
     }
-    groups = __syncthreads_and(groups) != 0;
-    if (!groups && tid == 0 && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+    if (!fine) atomicOr(p.c.err, ERRBIT_BOUNDS);
+#pragma unroll 1
+    for (int b = tid; b < p.b.n_seqs; b += THREADS) fine &= !kv8_seq(p.b, p.c.page_shift, b).bad;
+    line.shares = __syncthreads_and(fine) != 0;
+    if (p.own) {
+      // side by side: both passes add up both passes' work
+      long long units = 0, pieces = 0;
+#pragma unroll 1
+      for (int i = tid; line.shares && i < p.n_groups; i += THREADS) {
+        const Kv8Seq s = kv8_group(p, i);
+        if (s.n > 0) units += static_cast<long long>(((s.n - 1) >> p.shift_prefix) + 1) * (s.len / 128 + 2) * p.c.hkv;
+      }
+#pragma unroll 1
+      for (int b = tid; b < p.b.n_seqs; b += THREADS) {
+        const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
+        if (s.n <= 0) continue;
+        const int from = max(s.first, 0) - (line.shares ? kv8_base(p, s, b) : 0);
+        pieces += static_cast<long long>(((s.n - 1) >> p.shift_suffix) + 1) * ((from + s.n + 31) / 32 + 2) * p.c.hkv;
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        units += __shfl_xor_sync(0xffffffffu, units, o);
+        pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+      }
+      if ((tid & 31) == 0) {
+        s_warp[tid >> 5] = units;
+        s_warp[THREADS / 32 + (tid >> 5)] = pieces;
+      }
+      __syncthreads();
+      units = pieces = 0;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        units += s_warp[w];
+        pieces += s_warp[THREADS / 32 + w];
+      }
+      __syncthreads();
+      const int n = kv8_split(units, pieces, p.b.n_tokens <= (1 << p.shift_prefix), grid);
+      grid = MODE == KV8_SUFFIX ? n : grid - n;
+    }
   }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
@@ -290,42 +393,92 @@ __device__ __forceinline__ long long kv8_line(const Kv8AttnParams& p, long long*
     if constexpr (MODE == KV8_PREFIX) {
       s.n = 0;
       s.bad = false;
-      if (groups) s = kv8_group(p, b);
+      if (line.shares) s = kv8_group(p, b);
     } else {
       s = kv8_seq(p.b, p.c.page_shift, b);
-      if constexpr (MODE == KV8_SUFFIX) base[b] = s.base = groups ? kv8_base(p, s, b) : 0;
+      if constexpr (MODE == KV8_SUFFIX) line.base[b] = s.base = line.shares ? kv8_base(p, s, b) : 0;
     }
     // (fewer positions than new tokens: the tokens without one get zeros)
     if ((s.bad || (s.n > 0 && s.first < 0)) && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
-    sum += kv8_units_seq<U, C, MODE>(p, s) * p.c.hkv;
+    sum += kv8_units_seq<U, C, MODE>(p, 0, s) * p.c.hkv;
     prefix[b] = sum;                       // inside this thread's run for now
+    if (kv8_aligns(U, MODE) && s.n > 0) {
+      const int nt = (s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
+      tiles += nt * p.c.hkv;
+      top = max(top, kv8_units_tile<U, C, MODE>(p, 0, s, nt - 1));
+    }
   }
-  long long incl = sum;
+  constexpr int W = THREADS / 32;
+  const auto scan = [&](long long mine) {  // what the threads before this one have, and the total
+    long long incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if ((tid & 31) >= o) incl += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((tid & 31) >= o) incl += v;
+    }
+    if ((tid & 31) == 31) s_warp[tid >> 5] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const long long v = s_warp[w];
+      if (w < (tid >> 5)) before += v;
+      total += v;
+    }
+    return longlong2{before, total};
+  };
+  if constexpr (kv8_aligns(U, MODE)) {
+    const int wt = __reduce_add_sync(0xffffffffu, tiles), wm = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) {
+      s_warp[W + (tid >> 5)] = wt;
+      s_warp[2 * W + (tid >> 5)] = wm;
+    }
   }
-  if ((tid & 31) == 31) s_warp[tid >> 5] = incl;
-  __syncthreads();
-  long long before = incl - sum, total = 0;
+  longlong2 r = scan(sum);
+  Kv8Runs runs;
+  runs.n = static_cast<int>(min(r.y, static_cast<long long>(grid) * PER));
+  runs.span = runs.total = r.y;
+  if constexpr (kv8_aligns(U, MODE)) {
+    long long nt = 0;
+    int longest = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const long long v = s_warp[w];
-    if (w < (tid >> 5)) before += v;
-    total += v;
+    for (int w = 0; w < W; ++w) {
+      nt += s_warp[W + w];
+      longest = max(longest, static_cast<int>(s_warp[2 * W + w]));
+    }
+    static_assert(PER == 1, "a run per CTA");
+    const long long waves = (nt + grid - 1) / grid;
+    if (nt > 0 && waves * longest <= r.y / grid + JOIN * PER) {
+      line.uni = longest;
+      const int ctas = static_cast<int>((nt + waves - 1) / waves);
+      runs.n = ctas * PER;
+      runs.span = ctas * waves * longest;
+      runs.total = nt * longest;
+      __syncthreads();
+      r = scan(tiles);
+      long long at = r.x * longest;
+#pragma unroll 1
+      for (int b = b0; b < b1; ++b) {
+        prefix[b] = at;
+        Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
+        if (s.n > 0) at += static_cast<long long>((s.n + (1 << p.tq_shift) - 1) >> p.tq_shift) * p.c.hkv * longest;
+      }
+      if (tid == 0) prefix[B] = runs.total;
+      __syncthreads();
+      return runs;
+    }
   }
   // exclusive: prefix[b] = everything before b
-  long long prev = before;
+  long long prev = r.x;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const long long incl_b = before + prefix[b];
+    const long long incl_b = r.x + prefix[b];
     prefix[b] = prev;
     prev = incl_b;
   }
-  if (tid == 0) prefix[B] = total;
+  if (tid == 0) prefix[B] = r.y;
   __syncthreads();
-  return total;
+  return runs;
 }
 
 // Positions that the tile's last token sees.  (The tile's units are counted as if the sequence
@@ -351,18 +504,20 @@ __device__ __forceinline__ void kv8_seg_close(Kv8Seg& g, const Kv8AttnParams& p,
   g.u1 = end - C;
   if constexpr (MODE == KV8_WINDOW) {
     g.low = max(g.s.first + (g.t << p.tq_shift) + 1 - p.window, 0);
-    g.su = min((p.sinks + U - 1) / U, g.low / U);
-    g.skip = g.low / U - g.su;
-    g.units = max((kv8_seg_end<MODE>(g, p.tq_shift) + U - 1) / U - g.skip, 1);
-    g.u1 = min(g.u1, g.units);
+    constexpr int N = kv8_granule(U);
+    g.sunk = min((p.sinks + N - 1) / N, g.low / N) * N;
+    g.skip = g.low / N * N - g.sunk;
+    g.units = max((kv8_seg_end<MODE>(g, p.tq_shift) - g.skip + U - 1) / U, 1);
   }
+  if constexpr (MODE == KV8_SUFFIX) g.units = kv8_units_tile<U, 0, MODE>(p, 0, g.s, g.t);
+  if constexpr (MODE == KV8_WINDOW || kv8_aligns(U, MODE)) g.u1 = min(g.u1, g.units);
 }
 // The runs that hold the first and the last unit of positions of the segment's tile (the
 // segment starts at unit w).
-template <int C>
+template <int U, int C, int MODE>
 __device__ __forceinline__ int2 kv8_owners(const Kv8Seg& g, long long w, const Kv8Runs& runs) {
   const long long start = w - g.x;
-  return make_int2(kv8_run_of(runs, start + C), kv8_run_of(runs, start + C + g.units - 1));
+  return make_int2(kv8_run_of<U, MODE>(runs, start + C), kv8_run_of<U, MODE>(runs, start + C + g.units - 1));
 }
 
 // The last of 0 .. n - 1 that satisfies `ok`, which holds up to some point and not after it, and
@@ -384,14 +539,14 @@ __device__ __forceinline__ int kv8_last_of(int n, F ok) {
 
 // The segment that starts at unit w of the line (asked for by whole warps).
 template <int U, int C, int MODE>
-__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long long* prefix, const int* base, long long w,
-                                          long long w_end) {
+__device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const Kv8Line& line, long long w, long long w_end) {
+  const long long* const prefix = line.prefix;
   Kv8Seg g;
   const int lo = kv8_last_of(kv8_items<MODE>(p), [&](int i) { return prefix[i] <= w; });
   g.b = lo;
-  g.s = kv8_item<MODE>(p, base, lo);
+  g.s = kv8_item<MODE>(p, line.base, lo);
   long long x = w - prefix[lo];
-  const long long per_head = kv8_units_seq<U, C, MODE>(p, g.s);
+  const long long per_head = kv8_units_seq<U, C, MODE>(p, line.uni, g.s);
   g.g = 0;
   if (p.c.hkv > 4) {
     g.g = static_cast<int>(kv8_div(x, per_head));
@@ -401,28 +556,29 @@ __device__ __forceinline__ Kv8Seg kv8_seg(const Kv8AttnParams& p, const long lon
     for (; x >= per_head; x -= per_head) ++g.g;
   }
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
-  const int tl = kv8_last_of(tiles, [&](int t) { return kv8_units_before<U, C, MODE>(p, g.s, t) <= x; });
+  const int tl = kv8_last_of(tiles, [&](int t) { return kv8_units_before<U, C, MODE>(p, line.uni, g.s, t) <= x; });
   g.t = tl;
-  const int in_tile = static_cast<int>(tl ? x - kv8_units_before<U, C, MODE>(p, g.s, tl) : x);
-  kv8_seg_close<U, C, MODE>(g, p, in_tile, kv8_units_tile<U, C, MODE>(p, g.s, tl), w, w_end);
+  const int in_tile = static_cast<int>(tl ? x - kv8_units_before<U, C, MODE>(p, line.uni, g.s, tl) : x);
+  kv8_seg_close<U, C, MODE>(g, p, in_tile, kv8_units_tile<U, C, MODE>(p, line.uni, g.s, tl), w, w_end);
   return g;
 }
 
 // The segment after `g`, at unit w of the line (g was not the run's last): it begins a tile,
 // the sequence's next one, or the first of the next head or sequence.
 template <int U, int C, int MODE>
-__device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const long long* prefix, const int* base,
-                                         long long w, long long w_end) {
+__device__ __forceinline__ void kv8_next(Kv8Seg& g, const Kv8AttnParams& p, const Kv8Line& line, long long w,
+                                         long long w_end) {
+  const long long* const prefix = line.prefix;
   const int tiles = (g.s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
   if (++g.t >= tiles) {
     g.t = 0;
     if (++g.g >= p.c.hkv) {
       g.g = 0;
       do ++g.b; while (prefix[g.b + 1] <= w);      // sequences without new tokens have no units
-      g.s = kv8_item<MODE>(p, base, g.b);
+      g.s = kv8_item<MODE>(p, line.base, g.b);
     }
   }
-  kv8_seg_close<U, C, MODE>(g, p, 0, kv8_units_tile<U, C, MODE>(p, g.s, g.t), w, w_end);
+  kv8_seg_close<U, C, MODE>(g, p, 0, kv8_units_tile<U, C, MODE>(p, line.uni, g.s, g.t), w, w_end);
 }
 
 }  // namespace moe

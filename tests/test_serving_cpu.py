@@ -67,9 +67,9 @@ def test_prefix_workspace_bytes(lib):
     w = lib.gqa_kv8_prefix_workspace_bytes
     assert w(None, 16, 1, 4) == 0 and w(cache(), 15, 1, 4) == 0 and w(cache(), 16, 0, 4) == 0 and w(cache(), 16, 1, 0) == 0
     assert w(cache(), 16, 1, (1 << 20) + 1) == 0
-    # a row of sums per token and query head, past the 2^32 bytes of an ordinary size
-    assert w(cache(), 16, 1, 1 << 20) - w(cache(), 16, 1, 1) == ((1 << 20) - 1) * 16 * 136 * 4
+    # a row of sums (for few new tokens two) per token and query head, past the 2^32 bytes of an ordinary size
     for m in (1, 4, 5, 4096):
+        assert w(cache(), 16, m, 1 << 20) - w(cache(), 16, m, 1) == ((1 << 20) - 1) * 16 * 136 * 4 * (2 if m < 5 else 1)
         assert w(cache(), 16, m, 1) >= lib.gqa_kv8_workspace_bytes(cache(), 16, m) + 16 * 136 * 4
 
 
@@ -124,28 +124,33 @@ def test_reference_of_page_tables():
 
 # ----------------------------------------------------------------------------- the window's line of units
 def window_tile(first, n, tq, t, U, window, sinks):
-    """(units of the line but C, position units in order) of a tile, as the kernels count them."""
-    K = (window + tq - 1 + 2 * U - 2) // U + -(-sinks // U)
+    """(units of the line but C, positions of each unit's places or None) of a tile, as the kernels count them."""
+    g = 16 if U == 128 else U
+    K = -(-((window + tq - 1 + 2 * g - 2) // g + -(-sinks // g)) * g // U)
+    end = max(first + min((t + 1) * tq, n), 0)
     line = min(-(-(max(first, 0) + min((t + 1) * tq, n)) // U), K)
     low = max(first + t * tq + 1 - window, 0)
-    su = min(-(-sinks // U), low // U)
-    skip = low // U - su
-    units = max(-(-max(first + min((t + 1) * tq, n), 0) // U) - skip, 1)
-    return line, [u if u < su else u + skip for u in range(units)]
+    sunk = min(-(-sinks // g), low // g) * g
+    skip = low // g * g - sunk
+    units = max(-(-(end - skip) // U), 1)
+    at = [i + (0 if i < sunk else skip) for i in range(units * U)]
+    return line, [[p if p < end else None for p in at[u * U:(u + 1) * U]] for u in range(units)]
 
 
 def test_window_units():
-    """A tile's units of positions hold what its tokens see, each once and in order; none holds
-    nothing; and the line's closed form for the tiles before one is the sum over them."""
+    """A tile's units hold the positions that its tokens see, each once and in order, in whole granules that
+    each hold one; the masks, which are made from a unit's place in the row, are the definition's; and
+    the line's closed form for the tiles before one is the sum over them."""
     rng = random.Random(5)
-    for _ in range(4000):
+    for _ in range(1200):
         U = rng.choice([32, 128])
+        g = 16 if U == 128 else U
         tq = rng.choice([1, 2, 4, 8, 16, 32] + ([64, 128, 256] if U == 128 else []))
         first = rng.choice([0, rng.randint(0, 1500), -rng.randint(0, 40)])
-        n = rng.choice([1, rng.randint(1, 90), rng.randint(100, 700)])
+        n = rng.choice([1, rng.randint(1, 90), rng.randint(100, 400)])
         window = rng.choice([1, 2, 16, 31, 32, 33, 128, rng.randint(1, 2000), 1 << 24])
         sinks = rng.choice([0, 0, 1, 4, 16, 17, 128, rng.randint(0, 400), 1 << 24])
-        K = (window + tq - 1 + 2 * U - 2) // U + -(-sinks // U)
+        K = -(-((window + tq - 1 + 2 * g - 2) // g + -(-sinks // g)) * g // U)
         C, total = 2, 0
         for t in range(-(-n // tq)):
             full = max(((K - 1) * U - max(first, 0)) // tq, 0)
@@ -153,13 +158,27 @@ def test_window_units():
             assert _before(first, U, C, tq, done) + (t - done) * (K + C) == total
             line, units = window_tile(first, n, tq, t, U, window, sinks)
             total += line + C
-            assert len(units) <= line and units == sorted(set(units))
+            assert len(units) <= line
+            held = [p for u in units for p in u if p is not None]
+            assert held == sorted(set(held))
+            last = max(first + min((t + 1) * tq, n), 0)
+            low = max(first + t * tq + 1 - window, 0)
+            skip = low // g * g - min(-(-sinks // g), low // g) * g
+            tokens = [p for p in (first + t * tq, first + min((t + 1) * tq, n) - 1) if p >= 0]
             seen = set()
-            for p in range(first + t * tq, first + min((t + 1) * tq, n)):
-                if p >= 0:
-                    lo = max(0, p + 1 - window)
-                    seen |= set(range(lo // U, p // U + 1)) | set(range(0, -(-min(sinks, lo) // U)))
-            assert seen == set(units) or (not seen and len(units) == 1)
+            for p in tokens:
+                mine = set(range(max(0, p + 1 - window), p + 1)) | set(range(min(sinks, p + 1)))
+                seen |= mine
+                assert mine <= set(held)
+                if U == 128:                 # the prompt kernel's masks
+                    for u, places in enumerate(units):
+                        left = p + 1 - skip - u * U
+                        before, under = left - window, sinks - u * U
+                        got = {x for i, x in enumerate(places) if i < left and (i >= before or i < under)}
+                        assert got == mine & {x for x in places if x is not None}
+            if len(tokens) == 2 and tokens[0] >= 0:
+                seen |= set(range(max(0, low), last))
+                assert {x // g for x in held} == {x // g for x in seen}
 
 
 def test_a_run_that_holds_none_of_a_windows_units():
@@ -192,3 +211,33 @@ def test_a_run_that_holds_none_of_a_windows_units():
                     assert i < first or i > last
             assert done == n
             start += line + C
+
+
+@pytest.mark.parametrize("U,per_cta", [(32, 8), (128, 1)])
+def test_runs_that_hold_whole_tiles(U, per_cta):
+    """A line whose tiles all count as long as the longest, cut so that a CTA has whole tiles: the runs
+    cover the line, none is empty, every tile's units lie in one CTA, each once and in order, and the
+    runs between its first and its last one hold some of it."""
+    rng = random.Random(7)
+    C = 2
+    for _ in range(3000):
+        tiles = [rng.choice([1, 1, 2, 5, rng.randint(1, 60)]) for _ in range(rng.choice([1, 3, 20, 400]))]
+        grid = rng.choice([1, 7, 152])
+        waves = -(-len(tiles) // grid)
+        longest = max(max(tiles) + C, per_cta)
+        ctas = -(-len(tiles) // waves)
+        n, span, total = ctas * per_cta, ctas * waves * longest, len(tiles) * longest
+        assert ctas <= grid
+        begin = [min(i * span // n, total) for i in range(n + 1)]
+        assert begin[0] == 0 and begin[n] == total
+        run_of = lambda w: ((w + 1) * n - 1) // span  # noqa: E731
+        assert all(begin[i] < begin[i + 1] or begin[i] == total for i in range(n))
+        for t, units in enumerate(tiles):
+            start, done = t * longest, 0
+            first, last = run_of(start + C), run_of(start + C + units - 1)
+            assert first // per_cta == last // per_cta == t // waves
+            for i in range(first, last + 1):
+                u0, u1 = max(begin[i] - start - C, 0), min(begin[i + 1] - start - C, units)
+                assert u0 == done and u1 > u0
+                done = u1
+            assert done == units
