@@ -45,11 +45,10 @@ namespace {
 constexpr int KP_DEQ = 4;                         // dequantising warps
 constexpr int KP_THREADS = (8 + KP_DEQ + 2) * 32;
 constexpr int KP_U = 128;                         // positions per tile
-constexpr int KP_COST = 2;                        // a tile's start, in units
-#ifndef XKP
-#define XKP 6
-#endif
-constexpr int KP_JOIN = XKP;                      // parts of a tile meeting through the workspace, in units
+// A tile's start, in units.  (Shared prefixes have few tiles, most of whose CTAs start none: what it takes
+// in full, while the end of another one waits.)
+constexpr int kp_cost(int mode) { return mode == KV8_PREFIX ? 4 : 2; }
+constexpr int KP_JOIN = 6;                        // parts of a tile meeting through the workspace, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
 constexpr int KP_SLOTS = 8;                       // tiles whose scales the softmax can ask for
 constexpr int KP_PLANS = 4;                       // tiles planned ahead
@@ -61,10 +60,11 @@ constexpr float KP_LOW = -7.0f;                   // 128 positions: 128 * 2^-25 
 // keeps every bit of its codes (e4m3's smallest is 2^-9: 2^(-9 + 6 - 21) = 2^-24).
 __host__ __device__ constexpr int kp_head(int fmt) { return fmt == GQA_KV8_E4M3 ? 6 : 5; }
 __host__ __device__ constexpr int kp_tile(int D) { return KP_U * D * 2; }     // fp16 K or V tile (or 128 query rows)
-__host__ __device__ constexpr int kp_smem(int D, int B, bool suffix) {
+constexpr bool kp_extra(int mode) { return mode == KV8_SUFFIX || mode == KV8_WINDOW; }        // a word per sequence
+__host__ __device__ constexpr int kp_smem(int D, int B, bool extra) {
   // alignment, Q of two blocks, two K and two V tiles, scales, line, scan words, barriers and words
   return 1024 + 6 * kp_tile(D) + KP_SLOTS * 16 + 2 * KP_ROWS * 12 + (B + 2) * 8 + KP_THREADS / 32 * 3 * 8 + 25 * 8 + 64 + KP_PLANS * 128 +
-         (suffix ? B * 4 : 0);
+         (extra ? B * 4 : 0);
 }
 static_assert(kp_smem(128, KV8_MAX_SEQS, true) <= 232448, "shared memory per CTA exceeds 227 KB");
 
@@ -295,7 +295,7 @@ __device__ __forceinline__ float* kp_slot(float* part, int c, int c_first, int r
 // nblk: row blocks per CTA tile (1 or 2); p.tq_shift counts the tokens of all of them.
 template <int D, int FMT, int MODE>
 __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_constant__ Kv8AttnParams p, int nblk) {
-  constexpr int TILE = kp_tile(D);
+  constexpr int TILE = kp_tile(D), KP_COST = kp_cost(MODE);
   constexpr int BOX = KP_U * 128;               // bytes of 64 dims of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_N);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(const_cast<int*>(abort_flag) + 1);
   volatile int* s_n = reinterpret_cast<volatile int*>(s_tmem + 1);    // [2]
-  Kv8Line line = {prefix, reinterpret_cast<int*>(s_tmem + 3), 0, false};
+  volatile int* s_whole = s_n + 2;                                    // prefix mode: the run holds a whole tile
+  Kv8Line line = {prefix, reinterpret_cast<int*>(s_tmem + 4), 0, false};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * i; };
@@ -370,8 +371,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar(b), phase & 1, p.c.err, abort_flag, p.wait_ns))) dead = true;
       };
       const uint32_t inv_g = (65535u + p.G) / p.G;       // r / G = r inv_g >> 16 for r < 128, G <= 16
-      int it = 0, seg = 0, any_whole = 0;
-      if (tid == 0) kp_tiles(p.part)[cta].ns = kp_tiles(p.part)[cta].whole = 0;   // unless a tile that begins here goes on
+      int it = 0, seg = 0;
+      if (tid == 0) kp_tiles(p.part)[cta].ns = 0;        // unless a tile that begins here goes on
+      if (MODE == KV8_PREFIX && tid == 0) *s_whole = 0;
       Kv8Seg sg = first;
 #pragma unroll 1
       for (long long w = w_beg; w < w_end;) {
@@ -595,17 +597,17 @@ __global__ void __launch_bounds__(KP_THREADS, 1) kv8_prompt_kernel(const __grid_
         if (!whole) {
           *reinterpret_cast<float4*>(part + D) = make_float4(ms, d, l, 0.0f);
           if (tid == 0 && own.x == cta)
-            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, sg.s.base, any_whole, 0};
+            kp_tiles(p.part)[cta] = KpTile{own.y - own.x + 1, sg.t, sg.g, sg.s.off, sg.s.n, sg.s.base, 0, 0};
           // (a row whose parts are joined first says so)
           if (MODE == KV8_PREFIX && own.x == cta && live) row[D + 3] = 0.0f;
         } else if (MODE == KV8_PREFIX && live) {
           *reinterpret_cast<float4*>(row + D) = make_float4(ms, d, l, dead ? 0.0f : 1.0f);
-          any_whole = 1;
-          if (r == 0 && blk == 0) kp_tiles(p.part)[cta].whole = 1;
+          if (tid == 0) *s_whole = 1;
         }
         ++seg;
       }
       if (tid == 0) s_n[seg & 1] = 0;      // no more segments
+      if (MODE == KV8_PREFIX && tid == 0) kp_tiles(p.part)[cta].whole = *s_whole;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_Q + blk));
     }
@@ -957,9 +959,10 @@ __device__ __forceinline__ int kj_split(int ns) {          // warps of a row
   return ns <= KJ_FLIGHT ? 1 : ns <= 2 * KJ_FLIGHT ? 2 : ns <= 4 * KJ_FLIGHT ? 4 : 8;
 }
 template <int D, int MODE>
-__global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk, int ctas) {
+__global__ void __launch_bounds__(KJ_WARPS * 32, KJ_PER_SM) kv8_parts_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk, int ctas) {
   constexpr int PL = D / 32;                    // dims per lane
   __shared__ int s_start[KV8_MAX_CTAS + 1], s_sum[KJ_WARPS];
+  __shared__ KpTile s_tile[KV8_MAX_CTAS];
   __shared__ float s_o[KJ_WARPS][D];
   __shared__ float4 s_ref[KJ_WARPS];
   static_assert(KV8_MAX_CTAS <= KJ_WARPS * 32, "a thread per tile");
@@ -971,6 +974,7 @@ __global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __g
   int chunks = 0, whole = 0;
   if (tid < ctas && !(both && !p.tickets[KP_SHARES])) {
     const KpTile t = kp_tiles(p.part)[tid];
+    s_tile[tid] = t;
     whole = t.whole;
     if (t.ns > 0) chunks = (rows_of(t) * kj_split(t.ns) + KJ_WARPS - 1) / KJ_WARPS;
   }
@@ -991,20 +995,24 @@ __global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __g
   if (tid < KV8_MAX_CTAS) s_start[tid] = incl - chunks;
   whole = __syncthreads_or(whole);
   // a row's two sums, meeting: that of its shared positions (m, d, l, O) and its own
-  const auto meet = [&](size_t at, const float4& shared, float (&O)[PL]) {
+  float4 own = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float own_o[PL];
+  const auto fetch_own = [&](size_t at) {        // (on its way while the shared sums are)
     const float* src = p.own + at * kv8_row_floats(D);
-    const float4 own = *reinterpret_cast<const float4*>(src + D);
+    own = *reinterpret_cast<const float4*>(src + D);
+#pragma unroll
+    for (int q = 0; q < PL; q += 2) *reinterpret_cast<float2*>(own_o + q) = *reinterpret_cast<const float2*>(src + PL * lane + q);
+  };
+  const auto meet = [&](size_t at, const float4& shared, float (&O)[PL]) {
     if (own.w == 0.0f) return;                   // the sequence did without the prefix pass
     const Kv8Join jn = kv8_join(own, shared);
     const float inv = jn.sum == 0.0f ? 0.0f : 1.0f / jn.sum;
     __nv_bfloat16* dst = p.out + at * D + PL * lane;
 #pragma unroll
-    for (int q = 0; q < PL; q += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(src + PL * lane + q);
+    for (int q = 0; q < PL; q += 2)
       *reinterpret_cast<uint32_t*>(dst + q) =
-          pack_bf16x2(__float_as_uint(fmaf(jn.f[0], v.x, jn.f[1] * O[q]) * inv * jn.unit),
-                      __float_as_uint(fmaf(jn.f[0], v.y, jn.f[1] * O[q + 1]) * inv * jn.unit));
-    }
+          pack_bf16x2(__float_as_uint(fmaf(jn.f[0], own_o[q], jn.f[1] * O[q]) * inv * jn.unit),
+                      __float_as_uint(fmaf(jn.f[0], own_o[q + 1], jn.f[1] * O[q + 1]) * inv * jn.unit));
   };
   const int off0 = both && whole ? __ldg(p.b.offsets) : 0;
   const int rows = both && whole ? (__ldg(p.b.offsets + p.b.n_seqs) - off0) * p.hq : 0;
@@ -1015,7 +1023,7 @@ __global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __g
       const int i = (item - total) * KJ_WARPS + warp;
       if (i >= rows) continue;
       const size_t at = static_cast<size_t>(off0) * p.hq + i;
-      if (p.own[at * kv8_row_floats(D) + D + 3] == 0.0f) continue;
+      fetch_own(at);
       const float* src = p.rows + at * kv8_row_floats(D);
       const float4 ref = *reinterpret_cast<const float4*>(src + D);
       if (ref.w == 0.0f) continue;
@@ -1026,7 +1034,7 @@ __global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __g
       continue;
     }
     const int c0 = kv8_last_of(ctas, [&](int i) { return s_start[i] <= item; });
-    const KpTile tl = kp_tiles(p.part)[c0];
+    const KpTile tl = s_tile[c0];
     const int S = kj_split(tl.ns), sub = warp & (S - 1);
     const int j = ((item - s_start[c0]) * KJ_WARPS + warp) / S;         // the row among the tile's
     const bool live = j < rows_of(tl);
@@ -1054,6 +1062,8 @@ __global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __g
       l = r.z;
     }
     fetch(0);
+    const size_t at = static_cast<size_t>(tl.off + (tl.t << p.tq_shift) + tok) * p.hq + tl.g * p.G + hh;
+    if (both && sub == 0 && live) fetch_own(at);
     float M = m;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -1086,25 +1096,20 @@ __global__ void __launch_bounds__(KJ_WARPS * 32) kv8_parts_join_kernel(const __g
       if (lane == 0) s_ref[warp] = make_float4(M, top, L, 0.0f);
       __syncthreads();
       if (sub == 0) {
-        M = KV8_NO_REF;
-        for (int w = 0; w < S; ++w) M = fmaxf(M, s_ref[warp + w].x);
-        top = -INFINITY;
-        for (int w = 0; w < S; ++w) top = fmaxf(top, s_ref[warp + w].x - M + s_ref[warp + w].y);
-        L = 0.0f;
+#pragma unroll 1
+        for (int w = warp + 1; w < warp + S; ++w) {
+          const float4 a = make_float4(M, top, L, 0.0f), b = s_ref[w];
+          const Kv8Join jn = kv8_join(a, b);
+          top = fmaxf(a.x - fmaxf(a.x, b.x) + a.y, b.x - fmaxf(a.x, b.x) + b.y);
+          M = fmaxf(a.x, b.x);
+          L = jn.sum;
 #pragma unroll
-        for (int q = 0; q < PL; ++q) O[q] = 0.0f;
-        for (int w = 0; w < S; ++w) {
-          const float4 r = s_ref[warp + w];
-          L = fmaf(ex2(r.x - M), r.z, L);
-          const float f = ex2(r.x - M + r.y - top);
-#pragma unroll
-          for (int q = 0; q < PL; ++q) O[q] = fmaf(f, s_o[warp + w][PL * lane + q], O[q]);
+          for (int q = 0; q < PL; ++q) O[q] = fmaf(jn.f[0], O[q], jn.f[1] * s_o[w][PL * lane + q]);
         }
       }
       __syncthreads();
     }
     if (sub != 0 || !live) continue;
-    const size_t at = static_cast<size_t>(tl.off + (tl.t << p.tq_shift) + tok) * p.hq + tl.g * p.G + hh;
     if (both) {
       meet(at, make_float4(M, top, L, 0.0f), O);
       continue;
@@ -1147,12 +1152,12 @@ cudaError_t launch_prompt(const Kv8AttnParams& p, int nblk, int grid, int dev, c
   auto* k = kv8_prompt_kernel<D, FMT, MODE>;
   if (!set[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kp_smem(D, KV8_MAX_SEQS, MODE == KV8_SUFFIX));
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kp_smem(D, KV8_MAX_SEQS, kp_extra(MODE)));
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
   const cudaError_t e = launch_pdl(k, dim3(grid), dim3(KP_THREADS),
-                                   kp_smem(D, MODE == KV8_PREFIX ? p.n_groups : p.b.n_seqs, MODE == KV8_SUFFIX), s, p, nblk);
+                                   kp_smem(D, MODE == KV8_PREFIX ? p.n_groups : p.b.n_seqs, kp_extra(MODE)), s, p, nblk);
   if (e != cudaSuccess) return e;
   if constexpr (MODE == KV8_CAUSAL)
     return launch_pdl(kv8_prompt_join_kernel<D>, dim3(grid, nblk * KP_ROWS / 8), dim3(256), 0, s, p, nblk);

@@ -43,8 +43,8 @@ constexpr int KV8_MAX_CTAS = 160;
 constexpr int KV8_MAX_DEVICES = 64;
 constexpr int KV8_TICKET_BYTES = 1024;   // the workspace's first bytes: one ticket per CTA
 enum Kv8Mode { KV8_CAUSAL, KV8_WINDOW, KV8_PREFIX, KV8_SUFFIX };
-// Whether a kernel's runs may be aligned to tiles (see kv8_line): prompts, in these modes.
-__host__ __device__ constexpr bool kv8_aligns(int U, int mode) { return U == 128 && (mode == KV8_WINDOW || mode == KV8_SUFFIX); }
+// Whether a kernel's runs may be aligned to tiles (see kv8_line): prompts with a window.
+__host__ __device__ constexpr bool kv8_aligns(int U, int mode) { return U == 128 && mode == KV8_WINDOW; }
 __host__ __device__ constexpr int kv8_granule(int U) { return U == 128 ? 16 : U; }
 // Shared positions are worked on in whole units of either kernel; a sequence sees to the rest itself.
 constexpr int KV8_SHARED_UNIT = 128;
@@ -115,6 +115,10 @@ struct Kv8AttnParams {
   int shift_prefix, shift_suffix;   // side by side: tokens of the two passes' tiles, as shifts
 };
 
+// (see kv8_split)
+constexpr float KV8_SPLIT_SUFFIX = 11.0f, KV8_SPLIT_PREFIX = 11.0f, KV8_SPLIT_ROWS8 = 0.18f, KV8_SPLIT_ROWS16 = 0.27f,
+                KV8_SPLIT_ONE = 1.3f, KV8_SPLIT_TWO = 1.95f;
+
 // Workspace of a query row's sums (O, references ms and d, normaliser): 32-byte rows.
 __host__ __device__ constexpr int kv8_row_floats(int D) { return D + 8; }
 
@@ -160,14 +164,15 @@ __device__ __forceinline__ int kv8_skip(const Kv8Seg& g, int i) {
 }
 
 // The line cut into n runs: run i is units i span / n up to (i + 1) span / n, and unit w
-// belongs to run ((w + 1) n - 1) / span (whole divisions).  The span is the line's length, or in
-// window and suffix mode a little more, so that runs begin where tiles do: see kv8_line.
+// belongs to run ((w + 1) n - 1) / span (whole divisions).  The span is the line's length, or for
+// prompts with a window a little more, so that runs begin where tiles do: see kv8_line.
 struct Kv8Runs {
   long long total, span;
   int n;
 };
 // The line as it lies in shared memory: units before each item; in suffix mode what the prefix pass
-// has seen to of each sequence; and the length that every tile counts with, where it is one.
+// has seen to of each sequence (in window mode, while the line is made, tiles); and the length
+// that every tile counts with, where it is one.
 struct Kv8Line {
   long long* prefix;
   int* base;
@@ -244,7 +249,9 @@ __device__ __forceinline__ long long kv8_units_seq(const Kv8AttnParams& p, int u
 // each seeing `len` positions (whole units).  `bad` when something was out of range.
 __device__ __forceinline__ Kv8Seq kv8_group(const Kv8AttnParams& p, int i) {
   Kv8Seq s;
-  const int b0 = __ldg(p.groups + i), b1 = __ldg(p.groups + i + 1), shared = __ldg(p.shared + i);
+  // (kept to the batch here; kv8_line finds out whether they were)
+  const int b0 = min(max(__ldg(p.groups + i), 0), p.b.n_seqs), b1 = min(max(__ldg(p.groups + i + 1), 0), p.b.n_seqs);
+  const int shared = __ldg(p.shared + i);
   const int o0 = __ldg(p.b.offsets + b0), o1 = __ldg(p.b.offsets + b1);
   const int len = min(max(shared, 0), p.b.max_pages << p.c.page_shift);
   const bool rows = o0 >= 0 && o0 <= o1 && o1 <= p.b.n_tokens;
@@ -290,24 +297,24 @@ __device__ __forceinline__ const int* kv8_table(const Kv8AttnParams& p, int i) {
 }
 
 // How many of `grid` CTAs the suffix pass gets where the two passes run side by side: those under
-// which the longer of the two is shortest.  units, pieces: CTA-times of the prefix pass's units
-// (one or two row blocks) and of the suffix pass's pieces; the constants are microseconds
-// measured with 128 sequences over 32768 shared positions (2.3 us a unit of two blocks, 0.33 a
-// piece) and what either pass takes before and after its work.
-__device__ __forceinline__ int kv8_split(long long units, long long pieces, bool one_block, int grid) {
-  if (units == 0) return grid;
-  const float u = static_cast<float>(units) * (one_block ? 1.4f : 2.3f), s = static_cast<float>(pieces) * 0.33f;
+// which the longer of the two is shortest.  units, pieces: the prefix pass's units (of one or two
+// row blocks) and the suffix pass's pieces (of 8 or 16 query rows).  The constants are microseconds, measured with 128
+// sequences over 32768 shared positions: what a CTA takes for one, and before and after them.
+__device__ __forceinline__ int kv8_split(long long units, long long pieces, bool one_block, bool rows8, int grid) {
+  if (units <= 0) return grid;
+  const float u = static_cast<float>(units) * (one_block ? KV8_SPLIT_ONE : KV8_SPLIT_TWO);
+  const float s = static_cast<float>(pieces) * (rows8 ? KV8_SPLIT_ROWS8 : KV8_SPLIT_ROWS16);
   float best = INFINITY;
   int at = 1;
+#pragma unroll 1
   for (int i = lane_id() + 1; i < grid; i += 32) {
-    const float t = fmaxf(7.0f + s / i, 5.0f + u / (grid - i));
+    const float t = fmaxf(KV8_SPLIT_SUFFIX + __fdividef(s, i), KV8_SPLIT_PREFIX + __fdividef(u, grid - i));
     if (t < best) {
       best = t;
       at = i;
     }
   }
-  // the least time, then the fewest CTAs: the same in every warp of both passes
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o >= 1; o >>= 1) {
     const float t = __shfl_xor_sync(0xffffffffu, best, o);
     const int i = __shfl_xor_sync(0xffffffffu, at, o);
@@ -319,166 +326,207 @@ __device__ __forceinline__ int kv8_split(long long units, long long pieces, bool
   return at;
 }
 
+// A sequence's share of the suffix pass's pieces, from position `from` of its own on.  A tile counts
+// eight more: what its start and its parts' meeting in the CTA take.
+__device__ __forceinline__ long long kv8_pieces(const Kv8AttnParams& p, const Kv8Seq& s, int from) {
+  return static_cast<long long>(((s.n - 1) >> p.shift_suffix) + 1) * ((from + s.n + 31) / 32 + 8) * p.c.hkv;
+}
+
 // The line: prefix[b] = units before item b (all heads), in shared memory, filled by the whole
-// CTA (THREADS threads, s_warp: kv8_scan_words(THREADS)), and its runs, PER of them a CTA of `grid`.
-// In suffix mode base[b] becomes what the prefix pass has seen to of sequence b.
-//
-// In window and suffix mode prompts have tiles of much the same size, and often about as many as there
-// are CTAs.  Then every tile counts as long as the longest, and a CTA gets whole tiles, the same
-// number each: the longest run may grow, but no tile's parts meet through the workspace, which
-// costs about JOIN units of a run.  (Decode loses by it: a warp's pieces come one after the other,
-// 1 us each; one sequence of 33 pieces took 12.8 us in one CTA and 10.7 in five.)
-__host__ __device__ constexpr int kv8_scan_words(int threads) { return threads / 32 * 3; }
-template <int U, int C, int THREADS, int PER, int JOIN, int MODE>
-__device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& line, long long* s_warp, int grid) {
-  const int tid = threadIdx.x, B = kv8_items<MODE>(p);
+// CTA (THREADS threads, s_warp: KV8_SCAN_WORDS (THREADS / 32)), and its runs, PER of them a CTA
+// of `grid`.  In suffix mode base[b] becomes what the prefix pass has seen to of sequence b.
+constexpr int KV8_SCAN_WORDS = 3;
+template <int U, int C, int THREADS, int PER>
+__device__ __forceinline__ Kv8Runs kv8_line_causal(const Kv8AttnParams& p, Kv8Line& line, long long* s_warp, int grid) {
+  const int tid = threadIdx.x, B = p.b.n_seqs;
   const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long* const prefix = line.prefix;
-  line.uni = 0;
-  line.shares = false;
   long long sum = 0;
-  int tiles = 0, top = 0;
-  if constexpr (MODE == KV8_PREFIX || MODE == KV8_SUFFIX) {
-    // with groups out of order or range, or a sequence that contradicts the call, nothing is shared
-    bool fine = true;
-#pragma unroll 1
-    for (int i = tid; i <= p.n_groups; i += THREADS) {
-      const int b = __ldg(p.groups + i);
-      fine &= b >= 0 && b <= p.b.n_seqs && (i == 0 || __ldg(p.groups + i - 1) <= b);
-    }
-    if (!fine) atomicOr(p.c.err, ERRBIT_BOUNDS);
-#pragma unroll 1
-    for (int b = tid; b < p.b.n_seqs; b += THREADS) fine &= !kv8_seq(p.b, p.c.page_shift, b).bad;
-    line.shares = __syncthreads_and(fine) != 0;
-    if (p.own) {
-      // side by side: both passes add up both passes' work
-      long long units = 0, pieces = 0;
-#pragma unroll 1
-      for (int i = tid; line.shares && i < p.n_groups; i += THREADS) {
-        const Kv8Seq s = kv8_group(p, i);
-        if (s.n > 0) units += static_cast<long long>(((s.n - 1) >> p.shift_prefix) + 1) * (s.len / 128 + 2) * p.c.hkv;
-      }
-#pragma unroll 1
-      for (int b = tid; b < p.b.n_seqs; b += THREADS) {
-        const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
-        if (s.n <= 0) continue;
-        const int from = max(s.first, 0) - (line.shares ? kv8_base(p, s, b) : 0);
-        pieces += static_cast<long long>(((s.n - 1) >> p.shift_suffix) + 1) * ((from + s.n + 31) / 32 + 2) * p.c.hkv;
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        units += __shfl_xor_sync(0xffffffffu, units, o);
-        pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
-      }
-      if ((tid & 31) == 0) {
-        s_warp[tid >> 5] = units;
-        s_warp[THREADS / 32 + (tid >> 5)] = pieces;
-      }
-      __syncthreads();
-      units = pieces = 0;
-#pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        units += s_warp[w];
-        pieces += s_warp[THREADS / 32 + w];
-      }
-      __syncthreads();
-      const int n = kv8_split(units, pieces, p.b.n_tokens <= (1 << p.shift_prefix), grid);
-      grid = MODE == KV8_SUFFIX ? n : grid - n;
-    }
-  }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    Kv8Seq s;
-    if constexpr (MODE == KV8_PREFIX) {
-      s.n = 0;
-      s.bad = false;
-      if (line.shares) s = kv8_group(p, b);
-    } else {
-      s = kv8_seq(p.b, p.c.page_shift, b);
-      if constexpr (MODE == KV8_SUFFIX) line.base[b] = s.base = line.shares ? kv8_base(p, s, b) : 0;
-    }
+    const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
     // (fewer positions than new tokens: the tokens without one get zeros)
     if ((s.bad || (s.n > 0 && s.first < 0)) && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
-    sum += kv8_units_seq<U, C, MODE>(p, 0, s) * p.c.hkv;
+    sum += kv8_units_seq<U, C, KV8_CAUSAL>(p, 0, s) * p.c.hkv;
     prefix[b] = sum;                       // inside this thread's run for now
-    if (kv8_aligns(U, MODE) && s.n > 0) {
-      const int nt = (s.n + (1 << p.tq_shift) - 1) >> p.tq_shift;
-      tiles += nt * p.c.hkv;
-      top = max(top, kv8_units_tile<U, C, MODE>(p, 0, s, nt - 1));
-    }
   }
-  constexpr int W = THREADS / 32;
-  const auto scan = [&](long long mine) {  // what the threads before this one have, and the total
-    long long incl = mine;
+  long long incl = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if ((tid & 31) >= o) incl += v;
-    }
-    if ((tid & 31) == 31) s_warp[tid >> 5] = incl;
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const long long v = s_warp[w];
-      if (w < (tid >> 5)) before += v;
-      total += v;
-    }
-    return longlong2{before, total};
-  };
-  if constexpr (kv8_aligns(U, MODE)) {
-    const int wt = __reduce_add_sync(0xffffffffu, tiles), wm = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) {
-      s_warp[W + (tid >> 5)] = wt;
-      s_warp[2 * W + (tid >> 5)] = wm;
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if ((tid & 31) >= o) incl += v;
   }
-  longlong2 r = scan(sum);
-  Kv8Runs runs;
-  runs.n = static_cast<int>(min(r.y, static_cast<long long>(grid) * PER));
-  runs.span = runs.total = r.y;
-  if constexpr (kv8_aligns(U, MODE)) {
-    long long nt = 0;
-    int longest = 0;
+  if ((tid & 31) == 31) s_warp[tid >> 5] = incl;
+  __syncthreads();
+  long long before = incl - sum, total = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      nt += s_warp[W + w];
-      longest = max(longest, static_cast<int>(s_warp[2 * W + w]));
-    }
-    static_assert(PER == 1, "a run per CTA");
-    const long long waves = (nt + grid - 1) / grid;
-    if (nt > 0 && waves * longest <= r.y / grid + JOIN * PER) {
-      line.uni = longest;
-      const int ctas = static_cast<int>((nt + waves - 1) / waves);
-      runs.n = ctas * PER;
-      runs.span = ctas * waves * longest;
-      runs.total = nt * longest;
-      __syncthreads();
-      r = scan(tiles);
-      long long at = r.x * longest;
-#pragma unroll 1
-      for (int b = b0; b < b1; ++b) {
-        prefix[b] = at;
-        Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
-        if (s.n > 0) at += static_cast<long long>((s.n + (1 << p.tq_shift) - 1) >> p.tq_shift) * p.c.hkv * longest;
-      }
-      if (tid == 0) prefix[B] = runs.total;
-      __syncthreads();
-      return runs;
-    }
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const long long v = s_warp[w];
+    if (w < (tid >> 5)) before += v;
+    total += v;
   }
   // exclusive: prefix[b] = everything before b
-  long long prev = r.x;
+  long long prev = before;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const long long incl_b = r.x + prefix[b];
+    const long long incl_b = before + prefix[b];
     prefix[b] = prev;
     prev = incl_b;
   }
-  if (tid == 0) prefix[B] = r.y;
+  if (tid == 0) prefix[B] = total;
   __syncthreads();
-  return runs;
+  return Kv8Runs{total, total, static_cast<int>(min(total, static_cast<long long>(grid) * PER))};
+}
+
+// The same in the other modes.  (It runs once per launch, so its loops stay loops: see kv8_div.)
+//
+// Prompts with a window have tiles of much the same size, and often about as many as there are CTAs.
+// Then every tile counts as long as the longest, and a CTA gets whole tiles, the same number
+// each: the longest run may grow, but no tile's parts meet through the workspace, which costs
+// about JOIN units of a run.  (Decode loses by it: a warp's pieces come one after the other, 1 us
+// each; one sequence of 33 pieces took 12.8 us in one CTA and 10.7 in five.)
+template <int U, int C, int THREADS, int PER, int JOIN, int MODE>
+__device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& line, long long* s_warp, int grid) {
+  line.uni = 0;
+  line.shares = false;
+  if constexpr (MODE == KV8_CAUSAL) return kv8_line_causal<U, C, THREADS, PER>(p, line, s_warp, grid);
+  constexpr bool groups = MODE == KV8_PREFIX || MODE == KV8_SUFFIX, aligns = kv8_aligns(U, MODE);
+  constexpr int W = THREADS / 32;
+  static_assert(W <= 32, "a lane per warp");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = kv8_items<MODE>(p);
+  const int per = (B + THREADS - 1) / THREADS;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  long long* const prefix = line.prefix;
+  // With groups out of order or range, or a sequence that contradicts the call, nothing is shared:
+  // then once more.
+  bool share = groups;
+#pragma unroll 1
+  for (;; share = false) {
+    bool fine = true;
+    // the line's units; the tiles and the longest (window), or, where the passes run side by side, the
+    // prefix pass's units and the suffix pass's pieces
+    long long sum = 0, other = 0, pieces = 0;
+    int top = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      Kv8Seq s;
+      if constexpr (MODE == KV8_PREFIX) {
+        s = kv8_group(p, b);
+        if (!share) s.n = 0;
+        if (s.n > 0)         // (counted below as if nothing was shared)
+          pieces -= static_cast<long long>(__ldg(p.groups + b + 1) - __ldg(p.groups + b)) * s.len / 32 *
+                    (((p.b.max_new - 1) >> p.shift_suffix) + 1) * p.c.hkv;
+      } else {
+        s = kv8_seq(p.b, p.c.page_shift, b);
+        if constexpr (MODE == KV8_SUFFIX) line.base[b] = s.base = share ? kv8_base(p, s, b) : 0;
+        if constexpr (groups) fine &= !s.bad;
+        if (MODE == KV8_SUFFIX && s.n > 0) pieces += kv8_pieces(p, s, max(s.first, 0) - s.base);
+      }
+      // (fewer positions than new tokens: the tokens without one get zeros)
+      if ((s.bad || (s.n > 0 && s.first < 0)) && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+      sum += kv8_units_seq<U, C, MODE>(p, 0, s) * p.c.hkv;
+      prefix[b] = sum;                       // inside this thread's run for now
+      if constexpr (aligns) {
+        if (s.n > 0) {
+          const int nt = ((s.n - 1) >> p.tq_shift) + 1;
+          other += nt * p.c.hkv;
+          top = max(top, kv8_units_tile<U, C, MODE>(p, 0, s, nt - 1));
+        }
+        line.base[b] = static_cast<int>(other);
+      }
+    }
+    if constexpr (groups) {
+#pragma unroll 1
+      for (int i = tid; i <= p.n_groups; i += THREADS) {
+        const int b = __ldg(p.groups + i);
+        fine &= b >= 0 && b <= p.b.n_seqs && (i == 0 || __ldg(p.groups + i - 1) <= b);
+        if (MODE == KV8_SUFFIX && share && i < p.n_groups) {
+          const Kv8Seq s = kv8_group(p, i);
+          if (s.n > 0) other += static_cast<long long>(((s.n - 1) >> p.shift_prefix) + 1) * (s.len / 128 + 4) * p.c.hkv;
+        }
+      }
+      if constexpr (MODE == KV8_PREFIX) {
+#pragma unroll 1
+        for (int b = tid; b < p.b.n_seqs; b += THREADS) {
+          const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
+          fine &= !s.bad;
+          if (s.n > 0) pieces += kv8_pieces(p, s, max(s.first, 0));
+        }
+      }
+    }
+    // inclusive sums over the warp's lanes, then over the warps
+    long long incl = sum, rest = other;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o), x = __shfl_up_sync(0xffffffffu, rest, o);
+      if (lane >= o) {
+        incl += v;
+        rest += x;
+      }
+      if constexpr (groups) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+    }
+    if constexpr (aligns) top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 31) {
+      s_warp[warp] = incl;
+      s_warp[W + warp] = rest;
+      s_warp[2 * W + warp] = aligns ? top : pieces;
+    }
+    const bool ok = __syncthreads_and(fine) != 0;
+    long long total = lane < W ? s_warp[lane] : 0, all = lane < W ? s_warp[W + lane] : 0;
+    pieces = lane < W ? s_warp[2 * W + lane] : 0;
+    if constexpr (aligns) top = __reduce_max_sync(0xffffffffu, static_cast<int>(pieces));
+    __syncthreads();                         // the words are read: they may be written again
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, total, o), x = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) {
+        total += v;
+        all += x;
+      }
+      if constexpr (groups) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+    }
+    const int w1 = max(warp - 1, 0);
+    const long long before = incl - sum + (warp ? __shfl_sync(0xffffffffu, total, w1) : 0);
+    const long long before_rest = rest - other + (warp ? __shfl_sync(0xffffffffu, all, w1) : 0);
+    total = __shfl_sync(0xffffffffu, total, 31);
+    all = __shfl_sync(0xffffffffu, all, 31);
+    if (groups && share && !ok) continue;
+    if (groups && !ok && tid == 0 && blockIdx.x == 0) atomicOr(p.c.err, ERRBIT_BOUNDS);
+    line.shares = share;
+    Kv8Runs runs = {total, total, 0};
+    if (groups && p.own) {
+      const bool one = p.b.n_tokens <= (1 << p.shift_prefix), rows8 = p.G << p.shift_suffix <= 8;
+      const long long units = MODE == KV8_SUFFIX ? all : total;
+      // (no more to the prefix pass than it has units)
+      const int first = static_cast<int>(min(static_cast<long long>(grid - kv8_split(units, pieces, one, rows8, grid)), units));
+      grid = MODE == KV8_SUFFIX ? grid - first : first;
+    }
+    runs.n = static_cast<int>(min(total, static_cast<long long>(grid) * PER));
+    if constexpr (aligns) {
+      static_assert(PER == 1, "a run per CTA");
+      const int nt = static_cast<int>(all), waves = (nt + grid - 1) / grid;
+      if (nt > 0 && static_cast<long long>(waves) * top <= kv8_div(total, grid) + JOIN) {
+        line.uni = top;
+        runs.n = (nt - 1) / waves + 1;
+        runs.span = static_cast<long long>(runs.n) * waves * top;
+        runs.total = static_cast<long long>(nt) * top;
+      }
+    }
+    // exclusive: prefix[b] = everything before b
+    long long prev = before;
+    if (aligns && line.uni) prev = before_rest * line.uni;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      long long incl_b = before + prefix[b];
+      if (aligns && line.uni) incl_b = (before_rest + line.base[b]) * line.uni;
+      prefix[b] = prev;
+      prev = incl_b;
+    }
+    if (tid == 0) prefix[B] = runs.total;
+    __syncthreads();
+    return runs;
+  }
 }
 
 // Positions that the tile's last token sees.  (The tile's units are counted as if the sequence
