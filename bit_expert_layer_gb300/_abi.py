@@ -69,7 +69,7 @@ class GqaKv8Batch(C.Structure):
 
 
 class GqaKv8Prefix(C.Structure):
-    _fields_ = [("groups", C.c_void_p), ("shared", C.c_void_p), ("n_groups", C.c_int)]
+    _fields_ = [("groups", C.c_void_p), ("shared", C.c_void_p), ("n_groups", C.c_int), ("max_shared", C.c_int)]
 
 
 class GqaKv8Pages(C.Structure):

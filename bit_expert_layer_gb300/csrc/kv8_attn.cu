@@ -28,6 +28,7 @@
 // tile's join) are what is left.  With the query rows on the M side (half of each MMA and of O's
 // registers empty at 8 rows) a piece took 750 instructions and the same case 36.7 us; 16 warps of
 // 16-key pieces took 33.5 us, 12 of three stages 31.8, where 8 warps of 32 keys took 31.6.
+#include <algorithm>
 #include <cstring>
 
 #include "internal.h"
@@ -902,9 +903,25 @@ bool heads_ok(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new) {
          max_new <= (1 << 20) && n_q_heads >= 1 && n_q_heads % cache->n_kv_heads == 0 && n_q_heads / cache->n_kv_heads <= 16;
 }
 
-// Whether groups that hold `tokens` new tokens in all are worth a pass of their own over what they
-// share: with more than 32 query rows per key/value head and group in the mean.
-bool kv8_share(int G, int tokens, int groups) { return static_cast<long long>(G) * tokens > 32ll * groups; }
+// Whether a pass of its own over what the sequences share can pay, with at most `shared` positions: by
+// what it takes and what it saves the sequences, in microseconds.  Measured on 16 query and 2
+// key/value heads of 128, without and with it, one new token: 8 sequences over 4 thousand positions 13
+// and 20 us, 32 over 4 thousand 20 and 25, 8 over 32 thousand 28 and 28, 32 over 32 thousand 76 and
+// 33; in four groups 16 over 32 thousand 29 and 33, 32 47 and 37.  (Pages that sequences share come
+// from L2 after their first reader, twice as slowly where all sequences want the same ones at once.)
+// Four new tokens: 3 over 32 thousand 31 and 29, 16 97 and 42.  Prompts of 20 tokens, which have most
+// of a tile of their own each: 12 over 32 thousand 96 and 97, 16 123 and 112.
+bool kv8_share(const Kv8AttnParams& p, int R, int shared) {
+  const double units = shared / 128.0 * p.c.hkv / 152;       // of a tile of the prefix pass, per SM
+  const int shift = kv8_prompt_shift(p.G, kv8_prompt_tokens(p, KV8_PREFIX));
+  const double tiles = ((p.b.n_tokens - p.n_groups) >> shift) + p.n_groups;
+  const double pass = tiles * units * (p.G << shift <= 128 ? 1.3 : 1.95);
+  const long long n = p.b.n_seqs, own = R ? floor_log2(R / p.G) : kv8_prompt_shift(p.G, p.b.max_new);
+  const double mine = static_cast<double>(std::min<long long>(p.b.n_tokens, n * (((p.b.max_new - 1) >> own) + 1)));
+  if (!R) return mine * units * (p.G << own <= 128 ? 1.3 : 1.95) > 30 + pass;
+  const double piece = (R == 8 ? 1.05e-3 : 1.28e-3) * (p.n_groups > 1 ? 0.55 : 1.0);
+  return mine * (shared / 32.0) * p.c.hkv * piece > 13 + pass;
+}
 
 // The workspace of attention with shared prefixes: the suffix pass's, the prefix pass's (each has the
 // tickets' bytes before it), then the rows of sums of the one and of the other.
@@ -955,7 +972,10 @@ extern "C" moe_status_t gqa_kv8_window_attention(const gqa_kv8_cache_t* cache, c
 
 extern "C" size_t gqa_kv8_prefix_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new, int n_tokens) {
   if (!heads_ok(cache, n_q_heads, max_new) || n_tokens < 1 || n_tokens > (1 << 20)) return 0;
-  return kv8_prefix_ws_bytes(cache->head_size, ka_rows(n_q_heads / cache->n_kv_heads, max_new), n_q_heads, n_tokens);
+  // (enough for calls with fewer new tokens per sequence, too, which may need a second set of rows)
+  const int D = cache->head_size, R = ka_rows(n_q_heads / cache->n_kv_heads, max_new);
+  const size_t a = kv8_prefix_ws_bytes(D, R, n_q_heads, n_tokens), b = kv8_prefix_ws_bytes(D, 16, n_q_heads, n_tokens);
+  return R || a > b ? a : b;
 }
 
 extern "C" moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch,
@@ -963,7 +983,8 @@ extern "C" moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, c
                                                  int n_q_heads, float scale, void* out, void* workspace,
                                                  size_t workspace_bytes, moe_stream_t stream) {
   Kv8Call c;
-  if (!prefix || !prefix->groups || !prefix->shared || prefix->n_groups < 1 || prefix->n_groups > KV8_MAX_SEQS)
+  if (!prefix || !prefix->groups || !prefix->shared || prefix->n_groups < 1 || prefix->n_groups > KV8_MAX_SEQS ||
+      prefix->max_shared < 0 || prefix->max_shared > (1 << 24))
     return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(prefix->groups) | reinterpret_cast<uintptr_t>(prefix->shared)) & 3u)
     return MOE_ERR_ALIGNMENT;
@@ -973,10 +994,12 @@ extern "C" moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, c
   if (workspace_bytes < kv8_prefix_ws_bytes(D, c.R, n_q_heads, batch->n_tokens)) return MOE_ERR_WORKSPACE;
   if ((st = find_device(&c)) != MOE_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!kv8_share(c.p.G, batch->n_tokens, prefix->n_groups)) return attend<KV8_CAUSAL>(cache, c.p, c.R, c.grid, c.dev, s);
+  const int most = prefix->max_shared ? prefix->max_shared : batch->max_pages * cache->page_size;
   c.p.groups = prefix->groups;
   c.p.shared = prefix->shared;
   c.p.n_groups = prefix->n_groups;
+  c.p.max_shared = most;
+  if (!kv8_share(c.p, c.R, most)) return attend<KV8_CAUSAL>(cache, c.p, c.R, c.grid, c.dev, s);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   c.p.rows = reinterpret_cast<float*>(ws + kv8_prefix_rows_at(D, c.R));
   // Few new tokens: the passes run side by side, each on some of the SMs, and a third kernel joins what
@@ -985,7 +1008,7 @@ extern "C" moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, c
   first.part = reinterpret_cast<float*>(ws + kv8_prefix_part_at(D, c.R) + KV8_TICKET_BYTES);
   if (c.R) {
     c.p.own = reinterpret_cast<float*>(ws + kv8_prefix_rows_at(D, c.R) + kv8_prefix_rows(D, n_q_heads, batch->n_tokens));
-    c.p.shift_prefix = kv8_prompt_shift(c.p.G, batch->n_tokens);
+    c.p.shift_prefix = kv8_prompt_shift(c.p.G, kv8_prompt_tokens(c.p, KV8_PREFIX));
     c.p.shift_suffix = floor_log2(c.R / c.p.G);
     first.own = c.p.own;
     first.shift_prefix = c.p.shift_prefix;

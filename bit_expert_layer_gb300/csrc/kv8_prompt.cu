@@ -1175,10 +1175,13 @@ int kv8_prompt_shift(int G, int tokens) {
   const int shift = kp_block_shift(G);
   return shift + (tokens > (1 << shift));
 }
+int kv8_prompt_tokens(const Kv8AttnParams& p, int mode) {
+  return mode == KV8_PREFIX ? (p.b.n_tokens - 1) / p.n_groups + 1 : p.b.max_new;
+}
 
 template <int MODE>
 cudaError_t launch_kv8_join(Kv8AttnParams p, int D, int grid, cudaStream_t s) {
-  p.tq_shift = kv8_prompt_shift(p.G, MODE == KV8_PREFIX ? p.b.n_tokens : p.b.max_new);
+  p.tq_shift = kv8_prompt_shift(p.G, kv8_prompt_tokens(p, MODE));
   const int nblk = 1 + p.tq_shift - kp_block_shift(p.G);
   return launch_pdl(D == 128 ? kv8_parts_join_kernel<128, MODE> : kv8_parts_join_kernel<64, MODE>, dim3(grid * KJ_PER_SM),
                     dim3(KJ_WARPS * 32), 0, s, p, nblk, grid);
@@ -1186,7 +1189,7 @@ cudaError_t launch_kv8_join(Kv8AttnParams p, int D, int grid, cudaStream_t s) {
 
 template <int MODE>
 cudaError_t launch_kv8_prompt(Kv8AttnParams p, int D, int format, int grid, int dev, cudaStream_t s) {
-  p.tq_shift = kv8_prompt_shift(p.G, MODE == KV8_PREFIX ? p.b.n_tokens : p.b.max_new);
+  p.tq_shift = kv8_prompt_shift(p.G, kv8_prompt_tokens(p, MODE));
   const int nblk = 1 + p.tq_shift - kp_block_shift(p.G);
   if (MODE == KV8_WINDOW) p.win_units = kv8_win_units(KP_U, 1 << p.tq_shift, p.window, p.sinks);
   const bool e4 = format == GQA_KV8_E4M3;

@@ -109,7 +109,7 @@ struct Kv8AttnParams {
   int win_units;         // and the most units that a tile has there
   const int* groups;     // prefix and suffix modes: first sequence of each group, the end
   const int* shared;     // positions that each group shares
-  int n_groups;
+  int n_groups, max_shared;
   float* rows;           // sums of the query rows, [token][query head][kv8_row_floats(D)]: what the prefix pass leaves,
   float* own;            // and in side-by-side passes what the suffix pass leaves (else null)
   int shift_prefix, shift_suffix;   // side by side: tokens of the two passes' tiles, as shifts
@@ -256,7 +256,7 @@ __device__ __forceinline__ Kv8Seq kv8_group(const Kv8AttnParams& p, int i) {
   const int len = min(max(shared, 0), p.b.max_pages << p.c.page_shift);
   const bool rows = o0 >= 0 && o0 <= o1 && o1 <= p.b.n_tokens;
   s.off = rows ? o0 : 0;
-  s.len = len / KV8_SHARED_UNIT * KV8_SHARED_UNIT;
+  s.len = min(len, p.max_shared) / KV8_SHARED_UNIT * KV8_SHARED_UNIT;
   s.n = rows && s.len > 0 ? o1 - o0 : 0;
   s.first = 0;
   s.base = 0;
@@ -496,7 +496,7 @@ __device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& lin
     line.shares = share;
     Kv8Runs runs = {total, total, 0};
     if (groups && p.own) {
-      const bool one = p.b.n_tokens <= (1 << p.shift_prefix), rows8 = p.G << p.shift_suffix <= 8;
+      const bool one = p.G << p.shift_prefix <= 128, rows8 = p.G << p.shift_suffix <= 8;
       const long long units = MODE == KV8_SUFFIX ? all : total;
       // (no more to the prefix pass than it has units)
       const int first = static_cast<int>(min(static_cast<long long>(grid - kv8_split(units, pieces, one, rows8, grid)), units));

@@ -119,16 +119,21 @@ class KV8Batch(_Fixed):
 class KV8Prefix(_Fixed):
     """Sequences that begin alike: sequences ``groups[i]`` .. ``groups[i + 1] - 1`` share their first
     ``shared[i]`` positions (int32 [n_groups + 1] and [n_groups], on the device; they may be
-    changed in place between calls, also under a captured graph)."""
+    changed in place between calls, also under a captured graph).  ``max_shared`` is a bound on the
+    shared lengths, by which a call decides whether sharing pays (0: what a row of the batch's page
+    table holds)."""
 
-    def __init__(self, groups: torch.Tensor, shared: torch.Tensor):
+    def __init__(self, groups: torch.Tensor, shared: torch.Tensor, max_shared: int = 0):
         self.groups = _ints(groups, "groups", 1)
         self.device = groups.device
         self.shared = _ints(shared, "shared", 1, self.device)
         n = shared.shape[0]
         if n < 1 or groups.shape[0] != n + 1:
             raise ValueError(f"shared has {n} entries: one at least is wanted, and groups has to have {n + 1}")
-        self._c = ctypes.byref(GqaKv8Prefix(groups.data_ptr(), shared.data_ptr(), n))
+        self.max_shared = int(max_shared)
+        if not 0 <= self.max_shared <= 1 << 24:
+            raise ValueError(f"max_shared {max_shared}: 0 .. 2^24 is wanted")
+        self._c = ctypes.byref(GqaKv8Prefix(groups.data_ptr(), shared.data_ptr(), n, self.max_shared))
 
 
 class KV8Pages(_Fixed):

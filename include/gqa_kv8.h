@@ -146,6 +146,7 @@ typedef struct {
     const int32_t* groups;      /* [n_groups + 1] non-decreasing, 0 .. n_seqs */
     const int32_t* shared;      /* [n_groups] positions, 0 at least */
     int n_groups;               /* 1 .. 1024 */
+    int max_shared;             /* a bound on shared[], 1 .. 2^24; 0: what a row of the page table holds */
 } gqa_kv8_prefix_t;
 
 /* Bytes of device workspace of gqa_kv8_prefix_attention for calls of at most n_tokens rows
@@ -157,9 +158,11 @@ size_t gqa_kv8_prefix_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_head
  * from the pages of the group's first sequence, whose row has to hold them even if it has no
  * new tokens; each sequence then adds the rest of its own.  The result is that of
  * gqa_kv8_attention to within its error.  A sequence whose new tokens do not all lie behind the
- * shared positions is attended to by itself, and so is every one where the mean group has at
- * most 32 query rows per key/value head.  Groups out of order or range are recorded in the
- * error word and nothing is shared; a shared length past the page table is recorded and cut.
+ * shared positions is attended to by itself.  So is every one where sharing max_shared positions
+ * would not pay (a bound that is far too large is right but slow; shared positions past it are
+ * each sequence's own).  Groups out of order or range, or a sequence that contradicts the call,
+ * are recorded in the error word and nothing is shared; a shared length past the page table is
+ * recorded and cut.
  * Errors: as gqa_kv8_attention. */
 moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch,
                                       const gqa_kv8_prefix_t* prefix, const void* q, long long q_stride, int n_q_heads,

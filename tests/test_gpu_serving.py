@@ -145,6 +145,9 @@ def test_window_three_million_positions(kv8):
 
 
 # ----------------------------------------------------------------------------- shared prefixes
+ALWAYS = 1 << 24         # a bound under which sharing pays from few sequences on
+
+
 class Shared(Setup):
     """Groups of sequences: groups[i] sequences that share[i] positions; own[b] positions after them."""
 
@@ -166,7 +169,7 @@ class Shared(Setup):
                         for x in (self.cache.k_scale, self.cache.v_scale):
                             x[dst, :, :-(-m // 16)] = x[src, :, :-(-m // 16)]
         self.batch = kv8.KV8Batch(ints(self.table), ints(self.lens), ints(self.offsets), max_new=max(1, max(new)))
-        self.prefix = kv8.KV8Prefix(ints(first), ints(share))
+        self.prefix = kv8.KV8Prefix(ints(first), ints(share), ALWAYS)
 
 
 PREFIX = [([8], [256], [20] * 8, [1] * 8), ([5], [1000], [3, 1, 130, 40, 7], [3, 1, 2, 3, 3]),
@@ -218,7 +221,7 @@ def test_sequences_that_share_nothing(kv8, new):
     s = Shared(kv8, [12], [512], [40 + i for i in range(12)], [new] * 12, seed=53)
     c = s.cache
     for first, share in [([3, 7], [512]), ([0, 4, 4, 12], [512, 0, 512]), ([0, 12], [127]), ([0, 0], [512]), ([12, 12], [512])]:
-        check(s, c.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints(first), ints(share))))
+        check(s, c.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints(first), ints(share), ALWAYS)))
     assert c.get_error() == 0
     lens = list(s.lens)
     lens[4], lens[9] = 512 + new - 1, 300           # the first has a new token among the shared ones
@@ -227,12 +230,24 @@ def test_sequences_that_share_nothing(kv8, new):
     assert c.get_error() == 0
     # groups and lengths out of order or range: recorded, and the result is still theirs
     for first, share in [([4, 2], [512]), ([-1, 12], [512]), ([0, 13], [512]), ([0, 2 ** 31 - 1], [512]), ([0, 12], [-5])]:
-        check(s, c.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints(first), ints(share))))
+        check(s, c.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints(first), ints(share), ALWAYS)))
         assert c.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
-    check(s, c.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints([0, 12]), ints([2 ** 31 - 1]))))
+    check(s, c.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints([0, 12]), ints([2 ** 31 - 1]), ALWAYS)))
     assert c.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
-    one = Shared(kv8, [2], [512], [40, 50], [1, 1], seed=54)
-    assert torch.equal(one.cache.attention(one.batch, one.q, prefix=one.prefix), one.cache.attention(one.batch, one.q))
+    # too little to share for it to pay: the ordinary kernels
+    plain = c.attention(s.batch, s.q)
+    for few in (kv8.KV8Prefix(ints([0, 12]), ints([512])), kv8.KV8Prefix(ints([0, 12]), ints([512]), 100)):
+        assert torch.equal(c.attention(s.batch, s.q, prefix=few), plain)
+
+
+@pytest.mark.parametrize("bound", [127, 128, 300, 511, 513])
+def test_shared_positions_past_the_bound_are_the_sequences_own(kv8, bound):
+    """120 sequences, so that sharing pays from few positions on (or not at all); never a position twice."""
+    s = Shared(kv8, [120], [512], [20 + i for i in range(120)], [4] * 120, (16, 1, 64), seed=63)
+    check(s, s.cache.attention(s.batch, s.q, prefix=kv8.KV8Prefix(ints([0, 120]), ints([512]), bound)))
+    big = Shared(kv8, [60], [9000], [20 + i for i in range(60)], [1] * 60, seed=64)
+    check(big, big.cache.attention(big.batch, big.q, prefix=kv8.KV8Prefix(ints([0, 60]), ints([9000]), 16 * bound)))
+    assert s.cache.get_error() == 0 and big.cache.get_error() == 0
 
 
 @pytest.mark.parametrize("new", [1, 4, 90])
@@ -347,6 +362,9 @@ def test_attention_refusals(kv8):
         kv8.KV8Prefix(ints([0, 3]), ints([5, 5]))
     with pytest.raises(ValueError):
         kv8.KV8Prefix(ints([0]), ints([]))
+    for bound in (-1, (1 << 24) + 1):
+        with pytest.raises(ValueError):
+            kv8.KV8Prefix(ints([0, 3]), ints([5]), bound)
     with pytest.raises(ValueError):
         kv8.KV8Prefix(ints([0, 3]).cpu(), ints([5]))
     with pytest.raises(ValueError):
@@ -644,7 +662,7 @@ def test_a_server(kv8, fmt, layer):
             pages.lens[1:5] = 256
             pages.held[1:5] = 4
             borrowed[1:5] = 4
-            prefix = kv8.KV8Prefix(ints([0, 5]), ints([256]))
+            prefix = kv8.KV8Prefix(ints([0, 5]), ints([256]), ALWAYS)
         t = sum(new)
         offsets, positions, slots = pages.step(ints(new), t)
         batch = kv8.KV8Batch(pages.table, pages.lens, offsets, max(new))

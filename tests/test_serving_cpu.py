@@ -24,7 +24,7 @@ def lib():
 
 
 def prefix(**kw):
-    a = dict(groups=FAKE, shared=FAKE, n_groups=1)
+    a = dict(groups=FAKE, shared=FAKE, n_groups=1, max_shared=0)
     a.update(kw)
     return _abi.GqaKv8Prefix(*a.values())
 
@@ -58,7 +58,7 @@ def test_refused_windows(lib):
 
 def test_refused_prefixes(lib):
     for kw, st in [(dict(groups=None), I), (dict(shared=None), I), (dict(n_groups=0), I), (dict(n_groups=1025), I),
-                   (dict(groups=FAKE + 2), A), (dict(shared=FAKE + 1), A)]:
+                   (dict(max_shared=-1), I), (dict(max_shared=(1 << 24) + 1), I), (dict(groups=FAKE + 2), A), (dict(shared=FAKE + 1), A)]:
         assert lib.gqa_kv8_prefix_attention(cache(), batch(), prefix(**kw), FAKE, 2048, 16, 0.0, FAR, FAKE, BIG, None) == st
     assert lib.gqa_kv8_prefix_attention(cache(), batch(), None, FAKE, 2048, 16, 0.0, FAR, FAKE, BIG, None) == I
 
@@ -69,8 +69,12 @@ def test_prefix_workspace_bytes(lib):
     assert w(cache(), 16, 1, (1 << 20) + 1) == 0
     # a row of sums (for few new tokens two) per token and query head, past the 2^32 bytes of an ordinary size
     for m in (1, 4, 5, 4096):
-        assert w(cache(), 16, m, 1 << 20) - w(cache(), 16, m, 1) == ((1 << 20) - 1) * 16 * 136 * 4 * (2 if m < 5 else 1)
         assert w(cache(), 16, m, 1) >= lib.gqa_kv8_workspace_bytes(cache(), 16, m) + 16 * 136 * 4
+    assert w(cache(), 16, 1, 1 << 20) - w(cache(), 16, 1, 1) == ((1 << 20) - 1) * 16 * 136 * 4 * 2
+    # what is enough for many new tokens is enough for few, and for fewer rows
+    for t in (1, 100, 5000, 1 << 20):
+        sizes = [w(cache(), 16, m, t) for m in (1, 2, 4, 5, 4096)]
+        assert sizes == sorted(sizes) and sizes[0] > w(cache(), 16, 1, t - 1)
 
 
 def test_refused_norms(lib):
