@@ -45,8 +45,9 @@ namespace {
 constexpr int KP_DEQ = 4;                         // dequantising warps
 constexpr int KP_THREADS = (8 + KP_DEQ + 2) * 32;
 constexpr int KP_U = 128;                         // positions per tile
-// A tile's start, in units.  (Shared prefixes have few tiles, most of whose CTAs start none: what it takes
-// in full, while the end of another one waits.)
+// A tile's start, in units.  (A shared prefix has few tiles, and the few CTAs that see the end of one and
+// the start of the next have both on top of their units.  128 sequences over 32768 shared positions
+// took 62.2, 62.7 and 62 us with 4, 6 and 7, 24 sequences of 4 drafts 35.2, 37.3 and 37.)
 constexpr int kp_cost(int mode) { return mode == KV8_PREFIX ? 4 : 2; }
 constexpr int KP_JOIN = 6;                        // parts of a tile meeting through the workspace, in units
 constexpr int KP_ROWS = 128;                      // query rows per block
@@ -955,11 +956,12 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(const __grid_const
 // that pass ran beside it, meets that pass's sums, as those of rows do whose tile was whole.
 constexpr int KJ_WARPS = 8, KJ_PER_SM = 4;  // and blocks of a launch per SM
 constexpr int KJ_FLIGHT = 6;                // parts of a warp whose loads are under way together
-__device__ __forceinline__ int kj_split(int ns) {          // warps of a row
-  return ns <= KJ_FLIGHT ? 1 : ns <= 2 * KJ_FLIGHT ? 2 : ns <= 4 * KJ_FLIGHT ? 4 : 8;
+__device__ __forceinline__ int kj_split(int ns, int most) {          // warps of a row, a lane per part at least
+  const int wish = ns <= KJ_FLIGHT ? 1 : ns <= 2 * KJ_FLIGHT ? 2 : ns <= 4 * KJ_FLIGHT ? 4 : 8;
+  return max(min(wish, most), ns <= 32 ? 1 : ns <= 64 ? 2 : ns <= 128 ? 4 : 8);
 }
 template <int D, int MODE>
-__global__ void __launch_bounds__(KJ_WARPS * 32, KJ_PER_SM) kv8_parts_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk, int ctas) {
+__global__ void __launch_bounds__(KJ_WARPS * 32, KJ_PER_SM) kv8_parts_join_kernel(const __grid_constant__ Kv8AttnParams p, int nblk, int ctas, int most) {
   constexpr int PL = D / 32;                    // dims per lane
   __shared__ int s_start[KV8_MAX_CTAS + 1], s_sum[KJ_WARPS];
   __shared__ KpTile s_tile[KV8_MAX_CTAS];
@@ -976,7 +978,7 @@ __global__ void __launch_bounds__(KJ_WARPS * 32, KJ_PER_SM) kv8_parts_join_kerne
     const KpTile t = kp_tiles(p.part)[tid];
     s_tile[tid] = t;
     whole = t.whole;
-    if (t.ns > 0) chunks = (rows_of(t) * kj_split(t.ns) + KJ_WARPS - 1) / KJ_WARPS;
+    if (t.ns > 0) chunks = (rows_of(t) * kj_split(t.ns, most) + KJ_WARPS - 1) / KJ_WARPS;
   }
   int incl = chunks;
 #pragma unroll
@@ -1035,7 +1037,7 @@ __global__ void __launch_bounds__(KJ_WARPS * 32, KJ_PER_SM) kv8_parts_join_kerne
     }
     const int c0 = kv8_last_of(ctas, [&](int i) { return s_start[i] <= item; });
     const KpTile tl = s_tile[c0];
-    const int S = kj_split(tl.ns), sub = warp & (S - 1);
+    const int S = kj_split(tl.ns, most), sub = warp & (S - 1);
     const int j = ((item - s_start[c0]) * KJ_WARPS + warp) / S;         // the row among the tile's
     const bool live = j < rows_of(tl);
     const int tok = j / p.G, hh = j - tok * p.G, blk = tok >= blk_tokens;
@@ -1043,7 +1045,7 @@ __global__ void __launch_bounds__(KJ_WARPS * 32, KJ_PER_SM) kv8_parts_join_kerne
     const auto slot = [&](int i) { return kp_slot<D>(p.part, c0 + i, c0, row); };
     float m = KV8_NO_REF, d = -INFINITY, l = 0.0f, v[KJ_FLIGHT][PL];
     const int i = sub + lane * S;                                       // this lane's part
-    const int n = live ? (tl.ns - sub + S - 1) / S : 0;                 // the warp's parts, at most 20
+    const int n = live ? (tl.ns - sub + S - 1) / S : 0;                 // the warp's parts, at most 32
     const auto fetch = [&](int k0) {
 #pragma unroll
       for (int k = 0; k < KJ_FLIGHT; ++k)
@@ -1183,8 +1185,12 @@ template <int MODE>
 cudaError_t launch_kv8_join(Kv8AttnParams p, int D, int grid, cudaStream_t s) {
   p.tq_shift = kv8_prompt_shift(p.G, kv8_prompt_tokens(p, MODE));
   const int nblk = 1 + p.tq_shift - kp_block_shift(p.G);
+  // warps of a row: no more than leave every row a place in one round of the blocks (2048 rows of 15
+  // parts: 7 us with 4 warps in two rounds, 5 with 2 in one)
+  int most = 1;
+  while (most < KJ_WARPS && 2ll * most * p.b.n_tokens * p.hq <= 1ll * grid * KJ_PER_SM * KJ_WARPS) most *= 2;
   return launch_pdl(D == 128 ? kv8_parts_join_kernel<128, MODE> : kv8_parts_join_kernel<64, MODE>, dim3(grid * KJ_PER_SM),
-                    dim3(KJ_WARPS * 32), 0, s, p, nblk, grid);
+                    dim3(KJ_WARPS * 32), 0, s, p, nblk, grid, most);
 }
 
 template <int MODE>
