@@ -1,8 +1,9 @@
-// kv8_cache.cu -- the 8-bit key/value cache's write and read back, and rotary positions.
-// All three are bound by memory: each reads its rows once and writes them once.  Measured on 2
+// kv8_cache.cu -- the 8-bit key/value cache's write and read back, and rotary positions, with or
+// without norms of the heads.
+// All are bound by memory: each reads its rows once and writes them once.  Measured on 2
 // key/value and 16 query heads of 128: the write of 16 thousand tokens (int8, 23 MB) 5.9 us
 // (3.5 at the copy rate), 60 thousand rows read back (e4m3, 92 MB) 15.1 us (13.8), 16384 tokens
-// rotated (151 MB) 28.0 us (22.6).
+// rotated (151 MB) 28.0 us (22.6), normed and rotated 29.7 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -211,7 +212,7 @@ struct RopeParams {
   int heads[2];
   const int* pos;
   int T, n_axes, half, tokens;   // tokens per CTA, at most 4
-  uint32_t inv_heads;            // th / heads = th inv_heads >> 21 for th < 4 heads, heads <= 512
+  uint32_t inv_heads;            // th / heads = th inv_heads >> 21 for th < 4 heads, heads <= 512 (norms: 32 and 128 steps)
   uint64_t turn[GQA_ROPE_MAX_PAIRS];
   uint8_t axis[GQA_ROPE_MAX_PAIRS];
   const void* weight[2];         // norms: of the q heads, the k heads (null: ones)
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const __grid_constant_
 // ============================================================================ norms and rotary positions
 namespace {
 
-constexpr int NR_TOKENS = 8;               // tokens of a CTA at most
+constexpr int NR_TOKENS = 32;              // tokens of a CTA at most
 constexpr int NR_CTAS = 4;                 // resident CTAs per SM (64 registers)
 
 // Sums of squares between these need no care: none of their terms that matter left fp32's range.
@@ -339,17 +340,21 @@ __device__ __noinline__ float2 norm_far(uint4 a, uint4 b, uint32_t mask, float e
 // D / 16 neighbouring lanes share a head (two 16-byte chunks each, as in rope_kernel) and add
 // their squares by shuffles, so a step of a warp is 512 / D heads of q or of k of one token, and a
 // lane keeps its place in the head from step to step.  Arithmetic goes two elements at a time;
-// sines and weights (as factors) lie in shared memory with the halves of the 8-element chunks
-// apart, so that neighbours' 16-byte loads lie side by side.
+// sines, negated sines and weights (as factors) lie in shared memory with the halves of the
+// 8-element chunks apart, so that neighbours' 16-byte loads lie side by side.
+// Bound: memory (151 MB for 16384 tokens of 18 heads of 128: 22.5 us at a copy's rate); measured 29.7 us,
+// 5.1 TB/s, some 250 instructions a step at 0.7 a cycle and scheduler.  On the way there: 94.7 us with
+// a head's elements in local memory (their address went to the rare function), 37 to 39 with scalar
+// arithmetic and four tokens a CTA, whatever the registers; a warp per token, steps prefetched by
+// asynchronous copies, 31.6, but 5 us where this takes 2.5 (256 tokens).
 template <int D>
 __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ __align__(16) float s_cs[];          // [tokens][half] cosines, then sines, then [2][D] weights
+  extern __shared__ __align__(16) float s_cs[];          // [tokens][half] cosines, sines, negated sines, then [2][D] weights
   __shared__ uint64_t s_turn[GQA_ROPE_MAX_PAIRS];
   __shared__ const int* s_pos[GQA_ROPE_MAX_PAIRS];
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0), half = p.half;
-  float* s_cos = s_cs;
-  float* s_sin = s_cs + p.tokens * half;
-  float* s_w = s_sin + p.tokens * half;
+  const int all = p.tokens * half;
+  float* s_w = s_cs + 3 * all;
   constexpr int IPH = D / 16, NG = 32 / IPH, WARPS = RP_THREADS / 32;      // lanes of a head, heads of a step
   constexpr int NB = 2;                  // steps of a warp in flight
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, part = lane % IPH, grp = lane / IPH;
@@ -357,31 +362,40 @@ __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __
   const int ca = rot ? part * 8 : 2 * half + (part - half / 8) * 16, gap = rot ? half : 8, own = grp * D + ca;
   const int nq = (p.heads[0] + NG - 1) / NG, per = nq + (p.heads[1] + NG - 1) / NG, n = nt * per;
   struct Step {
-    int t, head, which;                  // token, first head, q or k
+    const __nv_bfloat16* src;            // the step's first head
+    __nv_bfloat16* dst;
+    const float *w, *cs;                 // its weights, its token's sines
     bool live;                           // the lane's head exists
   };
   const auto step = [&](int i) {
     Step r;
-    r.t = (static_cast<uint32_t>(i) * p.inv_heads) >> 21;
-    const int st = i - r.t * per;
-    r.which = st >= nq;
-    r.head = (r.which ? st - nq : st) * NG;
-    r.live = r.head + grp < (r.which ? p.heads[1] : p.heads[0]);
+    const int t = (static_cast<uint32_t>(i) * p.inv_heads) >> 21, st = i - t * per;
+    if (st < nq) {
+      r.src = p.in[0] + (t0 + t) * p.in_stride[0] + st * NG * D;
+      r.dst = p.out[0] + (t0 + t) * p.out_stride[0] + st * NG * D;
+      r.live = st * NG + grp < p.heads[0];
+      r.w = s_w;
+    } else {
+      r.src = p.in[1] + (t0 + t) * p.in_stride[1] + (st - nq) * NG * D;
+      r.dst = p.out[1] + (t0 + t) * p.out_stride[1] + (st - nq) * NG * D;
+      r.live = (st - nq) * NG + grp < p.heads[1];
+      r.w = s_w + D;
+    }
+    r.cs = s_cs + t * half;
     return r;
   };
   uint4 a[NB], b[NB];
+  Step at[NB];
   const auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       a[k] = b[k] = make_uint4(0, 0, 0, 0);
       const int i = i0 + k * WARPS;
       if (i >= n) break;
-      const Step r = step(i);
-      const __nv_bfloat16* src =
-          (r.which ? p.in[1] : p.in[0]) + (t0 + r.t) * (r.which ? p.in_stride[1] : p.in_stride[0]) + r.head * D;
-      if (r.live) {
-        a[k] = *reinterpret_cast<const uint4*>(src + own);
-        b[k] = *reinterpret_cast<const uint4*>(src + own + gap);
+      at[k] = step(i);
+      if (at[k].live) {
+        a[k] = *reinterpret_cast<const uint4*>(at[k].src + own);
+        b[k] = *reinterpret_cast<const uint4*>(at[k].src + own + gap);
       }
     }
   };
@@ -392,15 +406,19 @@ __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __
   grid_dep_wait();
   load(warp);                            // on their way while the sines are computed
   __syncthreads();
-  for (int i = threadIdx.x; i < nt * half; i += RP_THREADS) {
-    const int t = i / half, j = i - t * half;
-    const long long pos = __ldg(s_pos[j] + t);
-    const long long frac = static_cast<long long>(static_cast<unsigned long long>(pos) * s_turn[j]);
-    float s, c;
-    sincospif(static_cast<float>(frac) * 1.0842021724855044e-19f /* 2^-63 */, &s, &c);
-    const int at = t * half + (j >> 2 & 1) * (half / 2) + (j >> 3) * 4 + (j & 3);
-    s_cos[at] = c;
-    s_sin[at] = s;
+  const int rows = RP_THREADS / half, row = threadIdx.x / half, j = threadIdx.x - row * half;
+  if (row < rows) {
+    float* to = s_cs + (j >> 2 & 1) * (half / 2) + (j >> 3) * 4 + (j & 3);
+    const uint64_t turn = s_turn[j];
+    const int* pos = s_pos[j];
+    for (int t = row; t < nt; t += rows) {
+      const long long frac = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(__ldg(pos + t))) * turn);
+      float s, c;
+      sincospif(static_cast<float>(frac) * 1.0842021724855044e-19f /* 2^-63 */, &s, &c);
+      to[t * half] = c;
+      to[t * half + all] = s;
+      to[t * half + 2 * all] = -s;
+    }
   }
   for (int i = threadIdx.x; i < 2 * D; i += RP_THREADS) {
     const int which = i / D, e = i % D;
@@ -415,8 +433,7 @@ __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __
     if (i0 != warp) load(i0);
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      const int i = i0 + k * WARPS;
-      if (i >= n) break;
+      if (i0 + k * WARPS >= n) break;
       const uint32_t w[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
       uint64_t x[8], sum2[2] = {0, 0};
 #pragma unroll
@@ -438,9 +455,7 @@ __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __
         for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], f32x2(r2.x, r2.x));
         f = r2.y;
       }
-      const Step r = step(i);
-      const float* wt = s_w + r.which * D + ca / 2;
-      const float *cs = s_cos + r.t * half + part * 4, *sn = s_sin + r.t * half + part * 4;
+      const float *wt = at[k].w + ca / 2, *cs = at[k].cs + part * 4;
       const uint64_t f2 = f32x2(f, f);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -454,12 +469,13 @@ __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __
         }
         if (rot) {
           const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(cs + q * (half / 2));
-          const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(sn + q * (half / 2));
-          const uint64_t c[2] = {c2.x, c2.y}, s[2] = {s2.x, s2.y};
+          const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(cs + all + q * (half / 2));
+          const ulonglong2 n2 = *reinterpret_cast<const ulonglong2*>(cs + 2 * all + q * (half / 2));
+          const uint64_t c[2] = {c2.x, c2.y}, s[2] = {s2.x, s2.y}, ns[2] = {n2.x, n2.y};
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint64_t a0 = x[2 * q + j], b0 = x[4 + 2 * q + j];
-            x[2 * q + j] = fma2(b0, s[j] ^ 0x8000000080000000ull, mul2(a0, c[j]));
+            x[2 * q + j] = fma2(b0, ns[j], mul2(a0, c[j]));
             x[4 + 2 * q + j] = fma2(a0, s[j], mul2(b0, c[j]));
           }
         }
@@ -470,11 +486,9 @@ __global__ void __launch_bounds__(RP_THREADS, NR_CTAS) norm_rope_kernel(const __
         const float2 y = f32x2_get(x[j]);
         o[j] = pack_bf16x2(__float_as_uint(y.x), __float_as_uint(y.y));
       }
-      __nv_bfloat16* dst =
-          (r.which ? p.out[1] : p.out[0]) + (t0 + r.t) * (r.which ? p.out_stride[1] : p.out_stride[0]) + r.head * D;
-      if (r.live) {
-        *reinterpret_cast<uint4*>(dst + own) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + own + gap) = make_uint4(o[4], o[5], o[6], o[7]);
+      if (at[k].live) {
+        *reinterpret_cast<uint4*>(at[k].dst + own) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(at[k].dst + own + gap) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
   }
@@ -720,12 +734,14 @@ moe_status_t rope_launch(const gqa_rope_plan_t* plan, const gqa_norm_t* norm, co
   // for the sines (18 heads of 128): 64 tokens 2.1 us one by one and 2.7 by four, 512 2.6 and 2.8,
   // 1024 4.1 and 3.7, 2048 5.8 and 5.2, 16384 43.6 and 28.3.
   p.tokens = T >= 1024 ? 4 : 1;
-  // With norms, as many as make one wave of CTAs.
-  if (norm) p.tokens = std::min(NR_TOKENS, std::max(1, (T - 1) / (152 * NR_CTAS) + 1));
+  // With norms, as many as make whole waves of CTAs, as few as there can be with NR_TOKENS at most:
+  // 16384 tokens 29.7 us in one wave of 27 each, 31.3 in three of 9, 33.6 in four of 7.
+  constexpr int wave = 152 * NR_CTAS;
+  if (norm) p.tokens = (T - 1) / (wave * ((T - 1) / (wave * NR_TOKENS) + 1)) + 1;
   const int ng = 512 / D, per = norm ? (n_q_heads + ng - 1) / ng + (n_k_heads + ng - 1) / ng : n_q_heads + n_k_heads;
   p.inv_heads = ((1u << 21) + per - 1) / per;
   const dim3 grid((T + p.tokens - 1) / p.tokens);
-  const size_t smem = (2ull * p.tokens * p.half + (norm ? 2 * D : 0)) * sizeof(float);
+  const size_t smem = ((norm ? 3ull : 2ull) * p.tokens * p.half + (norm ? 2 * D : 0)) * sizeof(float);
   auto* kernel = norm ? (D == 128 ? norm_rope_kernel<128> : norm_rope_kernel<64>)
                       : (D == 128 ? rope_kernel<128> : rope_kernel<64>);
   e = launch_pdl(kernel, grid, dim3(RP_THREADS), smem, s, p);

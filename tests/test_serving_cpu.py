@@ -245,3 +245,12 @@ def test_runs_that_hold_whole_tiles(U, per_cta):
                 assert u0 == done and u1 > u0
                 done = u1
             assert done == units
+
+
+def test_step_numbers():
+    """The norm kernel's division of a step's number by a token's steps, by a multiplication: up to 32
+    tokens of up to 128 steps."""
+    for per in range(1, 129):
+        inv = ((1 << 21) + per - 1) // per
+        assert 32 * per * inv < 1 << 32
+        assert all(i * inv >> 21 == i // per for i in range(32 * per))
