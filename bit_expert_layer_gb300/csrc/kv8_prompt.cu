@@ -31,6 +31,20 @@
 // through weights to the next scores, which the other block's covers only in part.  A prompt of
 // 2048 tokens from the start takes 42 us: 128 tiles of 1 to 16 units each, where a tile's start
 // and end (queries in, result out, some 10 thousand cycles) weigh as much as its units.
+//
+// With a window (MODE, see kv8_sched.cuh) a tile's places are the 16-position blocks of its sinks and of
+// its windows, which the planning warp looks up one by one, so that they lie side by side; tiles
+// at their edges are masked column group by column group.  2048 tokens over 14 thousand positions, a
+// window of 1024 and 16 sinks, 33.4 us: 128 CTAs with a tile of 9 units each (17 us), the line and
+// the first queries before them 8, the result 3.5, the join that finds nothing to do 2.  (As parts of
+// an even line, sinks and window in units of 128 of their own, 54.4.)
+//
+// The prefix pass takes the tokens of all sequences of a group as rows of one tile and masks nothing; what
+// it leaves (sums) meets each sequence's own part: with few new tokens per sequence that of the
+// decode kernel, which runs beside it on the SMs that the work of either leaves it, in the
+// join.  128 sequences over 32768 shared positions and 64 to 2000 of their own, e4m3, 60 us (18 at
+// the tensor cores' measured rate, 76 us for a quarter of the sequences without it): 118 CTAs of
+// the prefix pass 47 to 52, 34 of the other beside them, the join of 16 MB of sums 5, launches between.
 #include <cstring>
 #include <type_traits>
 

@@ -213,6 +213,40 @@ def test_prefix_of_the_largest_batch(kv8):
     assert s.cache.get_error() == 0
 
 
+@pytest.mark.parametrize("new", [1, 3, 20])
+@pytest.mark.parametrize("page", [256, 1024])
+def test_prefix_and_window_with_large_pages(kv8, page, new):
+    """The shared positions end inside a page; the first rows of the call belong to no sequence."""
+    s = Shared(kv8, [7, 5], [1000, 640], [new + 30 * i for i in range(12)], [new] * 12, page=page, seed=65)
+    s.offsets = s.offsets + 3
+    qkv = torch.cat([s.qkv[:3], s.qkv])
+    s.q = qkv[:, :s.hq]
+    b = kv8.KV8Batch(s.batch.page_table, s.batch.lens, ints(s.offsets), new)
+    for kw in (dict(prefix=s.prefix), dict(window=100, sinks=20)):
+        out = torch.full(s.q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+        s.cache.attention(b, s.q, out=out, **kw)
+        want, bound = serving_ref.attention(s.ref(), s.table, s.lens, s.offsets, s.q.double(), **{k: v for k, v in kw.items() if k != "prefix"})
+        assert torch.all((out[3:].double() - want[3:]).abs() <= bound[3:]) and (out[:3] == 5).all()
+    assert s.cache.get_error() == 0
+
+
+def test_many_groups(kv8):
+    """100 groups of 10 sequences; as many groups as there can be, most of them of one sequence (which
+    share nothing); more groups than sequences."""
+    g = Shared(kv8, [10] * 100, [128 * (i % 4) + 5 for i in range(100)], [1 + i % 70 for i in range(1000)], [1] * 1000, (16, 1, 64), 16,
+               seed=68)
+    check(g, g.cache.attention(g.batch, g.q, prefix=g.prefix))
+    assert g.cache.get_error() == 0
+    n = 1023
+    s = Shared(kv8, [1] * 20 + [2] * 2 + [1] * (n - 24), [128 * (i % 3) for i in range(n - 2)], [1 + i % 50 for i in range(n)], [1] * n,
+               (16, 1, 64), 16, seed=66)
+    check(s, s.cache.attention(s.batch, s.q, prefix=s.prefix))
+    few = Shared(kv8, [12], [300], [20 + i for i in range(12)], [4] * 12, seed=67)
+    many = kv8.KV8Prefix(ints([0] * 500 + [12] * 525), ints([300] * 1024), ALWAYS)
+    check(few, few.cache.attention(few.batch, few.q, prefix=many))
+    assert s.cache.get_error() == 0 and few.cache.get_error() == 0
+
+
 @pytest.mark.parametrize("new", [1, 3, 40])
 def test_sequences_that_share_nothing(kv8, new):
     """Outside every group; new tokens that begin before the shared positions end; a group that shares
