@@ -13,8 +13,9 @@
 //               ones, so no call both reads and writes the list)
 // What a call reads of the state (lengths, pages held, the list's length) it may also have to
 // replace, so the CTA that arrives last writes it: by then every other has read it.
-// Bound: latency (the launch, the loads of the sequences' numbers, the sums); 8 bytes are written
-// per token.
+// Bound: latency (the launch, the loads of the sequences' numbers, the sums, a page's own loads, the last
+// CTA's turn); 8 bytes are written per token.  Measured: a step of 64 sequences, some of which need a
+// page and one in nine gives its own back, 5.2 us; 200 prompts of 184 thousand tokens 4.6 us.
 #include <algorithm>
 #include <cstring>
 
@@ -26,7 +27,9 @@ namespace moe {
 
 namespace {
 
-constexpr int PG_THREADS = 256, PG_SEQS = KV8_MAX_SEQS;
+// 512 threads: 64 tokens over 8 thousand pages 3.7 us, with 1024 4.1, with 256 3.5; a million tokens 7.9,
+// 8.2, 10.4; the 8 thousand pages given back at once 9.8, 7.2, 16.7.
+constexpr int PG_THREADS = 512, PG_SEQS = KV8_MAX_SEQS, PG_ENTRIES = 8192;
 
 struct PagesParams {
   int* table;
@@ -85,27 +88,38 @@ __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_cons
     sum[1] += max(held - rest, 0);
     sum[2] += max(after - held, 0);
   }
-  int before[3];
+  int before[3], total[3];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    int incl = sum[k];
+  for (int k = 0; k < 3; ++k) before[k] = sum[k];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    before[k] = incl - sum[k];
-    if (lane == 31) s_warp[warp][k] = incl;
-  }
-  __syncthreads();
-  int total[3] = {0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < PG_THREADS / 32; ++w)
+  for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      if (w < warp) before[k] += s_warp[w][k];
-      total[k] += s_warp[w][k];
+      const int v = __shfl_up_sync(0xffffffffu, before[k], o);
+      if (lane >= o) before[k] += v;
     }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s_warp[warp][k] = before[k];
+  __syncthreads();
+  // the warps' sums: a lane each
+  constexpr int W = PG_THREADS / 32;
+  int upto[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) upto[k] = lane < W ? s_warp[lane][k] : 0;
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int v = __shfl_up_sync(0xffffffffu, upto[k], o);
+      if (lane >= o) upto[k] += v;
+    }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    total[k] = __shfl_sync(0xffffffffu, upto[k], W - 1);
+    const int v = __shfl_sync(0xffffffffu, upto[k], max(warp - 1, 0));
+    before[k] += (warp ? v : 0) - sum[k];
+  }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     s_off[b] += before[0];
@@ -246,13 +260,13 @@ extern "C" moe_status_t gqa_kv8_pages_step(const gqa_kv8_pages_t* pages, const g
   p.n_tokens = n_tokens;
   while ((1 << p.page_shift) < pages->page_size) ++p.page_shift;
   p.wide = ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15u) == 0;
-  // A CTA for every 1024 tokens, or for every 1024 pages that may change hands, up to four an SM.  48
-  // thousand pages given back by 1024 sequences took 118 us in one CTA and 6.5 in 48, a step of 64
-  // tokens over 8 thousand pages 3.5 and 4.4; a million tokens 10.5 us in 608, 12.4 in 152.
+  // A CTA for every 2048 tokens, or for every 8192 pages that may change hands, up to two an SM.  (More
+  // for the pages would make most steps, which move few, wait for more CTAs: those 64 tokens 4.4 us with
+  // nine CTAs.)
   const long long rows = static_cast<long long>(pages->n_seqs) * pages->max_pages;
   const long long entries = rows < pages->n_pages ? rows : pages->n_pages;
-  const long long want = std::max<long long>(n_tokens / (4 * PG_THREADS), entries / (4 * PG_THREADS)) + 1;
-  const int grid = static_cast<int>(std::min<long long>(want, 4 * 152));
+  const long long want = std::max<long long>(n_tokens / (4 * PG_THREADS), entries / PG_ENTRIES) + 1;
+  const int grid = static_cast<int>(std::min<long long>(want, 1024 / PG_THREADS * 152));
   const cudaError_t e =
       launch_pdl(kv8_pages_kernel, dim3(grid), dim3(PG_THREADS), 0, reinterpret_cast<cudaStream_t>(stream), p);
   if (e != cudaSuccess) {

@@ -1,10 +1,11 @@
 /*
  * gqa_kv8.h -- C ABI of the 8-bit key/value cache of the same GB300 (sm_103a) library: the
  * cache write (quantising), its read back, grouped-query attention over it for prompts and
- * for single tokens, and the rotary positions that come before it.  Beside gqa_decode.h
- * (one token per sequence over a contiguous bf16 cache), this cache holds one byte per
- * number, so that decode, which is bound by the cache's bytes, reads half as much; it is
- * paged, and a call takes any number of new tokens per sequence.
+ * for single tokens (causal, with a sliding window, or with beginnings that sequences
+ * share), page tables built on the device, and the norms and rotary positions that come
+ * before it.  Beside gqa_decode.h (one token per sequence over a contiguous bf16 cache), this
+ * cache holds one byte per number, so that decode, which is bound by the cache's bytes, reads
+ * half as much; it is paged, and a call takes any number of new tokens per sequence.
  *
  * The cache.  Pages of page_size positions; for each of keys and values
  *   codes   uint8 [n_pages][n_kv_heads][page_size][head_size]   e4m3 bytes or int8
@@ -22,7 +23,8 @@
  * lens[b] cached positions, the last offsets[b+1] - offsets[b] of which are the call's
  * tokens (rows offsets[b] .. of q, k, v and the outputs; rows at or past offsets[n_seqs]
  * are neither read nor written).  One decode step is: gqa_rope, gqa_kv8_append,
- * gqa_kv8_attention, with lens already counting the new tokens.  All arrays are in device
+ * gqa_kv8_attention, with lens already counting the new tokens (gqa_kv8_pages_step makes
+ * lens, offsets and the page table, and the positions for gqa_rope).  All arrays are in device
  * memory and read when the kernels run, so a captured graph follows their contents.
  *
  * Conventions as in moe_layer.h: device pointers owned by the caller, status codes, no host
