@@ -57,9 +57,13 @@ __host__ __device__ constexpr int ka_ps(int D) { return D + 4; }            // f
 // the tile that goes on after it takes the warp's own ring, which is done by then), the line,
 // what the parts belong to, barriers and words
 __host__ __device__ constexpr int ka_parts(int D, int R) { return ka_warps(R) * R * ka_ps(D) * 4; }
-__host__ __device__ constexpr int ka_wsum(int R) { return R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
+// The parts' meeting: a thread per 8 dims of a row, and as many teams of them as the CTA has, which take
+// its tiles in turn.  (One sequence of 717 positions 9.5 us where the whole CTA took the tiles one by one
+// in 10.5, 64 of 64 to 16384 25.3 and 26.4, 8 of 32768 29.8 and 31.4.)
+__host__ __device__ constexpr int ka_teams(int D, int R) { return ka_warps(R) * 32 / (R * D / 8); }
+__host__ __device__ constexpr int ka_wsum(int D, int R) { return ka_teams(D, R) * R * KV8_MAX_CTAS * 4; }   // weights of a tile's CTAs
 __host__ __device__ constexpr int ka_smem(int D, int R, int B, bool suffix) {
-  return 1024 + ka_warps(R) * ka_own(D, R) + ka_parts(D, R) + ka_wsum(R) + (B + 2) * 8 +
+  return 1024 + ka_warps(R) * ka_own(D, R) + ka_parts(D, R) + ka_wsum(D, R) + (B + 2) * 8 +
          ka_warps(R) * (3 * 8 + ka_stages(R) * 8 + 2 * 32 + R * 4) + 64 + (suffix ? B * 4 : 0);
 }
 static_assert(ka_smem(128, 16, KV8_MAX_SEQS, true) <= 232448 && ka_smem(128, 8, KV8_MAX_SEQS, true) <= 232448,
@@ -146,14 +150,14 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* heads = reinterpret_cast<float*>(smem + KA_WARPS * OWN);
   float* wsum = heads + ka_parts(D, R) / 4;
-  long long* prefix = reinterpret_cast<long long*>(wsum + ka_wsum(R) / 4);
+  long long* prefix = reinterpret_cast<long long*>(wsum + ka_wsum(D, R) / 4);
   long long* s_warp = prefix + p.b.n_seqs + 1 + ((p.b.n_seqs + 1) & 1);      // 16-byte aligned
   KaPart* meta = reinterpret_cast<KaPart*>(s_warp + 3 * KA_WARPS);         // [warp][began before, goes on]
   uint64_t* bars = reinterpret_cast<uint64_t*>(meta + 2 * KA_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + KA_WARPS * KA_STAGES);
   int* s_last = const_cast<int*>(abort_flag) + 1;
-  float* s_peak = reinterpret_cast<float*>(s_last + 1) + (threadIdx.x >> 5) * R;   // [R] the highest ms + d of a row
-  Kv8Line line = {prefix, reinterpret_cast<int*>(s_last + 1) + KA_WARPS * R, 0, false};
+  float* s_peak = reinterpret_cast<float*>(s_last + 4) + (threadIdx.x >> 5) * R;   // [R] the highest ms + d of a row
+  Kv8Line line = {prefix, s_last + 4 + KA_WARPS * R, 0, false};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, c4 = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * OWN;
@@ -626,12 +630,22 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   // ---- the parts meet.  A tile's parts in this CTA are the tail of one warp and the heads
   // of the warps after it (or heads from warp 0 on, if it began in an earlier CTA).
   constexpr int TPR = D / 8;                 // threads per row, 8 dims each
-  constexpr int ACT = R * TPR;               // 64 .. 256 threads
-  const int row = tid / TPR, d0 = (tid % TPR) * 8;
+  constexpr int ACT = R * TPR;               // threads of a team, 64 .. 256
+  constexpr int TEAMS = ka_teams(D, R);
+  static_assert(TEAMS * ACT == KA_THREADS && TEAMS <= 4, "all threads, a word each");
+  const int team = TEAMS == 1 ? 0 : tid / ACT, at_t = tid - team * ACT;
+  const int row = at_t / TPR, d0 = (at_t % TPR) * 8;
+  const auto sync = [&] {
+    if constexpr (TEAMS == 1)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(ACT) : "memory");
+  };
+  int turn = 0;
 #pragma unroll 1
   for (int i0 = -1; i0 < KA_WARPS; ++i0) {
     const KaPart pt = i0 < 0 ? meta[0] : meta[2 * i0 + 1];
-    if (pt.b < 0) continue;
+    if (pt.b < 0 || (TEAMS > 1 && (turn++ & (TEAMS - 1)) != team)) continue;
     const int last = min(pt.r_last - cta * KA_WARPS, KA_WARPS - 1);   // the tile's last warp here
     const int c_first = pt.r_first / KA_WARPS, c_last = pt.r_last / KA_WARPS;
     const auto part = [&](int i) {           // i0: the tail (or nothing, for -1), above: heads
@@ -639,7 +653,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     };
     const int i1 = max(i0, 0);
     float M = KV8_NO_REF, top = -INFINITY, L = 0.0f, O[8] = {0, 0, 0, 0, 0, 0, 0, 0};   // references ms and d
-    if (tid < ACT) {
+    {
       // unrolled over all warps, so that the loads do not wait for one another
       float mw[KA_WARPS], dw[KA_WARPS], lw2[KA_WARPS];
 #pragma unroll
@@ -670,28 +684,28 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
     bool write = c_first == c_last;
     if (!write) {
       const auto slot = [&](int c) { return p.part + ((static_cast<size_t>(c) * 2 + (c == c_first)) * R + row) * PS; };
-      if (tid < ACT) {
+      {
         float* dst = slot(cta);
         *reinterpret_cast<float4*>(dst + d0) = make_float4(O[0], O[1], O[2], O[3]);
         *reinterpret_cast<float4*>(dst + d0 + 4) = make_float4(O[4], O[5], O[6], O[7]);
         if (d0 == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(M, top, L, 0.0f);
       }
-      __syncthreads();
+      sync();
       const int ns = c_last - c_first + 1;
-      if (tid == 0) {
+      if (at_t == 0) {
         // release after the barrier, so the whole CTA's sums come before the ticket; acquire for
         // the CTA that adds them up
         const bool all = ticket_add(p.tickets + c_first) == static_cast<unsigned>(ns) - 1u;
         if (all) p.tickets[c_first] = 0u;    // every part has arrived: ready for the next call
-        *s_last = all;
+        s_last[team] = all;
       }
-      __syncthreads();
-      write = *s_last != 0;
+      sync();
+      write = s_last[team] != 0;
       if (write) {
-        float* fs = wsum;                    // [R][ns] weights of the CTAs' sums, in the order of the line
+        float* fs = wsum + team * R * KV8_MAX_CTAS;   // [R][ns] weights of the CTAs' sums, in the order of the line
         L = 0.0f;
-        if (tid < ACT) {
-          const int j0 = tid % TPR;
+        {
+          const int j0 = at_t % TPR;
           constexpr int PER = (KV8_MAX_CTAS + TPR - 1) / TPR;
           float ml[PER], dl[PER], ll[PER];
           M = KV8_NO_REF;
@@ -729,8 +743,8 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
 #pragma unroll
           for (int s = TPR / 2; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
         }
-        __syncthreads();
-        if (tid < ACT) {
+        sync();
+        {
 #pragma unroll
           for (int k = 0; k < 8; ++k) O[k] = 0.0f;
 #pragma unroll 8
@@ -745,7 +759,7 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
       }
     }
     const int tok0 = pt.t << p.tq_shift;
-    if (write && tid < ACT && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
+    if (write && row < min(1 << p.tq_shift, pt.n - tok0) * p.G) {
       const int tok = row / p.G, hh = row - tok * p.G;
       const size_t at = static_cast<size_t>(pt.off + tok0 + tok) * p.hq + pt.g * p.G + hh;
       if (MODE == KV8_SUFFIX) {                          // as above
