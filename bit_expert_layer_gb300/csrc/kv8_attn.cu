@@ -24,13 +24,13 @@
 // Bound: the cache's bytes.  8 x 32768 positions of e4m3 (2 heads of 128, 134 MB) take 30 us; a
 // plain copy's rate would take 20.  Between its first piece and its last a CTA runs at the
 // memory's rate (8 KB per warp and 2400 cycles); 7000 cycles before it (the line, the first
-// segment, the first page, the first codes) and 8000 after it (the CTA's join, the ticket, the
+// segment, the first page, the first codes) and 6000 after it (the CTA's join, the ticket, the
 // tile's join) are what is left.  With the query rows on the M side (half of each MMA and of O's
 // registers empty at 8 rows) a piece took 750 instructions and the same case 36.7 us; 16 warps of
 // 16-key pieces took 33.5 us, 12 of three stages 31.8, where 8 warps of 32 keys took 31.6.
-// With a window of 4096 and 4 sinks, 64 sequences of 64 to 16384 positions (int8, 58 MB) take 20.6 us, 8.7
+// With a window of 4096 and 4 sinks, 64 sequences of 64 to 16384 positions (int8, 58 MB) take 19.5 us, 8.7
 // at a copy's rate: pieces from 3 to 13 us, then the CTAs' and the tiles' joins, which want up to
-// 6 more (all tiles' tickets drawn together instead of one by one: 22.5 us).
+// 5 more (all tiles' tickets drawn together after all parts are added up: 22.5 us).
 #include <algorithm>
 #include <cstring>
 
