@@ -245,6 +245,13 @@ __device__ __forceinline__ long long kv8_units_seq(const Kv8AttnParams& p, int u
   return kv8_units_before<U, C, MODE>(p, uni, s, tiles - 1) + kv8_units_tile<U, C, MODE>(p, uni, s, tiles - 1);
 }
 
+// The positions of a group that the prefix pass works on, of the `shared` that it says it shares; `fits` when
+// the page table holds those.
+__device__ __forceinline__ int kv8_group_len(const Kv8AttnParams& p, int shared, bool* fits) {
+  const int len = min(max(shared, 0), p.b.max_pages << p.c.page_shift);
+  *fits = len == shared;
+  return min(len, p.max_shared) / KV8_SHARED_UNIT * KV8_SHARED_UNIT;
+}
 // A group of sequences with a shared prefix as an item of the line: the tokens of all of them,
 // each seeing `len` positions (whole units).  `bad` when something was out of range.
 __device__ __forceinline__ Kv8Seq kv8_group(const Kv8AttnParams& p, int i) {
@@ -253,18 +260,19 @@ __device__ __forceinline__ Kv8Seq kv8_group(const Kv8AttnParams& p, int i) {
   const int b0 = min(max(__ldg(p.groups + i), 0), p.b.n_seqs), b1 = min(max(__ldg(p.groups + i + 1), 0), p.b.n_seqs);
   const int shared = __ldg(p.shared + i);
   const int o0 = __ldg(p.b.offsets + b0), o1 = __ldg(p.b.offsets + b1);
-  const int len = min(max(shared, 0), p.b.max_pages << p.c.page_shift);
   const bool rows = o0 >= 0 && o0 <= o1 && o1 <= p.b.n_tokens;
+  bool fits;
   s.off = rows ? o0 : 0;
-  s.len = min(len, p.max_shared) / KV8_SHARED_UNIT * KV8_SHARED_UNIT;
+  s.len = kv8_group_len(p, shared, &fits);
   s.n = rows && s.len > 0 ? o1 - o0 : 0;
   s.first = 0;
   s.base = 0;
-  s.bad = !rows || len != shared;
+  s.bad = !rows || !fits;
   return s;
 }
 // The positions of sequence b that the prefix pass sees to: those of its group, if all of its new
-// tokens come after them.
+// tokens come after them.  (Where that counts, kv8_line has found every sequence's rows in order, so that
+// the group's are those of its sequences.)
 __device__ __forceinline__ int kv8_base(const Kv8AttnParams& p, const Kv8Seq& s, int b) {
   int lo = 0, hi = p.n_groups;           // the last group that begins at b or before
   while (hi - lo > 1) {
@@ -272,9 +280,10 @@ __device__ __forceinline__ int kv8_base(const Kv8AttnParams& p, const Kv8Seq& s,
     if (__ldg(p.groups + mid) <= b) lo = mid;
     else hi = mid;
   }
-  if (s.n <= 0 || b < __ldg(p.groups + lo) || b >= __ldg(p.groups + lo + 1)) return 0;
-  const Kv8Seq g = kv8_group(p, lo);
-  return s.first >= g.len && s.off >= g.off && s.off + s.n <= g.off + g.n ? g.len : 0;
+  const int g0 = __ldg(p.groups + lo), g1 = __ldg(p.groups + lo + 1), shared = __ldg(p.shared + lo);
+  bool fits;
+  const int len = kv8_group_len(p, shared, &fits);
+  return s.n > 0 && b >= g0 && b < g1 && s.first >= len ? len : 0;
 }
 // Item i of the line: a sequence, or in prefix mode a group.  (base: filled by kv8_line.)
 template <int MODE>
@@ -414,9 +423,6 @@ __device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& lin
       if constexpr (MODE == KV8_PREFIX) {
         s = kv8_group(p, b);
         if (!share) s.n = 0;
-        if (s.n > 0)         // (counted below as if nothing was shared)
-          pieces -= static_cast<long long>(__ldg(p.groups + b + 1) - __ldg(p.groups + b)) * s.len / 32 *
-                    (((p.b.max_new - 1) >> p.shift_suffix) + 1) * p.c.hkv;
       } else {
         s = kv8_seq(p.b, p.c.page_shift, b);
         if constexpr (MODE == KV8_SUFFIX) line.base[b] = s.base = share ? kv8_base(p, s, b) : 0;
@@ -451,7 +457,8 @@ __device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& lin
         for (int b = tid; b < p.b.n_seqs; b += THREADS) {
           const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
           fine &= !s.bad;
-          if (s.n > 0) pieces += kv8_pieces(p, s, max(s.first, 0));
+          // (the same sum as the suffix pass's, so that both divide the SMs alike)
+          if (p.own && s.n > 0) pieces += kv8_pieces(p, s, max(s.first, 0) - (share ? kv8_base(p, s, b) : 0));
         }
       }
     }
