@@ -54,7 +54,8 @@ __device__ __forceinline__ int pg_find(const int* a, int n, int x) {
 }  // namespace
 
 __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_constant__ PagesParams p) {
-  // per sequence: tokens, pages given and taken before it; positions kept, pages held and wanted
+  // per sequence: tokens, pages given and taken before it; positions kept (their complement: its tokens get no
+  // slots, and nothing is kept), pages held and wanted
   __shared__ int s_off[PG_SEQS + 1], s_give[PG_SEQS + 1], s_take[PG_SEQS + 1];
   __shared__ int s_keep[PG_SEQS], s_held[PG_SEQS], s_rest[PG_SEQS];
   __shared__ int s_warp[PG_THREADS / 32][3];
@@ -75,13 +76,16 @@ __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_cons
   for (int b = b0; b < b1; ++b) {
     const int len = within(p.lens[b], cap), held = within(p.held[b], p.max_pages), fresh = within(p.n_new[b], p.n_tokens);
     const int keep = p.keep ? within(p.keep[b], len) : len;
-    bad |= keep + fresh > cap;
-    const int after = min((keep + fresh + page - 1) >> p.page_shift, p.max_pages);
-    const int rest = max(after, p.borrowed ? max(p.borrowed[b], 0) : 0);     // pages below it are not given back
+    const int borrowed = p.borrowed ? within(p.borrowed[b], p.max_pages) : 0;
+    // tokens that begin in a borrowed page would go over another sequence's: the sequence is done
+    const bool lost = fresh > 0 && keep >> p.page_shift < borrowed;
+    bad |= lost || keep + fresh > cap;
+    const int after = lost ? 0 : min((keep + fresh + page - 1) >> p.page_shift, p.max_pages);
+    const int rest = max(after, borrowed);                   // pages below it are not given back
     s_off[b] = sum[0];
     s_give[b] = sum[1];
     s_take[b] = sum[2];
-    s_keep[b] = keep;
+    s_keep[b] = lost ? ~keep : keep;
     s_held[b] = held;
     s_rest[b] = rest;
     sum[0] += fresh;
@@ -172,9 +176,10 @@ __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_cons
       pos[i] = slot[i] = 0;
       if (t >= T) break;
       while (t >= s_off[b + 1]) ++b;                       // sequences without tokens among them
-      pos[i] = s_keep[b] + t - s_off[b];
+      const int keep = s_keep[b];
+      pos[i] = (keep < 0 ? ~keep : keep) + t - s_off[b];
       const int j = pos[i] >> p.page_shift;
-      if (b != last_b || j != last_j) id = page_of(b, j);
+      if (b != last_b || j != last_j) id = keep < 0 ? -1 : page_of(b, j);
       last_b = b;
       last_j = j;
       slot[i] = id < 0 || id >= p.n_pages ? -1 : (id << p.page_shift) + (pos[i] & (page - 1));
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_cons
   for (int b = tid; b <= B; b += PG_THREADS) {
     p.offsets[b] = s_off[b];
     if (b == B) break;
-    const int fresh = s_off[b + 1] - s_off[b], len = s_keep[b] + fresh;
+    const int fresh = s_off[b + 1] - s_off[b], len = s_keep[b] < 0 ? 0 : s_keep[b] + fresh;
     const int after = min((len + page - 1) >> p.page_shift, p.max_pages);
     p.lens_out[b] = len;
     p.held_out[b] = min(after, s_held[b] + min(max(taken - s_take[b], 0), s_take[b + 1] - s_take[b]));

@@ -141,7 +141,9 @@ class KV8Pages(_Fixed):
     max_pages], ``free`` int32 [n_pages] (a stack), and the state that a step changes: ``lens``
     int32 [n_seqs] (cached positions), ``held`` int32 [n_seqs] (pages in the sequence's row)
     and ``n_free`` int32 [1].  Sequences that begin with pages of another one's (a shared
-    prefix) say how many in ``borrowed`` int32 [n_seqs]; those are not given back."""
+    prefix) say how many in ``borrowed`` int32 [n_seqs]; those are not given back, and new tokens
+    have to begin behind them: a sequence whose tokens do not is recorded and done.  Lower its entry
+    (in place) after a step that keeps less than them, and after the one that ends it."""
 
     def __init__(self, table: torch.Tensor, free: torch.Tensor, page_size: int, lens: torch.Tensor, held: torch.Tensor,
                  n_free: torch.Tensor, borrowed: torch.Tensor | None = None, control: torch.Tensor | None = None):

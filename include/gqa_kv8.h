@@ -200,7 +200,7 @@ typedef struct {
  * they are.)
  *   to         the state after the step: arrays of from's own, or others that do not overlap
  *   borrowed   [n_seqs] or NULL: a sequence's first pages that are not its own (a shared
- *              prefix's); it does not give them back
+ *              prefix's); it does not give them back, and no token is kept in them (see below)
  *   offsets    [n_seqs + 1] tokens before each sequence
  *   positions  [n_tokens] or NULL: position of every token
  *   slots      [n_tokens] or NULL: page * page_size + position % page_size, where the token
@@ -210,6 +210,14 @@ typedef struct {
  * as they are.  Recorded in control[0]: a free list that runs out (entries without a page
  * become -1, and the sequence asks for them again at its next step), and lengths, counts or
  * pages out of range, which are cut to it.  Two calls on one pool must not overlap in time.
+ * A sequence's new tokens have to begin behind the pages it has borrowed, at position borrowed *
+ * page_size or later.  One whose tokens begin before it (it has fallen back into them, or its row
+ * is used again in the step in which it is done) is recorded and done: its tokens have slots of
+ * -1, its length is 0 and it holds no pages after the step, so that the calls above write none of
+ * them.  The caller lowers borrowed: to keep / page_size after a step without new tokens that
+ * keeps fewer whole pages than that (the last of them, if it is kept in part, has to be replaced
+ * by a copy of its own first), and to 0 after the step in which the sequence is done, before
+ * another request begins in its row.  The sequence that lends pages has to hold them for as long.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 moe_status_t gqa_kv8_pages_step(const gqa_kv8_pages_t* pages, const gqa_kv8_pages_state_t* from,
                                 const gqa_kv8_pages_state_t* to, const int32_t* keep, const int32_t* n_new,

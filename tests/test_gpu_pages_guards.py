@@ -1,0 +1,93 @@
+"""Page tables: sequences that fall back into pages they have borrowed, pages that cannot be, tokens past
+the end.  (The steps in general: test_gpu_serving.py.)"""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+from test_gpu_kv8 import gen, ints, kv8  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+PAGE = 64
+
+
+def lender_and_borrower(kv8, own, borrowed=4, n_pages=40):
+    """Sequence 0 has 300 positions; sequence 1 begins with its first pages and has `own` positions after them."""
+    pages = kv8.KV8Pages.all_free(n_pages, PAGE, 2, 12)
+    pages = kv8.KV8Pages(pages.table, pages.free, PAGE, pages.lens, pages.held, pages.n_free, ints([0, borrowed]))
+    pages.step(ints([300, 0]), 300)
+    pages.table[1, :borrowed] = pages.table[0, :borrowed]
+    pages.lens[1], pages.held[1] = borrowed * PAGE, borrowed
+    pages.step(ints([0, own]), own)
+    assert pages.get_error() == 0
+    return pages
+
+
+def whole(pages):
+    """Every page of the pool is on the free list or in one sequence's own part of its row, once."""
+    n, own = pages.n_free.item(), pages.free[:pages.n_free.item()].tolist()
+    for row, held, skip in zip(pages.table.tolist(), pages.held.tolist(), pages.borrowed.tolist()):
+        own += row[skip:held]
+    return sorted(own) == list(range(pages.free.numel())) and 0 <= n
+
+
+@pytest.mark.parametrize("keep", [0, 100, 128, 255])
+@pytest.mark.parametrize("own", [1, 150])
+@pytest.mark.parametrize("new", [1, 200])
+def test_no_token_goes_to_a_borrowed_page(kv8, own, keep, new):
+    """A sequence that falls back into its prefix, or whose row is used again at once, and adds tokens: recorded,
+    and done.  The prefix stays as it was, and all pages of its own come back."""
+    from bit_expert_layer_gb300 import _abi
+    pages = lender_and_borrower(kv8, own)
+    cache = kv8.KV8Cache.empty(40, 2, PAGE, 64, "int8")
+    g = gen(keep + own)
+    cache.k.copy_(torch.randint(0, 256, cache.k.shape, generator=g, device="cuda", dtype=torch.uint8))
+    lent = pages.table[0, :5].long()
+    before = [x[lent].clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    t = new + 1
+    offsets, positions, slots = pages.step(ints([1, new]), t, keep=ints([256, keep]))
+    assert pages.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert offsets.tolist() == [0, 1, t] and positions.tolist() == [256] + list(range(keep, keep + new))
+    assert slots[1:].tolist() == [-1] * new and slots[0].item() == pages.table[0, 4].item() * PAGE
+    assert pages.lens.tolist() == [257, 0] and pages.held.tolist() == [5, 0] and whole(pages)
+    # what follows writes none of its tokens, and gives them zeros
+    batch = kv8.KV8Batch(pages.table, pages.lens, offsets, new)
+    q = torch.randn(t, 4, 64, generator=g, device="cuda").to(torch.bfloat16)
+    cache.append(batch, q[:, :2], q[:, 2:])
+    for x, was in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), before):
+        assert torch.equal(x[lent[:4]], was[:4])
+    assert torch.isfinite(cache.attention(batch, q)[0]).all() and (cache.attention(batch, q)[1:] == 0).all()
+    # the row is free for another request
+    pages.borrowed[1] = 0
+    pages.step(ints([0, 70]), 70)
+    assert pages.get_error() == 0 and pages.lens.tolist() == [257, 70] and whole(pages)
+
+
+def test_falling_back_and_going_on(kv8):
+    """To the end of the borrowed pages and on; into them by whole pages, lowering `borrowed`; done, then another
+    request in the row: as the description has it, nothing recorded and no page lost."""
+    pages = lender_and_borrower(kv8, 150)
+    pages.step(ints([0, 90]), 90, keep=ints([300, 256]))
+    assert pages.get_error() == 0 and pages.lens.tolist() == [300, 346] and whole(pages)
+    pages.step(ints([0, 0]), 0, keep=ints([300, 128]))
+    pages.borrowed[1] = 2
+    offsets, positions, slots = pages.step(ints([0, 100]), 100)
+    assert pages.get_error() == 0 and pages.held.tolist() == [5, 4] and whole(pages)
+    assert not set((slots // PAGE).tolist()) & set(pages.table[0, :5].tolist())
+    pages.step(ints([0, 0]), 0, keep=ints([300, 0]))
+    pages.borrowed[1] = 0
+    pages.step(ints([0, 300]), 300)
+    assert pages.get_error() == 0 and pages.held.tolist() == [5, 5] and whole(pages)
+    pages.step(ints([0, 0]), 0, keep=ints([0, 0]))
+    assert pages.get_error() == 0 and pages.n_free.item() == 40
+
+
+@pytest.mark.parametrize("count", [13, 2 ** 31 - 1, -1, -2 ** 31])
+def test_a_count_of_borrowed_pages_that_cannot_be(kv8, count):
+    from bit_expert_layer_gb300 import _abi
+    pages = lender_and_borrower(kv8, 20)
+    pages.borrowed[1] = count
+    pages.step(ints([1, 1]), 2)
+    assert pages.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert pages.lens.tolist() == [301, 0 if count > 0 else 277]
