@@ -148,6 +148,11 @@ __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_cons
     if (k >= taken) return -1;
     return k < given ? page_given(given - 1 - k) : p.free_pages[n_free - 1 - (k - given)];
   };
+  const auto checked = [&](int id) {                       // what changes hands is a page of the pool, or -1
+    const bool ok = id >= 0 && id < p.n_pages;
+    bad |= !ok;
+    return ok ? id : -1;
+  };
   const auto page_of = [&](int b, int j) {                 // page j of sequence b, in this step
     if (j >= p.max_pages) return -1;
     return j < s_held[b] ? row(b)[j] : page_taken(s_take[b] + j - s_held[b]);
@@ -158,12 +163,12 @@ __global__ void __launch_bounds__(PG_THREADS) kv8_pages_kernel(const __grid_cons
 #pragma unroll 1
   for (int k = at; k < wanted; k += step) {
     const int b = pg_find(s_take, B, k);
-    row(b)[s_held[b] + k - s_take[b]] = page_taken(k);
+    row(b)[s_held[b] + k - s_take[b]] = checked(page_taken(k));
   }
   // ---- pages given back and not taken
 #pragma unroll 1
   for (int r = at; r < given - taken; r += step) {
-    if (n_free + r < p.n_pages) p.free_pages[n_free + r] = page_given(r);
+    if (n_free + r < p.n_pages) p.free_pages[n_free + r] = checked(page_given(r));
     else bad = true;
   }
   // ---- the tokens, four at a time

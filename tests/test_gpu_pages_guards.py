@@ -91,3 +91,28 @@ def test_a_count_of_borrowed_pages_that_cannot_be(kv8, count):
     pages.step(ints([1, 1]), 2)
     assert pages.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
     assert pages.lens.tolist() == [301, 0 if count > 0 else 277]
+
+
+@pytest.mark.parametrize("bad", [-1, -7, 6, 2 ** 31 - 1])
+def test_pages_that_cannot_be_do_not_change_hands(kv8, bad):
+    """A held entry out of range that is given back, to the list or straight to another sequence, and an entry of
+    the list that is taken: recorded, and -1 from then on."""
+    from bit_expert_layer_gb300 import _abi
+
+    def pool(held, table, free, n_free):
+        z = [n * PAGE for n in held]
+        return kv8.KV8Pages(ints(table), ints(free), PAGE, ints(z), ints(held), ints([n_free]))
+
+    p = pool([2, 1], [[4, bad, 0], [5, 0, 0]], [0, 1, 9, 9, 9, 9], 2)     # to the list
+    p.step(ints([0, 0]), 0, keep=ints([0, 64]))
+    assert p.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert p.n_free.item() == 4 and p.free[:4].tolist() == [0, 1, 4, -1]
+    assert p.step(ints([1, 0]), 1, keep=ints([0, 64]))[2].tolist() == [-1]     # what the list has is taken
+    assert p.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS and p.table[0, 0].item() == -1
+    p = pool([2, 1], [[4, bad, 0], [5, 0, 0]], [0, 1, 9, 9, 9, 9], 2)     # from hand to hand
+    slots = p.step(ints([0, 70]), 70, keep=ints([0, 64]))[2].tolist()
+    assert p.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert p.table[1].tolist() == [5, -1, 4] and slots == [-1] * 64 + [4 * PAGE + i for i in range(6)]
+    p = pool([0, 1], [[0, 0, 0], [5, 0, 0]], [0, bad, 9, 9, 9, 9], 2)     # from the list
+    assert p.step(ints([1, 0]), 1)[2].tolist() == [-1] and p.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert p.table[0, 0].item() == -1 and p.n_free.item() == 1
