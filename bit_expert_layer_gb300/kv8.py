@@ -143,7 +143,8 @@ class KV8Pages(_Fixed):
     and ``n_free`` int32 [1].  Sequences that begin with pages of another one's (a shared
     prefix) say how many in ``borrowed`` int32 [n_seqs]; those are not given back, and new tokens
     have to begin behind them: a sequence whose tokens do not is recorded and done.  Lower its entry
-    (in place) after a step that keeps less than them, and after the one that ends it."""
+    (in place) after a step that keeps less than them, and after the one that ends it.  ``control``
+    is the pool's error word and a ticket, zero at first (made here if it is not given)."""
 
     def __init__(self, table: torch.Tensor, free: torch.Tensor, page_size: int, lens: torch.Tensor, held: torch.Tensor,
                  n_free: torch.Tensor, borrowed: torch.Tensor | None = None, control: torch.Tensor | None = None):
@@ -158,6 +159,9 @@ class KV8Pages(_Fixed):
                 raise ValueError(f"{name}: {m} entries are wanted, got {x.shape[0]}")
         self.page_size = int(page_size)
         self.control = torch.zeros(2, dtype=_INT, device=dev) if control is None else control
+        words = self.control.view(_INT) if self.control.dtype is torch.uint32 else self.control
+        if _ints(words, "control", 1, dev).shape[0] < 2:
+            raise ValueError(f"control: 2 entries are wanted, got {words.shape[0]}")
         self._pages = ctypes.byref(GqaKv8Pages(table.data_ptr(), free.data_ptr(), self.control.data_ptr(), n, table.shape[1],
                                                free.shape[0], self.page_size))
         self._state = ctypes.byref(GqaKv8PagesState(lens.data_ptr(), held.data_ptr(), n_free.data_ptr()))

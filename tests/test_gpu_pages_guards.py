@@ -116,3 +116,17 @@ def test_pages_that_cannot_be_do_not_change_hands(kv8, bad):
     p = pool([0, 1], [[0, 0, 0], [5, 0, 0]], [0, bad, 9, 9, 9, 9], 2)     # from the list
     assert p.step(ints([1, 0]), 1)[2].tolist() == [-1] and p.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
     assert p.table[0, 0].item() == -1 and p.n_free.item() == 1
+
+
+def test_control_is_checked(kv8):
+    """Like the other tensors, before anything is launched."""
+    p = kv8.KV8Pages.all_free(6, PAGE, 2, 3)
+    zeros = lambda *s, **kw: torch.zeros(*s, **dict(dict(dtype=torch.int32, device="cuda"), **kw))  # noqa: E731
+    for control in (zeros(2, device="cpu"), zeros(1), zeros(0), zeros(2, dtype=torch.int64), zeros(2, dtype=torch.float32),
+                    zeros(1, 2), zeros(4)[::2]):
+        with pytest.raises(ValueError):
+            kv8.KV8Pages(p.table, p.free, PAGE, p.lens, p.held, p.n_free, control=control)
+    for control in (zeros(2), zeros(5), zeros(2, dtype=torch.uint32)):
+        q = kv8.KV8Pages(p.table, p.free, PAGE, p.lens, p.held, p.n_free, control=control)
+        q.fork()
+        assert q.control is control and q.step(ints([0, 0]), 0)[0].tolist() == [0, 0, 0] and q.get_error() == 0
