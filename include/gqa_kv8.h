@@ -209,8 +209,13 @@ typedef struct {
  * n_tokens (0 .. 2^20) is the rows of positions and slots; rows from offsets[n_seqs] on stay
  * as they are.  Recorded in control[0]: a free list that runs out (entries without a page
  * become -1, and the sequence asks for them again at its next step), and lengths, counts or
- * pages out of range, which are cut to it (a page that changes hands becomes -1).  Two calls on
- * one pool must not overlap in time.
+ * pages that are out of range when they are read, which are cut to it (a page that changes
+ * hands becomes -1).  Two calls on one pool must not overlap in time.
+ * Tokens past the end are recorded, but not cut off: with more tokens than rows in all, offsets,
+ * lens and pages still count every one of them, and so does the length of a sequence with more
+ * positions than its row of the table holds (its pages end with the row).  That way every other
+ * token keeps its row and its position: tokens past the table have slots of -1, the calls above
+ * leave those out, and sequences whose rows do not all exist; the next step cuts the length.
  * A sequence's new tokens have to begin behind the pages it has borrowed, at position borrowed *
  * page_size or later.  One whose tokens begin before it (it has fallen back into them, or its row
  * is used again in the step in which it is done) is recorded and done: its tokens have slots of

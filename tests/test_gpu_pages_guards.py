@@ -130,3 +130,40 @@ def test_control_is_checked(kv8):
         q = kv8.KV8Pages(p.table, p.free, PAGE, p.lens, p.held, p.n_free, control=control)
         q.fork()
         assert q.control is control and q.step(ints([0, 0]), 0)[0].tolist() == [0, 0, 0] and q.get_error() == 0
+
+
+def test_tokens_past_the_rows_and_past_the_table(kv8):
+    """Recorded; the others keep their rows and positions, nothing that is cached moves, and what follows leaves out
+    the tokens past the table and the sequences whose rows do not exist."""
+    from bit_expert_layer_gb300 import _abi
+    pages = kv8.KV8Pages.all_free(20, PAGE, 3, 4)
+    cache = kv8.KV8Cache.empty(20, 1, PAGE, 64, "int8")
+    g = gen(5)
+    rows = lambda n: torch.randint(-127, 128, (n, 2, 64), generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+
+    def append(new, n_tokens, max_new):
+        offsets, positions, slots = pages.step(ints(new), n_tokens)
+        x = rows(n_tokens)
+        cache.append(kv8.KV8Batch(pages.table, pages.lens, offsets, max_new), x[:, :1], x[:, 1:])
+        return offsets.tolist(), positions.tolist(), slots, x
+
+    append([250, 10, 20], 280, 250)
+    codes = cache.k.clone()
+    *_, slots, x = append([10, 3, 4], 17, 10)             # the first one ends at 260 of 256
+    assert pages.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS and cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert pages.lens.tolist() == [260, 13, 24] and pages.held.tolist() == [4, 1, 1]
+    assert slots[6:10].tolist() == [-1] * 4 and (slots[:6] >= 0).all() and (slots[10:] >= 0).all()
+    at = torch.cat([slots[:6], slots[10:]]).long()
+    changed = (cache.k != codes).any(-1).squeeze(1).flatten().nonzero().flatten().tolist()
+    blocks = {i // 16 for i in at.tolist()}               # (older codes of a block change with its scale)
+    assert {i // 16 for i in changed} <= blocks
+    scale = cache.k_scale.view(-1)[at // 16]
+    values = cache.k.view(torch.int8).view(-1, 64)[at].float() * scale[:, None]
+    assert torch.equal(values, torch.cat([x[:6, 0], x[10:, 0]]).float())
+    codes = cache.k.clone()
+    offsets, positions, slots, x = append([0, 5, 6], 7, 6)     # 11 tokens, 7 rows: the last sequence's do not fit
+    assert pages.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS and cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+    assert offsets == [0, 0, 5, 11] and positions == [13, 14, 15, 16, 17, 24, 25]
+    assert pages.lens.tolist() == [256, 18, 30]
+    changed = (cache.k != codes).any(-1).squeeze(1).flatten().nonzero().flatten()
+    assert set((changed // PAGE).tolist()) == {pages.table[1, 0].item()}
