@@ -2,6 +2,8 @@
 divide the SMs, and what they leave out.  (Results in general: test_gpu_serving.py.)"""
 from __future__ import annotations
 
+import random
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -87,3 +89,103 @@ def test_the_passes_divide_the_sms_by_the_same_work(kv8, groups, share, new):
     assert shared(ws) and s.cache.get_error() == 0
     sms = min(torch.cuda.get_device_properties(0).multi_processor_count, MAX_CTAS)
     assert abs(prefix_ctas(s, ws) - best_split(s, groups, share, sms)) <= 1
+
+
+def run(s, prefix=None, **kw):
+    """The call on a fresh workspace; it has to share."""
+    ws = workspace(s)
+    out = s.cache.attention(s.batch, s.q, workspace=ws, prefix=prefix or s.prefix, **kw)
+    assert shared(ws)
+    return out
+
+
+def check_some(s, out, rng, n=60):
+    """check(), for some of the sequences: the reference takes milliseconds for each."""
+    pick = set(rng.sample(range(len(s.lens)), n))
+    rows = [r for b in sorted(pick) for r in range(int(s.offsets[b]), int(s.offsets[b + 1]))]
+    want, bound = serving_ref.attention(s.ref(), s.table, [m if b in pick else 0 for b, m in enumerate(s.lens)], s.offsets,
+                                        s.q[:int(s.offsets[-1])].double())
+    assert rows and torch.all((out[rows].double() - want[rows]).abs() <= bound[rows])
+
+
+def sizes(n, parts, rng):
+    """`parts` group sizes of n sequences, empty ones among them."""
+    cut = sorted(rng.choices(range(n + 1), k=parts - 1))
+    return [b - a for a, b in zip([0] + cut, cut + [n])]
+
+
+@pytest.mark.parametrize("parts,new", [(340, 2), (700, 3)], ids=["decode", "prompt"])
+def test_hundreds_of_groups(kv8, parts, new):
+    """1024 sequences in about as many groups as it pays for, of none to some sequences, some that share nothing, the
+    last ones empty."""
+    rng = random.Random(parts)
+    groups = sizes(1024, parts - 20, rng) + [0] * 20
+    share = [rng.choice([0, 100, 128, 260, 300]) for _ in groups]
+    fresh = [0 if i % 13 == 5 else new - (i % 5 == 2) for i in range(1024)]
+    s = Shared(kv8, groups, share, [new + i % 40 for i in range(1024)], fresh, (16, 1, 64), 16, seed=parts, pad=3)
+    out = torch.full(s.q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    run(s, out=out)
+    check_some(s, out, rng, 200)
+    assert (out[int(s.offsets[-1]):] == 5).all() and s.cache.get_error() == 0
+
+
+@pytest.mark.parametrize("bound", [127, 128, 300, 511, 513])
+def test_a_bound_below_what_is_shared(kv8, bound):
+    """Positions past the bound are each sequence's own; never a position twice, none lost."""
+    s = Shared(kv8, [1000], [512], [20 + i % 50 for i in range(1000)], [2] * 1000, (32, 2, 64), seed=74)
+    check_some(s, run(s, kv8.KV8Prefix(ints([0, 1000]), ints([512]), bound)), random.Random(bound))
+    assert s.cache.get_error() == 0
+
+
+@pytest.mark.parametrize("new", [1, 2, 4, 40])
+@pytest.mark.parametrize("at", [0, 3, 31])
+def test_a_missing_shared_page_is_missing_for_the_group(kv8, at, new):
+    """The first sequence's row is the one that is read: a page out of range there is left out for all, one in
+    another sequence's row for none."""
+    from bit_expert_layer_gb300 import _abi
+    s = Shared(kv8, [6, 5], [512, 256], [100 + i for i in range(11)], [new] * 11, page=16, seed=75)
+    good = run(s)
+    check(s, good)
+    for row, bad in ((0, s.n_pages), (0, -1), (2, -1)):
+        t = s.table.copy()
+        t[row, at] = bad
+        s.batch.page_table.copy_(ints(t))
+        out = run(s)
+        if row:
+            assert torch.equal(out, good) and s.cache.get_error() == 0
+            continue
+        assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+        # the same without the page: it holds 16 positions that every token sees
+        less, lens = s.table.copy(), list(s.lens)
+        for b in range(6):
+            less[b, at:-1] = s.table[b, at + 1:]
+            lens[b] -= 16
+        check(s, out, lens=lens, table=less)
+        assert torch.equal(out[6 * new:], good[6 * new:])
+
+
+@pytest.mark.parametrize("new", [1, 2, 4, 40])
+def test_a_missing_own_page_is_missing_for_its_sequence(kv8, new):
+    from bit_expert_layer_gb300 import _abi
+    s = Shared(kv8, [6], [512], [100 + i for i in range(6)], [new] * 6, page=16, seed=76)
+    good = run(s)
+    for b, at in ((0, 32), (3, 34)):
+        t = s.table.copy()
+        t[b, at] = 2 ** 31 - 1
+        s.batch.page_table.copy_(ints(t))
+        out = run(s)
+        assert s.cache.get_error() == _abi.MOE_ERR_DEVICE_BOUNDS
+        less, lens = s.table.copy(), list(s.lens)
+        less[b, at:-1] = s.table[b, at + 1:]
+        lens[b] -= 16
+        check(s, out, lens=lens, table=less)
+        rest = [i for i in range(6 * new) if i // new != b]
+        assert torch.equal(out[rest], good[rest])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_rows_that_see_nothing(kv8, new):
+    """All pages out of range, shared and own: zeros."""
+    s = Shared(kv8, [6], [512], [100] * 6, [new] * 6, page=64, seed=77)
+    s.batch.page_table.fill_(-1)
+    assert (run(s) == 0).all() and s.cache.get_error() != 0
