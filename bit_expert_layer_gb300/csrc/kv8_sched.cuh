@@ -443,8 +443,10 @@ __device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& lin
       }
     }
     if constexpr (groups) {
+      // (other threads than those of the items above, as long as there are enough: their loads overlap)
+      const int back = THREADS - 1 - tid;
 #pragma unroll 1
-      for (int i = tid; i <= p.n_groups; i += THREADS) {
+      for (int i = MODE == KV8_SUFFIX ? back : tid; i <= p.n_groups; i += THREADS) {
         const int b = __ldg(p.groups + i);
         fine &= b >= 0 && b <= p.b.n_seqs && (i == 0 || __ldg(p.groups + i - 1) <= b);
         if (MODE == KV8_SUFFIX && share && i < p.n_groups) {
@@ -454,7 +456,7 @@ __device__ __forceinline__ Kv8Runs kv8_line(const Kv8AttnParams& p, Kv8Line& lin
       }
       if constexpr (MODE == KV8_PREFIX) {
 #pragma unroll 1
-        for (int b = tid; b < p.b.n_seqs; b += THREADS) {
+        for (int b = back; b < p.b.n_seqs; b += THREADS) {
           const Kv8Seq s = kv8_seq(p.b, p.c.page_shift, b);
           fine &= !s.bad;
           // (the same sum as the suffix pass's, so that both divide the SMs alike)
