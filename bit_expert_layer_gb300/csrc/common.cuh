@@ -158,8 +158,12 @@ __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 // that wait on SMs while this one runs measured slower than letting them in at exit.)
 // Launched without the attribute, the wait does nothing.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next kernel of the stream may start once every CTA has called this or left (the exception to
-// the rule above: it must touch nothing that this kernel writes before it waits itself).
+// The next kernel of the stream may start once every CTA has called this or left: the exception to
+// the rule above, for a kernel that works beside this one.  Before it waits itself, that kernel must
+// touch nothing that this one writes, and it sees what earlier kernels wrote only because every CTA of
+// this one calls grid_dep_wait() first, in all threads: its own CTAs start after that, so after
+// those kernels have completed and their writes have left the SMs.  One CTA of it at least waits
+// before it ends, so that what comes after it finds both done.
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ----------------------------------------------------------------- mbarrier

@@ -28,7 +28,7 @@
 // tile's join) are what is left.  With the query rows on the M side (half of each MMA and of O's
 // registers empty at 8 rows) a piece took 750 instructions and the same case 36.7 us; 16 warps of
 // 16-key pieces took 33.5 us, 12 of three stages 31.8, where 8 warps of 32 keys took 31.6.
-// With a window of 4096 and 4 sinks, 64 sequences of 64 to 16384 positions (int8, 58 MB) take 19.5 us, 8.7
+// With a window of 4096 and 4 sinks, 64 sequences of 64 to 16384 positions (int8, 58 MB) take 19.9 us, 8.7
 // at a copy's rate: pieces from 3 to 13 us, then the CTAs' and the tiles' joins, which want up to
 // 5 more (all tiles' tickets drawn together after all parts are added up: 22.5 us).
 #include <algorithm>
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(ka_warps(R) * 32, 1)
   }
   if (tid < 2 * KA_WARPS) meta[tid].b = -1;
   // What follows reads and writes what earlier kernels wrote.  (The suffix pass starts beside the prefix
-  // pass, whose CTAs have waited for those kernels before they let it; its last CTA waits for the
-  // prefix pass, so that what comes after finds both done.)
+  // pass, as grid_dep_launch() has it: that pass has waited for those kernels in all of its CTAs, and this
+  // one's last CTA waits for that pass.)
   if (MODE != KV8_SUFFIX) grid_dep_wait();
   const auto leave = [] {
     if (MODE == KV8_SUFFIX && blockIdx.x == gridDim.x - 1) grid_dep_wait();
@@ -928,6 +928,11 @@ bool heads_ok(const gqa_kv8_cache_t* cache, int n_q_heads, int max_new) {
 // from L2 after their first reader, twice as slowly where all sequences want the same ones at once.)
 // Four new tokens: 3 over 32 thousand 31 and 29, 16 97 and 42.  Prompts of 20 tokens, which have most
 // of a tile of their own each: 12 over 32 thousand 96 and 97, 16 123 and 112.
+// The constants hold for other layouts too: 1 to 16 query heads to 1 to 8 key/value heads of 64 and
+// 128, both formats, 1 to 40 new tokens, 4 to 64 sequences over 1 to 32 thousand positions: of 340 pairs of
+// times the rule took the slower side by more than 8 % in six (24 sequences of 2 tokens over 4 thousand 24
+// and 27; the others prompts, the worst 16 of 40 tokens and 7 heads of 64 over 4 thousand, 53 and 42).
+// A list of groups counts a tile at least for each, empty ones too; the host cannot see which they are.
 bool kv8_share(const Kv8AttnParams& p, int R, int shared) {
   const double units = shared / 128.0 * p.c.hkv / 152;       // of a tile of the prefix pass, per SM
   const int shift = kv8_prompt_shift(p.G, kv8_prompt_tokens(p, KV8_PREFIX));

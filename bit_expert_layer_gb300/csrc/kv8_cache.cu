@@ -3,7 +3,7 @@
 // All are bound by memory: each reads its rows once and writes them once.  Measured on 2
 // key/value and 16 query heads of 128: the write of 16 thousand tokens (int8, 23 MB) 5.9 us
 // (3.5 at the copy rate), 60 thousand rows read back (e4m3, 92 MB) 15.1 us (13.8), 16384 tokens
-// rotated (151 MB) 28.0 us (22.6), normed and rotated 29.7 us.
+// rotated (151 MB) 28.0 us (22.6), normed and rotated 29.6 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -342,7 +342,7 @@ __device__ __noinline__ float2 norm_far(uint4 a, uint4 b, uint32_t mask, float e
 // lane keeps its place in the head from step to step.  Arithmetic goes two elements at a time;
 // sines, negated sines and weights (as factors) lie in shared memory with the halves of the
 // 8-element chunks apart, so that neighbours' 16-byte loads lie side by side.
-// Bound: memory (151 MB for 16384 tokens of 18 heads of 128: 22.5 us at a copy's rate); measured 29.7 us,
+// Bound: memory (151 MB for 16384 tokens of 18 heads of 128: 22.5 us at a copy's rate); measured 29.6 us,
 // 5.1 TB/s, some 250 instructions a step at 0.7 a cycle and scheduler.  On the way there: 94.7 us with
 // a head's elements in local memory (their address went to the rare function), 37 to 39 with scalar
 // arithmetic and four tokens a CTA, whatever the registers; a warp per token, steps prefetched by
@@ -735,7 +735,7 @@ moe_status_t rope_launch(const gqa_rope_plan_t* plan, const gqa_norm_t* norm, co
   // 1024 4.1 and 3.7, 2048 5.8 and 5.2, 16384 43.6 and 28.3.
   p.tokens = T >= 1024 ? 4 : 1;
   // With norms, as many as make whole waves of CTAs, as few as there can be with NR_TOKENS at most:
-  // 16384 tokens 29.7 us in one wave of 27 each, 31.3 in three of 9, 33.6 in four of 7.
+  // 16384 tokens 29.6 us in one wave of 27 each, 31.3 in three of 9, 33.6 in four of 7.
   constexpr int wave = 152 * NR_CTAS;
   if (norm) p.tokens = (T - 1) / (wave * ((T - 1) / (wave * NR_TOKENS) + 1)) + 1;
   const int ng = 512 / D, per = norm ? (n_q_heads + ng - 1) / ng + (n_k_heads + ng - 1) / ng : n_q_heads + n_k_heads;

@@ -42,7 +42,7 @@
 // The prefix pass takes the tokens of all sequences of a group as rows of one tile and masks nothing; what
 // it leaves (sums) meets each sequence's own part: with few new tokens per sequence that of the
 // decode kernel, which runs beside it on the SMs that the work of either leaves it, in the
-// join.  128 sequences over 32768 shared positions and 64 to 2000 of their own, e4m3, 60 us (18 at
+// join.  128 sequences over 32768 shared positions and 64 to 2000 of their own, e4m3, 59 us (18 at
 // the tensor cores' measured rate, 76 us for a quarter of the sequences without it): 118 CTAs of
 // the prefix pass 47 to 52, 34 of the other beside them, the join of 16 MB of sums 5, launches between.
 #include <cstring>
