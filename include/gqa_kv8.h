@@ -166,9 +166,9 @@ size_t gqa_kv8_prefix_workspace_bytes(const gqa_kv8_cache_t* cache, int n_q_head
  * sequences of one new token over 1024 shared positions take 20 us so, 11 with the bound; 24
  * prompts of 20 tokens 51 and 27).  Nor does sharing seem to pay with a group for nearly every
  * sequence, since the call counts each as work of its own, and cannot see on the host which are
- * empty: a list padded with empty groups is right, but may share nothing.  Groups out of order or range, or a sequence that contradicts the call,
- * are recorded in the error word and nothing is shared; a shared length past the page table is
- * recorded and cut.
+ * empty: a list padded with empty groups is right, but may share nothing.
+ * Groups out of order or range, or a sequence that contradicts the call, are recorded in the
+ * error word and nothing is shared; a shared length past the page table is recorded and cut.
  * Errors: as gqa_kv8_attention. */
 moe_status_t gqa_kv8_prefix_attention(const gqa_kv8_cache_t* cache, const gqa_kv8_batch_t* batch,
                                       const gqa_kv8_prefix_t* prefix, const void* q, long long q_stride, int n_q_heads,
@@ -224,10 +224,10 @@ typedef struct {
  * page_size or later.  One whose tokens begin before it (it has fallen back into them, or its row
  * is used again in the step in which it is done) is recorded and done: its tokens have slots of
  * -1, its length is 0 and it holds no pages after the step, so that the calls above write none of
- * them.  The caller lowers borrowed: to keep / page_size after a step without new tokens that
- * keeps fewer whole pages than that (the last of them, if it is kept in part, has to be replaced
- * by a copy of its own first), and to 0 after the step in which the sequence is done, before
- * another request begins in its row.  The sequence that lends pages has to hold them for as long.
+ * them.  The caller lowers borrowed, between steps: to keep / page_size after a step without new
+ * tokens that keeps fewer of the borrowed pages, which have to be whole ones if tokens are to
+ * follow; and to 0 after the step in which the sequence is done, before another request begins
+ * in its row.  The sequence that lends pages has to hold them for as long.
  * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 moe_status_t gqa_kv8_pages_step(const gqa_kv8_pages_t* pages, const gqa_kv8_pages_state_t* from,
                                 const gqa_kv8_pages_state_t* to, const int32_t* keep, const int32_t* n_new,
